@@ -208,7 +208,6 @@ def prepare(case, seed):
             s["rope"] = vc.vc_rope_init(case["rotary"], 500000.0)
         elif case["op"] == "evict":
             s["cache2"] = vc.PagedCache(s["k2"], s["v2"], s["table2"])
-            s["ws"] = vc.Workspace(vc.vc_paged_evict_workspace_bytes(s["cache"]))
         elif case["op"] == "mass":
             s["ws"] = vc.Workspace(vc.vc_paged_attn_h2o_workspace_bytes(s["cache"], s["T"], case["Hq"]))
         else:
@@ -289,7 +288,7 @@ def _evict(s):
     if own:
         from lossless_draft_verify_gb300 import vc
         vc.vc_paged_evict(s["scores"], s["cache"], s["ctx"], c["top"], c["recent"], s["cache2"], s["len2"], s["kept"],
-                          s["ws"], scores_out=s["scores2"])
+                          scores_out=s["scores2"])
         return s["kept"], s["len2"], s["k2"], s["v2"], s["scores2"]
     B, Hkv, page, most = c["B"], c["Hkv"], c["page"], s["most"]
     L = s["ctx"].long()[:, None, None]
