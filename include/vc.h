@@ -748,6 +748,136 @@ vc_status vc_gemm_rms(const void *x, const void *w, void *out, vc_dtype dt, int 
 vc_status vc_gemm_ex(const void *x, const void *w, const void *resid, void *out, vc_dtype dt, int M, int N, int K,
                      int decode_plan, void *ws, size_t ws_bytes, cudaStream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* (8) paged cache                                                           */
+/* ------------------------------------------------------------------------ */
+/*
+ * The caches above are dense: one row stride, one block length per call.  A
+ * server keeps its full cache in pages and feeds batches in which every
+ * sequence brings its own number of new tokens, one while decoding, a drafted
+ * block while verifying, hundreds while a prompt is read in (no counterpart in
+ * the paper, whose system sits in a paged server; the attention is that of the
+ * verify pass, the scores and the eviction those of H2O, source 3 on the
+ * podparley page).
+ *
+ * Pool.  k_pages, v_pages: device [n_pages][Hkv][page][d] in dt.  Slot s of
+ * sequence b (its s-th cached token) is row s % page of page
+ * block_table[b * max_blocks + s / page].  Table entries past a sequence's last
+ * used page are never read.  Rows that hold tokens are finite; slots past a
+ * sequence's end may hold any bits.  Sequences may share pages that a call only
+ * reads (a common prefix).
+ *
+ * Batch.  The T packed rows of a call belong to the sequences in order:
+ * sequence b owns rows q_start[b] .. q_start[b+1] - 1 (device int32 [B + 1],
+ * ascending, q_start[B] <= T), its chunk, possibly none.  ctx_len (device int32 [B]):
+ * tokens cached before the chunk; row i of the chunk is slot ctx_len[b] + i.
+ * Rows before q_start[0] or from q_start[B] on are left as they are.
+ *
+ * Errors on the device go to *status (one word, not cleared by the library):
+ * VC_PAGED_BAD_PAGE, a table entry outside [0, n_pages) (nothing is read or
+ * written through it; the sequence's results are unspecified), and
+ * VC_PAGED_BAD_LENGTH, lengths that do not fit: rows outside [0, T] or
+ * descending, a negative context, or more tokens than max_blocks pages hold
+ * (that sequence is treated as having no tokens).
+ *
+ * Supported: d in {64, 128}, page in {16, 32, 64, 128, 256}, any Hq that is a
+ * multiple of Hkv; fewer than 2^31 slots n_pages * Hkv * page, and T * Hq <=
+ * 2^30.
+ */
+#define VC_PAGED_BAD_PAGE 1
+#define VC_PAGED_BAD_LENGTH 2
+
+typedef struct vc_paged_cache {
+    void *k_pages, *v_pages;      /* device, 16-byte aligned */
+    const int32_t *block_table;   /* device [B][max_blocks] */
+    int32_t *status;              /* device, 1 word: VC_PAGED_* bits are ORed in */
+    int32_t B, Hkv, d, page, n_pages, max_blocks;
+    vc_dtype dt;
+} vc_paged_cache;
+
+/*
+ * Position rotation: channel pair (j, j + rotary_dim / 2), j < rotary_dim / 2,
+ * turns by position * w_j; channels from rotary_dim on pass unchanged.  turn[j]
+ * is w_j / 2 pi as a 64-bit fraction of one turn, so that the angle of any
+ * 32-bit position is reduced exactly.  A host object, passed by value.
+ */
+typedef struct vc_rope {
+    uint64_t turn[64];
+    int32_t rotary_dim;
+    int32_t reserved;
+} vc_rope;
+
+/* w_j = theta^(-2j / rotary_dim); rotary_dim a multiple of 16, 16..128. */
+vc_status vc_rope_init(vc_rope *rope, int rotary_dim, double theta);
+/* The same with the caller's frequencies, inv_freq[rotary_dim / 2] (radians per
+ * position, finite): scaled or interpolated tables. */
+vc_status vc_rope_init_freqs(vc_rope *rope, int rotary_dim, const double *inv_freq);
+
+/*
+ * vc_paged_append -- the chunk's q, k and v on their way to attention: qkv
+ * [T][(Hq + 2 Hkv) d] (the rows of a q | k | v projection) in cache->dt.
+ * Every q head goes to q_out [T][Hq][d], every k and v head into the pages at
+ * its token's slot.  With q_gain and k_gain ([d] each, cache->dt; both or
+ * neither NULL) each q and k head is first normalised,
+ *   x / sqrt(mean(x^2) + eps) * gain.
+ * Then q and k are rotated at positions[row] (device int32 [T]; NULL: the
+ * token's slot), which after an eviction is no longer the slot.  fp32
+ * arithmetic, one rounding to dt.  The tokens' pages must not be shared with
+ * another sequence of the batch.  The caller advances its lengths.
+ */
+vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gain, float eps, const vc_rope *rope,
+                          const int32_t *positions, const int32_t *q_start, const int32_t *ctx_len, int T, int Hq,
+                          const vc_paged_cache *cache, void *q_out, cudaStream_t stream);
+
+/*
+ * vc_paged_attn -- causal attention of the chunks over the pages, the chunk's
+ * own rows being in the pages already: row i of sequence b attends slots
+ * 0 .. ctx_len[b] + i, query head hq reading kv head hq / (Hq / Hkv).
+ * q, out: device [T][Hq][d] in cache->dt, 16-byte aligned.  bf16 caches run on
+ * the tensor cores (fp32 accumulation, the softmax weights rounded to bf16),
+ * fp32 caches on the CUDA cores in fp32.  sm_scale: finite, not negative.
+ */
+size_t vc_paged_attn_workspace_bytes(const vc_paged_cache *cache, int T, int Hq);
+vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_t *q_start, const int32_t *ctx_len,
+                        int T, int Hq, float sm_scale, void *out, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * vc_paged_attn_h2o -- vc_paged_attn that also accumulates the attention
+ * weight every cached token receives: for kv unit u = b * Hkv + h and slot
+ * j < ctx_len[b] + n_b,
+ *   scores[u * scores_stride + j] += sum over the chunk's rows and the query
+ *       heads of h that see j of softmax_j(q . k_j * sm_scale),
+ * with every row's final maximum and sum, in fp32, each slot summed in an order
+ * fixed by the lengths.  scores: device fp32, scores_stride >= max_blocks *
+ * page.  Sequences without rows keep their scores.
+ */
+size_t vc_paged_attn_h2o_workspace_bytes(const vc_paged_cache *cache, int T, int Hq);
+vc_status vc_paged_attn_h2o(const void *q, const vc_paged_cache *cache, const int32_t *q_start,
+                            const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out, float *scores,
+                            int scores_stride, void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/*
+ * vc_paged_evict -- vc_drop_tokens for a paged cache: of the src_len[b] tokens
+ * (device int32 [B]) of every sequence, per kv head, keep the cfg.keep_recent
+ * newest and the cfg.keep_top best of the others by score (descending, ties by
+ * ascending slot, -0 == +0, NaN below every number), n_b =
+ * vc_drop_kept_count(src_len[b], cfg) in all.  The kept rows are copied in
+ * ascending slot order to slots 0 .. n_b - 1 of dst, whose pages must be none
+ * of src's (src and dst may name one pool: the pages a server hands out for the
+ * shortened sequences; src's can then be freed, and pages shared with other
+ * sequences stay intact).  dst_len[b] = n_b (device int32 [B], not src_len);
+ * kept_idx[u * kept_stride + j] = the slot that went to slot j of unit u;
+ * scores_out, unless NULL: its score at [u * scores_out_stride + j], the
+ * accumulated scores of the shortened cache.  Entries and rows from n_b on are left
+ * as they are.
+ * scores as in vc_paged_attn_h2o.  src and dst agree in B, Hkv, d and dt; dst's
+ * max_blocks * dst's page, kept_stride and scores_out_stride are each at least
+ * min(keep_top + keep_recent, src's max_blocks * page).
+ */
+vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_cache *src, const int32_t *src_len,
+                         vc_drop_cfg cfg, const vc_paged_cache *dst, int32_t *dst_len, int32_t *kept_idx,
+                         int kept_stride, float *scores_out, int scores_out_stride, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,314 @@
+// paged.cuh -- what the paged-cache kernels share: the device view of a page
+// pool, the checks of lengths and page numbers that live on the device, and
+// the division of ragged attention work over a fixed number of CTAs.
+#pragma once
+
+#include <algorithm>
+
+#include "vc_common.cuh"
+#include "vc_internal.h"
+
+namespace vc {
+namespace paged {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNegBig = -1.0e30f;
+
+__host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// The checks and the division of work below also compile for the host, where
+// tests run them over many batches.
+#ifdef __CUDA_ARCH__
+__device__ __forceinline__ void set_flag(int32_t *status, int bit) { atomicOr(status, bit); }
+#else
+inline void set_flag(int32_t *status, int bit) { *status |= bit; }
+#endif
+__host__ __device__ inline long lmin(long a, long b) { return a < b ? a : b; }
+__host__ __device__ inline long lmax(long a, long b) { return a > b ? a : b; }
+
+// The pool as the kernels see it.  Pages hold 2^page_log2 slots.
+struct Pool {
+    void *k, *v;               // [n_pages][Hkv][page][d]
+    const int32_t *table;      // [B][max_blocks]
+    int32_t *status;
+    int32_t B, Hkv, page_log2, n_pages, max_blocks;
+
+    __host__ __device__ __forceinline__ int page() const { return 1 << page_log2; }
+    __host__ __device__ __forceinline__ long capacity() const { return (long)max_blocks << page_log2; }
+    // page number of block `blk` of sequence b; -1 (and the status bit) when
+    // the table's entry lies outside the pool
+    __host__ __device__ __forceinline__ int page_of(int b, int blk) const
+    {
+        const int p = table[(size_t)b * max_blocks + blk];
+        if ((unsigned)p < (unsigned)n_pages) return p;
+        set_flag(status, VC_PAGED_BAD_PAGE);
+        return -1;
+    }
+    // first row (of d elements) of head h in page p: 64 bits, a pool may hold
+    // more than 2^31 elements
+    __host__ __device__ __forceinline__ size_t row(int p, int h, int slot_in_page) const
+    {
+        return (((size_t)p * Hkv + h) << page_log2) + slot_in_page;
+    }
+};
+
+// One sequence of a ragged batch: its rows [tok0, tok0 + n) of the packed
+// tokens and its cached tokens.  Lengths that do not fit (rows outside the
+// packed range, a negative context, more slots than the table has) make the
+// sequence empty and set the status bit.
+struct Seq {
+    int tok0, n, ctx;
+};
+
+__host__ __device__ __forceinline__ Seq load_seq(const Pool &P, const int32_t *__restrict__ q_start,
+                                        const int32_t *__restrict__ ctx_len, int T, int b)
+{
+    Seq s;
+    s.tok0 = q_start[b];
+    const int end = q_start[b + 1];
+    s.ctx = ctx_len[b];
+    s.n = end - s.tok0;
+    const bool ok = s.tok0 >= 0 && end >= s.tok0 && end <= T && s.ctx >= 0 && (long)s.ctx + s.n <= P.capacity();
+    if (!ok) {
+        set_flag(P.status, VC_PAGED_BAD_LENGTH);
+        s.tok0 = s.n = s.ctx = 0;
+    }
+    return s;
+}
+
+// ----- division of the attention work ----------------------------------------
+// A unit is (sequence b, kv head h, row tile mt): BM consecutive rows of the
+// n * G (query, head of the group) rows that share a kv head, row = i * G + g.
+// It takes the key tiles (BN keys) its last query can see.  The units of a
+// batch, laid end to end with kUnitCost extra tiles each (loading Q, writing
+// the output), are cut into equal pieces, one per CTA: a piece may begin and
+// end inside a unit, whose partial results are then merged.  One long sequence
+// and many short ones thus fill the GPU alike, and the division depends on the
+// lengths only.
+struct WorkDim {
+    const int32_t *q_start, *ctx_len;
+    int T, G;
+    int min_tiles;     // a piece is at least this long
+};
+
+constexpr int kUnitCost = 2;
+
+// What one CTA has to do: from unit (b, h, mt), cost offset `off` within it,
+// `len` cost units on.  Written to shared memory by one warp, read by all.
+struct Piece {
+    int b, h, mt;
+    long off, len;     // off: cost already covered by earlier CTAs
+    long per;          // the length of a full piece
+};
+
+__host__ __device__ inline long piece_len(long total, int n_cta, int min_len)
+{
+    return lmax((total + n_cta - 1) / n_cta, min_len);
+}
+
+template <int BM, int BN>
+struct Units {
+    static __host__ __device__ __forceinline__ int tiles(const Seq &s, int G, int mt)
+    {
+        const long last = lmin((long)s.n * G, (long)(mt + 1) * BM) - 1;    // last row of the tile
+        return (s.ctx + (int)(last / G) + 1 + BN - 1) / BN;
+    }
+    static __host__ __device__ __forceinline__ int mtiles(const Seq &s, int G)
+    {
+        return (int)(((long)s.n * G + BM - 1) / BM);
+    }
+    static __host__ __device__ __forceinline__ long head_cost(const Seq &s, int G)
+    {
+        long c = 0;
+        const int m = mtiles(s, G);
+        for (int i = 0; i < m; ++i) c += tiles(s, G, i) + kUnitCost;
+        return c;
+    }
+    // head, row tile and offset of cost unit x of a sequence (hc: head_cost)
+    static __host__ __device__ __forceinline__ void place(const Seq &s, int G, long hc, long x, Piece &out)
+    {
+        out.h = (int)(x / hc);
+        x -= out.h * hc;
+        int mt = 0;
+        for (;;) {
+            const int t = tiles(s, G, mt) + kUnitCost;
+            if (x < t) break;
+            x -= t;
+            ++mt;
+        }
+        out.mt = mt;
+        out.off = x;
+    }
+};
+
+template <int BM, int BN>
+__device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int cta, int n_cta, Piece *out)
+{
+    using U = Units<BM, BN>;
+    const int lane = threadIdx.x & 31;
+    long total = 0;
+    for (int b0 = 0; b0 < P.B; b0 += 32) {
+        long c = 0;
+        if (b0 + lane < P.B) c = U::head_cost(load_seq(P, W.q_start, W.ctx_len, W.T, b0 + lane), W.G) * P.Hkv;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+        total += c;
+    }
+    const long per = piece_len(total, n_cta, W.min_tiles);
+    const long lo = per * cta, hi = lmin(total, lo + per);
+    if (lo >= hi) {
+        if (lane == 0) out->len = 0;
+        return;
+    }
+    long before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += 32) {
+        long hc = 0;
+        Seq s = {0, 0, 0};
+        if (b0 + lane < P.B) {
+            s = load_seq(P, W.q_start, W.ctx_len, W.T, b0 + lane);
+            hc = U::head_cost(s, W.G);
+        }
+        const long c = hc * P.Hkv;
+        long incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const long start = before + incl - c;
+        if (c > 0 && start <= lo && lo < start + c) {
+            U::place(s, W.G, hc, lo - start, *out);
+            out->b = b0 + lane;
+            out->len = hi - lo;
+            out->per = per;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+// One unit, or the part of it that falls to this CTA.
+struct Item {
+    int b, h, mt;
+    int tok0, n, ctx;      // the sequence
+    int rows;              // valid rows of the tile
+    int t_lo, t_hi;        // key tiles of this part
+    bool whole;            // the part is the whole unit: written to the output
+    bool head;             // a partial unit's first part
+    int parts;             // head: how many CTAs share the unit
+};
+
+// Walks a piece; every role of a CTA walks it alike.
+template <int BM, int BN>
+struct Walk {
+    using U = Units<BM, BN>;
+    int b, h, mt;
+    long off, left, per;
+    Seq s;
+    int m;
+
+    __host__ __device__ __forceinline__ void start(const Pool &P, const WorkDim &W, const Piece &p)
+    {
+        b = p.b;
+        h = p.h;
+        mt = p.mt;
+        off = p.off;
+        left = p.len;
+        per = p.per;
+        if (left > 0) {
+            s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
+            m = U::mtiles(s, W.G);
+        }
+    }
+    // The next part with at least one key tile; false at the piece's end.
+    __host__ __device__ __forceinline__ bool next(const Pool &P, const WorkDim &W, Item &it)
+    {
+        while (left > 0) {
+            const int nt = U::tiles(s, W.G, mt), cost = nt + kUnitCost;
+            const long take = lmin(left, (long)cost - off);
+            const long a = off, e = off + take;
+            it.b = b;
+            it.h = h;
+            it.mt = mt;
+            it.tok0 = s.tok0;
+            it.n = s.n;
+            it.ctx = s.ctx;
+            it.rows = (int)lmin((long)BM, (long)s.n * W.G - (long)mt * BM);
+            // the unit's first kUnitCost cost units carry no tile
+            it.t_lo = (int)lmax(a - kUnitCost, 0);
+            it.t_hi = (int)lmax(e - kUnitCost, 0);
+            // the first part with tiles is the CTA holding cost unit kUnitCost
+            const bool starts = a <= kUnitCost, ends = e == cost;
+            it.head = starts;
+            it.whole = starts && ends;
+            it.parts = 0;
+            if (starts && !ends) it.parts = 1 + (int)((cost - e + per - 1) / per);
+            left -= take;
+            off = 0;
+            if (++mt == m) {
+                mt = 0;
+                if (++h == P.Hkv) {
+                    h = 0;
+                    m = 0;
+                    while (left > 0 && m == 0 && ++b < P.B) {
+                        s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
+                        m = U::mtiles(s, W.G);
+                    }
+                    if (m == 0) left = 0;
+                }
+            }
+            if (it.t_hi > it.t_lo) return true;
+        }
+        return false;
+    }
+};
+
+// ----- partial results ------------------------------------------------------------
+// A CTA takes part in at most two units that others share: one that began in
+// an earlier CTA (slot 0; it is the first of the piece) and one whose first
+// part it holds (slot 1; it is the last of the piece).  desc[c] describes the
+// latter: its parts are slot 1 of CTA c and slot 0 of CTAs c + 1 ..
+// c + parts - 1; parts = 0 when there is none.
+struct PartDesc {
+    int parts, tok0, h, row0, rows, pad[3];
+};
+
+struct Parts {
+    PartDesc *desc;    // [n_cta]
+    float2 *ml;        // [n_cta][2][rows_cap]: running maximum (log2 domain) and sum
+    float *o;          // [n_cta][2][rows_cap][d], not divided by the sum
+    int rows_cap;
+
+    __device__ __forceinline__ size_t row(int cta, int slot, int r) const
+    {
+        return ((size_t)cta * 2 + slot) * rows_cap + r;
+    }
+};
+
+// ----- launchers ----------------------------------------------------------------------
+// paged_attn_simt.cu: fp32 on the CUDA cores
+int simt_rows(int T, int G);
+int simt_ctas();
+template <typename T>
+cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+                      const Parts &parts, cudaStream_t st);
+template <typename T>
+cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float2 *ml,
+                      float *scores, int scores_stride, cudaStream_t st);
+
+// paged_attn.cu: attention, with scores != null also the attention mass
+size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, bool mass);
+cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
+                 int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st);
+
+// paged_append.cu
+cudaError_t append(const Pool &P, vc_dtype dt, int d, const void *qkv, const void *q_gain, const void *k_gain,
+                   float eps, const vc_rope &rope, const int32_t *positions, const int32_t *q_start,
+                   const int32_t *ctx_len, int T, int Hq, void *q_out, cudaStream_t st);
+
+// paged_evict.cu
+cudaError_t evict(const Pool &S, const Pool &Dp, int row_bytes, const float *scores, int scores_stride,
+                  const int32_t *src_len, long top, long recent, int32_t *dst_len, int32_t *kept_idx, int kept_stride,
+                  float *scores_out, int out_stride, cudaStream_t st);
+
+}  // namespace paged
+}  // namespace vc

@@ -1,0 +1,124 @@
+// paged_attn.cu -- causal attention of ragged chunks over a paged cache.
+#include "paged.cuh"
+
+namespace vc {
+namespace paged {
+namespace {
+
+// Merge the parts of the units that several CTAs share.  blockIdx.x: the CTA
+// that holds the unit's first part; a warp per row, lane l at channels
+// 4 l (+ 128).  With maxima m_i and sums l_i: o = sum 2^(m_i - M) o_i / sum 2^(m_i - M) l_i.
+constexpr int kMergeWarps = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kMergeWarps)
+merge_kernel(Parts parts, int G, int Hq, T *__restrict__ out, float2 *__restrict__ ml_out)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const PartDesc d = parts.desc[c];
+    if (d.parts == 0) return;
+    for (int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); r < d.rows; r += gridDim.y * kMergeWarps) {
+        float M = kNegBig;
+        for (int p = lane; p < d.parts; p += 32) M = fmaxf(M, parts.ml[parts.row(c + p, p == 0 ? 1 : 0, r)].x);
+        M = warp_max(M);
+        constexpr int V = D / 32;
+        float acc[V], L = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+#pragma unroll 4
+        for (int p = 0; p < d.parts; ++p) {
+            const size_t pr = parts.row(c + p, p == 0 ? 1 : 0, r);
+            const float2 ml = parts.ml[pr];
+            const float w = exp2f(ml.x - M);
+            L = fmaf(w, ml.y, L);
+            if constexpr (V == 4) {
+                const float4 o = *reinterpret_cast<const float4 *>(parts.o + pr * D + 4 * lane);
+                acc[0] = fmaf(w, o.x, acc[0]);
+                acc[1] = fmaf(w, o.y, acc[1]);
+                acc[2] = fmaf(w, o.z, acc[2]);
+                acc[3] = fmaf(w, o.w, acc[3]);
+            } else {
+                const float2 o = *reinterpret_cast<const float2 *>(parts.o + pr * D + 2 * lane);
+                acc[0] = fmaf(w, o.x, acc[0]);
+                acc[1] = fmaf(w, o.y, acc[1]);
+            }
+        }
+        const int R = d.row0 + r;
+        const size_t row = (size_t)(d.tok0 + R / G) * Hq + d.h * G + R % G;
+        const float inv = 1.f / L;
+        T *o = out + row * D + V * lane;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = Elem<T>::from_f(acc[e] * inv);
+        if (ml_out && lane == 0) ml_out[row] = make_float2(M, inv);
+    }
+}
+
+struct WsLayout {
+    size_t desc, ml, o, rows, bytes;
+    int rows_cap, n_cta;
+};
+
+// [status | desc | partial (m, l) | partial o | (m, 1/l) of every row]
+WsLayout layout(int d, int T, int G, int Hq, bool with_rows)
+{
+    WsLayout w;
+    w.n_cta = simt_ctas();
+    const long unit = 64;
+    w.rows_cap = (int)std::min<long>(unit, (long)T * G);
+    const size_t n = (size_t)w.n_cta * 2 * w.rows_cap;
+    w.desc = kStatusBytes;
+    w.ml = w.desc + align256((size_t)w.n_cta * sizeof(PartDesc));
+    w.o = w.ml + align256(n * sizeof(float2));
+    w.rows = w.o + align256(n * d * sizeof(float));
+    w.bytes = w.rows + (with_rows ? align256((size_t)T * Hq * sizeof(float2)) : 0);
+    return w;
+}
+
+template <typename T>
+cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq, void *out, float2 *ml,
+                  cudaStream_t st)
+{
+    const dim3 grid(n_cta, cdiv(rows, kMergeWarps));
+    return d == 128 ? launch_pdl(merge_kernel<T, 128>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, ml)
+                    : launch_pdl(merge_kernel<T, 64>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, ml);
+}
+
+template <typename T>
+cudaError_t run(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *scores,
+                int scores_stride, uint8_t *ws, cudaStream_t st)
+{
+    const WsLayout w = layout(d, W.T, W.G, Hq, scores != nullptr);
+    Parts parts = {(PartDesc *)(ws + w.desc), (float2 *)(ws + w.ml), (float *)(ws + w.o), w.rows_cap};
+    float2 *ml = scores ? (float2 *)(ws + w.rows) : nullptr;
+    cudaError_t e = attn_simt<T>(P, W, d, q, Hq, sl2, out, ml, parts, st);
+    if (e == cudaSuccess) e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, ml, st);
+    if (e == cudaSuccess && scores) e = mass_simt<T>(P, W, d, q, Hq, sl2, ml, scores, scores_stride, st);
+    return e;
+}
+
+}  // namespace
+
+size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, bool mass)
+{
+    (void)dt;
+    return layout(d, T, Hq / Hkv, Hq, mass).bytes;
+}
+
+cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
+                 int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st)
+{
+    WorkDim W;
+    W.q_start = q_start;
+    W.ctx_len = ctx_len;
+    W.T = T;
+    W.G = Hq / P.Hkv;
+    W.min_tiles = 4 + kUnitCost;
+    const float sl2 = sm_scale * kLog2e;
+    return dt == VC_BF16 ? run<__nv_bfloat16>(P, W, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st)
+                         : run<float>(P, W, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st);
+}
+
+}  // namespace paged
+}  // namespace vc

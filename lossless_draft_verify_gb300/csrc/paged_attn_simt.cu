@@ -1,0 +1,386 @@
+// paged_attn_simt.cu -- causal attention of ragged chunks over a paged cache
+// and its attention mass on the CUDA cores, fp32 throughout: the path of fp32
+// caches, whose products may not be rounded to the tensor cores' input types.
+//
+//   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j),
+//   j <= ctx + i, in one pass over the keys with a running maximum and sum;
+//   mass_j = sum_i p_ij / sum_j' p_ij' in a second one, with the final ones.
+#include "paged.cuh"
+
+namespace vc {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256;
+
+// 16 bytes of a K, V or q row as fp32
+template <typename T> struct Chunk;
+template <> struct Chunk<float> {
+    static constexpr int N = 4;
+    static __device__ __forceinline__ void load(const float *p, float *o)
+    {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
+        o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w;
+    }
+};
+template <> struct Chunk<__nv_bfloat16> {
+    static constexpr int N = 8;
+    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *o)
+    {
+        const uint4 x = *reinterpret_cast<const uint4 *>(p);
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[2 * i] = bf16_lo(w[i]), o[2 * i + 1] = bf16_hi(w[i]);
+    }
+};
+
+// rows [0, n_rows) of a tile into shared memory (pitch floats apart); row r at
+// src(r), null: zeros
+template <typename T, int D, typename F>
+__device__ __forceinline__ void load_rows(float *dst, int pitch, int n_rows, F src)
+{
+    constexpr int N = Chunk<T>::N, C = D / N;
+    for (int i = threadIdx.x; i < n_rows * C; i += kThreads) {
+        const int r = i / C, c = (i % C) * N;
+        float x[N];
+        const T *p = src(r);
+        if (p) {
+            Chunk<T>::load(p + c, x);
+        } else {
+#pragma unroll
+            for (int e = 0; e < N; ++e) x[e] = 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < N; e += 4)
+            *reinterpret_cast<float4 *>(dst + r * pitch + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    }
+}
+
+template <int D, int BM, int BN>
+struct Geom {
+    static constexpr int PQ = D + 4, PP = BN + 4;      // pitches: rows 4 banks apart
+    static constexpr int SMEM = (BM * PQ + BN * PQ + BN * D + BM * PP) * 4;
+};
+
+// One CTA per piece of the batch's work (paged.cuh).  256 threads as 16 x 16:
+// thread (ty, tx) holds rows ty * RT .. + RT - 1 against keys tx + 16 j, and
+// the same rows' outputs at channels 4 tx + 64 j.
+template <typename T, int D, int BM, int BN>
+__global__ void __launch_bounds__(kThreads)
+attn_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale_log2, T *__restrict__ out,
+                 float2 *__restrict__ ml_out, Parts parts)
+{
+    constexpr int RT = BM / 16, KT = BN / 16, CT = D / 64;
+    using G = Geom<D, BM, BN>;
+    extern __shared__ __align__(16) float smf[];
+    float *sQ = smf, *sK = sQ + BM * G::PQ, *sV = sK + BN * G::PQ, *sP = sV + BN * D;
+    __shared__ Piece piece;
+    __shared__ int s_page[BN / 16];
+    pdl_wait();
+    pdl_trigger();
+    if (threadIdx.x < 32) find_piece<BM, BN>(P, W, blockIdx.x, gridDim.x, &piece);
+    __syncthreads();
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const T *pk = (const T *)P.k, *pv = (const T *)P.v;
+    Walk<BM, BN> walk;
+    walk.start(P, W, piece);
+    if (threadIdx.x == 0) parts.desc[blockIdx.x].parts = 0;
+    Item it;
+    while (walk.next(P, W, it)) {
+        const int row0 = it.mt * BM, len = it.ctx + it.n;
+        auto token_row = [&](int r) {                  // row of q / out of tile row r
+            const int R = row0 + r;
+            return ((size_t)(it.tok0 + R / W.G) * Hq + it.h * W.G + R % W.G) * D;
+        };
+        __syncthreads();
+        load_rows<T, D>(sQ, G::PQ, BM, [&](int r) { return r < it.rows ? q + token_row(r) : nullptr; });
+        float m[RT], l[RT], acc[RT][CT][4];
+        int kmax[RT];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            m[i] = kNegBig;
+            l[i] = 0.f;
+            const int r = ty * RT + i;
+            kmax[i] = r < it.rows ? it.ctx + (row0 + r) / W.G : -1;
+#pragma unroll
+            for (int j = 0; j < CT; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
+        }
+        for (int t = it.t_lo; t < it.t_hi; ++t) {
+            const int key0 = t * BN;
+            __syncthreads();
+            if (threadIdx.x < BN / 16) {
+                const int slot = key0 + threadIdx.x * 16;
+                s_page[threadIdx.x] = slot < len ? P.page_of(it.b, slot >> P.page_log2) : -1;
+            }
+            __syncthreads();
+            auto slot_row = [&](const T *base, int r) -> const T * {
+                const int pg = s_page[r >> 4], slot = key0 + r;
+                return pg >= 0 && slot < len ? base + P.row(pg, it.h, slot & (P.page() - 1)) * D : nullptr;
+            };
+            load_rows<T, D>(sK, G::PQ, BN, [&](int r) { return slot_row(pk, r); });
+            load_rows<T, D>(sV, D, BN, [&](int r) { return slot_row(pv, r); });
+            __syncthreads();
+            float s[RT][KT];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int j = 0; j < KT; ++j) s[i][j] = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                float4 a[RT], b[KT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    a[i] = *reinterpret_cast<const float4 *>(sQ + (ty * RT + i) * G::PQ + c);
+#pragma unroll
+                for (int j = 0; j < KT; ++j) b[j] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * G::PQ + c);
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) {
+                        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
+                        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
+                        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
+                        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < RT; ++i) {
+                float mx = kNegBig;
+#pragma unroll
+                for (int j = 0; j < KT; ++j) {
+                    s[i][j] = key0 + tx + 16 * j <= kmax[i] ? s[i][j] * scale_log2 : -INFINITY;
+                    mx = fmaxf(mx, s[i][j]);
+                }
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+                const float mn = fmaxf(m[i], mx), alpha = exp2f(m[i] - mn);
+                m[i] = mn;
+                float sum = 0.f;
+#pragma unroll
+                for (int j = 0; j < KT; ++j) {
+                    const float p = exp2f(s[i][j] - mn);
+                    sum += p;
+                    sP[(ty * RT + i) * G::PP + tx + 16 * j] = p;
+                }
+                l[i] = l[i] * alpha + sum;             // this thread's keys only
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] *= alpha;
+            }
+            __syncwarp();                              // a row's 16 threads are in one warp
+#pragma unroll 2
+            for (int key = 0; key < BN; key += 4) {
+                float4 p[RT];
+#pragma unroll
+                for (int i = 0; i < RT; ++i)
+                    p[i] = *reinterpret_cast<const float4 *>(sP + (ty * RT + i) * G::PP + key);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+#pragma unroll
+                    for (int j = 0; j < CT; ++j) {
+                        const float4 v = *reinterpret_cast<const float4 *>(sV + (key + kk) * D + 4 * tx + 64 * j);
+#pragma unroll
+                        for (int i = 0; i < RT; ++i) {
+                            const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
+                            acc[i][j][0] = fmaf(w, v.x, acc[i][j][0]);
+                            acc[i][j][1] = fmaf(w, v.y, acc[i][j][1]);
+                            acc[i][j][2] = fmaf(w, v.z, acc[i][j][2]);
+                            acc[i][j][3] = fmaf(w, v.w, acc[i][j][3]);
+                        }
+                    }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+#pragma unroll
+            for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+            const int r = ty * RT + i;
+            if (r >= it.rows) continue;
+            if (it.whole) {
+                T *o = out + token_row(r);
+                const float inv = 1.f / l[i];
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[4 * tx + 64 * j + e] = Elem<T>::from_f(acc[i][j][e] * inv);
+                if (ml_out && tx == 0) ml_out[token_row(r) / D] = make_float2(m[i], inv);
+            } else {
+                const size_t pr = parts.row(blockIdx.x, it.head ? 1 : 0, r);
+#pragma unroll
+                for (int j = 0; j < CT; ++j)
+                    *reinterpret_cast<float4 *>(parts.o + pr * D + 4 * tx + 64 * j) =
+                        make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+                if (tx == 0) parts.ml[pr] = make_float2(m[i], l[i]);
+            }
+        }
+        if (!it.whole && it.head && threadIdx.x == 0) {
+            PartDesc &d = parts.desc[blockIdx.x];
+            d.parts = it.parts;
+            d.tok0 = it.tok0;
+            d.h = it.h;
+            d.row0 = row0;
+            d.rows = it.rows;
+        }
+    }
+}
+
+// ----- attention mass ---------------------------------------------------------------
+// scores[b][h][slot] += sum over the rows that see the slot of p, with every
+// row's final maximum and 1 / sum.  One CTA per (b, h, 64-key tile), the
+// sequence's rows in tiles of 64; every slot is written by one thread, in an
+// order that the lengths fix.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+mass_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale_log2,
+                 const float2 *__restrict__ ml, float *__restrict__ scores, int scores_stride)
+{
+    constexpr int BM = 64, BN = 64, PQ = D + 4;
+    extern __shared__ __align__(16) float smf[];
+    float *sQ = smf, *sK = sQ + BM * PQ, *sSum = sK + BN * PQ;      // sSum [16][BN]
+    __shared__ float2 sML[BM];
+    __shared__ int s_page[BN / 16];
+    pdl_wait();
+    pdl_trigger();
+    const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
+    const T *pk = (const T *)P.k;
+    for (long u = blockIdx.x; u < (long)P.B * P.Hkv; u += gridDim.x) {
+        const int b = (int)(u / P.Hkv), h = (int)(u % P.Hkv);
+        const Seq s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
+        const int len = s.ctx + s.n;
+        if (s.n == 0) continue;
+        for (int key0 = blockIdx.y * BN; key0 < len; key0 += gridDim.y * BN) {
+            __syncthreads();
+            if (threadIdx.x < BN / 16) {
+                const int slot = key0 + threadIdx.x * 16;
+                s_page[threadIdx.x] = slot < len ? P.page_of(b, slot >> P.page_log2) : -1;
+            }
+            __syncthreads();
+            load_rows<T, D>(sK, PQ, BN, [&](int r) -> const T * {
+                const int pg = s_page[r >> 4], slot = key0 + r;
+                return pg >= 0 && slot < len ? pk + P.row(pg, h, slot & (P.page() - 1)) * D : nullptr;
+            });
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+            const long rows = (long)s.n * W.G;
+            // rows before the first one that sees the tile's first key contribute nothing
+            const long first = (long)max(key0 - s.ctx, 0) * W.G / BM * BM;
+            for (long r0 = first; r0 < rows; r0 += BM) {
+                __syncthreads();
+                auto token_row = [&](int r) {
+                    const long R = r0 + r;
+                    return (size_t)(s.tok0 + R / W.G) * Hq + h * W.G + R % W.G;
+                };
+                load_rows<T, D>(sQ, PQ, BM,
+                                [&](int r) { return r0 + r < rows ? q + token_row(r) * D : nullptr; });
+                if (threadIdx.x < BM)
+                    sML[threadIdx.x] = r0 + threadIdx.x < rows ? ml[token_row(threadIdx.x)] : make_float2(0.f, 0.f);
+                __syncthreads();
+                float a4[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) a4[i][j] = 0.f;
+#pragma unroll 4
+                for (int c = 0; c < D; c += 4) {
+                    float4 a[4], k4[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4 *>(sQ + (ty * 4 + i) * PQ + c);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) k4[j] = *reinterpret_cast<const float4 *>(sK + (tx + 16 * j) * PQ + c);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            a4[i][j] = fmaf(a[i].x, k4[j].x, a4[i][j]);
+                            a4[i][j] = fmaf(a[i].y, k4[j].y, a4[i][j]);
+                            a4[i][j] = fmaf(a[i].z, k4[j].z, a4[i][j]);
+                            a4[i][j] = fmaf(a[i].w, k4[j].w, a4[i][j]);
+                        }
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const long R = r0 + ty * 4 + i;
+                    const int kmax = R < rows ? s.ctx + (int)(R / W.G) : -1;
+                    const float2 mi = sML[ty * 4 + i];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (key0 + tx + 16 * j <= kmax) sum[j] += exp2f(a4[i][j] * scale_log2 - mi.x) * mi.y;
+                }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sSum[ty * BN + tx + 16 * j] = sum[j];
+            __syncthreads();
+            if (threadIdx.x < BN && key0 + threadIdx.x < len) {
+                float tot = 0.f;
+#pragma unroll
+                for (int i = 0; i < 16; ++i) tot += sSum[i * BN + threadIdx.x];
+                scores[(size_t)u * scores_stride + key0 + threadIdx.x] += tot;
+            }
+        }
+    }
+}
+
+template <typename T, int D, int BM, int BN>
+cudaError_t launch_attn(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float2 *ml,
+                        const Parts &parts, int n_cta, cudaStream_t st)
+{
+    auto kern = attn_simt_kernel<T, D, BM, BN>;
+    constexpr int smem = Geom<D, BM, BN>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(n_cta), dim3(kThreads), smem, st, P, W, (const T *)q, Hq, sl2, (T *)out, ml, parts);
+}
+
+template <typename T, int D>
+cudaError_t launch_mass(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, const float2 *ml,
+                        float *scores, int scores_stride, cudaStream_t st)
+{
+    auto kern = mass_simt_kernel<T, D>;
+    constexpr int smem = (2 * 64 * (D + 4) + 16 * 64) * 4;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    // about six CTAs per SM over the units; a CTA strides over its unit's key tiles
+    const int units = (int)std::min<long>((long)P.B * P.Hkv, 1 << 20);
+    const int per_unit = std::max(1, std::min(6 * device_sm_count() / units, 65535));
+    return launch_pdl(kern, dim3(units, per_unit), dim3(kThreads), smem, st, P, W, (const T *)q, Hq, sl2, ml, scores,
+                      scores_stride);
+}
+
+}  // namespace
+
+// rows a CTA holds: 64, or 16 when no unit of the batch can have more
+int simt_rows(int T, int G) { return (long)T * G <= 16 ? 16 : 64; }
+int simt_ctas() { return 2 * device_sm_count(); }
+
+template <typename T>
+cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+                      const Parts &parts, cudaStream_t st)
+{
+    const int n = simt_ctas();
+    if (simt_rows(W.T, W.G) == 16)
+        return d == 128 ? launch_attn<T, 128, 16, 64>(P, W, q, Hq, sl2, out, ml, parts, n, st)
+                        : launch_attn<T, 64, 16, 64>(P, W, q, Hq, sl2, out, ml, parts, n, st);
+    return d == 128 ? launch_attn<T, 128, 64, 32>(P, W, q, Hq, sl2, out, ml, parts, n, st)
+                    : launch_attn<T, 64, 64, 32>(P, W, q, Hq, sl2, out, ml, parts, n, st);
+}
+
+template <typename T>
+cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float2 *ml,
+                      float *scores, int scores_stride, cudaStream_t st)
+{
+    return d == 128 ? launch_mass<T, 128>(P, W, q, Hq, sl2, ml, scores, scores_stride, st)
+                    : launch_mass<T, 64>(P, W, q, Hq, sl2, ml, scores, scores_stride, st);
+}
+
+template cudaError_t attn_simt<float>(const Pool &, const WorkDim &, int, const void *, int, float, void *, float2 *,
+                                      const Parts &, cudaStream_t);
+template cudaError_t attn_simt<__nv_bfloat16>(const Pool &, const WorkDim &, int, const void *, int, float, void *,
+                                              float2 *, const Parts &, cudaStream_t);
+template cudaError_t mass_simt<float>(const Pool &, const WorkDim &, int, const void *, int, float, const float2 *,
+                                      float *, int, cudaStream_t);
+template cudaError_t mass_simt<__nv_bfloat16>(const Pool &, const WorkDim &, int, const void *, int, float,
+                                              const float2 *, float *, int, cudaStream_t);
+
+}  // namespace paged
+}  // namespace vc

@@ -1,0 +1,271 @@
+// paged_evict.cu -- eviction from a paged cache by accumulated attention
+// weight: per (sequence, kv head) the `recent` newest slots and the `top`
+// best-scored older ones move, in ascending order, to other pages.
+//
+// Selection is exact: the kept set is the largest by (score descending, slot
+// ascending).  A cluster of eight CTAs takes one (sequence, head): an
+// MSB-first radix select (11 + 11 + 10 bits of an order-preserving integer
+// image of the scores) with one histogram per CTA in shared memory, summed
+// over the cluster through distributed shared memory, finds the threshold;
+// counts exchanged the same way give every CTA the place of its first kept
+// slot, and an ordered block scan writes the kept slots and their scores.  The
+// scores are read once per pass, from L2 after the first.  A second kernel moves the rows:
+// one read and one write of every kept row, which is what bounds the call.
+#include <cooperative_groups.h>
+
+#include "paged.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace vc {
+namespace paged {
+namespace {
+
+constexpr int kCluster = 8;
+constexpr int kThreads = 512;
+constexpr int kBins = 2048;
+
+// larger score -> larger key; -0 and +0 are one score, NaN is below every number
+__device__ __forceinline__ uint32_t score_key(float s)
+{
+    if (s != s) return 0u;
+    const uint32_t u = s == 0.f ? 0u : __float_as_uint(s);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+struct EvictParams {
+    const float *scores;
+    const int32_t *src_len;
+    int32_t *dst_len, *kept_idx;
+    float *scores_out;
+    int scores_stride, kept_stride, out_stride;
+    long top, recent;
+};
+
+// tokens of sequence b; 0 (and the status bit) when they do not fit the table
+__device__ __forceinline__ int src_tokens(const Pool &S, const int32_t *src_len, int b)
+{
+    const int L = src_len[b];
+    if (L >= 0 && L <= S.capacity()) return L;
+    atomicOr(S.status, VC_PAGED_BAD_LENGTH);
+    return 0;
+}
+
+// inclusive scan over the block's threads
+__device__ __forceinline__ int block_scan(int v, int *warp_sums)
+{
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int up = __shfl_up_sync(0xffffffffu, v, o);
+        if (lane >= o) v += up;
+    }
+    __syncthreads();
+    if (lane == 31) warp_sums[warp] = v;
+    __syncthreads();
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w)
+        if (w < warp) before += warp_sums[w];
+    return v + before;
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+select_kernel(Pool S, EvictParams E)
+{
+    __shared__ int hist[kBins];
+    __shared__ int warp_sums[kThreads / 32];
+    __shared__ int s_digit, s_above;
+    __shared__ int s_count[2];                         // this CTA's slots above / at the threshold
+    cg::cluster_group cluster = cg::this_cluster();
+    pdl_wait();
+    pdl_trigger();
+    const int unit = blockIdx.x / kCluster, rank = (int)cluster.block_rank();
+    const int b = unit / S.Hkv;
+    const int L = src_tokens(S, E.src_len, b);
+    const int recent = (int)min(E.recent, (long)L), cand = L - recent;
+    const int top = (int)min(E.top, (long)cand), keep = top + recent;
+    const float *sc = E.scores + (size_t)unit * E.scores_stride;
+    int32_t *kept = E.kept_idx + (size_t)unit * E.kept_stride;
+    float *sc_out = E.scores_out ? E.scores_out + (size_t)unit * E.out_stride : nullptr;
+    if (unit % S.Hkv == 0 && rank == 0 && threadIdx.x == 0) E.dst_len[b] = keep;
+    // this CTA's candidates [lo, hi), a multiple of the block size but for the last
+    const int seg = cdiv(cdiv(cand, kCluster), kThreads) * kThreads;
+    const int lo = min(cand, rank * seg), hi = min(cand, lo + seg);
+
+    uint32_t prefix = 0;
+    int remaining = top;                               // still to be taken among keys that match the prefix
+    if (top > 0 && top < cand) {
+        int shift = 32;
+#pragma unroll 1
+        for (int pass = 0; pass < 3; ++pass) {
+            const int width = pass == 2 ? 10 : 11, bins = 1 << width;
+            shift -= width;
+            for (int i = threadIdx.x; i < bins; i += kThreads) hist[i] = 0;
+            __syncthreads();
+            for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
+                const uint32_t key = score_key(sc[i]);
+                if (pass == 0 || (key >> (shift + width)) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+            }
+            cluster.sync();
+            // totals from the highest digit down, kBins / kThreads digits per thread
+            constexpr int PER = kBins / kThreads;
+            int cnt[PER], sum = 0;
+#pragma unroll
+            for (int e = 0; e < PER; ++e) {
+                const int dgt = bins - 1 - (threadIdx.x * PER + e);
+                int c = 0;
+                if (dgt >= 0)
+#pragma unroll
+                    for (int r = 0; r < kCluster; ++r) c += *cluster.map_shared_rank(&hist[dgt], r);
+                cnt[e] = c;
+                sum += c;
+            }
+            const int incl = block_scan(sum, warp_sums);
+            int above = incl - sum;
+            if (above < remaining && remaining <= incl) {
+#pragma unroll
+                for (int e = 0; e < PER; ++e) {
+                    if (above < remaining && remaining <= above + cnt[e]) {
+                        s_digit = bins - 1 - (threadIdx.x * PER + e);
+                        s_above = above;
+                    }
+                    above += cnt[e];
+                }
+            }
+            cluster.sync();                            // the histograms have been read; s_digit is visible
+            prefix = (prefix << width) | (uint32_t)s_digit;
+            remaining -= s_above;
+        }
+    }
+    // prefix is now the threshold key; of the slots that hold it the first
+    // `remaining` are kept.  top = 0 keeps none, top = cand all.
+    const bool none = top == 0, all = top == cand;
+    int above = 0, at = 0;
+    for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
+        const uint32_t key = score_key(sc[i]);
+        above += all || (!none && key > prefix);
+        at += !all && !none && key == prefix;
+    }
+    if (threadIdx.x < 2) s_count[threadIdx.x] = 0;
+    __syncthreads();
+    above = (int)__reduce_add_sync(0xffffffffu, (unsigned)above);
+    at = (int)__reduce_add_sync(0xffffffffu, (unsigned)at);
+    if ((threadIdx.x & 31) == 0) {
+        atomicAdd(&s_count[0], above);
+        atomicAdd(&s_count[1], at);
+    }
+    cluster.sync();
+    int above_before = 0, at_before = 0;
+    for (int r = 0; r < rank; ++r) {
+        above_before += *cluster.map_shared_rank(&s_count[0], r);
+        at_before += *cluster.map_shared_rank(&s_count[1], r);
+    }
+    // ordered write: kept slots above the threshold and the first `remaining` at it
+    int base = above_before + min(at_before, remaining), at_base = at_before;
+    for (int i0 = lo; i0 < hi; i0 += kThreads) {
+        const int i = i0 + threadIdx.x;
+        const float s = i < hi ? sc[i] : 0.f;
+        const uint32_t key = score_key(s);
+        const bool gt = i < hi && (all || (!none && key > prefix));
+        const bool eq = i < hi && !all && !none && key == prefix;
+        // both counts in one scan: at most kThreads of each
+        const int incl = block_scan((gt ? 1 : 0) | (eq ? 1 << 16 : 0), warp_sums);
+        const int gt_i = incl & 0xffff, eq_i = incl >> 16;
+        const int eq_room = max(0, remaining - at_base);           // ties this step may still keep
+        const int eq_kept = min(eq_i, eq_room);
+        if (gt || (eq && eq_i <= eq_room)) {
+            const int j = base + gt_i + eq_kept - 1;
+            kept[j] = i;
+            if (sc_out) sc_out[j] = s;
+        }
+        // totals of the step
+        __syncthreads();
+        if (threadIdx.x == kThreads - 1) {
+            s_digit = gt_i + eq_kept;
+            s_above = eq_i;
+        }
+        __syncthreads();
+        base += s_digit;
+        at_base += s_above;
+    }
+    for (int i = rank * kThreads + threadIdx.x; i < recent; i += kCluster * kThreads) {
+        kept[top + i] = cand + i;
+        if (sc_out) sc_out[top + i] = sc[cand + i];
+    }
+    cluster.sync();                                    // no CTA leaves while its counts may be read
+}
+
+// Rows of kept slots from the source pages to the destination's.  16 bytes per
+// lane; kRows rows of K and V are in flight per thread.
+constexpr int kMoveThreads = 256, kRows = 4;
+
+__global__ void __launch_bounds__(kMoveThreads)
+move_kernel(Pool S, Pool Dp, EvictParams E, int row_bytes, int blocks_per_unit)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int unit = blockIdx.x / blocks_per_unit, part = blockIdx.x % blocks_per_unit;
+    const int b = unit / S.Hkv, h = unit % S.Hkv;
+    const int L = src_tokens(S, E.src_len, b);
+    const int recent = (int)min(E.recent, (long)L);
+    const int keep = (int)min(E.top, (long)(L - recent)) + recent;
+    const int32_t *kept = E.kept_idx + (size_t)unit * E.kept_stride;
+    const int lanes = row_bytes / 16, per = kMoveThreads / lanes;
+    const int lane = threadIdx.x % lanes, g = threadIdx.x / lanes;
+    for (int j0 = part * per * kRows; j0 < keep; j0 += blocks_per_unit * per * kRows) {
+        uint4 kx[kRows], vx[kRows];
+        size_t dst[kRows];
+        bool on[kRows];
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int j = j0 + i * per + g;
+            on[i] = j < keep;
+            if (!on[i]) continue;
+            const int slot = kept[j];
+            const int ps = S.page_of(b, slot >> S.page_log2), pd = Dp.page_of(b, j >> Dp.page_log2);
+            on[i] = ps >= 0 && pd >= 0;
+            if (!on[i]) continue;
+            const size_t src = S.row(ps, h, slot & (S.page() - 1)) * row_bytes + lane * 16;
+            dst[i] = Dp.row(pd, h, j & (Dp.page() - 1)) * row_bytes + lane * 16;
+            kx[i] = ldg_stream((const uint8_t *)S.k + src);
+            vx[i] = ldg_stream((const uint8_t *)S.v + src);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+            if (on[i]) {
+                *reinterpret_cast<uint4 *>((uint8_t *)Dp.k + dst[i]) = kx[i];
+                *reinterpret_cast<uint4 *>((uint8_t *)Dp.v + dst[i]) = vx[i];
+            }
+    }
+}
+
+}  // namespace
+
+cudaError_t evict(const Pool &S, const Pool &Dp, int row_bytes, const float *scores, int scores_stride,
+                  const int32_t *src_len, long top, long recent, int32_t *dst_len, int32_t *kept_idx, int kept_stride,
+                  float *scores_out, int out_stride, cudaStream_t st)
+{
+    EvictParams E;
+    E.scores = scores;
+    E.src_len = src_len;
+    E.dst_len = dst_len;
+    E.kept_idx = kept_idx;
+    E.scores_out = scores_out;
+    E.scores_stride = scores_stride;
+    E.kept_stride = kept_stride;
+    E.out_stride = out_stride;
+    E.top = top;
+    E.recent = recent;
+    const int units = S.B * S.Hkv;
+    cudaError_t e = launch_pdl(select_kernel, dim3(units * kCluster), dim3(kThreads), 0, st, S, E);
+    if (e != cudaSuccess) return e;
+    // about 12 CTAs per SM, none without a row to move
+    const long most = std::min<long>((long)S.max_blocks << S.page_log2, top + recent);
+    const int per = kMoveThreads / (row_bytes / 16) * kRows;
+    const int bpu = (int)std::max<long>(1, std::min<long>(cdiv(most, per), cdiv(12l * device_sm_count(), units)));
+    return launch_pdl(move_kernel, dim3((unsigned)units * bpu), dim3(kMoveThreads), 0, st, S, Dp, E, row_bytes, bpu);
+}
+
+}  // namespace paged
+}  // namespace vc

@@ -1,7 +1,10 @@
 // vc_api.cu -- the C-ABI entry points declared in include/vc.h: host-side
 // argument validation, then dispatch to the kernel launchers.
+#include <cfloat>
+#include <cmath>
 #include <cstring>
 
+#include "paged.cuh"
 #include "vc_common.cuh"
 #include "vc_internal.h"
 
@@ -396,6 +399,159 @@ vc_status vc_swap_in_rows(void *dst_dev, const void *src_pinned_host, size_t row
     }
     if (done && cudaEventRecord(done, side_stream) != cudaSuccess) return VC_ERR_CUDA;
     return VC_OK;
+}
+
+// ---- paged cache ----
+
+namespace {
+
+bool paged_ok(const vc_paged_cache *c)
+{
+    if (!c || !c->k_pages || !c->v_pages || !c->block_table || !c->status) return false;
+    if (c->B <= 0 || c->Hkv <= 0 || c->n_pages <= 0 || c->max_blocks <= 0 || c->page <= 0) return false;
+    if (!dtype_ok(c->dt)) return false;
+    return aligned(c->k_pages, 16) && aligned(c->v_pages, 16) && aligned(c->block_table, 4) && aligned(c->status, 4);
+}
+
+// valid but not implemented: head sizes, page sizes, pools past 31-bit slot numbers
+bool paged_supported(const vc_paged_cache *c)
+{
+    if (c->d != 64 && c->d != 128) return false;
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return false;
+    constexpr int64_t kMax = INT32_MAX;
+    return (int64_t)c->n_pages * c->page <= kMax / c->Hkv && c->max_blocks <= kMax / c->page &&
+           c->B <= kMax / 64 / c->Hkv;
+}
+
+bool paged_heads_ok(const vc_paged_cache *c, int T, int Hq)
+{
+    return T >= 0 && Hq > 0 && Hq % c->Hkv == 0;
+}
+
+bool paged_rows_ok(int T, int Hq) { return (int64_t)T * Hq <= (1 << 30); }
+
+paged::Pool paged_pool(const vc_paged_cache *c)
+{
+    paged::Pool P;
+    P.k = c->k_pages;
+    P.v = c->v_pages;
+    P.table = c->block_table;
+    P.status = c->status;
+    P.B = c->B;
+    P.Hkv = c->Hkv;
+    P.page_log2 = 0;
+    while ((1 << P.page_log2) < c->page) ++P.page_log2;
+    P.n_pages = c->n_pages;
+    P.max_blocks = c->max_blocks;
+    return P;
+}
+
+size_t paged_attn_ws(const vc_paged_cache *c, int T, int Hq, bool mass)
+{
+    if (!paged_ok(c) || !paged_supported(c) || !paged_heads_ok(c, T, Hq) || !paged_rows_ok(T, Hq)) return 0;
+    return paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, mass);
+}
+
+vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t *q_start, const int32_t *ctx_len,
+                          int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws,
+                          size_t ws_bytes, cudaStream_t stream)
+{
+    if (!paged_ok(c) || !q || !q_start || !ctx_len || !out || !ws || !paged_heads_ok(c, T, Hq)) return VC_ERR_INVALID;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
+    if (!(sm_scale >= 0.f) || sm_scale > FLT_MAX) return VC_ERR_INVALID;
+    if (!paged_supported(c) || !paged_rows_ok(T, Hq)) return VC_ERR_UNSUPPORTED;
+    if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
+    if (ws_bytes < paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, scores != nullptr)) return VC_ERR_INVALID;
+    if (T == 0) return VC_OK;
+    return cuda_status(paged::attn(paged_pool(c), c->dt, c->d, q, q_start, ctx_len, T, Hq, sm_scale, out, scores,
+                                   scores_stride, ws, stream));
+}
+
+}  // namespace
+
+vc_status vc_rope_init_freqs(vc_rope *rope, int rotary_dim, const double *inv_freq)
+{
+    if (!rope || !inv_freq || rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16) return VC_ERR_INVALID;
+    vc_rope r = {};
+    r.rotary_dim = rotary_dim;
+    for (int j = 0; j < rotary_dim / 2; ++j) {
+        if (!std::isfinite(inv_freq[j])) return VC_ERR_INVALID;
+        // the fraction of a turn in [0, 1), times 2^64 (a fraction that rounds up to one turn is none)
+        const double turns = inv_freq[j] / 6.283185307179586476925287;
+        const double scaled = std::ldexp(turns - std::floor(turns), 64);
+        r.turn[j] = scaled >= 18446744073709551616.0 ? 0 : (uint64_t)scaled;
+    }
+    *rope = r;
+    return VC_OK;
+}
+
+vc_status vc_rope_init(vc_rope *rope, int rotary_dim, double theta)
+{
+    if (!rope || rotary_dim < 16 || rotary_dim > 128 || rotary_dim % 16) return VC_ERR_INVALID;
+    if (!(theta > 0.0) || !std::isfinite(theta)) return VC_ERR_INVALID;
+    double f[64];
+    for (int j = 0; j < rotary_dim / 2; ++j) f[j] = std::pow(theta, -2.0 * j / rotary_dim);
+    return vc_rope_init_freqs(rope, rotary_dim, f);
+}
+
+vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gain, float eps, const vc_rope *rope,
+                          const int32_t *positions, const int32_t *q_start, const int32_t *ctx_len, int T, int Hq,
+                          const vc_paged_cache *cache, void *q_out, cudaStream_t stream)
+{
+    if (!paged_ok(cache) || !qkv || !rope || !q_start || !ctx_len || !q_out) return VC_ERR_INVALID;
+    if (!paged_heads_ok(cache, T, Hq) || (q_gain == nullptr) != (k_gain == nullptr)) return VC_ERR_INVALID;
+    if (!(eps >= 0.f) || !aligned(qkv, 16) || !aligned(q_out, 16)) return VC_ERR_INVALID;
+    if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > cache->d) return VC_ERR_INVALID;
+    if (!paged_supported(cache) || !paged_rows_ok(T, Hq)) return VC_ERR_UNSUPPORTED;
+    if (T == 0) return VC_OK;
+    return cuda_status(paged::append(paged_pool(cache), cache->dt, cache->d, qkv, q_gain, k_gain, eps, *rope, positions,
+                                     q_start, ctx_len, T, Hq, q_out, stream));
+}
+
+size_t vc_paged_attn_workspace_bytes(const vc_paged_cache *cache, int T, int Hq)
+{
+    return paged_attn_ws(cache, T, Hq, false);
+}
+
+vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_t *q_start, const int32_t *ctx_len,
+                        int T, int Hq, float sm_scale, void *out, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    return paged_attn_call(q, cache, q_start, ctx_len, T, Hq, sm_scale, out, nullptr, 0, ws, ws_bytes, stream);
+}
+
+size_t vc_paged_attn_h2o_workspace_bytes(const vc_paged_cache *cache, int T, int Hq)
+{
+    return paged_attn_ws(cache, T, Hq, true);
+}
+
+vc_status vc_paged_attn_h2o(const void *q, const vc_paged_cache *cache, const int32_t *q_start,
+                            const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out, float *scores,
+                            int scores_stride, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!scores) return VC_ERR_INVALID;
+    return paged_attn_call(q, cache, q_start, ctx_len, T, Hq, sm_scale, out, scores, scores_stride, ws, ws_bytes,
+                           stream);
+}
+
+vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_cache *src, const int32_t *src_len,
+                         vc_drop_cfg cfg, const vc_paged_cache *dst, int32_t *dst_len, int32_t *kept_idx,
+                         int kept_stride, float *scores_out, int scores_out_stride, cudaStream_t stream)
+{
+    if (!scores || !paged_ok(src) || !paged_ok(dst) || !src_len || !dst_len || !kept_idx) return VC_ERR_INVALID;
+    if (src_len == dst_len || scores == scores_out) return VC_ERR_INVALID;
+    if (src->B != dst->B || src->Hkv != dst->Hkv || src->d != dst->d || src->dt != dst->dt) return VC_ERR_INVALID;
+    if (cfg.keep_top < 0 || cfg.keep_recent < 0) return VC_ERR_INVALID;
+    if (!paged_supported(src) || !paged_supported(dst)) return VC_ERR_UNSUPPORTED;
+    const int64_t cap = (int64_t)src->max_blocks * src->page;
+    // neither count can matter past the capacity (and the sum stays in range)
+    const int64_t top = cfg.keep_top < cap ? cfg.keep_top : cap, recent = cfg.keep_recent < cap ? cfg.keep_recent : cap;
+    const int64_t most = top + recent < cap ? top + recent : cap;
+    if (scores_stride < cap || kept_stride < most || (scores_out && scores_out_stride < most) ||
+        (int64_t)dst->max_blocks * dst->page < most)
+        return VC_ERR_INVALID;
+    return cuda_status(paged::evict(paged_pool(src), paged_pool(dst), src->d * (int)esize(src->dt), scores,
+                                    scores_stride, src_len, top, recent, dst_len, kept_idx, kept_stride, scores_out,
+                                    scores_out_stride, stream));
 }
 
 }  // extern "C"

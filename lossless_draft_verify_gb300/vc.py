@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libvc.so")
 VC_OK, VC_ERR_INVALID, VC_ERR_UNSUPPORTED, VC_ERR_CUDA, VC_ERR_TIMEOUT = 0, 1, 2, 3, 4
 VC_BF16, VC_F32 = 0, 1
 VC_CACHE_KIVI, VC_CACHE_DENSE = 0, 1
+VC_PAGED_BAD_PAGE, VC_PAGED_BAD_LENGTH = 1, 2
 
 c_void_p, c_int, c_float, c_size_t, c_int64 = (ctypes.c_void_p, ctypes.c_int, ctypes.c_float,
                                                 ctypes.c_size_t, ctypes.c_int64)
@@ -50,6 +51,16 @@ class CacheView(ctypes.Structure):
     _fields_ = [("kind", c_int), ("kivi", ctypes.POINTER(QCacheC)), ("k", c_void_p), ("v", c_void_p),
                 ("dt", c_int), ("seq_len", c_void_p), ("B", c_int32), ("Hkv", c_int32), ("d", c_int32),
                 ("L_stride", c_int32), ("max_len", c_int32), ("flags", c_int32)]
+
+
+class PagedCacheC(ctypes.Structure):
+    _fields_ = [("k_pages", c_void_p), ("v_pages", c_void_p), ("block_table", c_void_p), ("status", c_void_p),
+                ("B", c_int32), ("Hkv", c_int32), ("d", c_int32), ("page", c_int32), ("n_pages", c_int32),
+                ("max_blocks", c_int32), ("dt", c_int)]
+
+
+class Rope(ctypes.Structure):
+    _fields_ = [("turn", ctypes.c_uint64 * 64), ("rotary_dim", c_int32), ("reserved", c_int32)]
 
 
 class DecoderCfg(ctypes.Structure):
@@ -178,6 +189,23 @@ def load() -> ctypes.CDLL:
     L.vc_kv_unpack.argtypes = [P, P, c_int64, c_int, P]
     L.vc_kv_writeback_packed.restype = c_int
     L.vc_kv_writeback_packed.argtypes = [P, P, c_int, c_int, c_int, c_int, c_int, P, P, P, P, c_int, P, P]
+    PC = ctypes.POINTER(PagedCacheC)
+    L.vc_rope_init.restype = c_int
+    L.vc_rope_init.argtypes = [ctypes.POINTER(Rope), c_int, ctypes.c_double]
+    L.vc_rope_init_freqs.restype = c_int
+    L.vc_rope_init_freqs.argtypes = [ctypes.POINTER(Rope), c_int, ctypes.POINTER(ctypes.c_double)]
+    L.vc_paged_append.restype = c_int
+    L.vc_paged_append.argtypes = [P, P, P, c_float, ctypes.POINTER(Rope), P, P, P, c_int, c_int, PC, P, P]
+    L.vc_paged_attn_workspace_bytes.restype = c_size_t
+    L.vc_paged_attn_workspace_bytes.argtypes = [PC, c_int, c_int]
+    L.vc_paged_attn.restype = c_int
+    L.vc_paged_attn.argtypes = [P, PC, P, P, c_int, c_int, c_float, P, P, c_size_t, P]
+    L.vc_paged_attn_h2o_workspace_bytes.restype = c_size_t
+    L.vc_paged_attn_h2o_workspace_bytes.argtypes = [PC, c_int, c_int]
+    L.vc_paged_attn_h2o.restype = c_int
+    L.vc_paged_attn_h2o.argtypes = [P, PC, P, P, c_int, c_int, c_float, P, P, c_int, P, c_size_t, P]
+    L.vc_paged_evict.restype = c_int
+    L.vc_paged_evict.argtypes = [P, c_int, PC, P, DropCfg, PC, P, P, c_int, P, c_int, P]
     _lib = L
     return L
 
@@ -194,7 +222,9 @@ EXPORTED = ["vc_status_str", "vc_version", "vc_check", "vc_workspace_init", "vc_
             "vc_swap_in_paced", "vc_gemm_argmax", "vc_accept_tiles", "vc_decoder_verify",
             "vc_kv_packed_row_bytes", "vc_kv_pack", "vc_kv_unpack", "vc_kv_writeback_packed",
             "vc_verify_attn_h2o_workspace_bytes", "vc_verify_attn_h2o", "vc_decoder_set_layer_events",
-            "vc_gemm_swiglu", "vc_swap_in_rows", "vc_gemm_rms"]
+            "vc_gemm_swiglu", "vc_swap_in_rows", "vc_gemm_rms", "vc_rope_init", "vc_rope_init_freqs",
+            "vc_paged_append", "vc_paged_attn_workspace_bytes", "vc_paged_attn",
+            "vc_paged_attn_h2o_workspace_bytes", "vc_paged_attn_h2o", "vc_paged_evict"]
 
 TRACE_KINDS = ["gemm_qkv", "gemm_o", "gemm_gate_up", "gemm_down", "gemm_head", "draft_attn", "verify_attn"]
 
@@ -731,3 +761,138 @@ def vc_swap_in_paced(dst: torch.Tensor, src_pinned: torch.Tensor, gbps: float, p
         ev = done_event.cuda_event
     _check(load().vc_swap_in_paced(dst.data_ptr(), src_pinned.data_ptr(), n, float(gbps), int(chunk_bytes),
                                    pace_ws.data_ptr(), _stream(stream), ev), "vc_swap_in_paced")
+
+
+# ------------------------------------------------------------- paged cache --
+
+class PagedCache:
+    """A page pool and the block table of one batch (include/vc.h,
+    vc_paged_cache): k, v [n_pages][Hkv][page][d], block_table int32
+    [B][max_blocks].  The tensors stay the caller's; several caches may name
+    one pool."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor):
+        assert k.dim() == 4 and k.shape == v.shape and k.dtype == v.dtype and k.device == v.device
+        assert k.is_contiguous() and v.is_contiguous()
+        assert block_table.dim() == 2 and block_table.dtype == torch.int32 and block_table.is_contiguous()
+        assert block_table.device == k.device
+        self.k, self.v, self.block_table = k, v, block_table
+        self.n_pages, self.Hkv, self.page, self.d = k.shape
+        self.B, self.max_blocks = block_table.shape
+        self.dtype, self.device = k.dtype, k.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.c = PagedCacheC(k.data_ptr(), v.data_ptr(), block_table.data_ptr(), self.status.data_ptr(), self.B,
+                             self.Hkv, self.d, self.page, self.n_pages, self.max_blocks, _dt(k))
+
+    @property
+    def slots(self) -> int:
+        """Slots the block table can hold per sequence."""
+        return self.max_blocks * self.page
+
+    def _check(self, *tensors):
+        """Contiguous tensors on the pool's device, which is the current one."""
+        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+            raise ValueError(f"the pool is on {self.device}, the current device is {torch.cuda.current_device()}")
+        for t in tensors:
+            if t is not None and (t.device != self.device or not t.is_contiguous()):
+                raise ValueError("tensors must be contiguous and on the pool's device")
+
+    def _check_batch(self, q_start, ctx_len):
+        if q_start.dtype != torch.int32 or ctx_len.dtype != torch.int32:
+            raise TypeError("q_start and ctx_len are int32")
+        if q_start.shape != (self.B + 1,) or ctx_len.shape != (self.B,):
+            raise ValueError(f"q_start [{self.B + 1}] and ctx_len [{self.B}] expected")
+
+
+def vc_rope_init(rotary_dim: int, theta: float) -> Rope:
+    r = Rope()
+    _check(load().vc_rope_init(ctypes.byref(r), int(rotary_dim), float(theta)), "vc_rope_init")
+    return r
+
+
+def vc_rope_init_freqs(inv_freq) -> Rope:
+    """inv_freq: radians per position of the rotary_dim / 2 channel pairs."""
+    f = [float(x) for x in inv_freq]
+    r = Rope()
+    _check(load().vc_rope_init_freqs(ctypes.byref(r), 2 * len(f), (ctypes.c_double * max(len(f), 1))(*f)),
+           "vc_rope_init_freqs")
+    return r
+
+
+def vc_paged_append(qkv, cache: PagedCache, q_start, ctx_len, q_out, rope: Rope, positions=None, q_gain=None,
+                    k_gain=None, eps: float = 1e-6, stream=None):
+    """qkv [T][(Hq + 2 Hkv) d] -> q_out [T][Hq][d] and the cache's pages, with
+    per-head RMS norm (q_gain, k_gain [d]; both or neither) and rotation at
+    positions int32 [T] (None: the tokens' slots)."""
+    T, Hq, d = q_out.shape
+    cache._check(qkv, q_start, ctx_len, q_out, positions, q_gain, k_gain)
+    cache._check_batch(q_start, ctx_len)
+    if d != cache.d or qkv.numel() != T * (Hq + 2 * cache.Hkv) * d:
+        raise ValueError(f"qkv {tuple(qkv.shape)} and q_out {tuple(q_out.shape)} do not fit {cache.Hkv} kv heads")
+    for t, n in ((qkv, None), (q_out, None), (q_gain, d), (k_gain, d)):
+        if t is not None and (t.dtype != cache.dtype or (n is not None and t.numel() != n)):
+            raise TypeError("qkv, q_out and the gains have the cache's dtype, the gains d entries")
+    if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
+        raise TypeError("positions is int32 [T]")
+    _check(load().vc_paged_append(qkv.data_ptr(), _ptr(q_gain), _ptr(k_gain), float(eps), ctypes.byref(rope),
+                                  _ptr(positions), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
+                                  ctypes.byref(cache.c), q_out.data_ptr(), _stream(stream)), "vc_paged_append")
+
+
+def vc_paged_attn_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
+    return int(load().vc_paged_attn_workspace_bytes(ctypes.byref(cache.c), T, Hq))
+
+
+def vc_paged_attn_h2o_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
+    return int(load().vc_paged_attn_h2o_workspace_bytes(ctypes.byref(cache.c), T, Hq))
+
+
+def _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores=None):
+    cache._check(q, q_start, ctx_len, out, ws.buf, scores)
+    cache._check_batch(q_start, ctx_len)
+    if q.dim() != 3 or q.shape != out.shape or q.shape[2] != cache.d:
+        raise ValueError(f"q and out [T][Hq][{cache.d}] expected")
+    if q.dtype != cache.dtype or out.dtype != cache.dtype:
+        raise TypeError("q and out have the cache's dtype")
+    return q.shape[0], q.shape[1]
+
+
+def vc_paged_attn(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, ws: Workspace, stream=None):
+    """Causal attention of the batch's chunks over the pages: q, out [T][Hq][d],
+    q_start int32 [B + 1], ctx_len int32 [B]."""
+    T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws)
+    _check(load().vc_paged_attn(q.data_ptr(), ctypes.byref(cache.c), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
+                                float(sm_scale), out.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
+           "vc_paged_attn")
+
+
+def vc_paged_attn_h2o(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, scores, ws: Workspace,
+                      stream=None):
+    """vc_paged_attn that adds every cached token's attention weight to scores
+    fp32 [B][Hkv][S], S >= the cache's slots."""
+    T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores)
+    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (cache.B, cache.Hkv):
+        raise ValueError(f"scores is fp32 [{cache.B}][{cache.Hkv}][slots]")
+    _check(load().vc_paged_attn_h2o(q.data_ptr(), ctypes.byref(cache.c), q_start.data_ptr(), ctx_len.data_ptr(), T,
+                                    Hq, float(sm_scale), out.data_ptr(), scores.data_ptr(), scores.shape[2], ws.ptr,
+                                    ws.nbytes, _stream(stream)), "vc_paged_attn_h2o")
+
+
+def vc_paged_evict(scores, src: PagedCache, src_len, keep_top: int, keep_recent: int, dst: PagedCache, dst_len,
+                   kept_idx, scores_out=None, stream=None):
+    """The keep_recent newest and keep_top best-scored other tokens of every
+    (sequence, kv head) of src, into dst's pages: scores fp32 [B][Hkv][S],
+    kept_idx int32 [B][Hkv][n], scores_out fp32 [B][Hkv][n] or None."""
+    src._check(scores, src_len, dst.k, dst_len, kept_idx, scores_out)
+    for t, dt, shape in ((scores, torch.float32, (src.B, src.Hkv)), (kept_idx, torch.int32, (src.B, src.Hkv)),
+                         (scores_out, torch.float32, (src.B, src.Hkv))):
+        if t is not None and (t.dtype != dt or t.dim() != 3 or t.shape[:2] != shape):
+            raise ValueError(f"scores, kept_idx and scores_out are [{src.B}][{src.Hkv}][..], fp32, int32 and fp32")
+    for t in (src_len, dst_len):
+        if t.dtype != torch.int32 or t.shape != (src.B,):
+            raise ValueError(f"src_len and dst_len are int32 [{src.B}]")
+    _check(load().vc_paged_evict(scores.data_ptr(), scores.shape[2], ctypes.byref(src.c), src_len.data_ptr(),
+                                 DropCfg(int(keep_top), int(keep_recent)), ctypes.byref(dst.c), dst_len.data_ptr(),
+                                 kept_idx.data_ptr(), kept_idx.shape[2], _ptr(scores_out),
+                                 scores_out.shape[2] if scores_out is not None else 0, _stream(stream)),
+           "vc_paged_evict")
