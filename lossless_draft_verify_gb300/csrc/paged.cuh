@@ -295,6 +295,12 @@ template <typename T>
 cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float2 *ml,
                       float *scores, int scores_stride, cudaStream_t st);
 
+// paged_attn_tc.cu: bf16 on the tensor cores, row tiles of 256
+constexpr int kTcRows = 256;
+int tc_ctas();
+cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+                    const Parts &parts, int32_t *status, cudaStream_t st);
+
 // paged_attn.cu: attention, with scores != null also the attention mass
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, bool mass);
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,

@@ -1,4 +1,6 @@
 // paged_attn.cu -- causal attention of ragged chunks over a paged cache.
+#include <type_traits>
+
 #include "paged.cuh"
 
 namespace vc {
@@ -61,11 +63,11 @@ struct WsLayout {
 };
 
 // [status | desc | partial (m, l) | partial o | (m, 1/l) of every row]
-WsLayout layout(int d, int T, int G, int Hq, bool with_rows)
+WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, bool with_rows)
 {
     WsLayout w;
-    w.n_cta = simt_ctas();
-    const long unit = 64;
+    w.n_cta = dt == VC_BF16 ? tc_ctas() : simt_ctas();
+    const long unit = dt == VC_BF16 ? kTcRows : simt_rows(T, G);
     w.rows_cap = (int)std::min<long>(unit, (long)T * G);
     const size_t n = (size_t)w.n_cta * 2 * w.rows_cap;
     w.desc = kStatusBytes;
@@ -86,13 +88,15 @@ cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq,
 }
 
 template <typename T>
-cudaError_t run(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *scores,
-                int scores_stride, uint8_t *ws, cudaStream_t st)
+cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void *q, int Hq, float sl2, void *out,
+                float *scores, int scores_stride, uint8_t *ws, cudaStream_t st)
 {
-    const WsLayout w = layout(d, W.T, W.G, Hq, scores != nullptr);
+    const WsLayout w = layout(dt, d, W.T, W.G, Hq, scores != nullptr);
     Parts parts = {(PartDesc *)(ws + w.desc), (float2 *)(ws + w.ml), (float *)(ws + w.o), w.rows_cap};
     float2 *ml = scores ? (float2 *)(ws + w.rows) : nullptr;
-    cudaError_t e = attn_simt<T>(P, W, d, q, Hq, sl2, out, ml, parts, st);
+    cudaError_t e;
+    if constexpr (std::is_same_v<T, float>) e = attn_simt<T>(P, W, d, q, Hq, sl2, out, ml, parts, st);
+    else e = attn_tc(P, W, d, q, Hq, sl2, out, ml, parts, (int32_t *)ws, st);
     if (e == cudaSuccess) e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, ml, st);
     if (e == cudaSuccess && scores) e = mass_simt<T>(P, W, d, q, Hq, sl2, ml, scores, scores_stride, st);
     return e;
@@ -102,8 +106,7 @@ cudaError_t run(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, f
 
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, bool mass)
 {
-    (void)dt;
-    return layout(d, T, Hq / Hkv, Hq, mass).bytes;
+    return layout(dt, d, T, Hq / Hkv, Hq, mass).bytes;
 }
 
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
@@ -116,8 +119,8 @@ cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t
     W.G = Hq / P.Hkv;
     W.min_tiles = 4 + kUnitCost;
     const float sl2 = sm_scale * kLog2e;
-    return dt == VC_BF16 ? run<__nv_bfloat16>(P, W, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st)
-                         : run<float>(P, W, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st);
+    return dt == VC_BF16 ? run<__nv_bfloat16>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st)
+                         : run<float>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st);
 }
 
 }  // namespace paged

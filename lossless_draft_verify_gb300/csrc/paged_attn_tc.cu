@@ -1,0 +1,590 @@
+// paged_attn_tc.cu -- causal attention of ragged chunks over a paged bf16
+// cache on the tensor cores (TMA, tcgen05, tensor memory).
+//
+//   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j), j <= ctx + i
+//
+// A unit (paged.cuh) is up to 256 (query, head) rows of one kv head against
+// tiles of 128 keys.  A persistent CTA per SM walks its share of the batch:
+//   warps 0-3, 4-7  softmax of stream 0 and 1, one thread per row;
+//   warp 8          producer: one TMA box per (page, 64 channels), each lane a
+//                   box, into a ring of 128-key K and V tiles;
+//   warp 9          issues the MMAs: S = Q K^T and O += P V, accumulators and
+//                   P (bf16, over S's columns) in tensor memory;
+//   warps 10, 11    idle: they complete the warpgroup whose registers go to
+//                   the softmax threads, which hold a row of 128 scores each.
+// The two streams keep the tensor cores busy in turn: while stream 0 takes the
+// exponentials of its S, stream 1's products run.  With more than 128 rows the
+// streams are the unit's two row tiles, sharing every K/V tile; with fewer they
+// take the key tiles alternately for the same rows and are merged at the end,
+// so that a short unit, which HBM bounds, has both softmax groups on it.
+//
+// The running maximum is raised only when it grows by more than 2^8 (P and the
+// sum then stay within fp32 and bf16 range), so O is rarely rescaled; the sum
+// is taken over the unrounded exponentials, in fp32.  P is rounded to bf16 for
+// the second product (half a step of bf16 per weight, the type the matrix unit
+// takes), out once.
+//
+// V rows past the sequence's end may hold any bits and 0 * NaN is not 0: those
+// that share the last page with tokens are cleared in shared memory, further
+// pages are not read (their boxes lie outside the map and fill with zeros).
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace vc {
+namespace paged {
+namespace {
+
+constexpr int BN = 128;
+constexpr int kRowsTile = 128;
+constexpr int kThreads = 384;
+constexpr int kSoftmax = 256;
+constexpr float kLazy = 8.f;
+
+template <int D>
+struct Geom {
+    static constexpr int HALVES = D / 64;
+    static constexpr int TILE = BN * D * 2;                  // bytes of a K or V tile (and of a Q row tile)
+    static constexpr int STAGES = 5 * (128 / D);
+    static constexpr int SM_Q = 0;
+    static constexpr int SM_KV = 2 * TILE;
+    static constexpr int SM_BAR = SM_KV + STAGES * TILE;
+    static constexpr int SMEM = SM_BAR + 3072;
+    static constexpr uint32_t COL_O = 256;                   // S0 | S1 | O0 | O1
+};
+
+struct Shared {
+    uint64_t full[10], empty[10];
+    uint64_t q_ready, s_full[2], p_ready[2], o_full[2], meet;
+    uint32_t tmem;
+    int32_t abort_flag;
+    Piece piece;
+    struct {
+        Walk<256, BN> walk;
+        Item it;
+        bool more;
+    } role[10];        // each warp's walk through the piece: in registers it would make the softmax threads spill
+};
+
+struct Params {
+    Pool P;
+    WorkDim W;
+    const __nv_bfloat16 *q;
+    __nv_bfloat16 *out;
+    float2 *ml_out;
+    Parts parts;
+    int32_t *status;
+    int Hq, box_rows, n_rows;      // n_rows: rows of the pool's tensor map
+    float sl2;
+};
+
+// The launch gives 384 x 168 registers; the softmax warpgroups take 224 each,
+// the third keeps 56: 2 x 128 x 224 + 128 x 56 = 384 x 168.
+constexpr int kRegsSoftmax = 224, kRegsOther = 56;
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Shared *S, int32_t *status, int where)
+{
+    if (mbar_wait(bar, parity)) return true;
+    report_timeout(status, where);
+    atomicExch(&S->abort_flag, 1);
+    return false;
+}
+
+// The same by a whole warp, which stays together.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Shared *S, int32_t *status, int where)
+{
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, S, status, where));
+}
+
+// A place in the ring of K and V tiles; items are taken in the order in which
+// the products need them: K_0 (K_1), then V_i, K_{i + ahead}.
+template <int NST>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == NST) slot = 0, phase ^= 1;
+    }
+    __device__ __forceinline__ Ring after() const
+    {
+        Ring r = *this;
+        r.next();
+        return r;
+    }
+};
+
+// The warp's next part; false at the end of the piece.
+__device__ __forceinline__ bool step(Shared *S, int warp, const Params &A)
+{
+    auto &x = S->role[warp];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) x.more = x.walk.next(A.P, A.W, x.it);
+    __syncwarp();
+    return x.more;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Params A)
+{
+    using G = Geom<D>;
+    constexpr int NST = G::STAGES;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    Shared *S = reinterpret_cast<Shared *>(sm + G::SM_BAR);
+    static_assert(sizeof(Shared) <= 3072, "shared block");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    if (smem_u32(sm) & 1023u) {                              // never expected: the swizzled tiles need it
+        if (threadIdx.x == 0) report_timeout(A.status, 90);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&S->full[i], 1);
+            mbar_init(&S->empty[i], 1);
+        }
+        mbar_init(&S->q_ready, kSoftmax);
+        mbar_init(&S->meet, kSoftmax);
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&S->s_full[t], 1);
+            mbar_init(&S->p_ready[t], 128);
+            mbar_init(&S->o_full[t], 1);
+        }
+        S->abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(&S->tmem, 512);
+        tc::tmem_relinquish();
+    }
+    if (warp == 8) find_piece<256, BN>(A.P, A.W, blockIdx.x, gridDim.x, &S->piece);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    pdl_trigger();
+    const uint32_t tmem = S->tmem;
+    if (warp < 10 && lane == 0) S->role[warp].walk.start(A.P, A.W, S->piece);
+
+    if (warp >= 10) {
+        regs_down<kRegsOther>();
+    } else if (warp == 8) {
+        // ------------------------------------------------------- producer --
+        regs_down<kRegsOther>();
+        const Item &it = S->role[warp].it;
+        if (lane == 0) {
+            tc::prefetch_tmap(&tmK);
+            tc::prefetch_tmap(&tmV);
+        }
+        const int boxes = BN / A.box_rows * G::HALVES;       // per tile, at most 16
+        const int bp = lane / G::HALVES, half = lane % G::HALVES;
+        Ring<NST> ring;
+        bool ok = true, filled = false;                      // filled: the ring has been round once
+        auto load = [&](const CUtensorMap *map, int row) {
+            const int s = ring.slot;
+            if (filled) {
+                if (lane == 0) ok = wait_bar(&S->empty[s], ring.phase ^ 1, S, A.status, 91);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) return;
+            }
+            uint8_t *dst = sm + G::SM_KV + s * G::TILE;
+            if (lane == 0) mbar_arrive_expect_tx(&S->full[s], G::TILE);
+            __syncwarp();
+            if (lane < boxes)
+                tc::tma_load_3d(dst + half * (BN * 128) + bp * A.box_rows * 128, map, half * 64, row, 0, &S->full[s]);
+            ring.next();
+            filled = filled || ring.slot == 0;
+        };
+        while (ok && step(S, warp, A)) {
+            const int n = it.t_hi - it.t_lo, len = it.ctx + it.n;
+            const int ahead = it.rows > kRowsTile ? 1 : 2;
+            // row of the lane's box of key tile i; past the sequence's end or
+            // through a bad page number: outside the map
+            auto locate = [&](int i) {
+                const int slot = (it.t_lo + i) * BN + bp * A.box_rows;
+                if (lane >= boxes || i >= n || slot >= len) return A.n_rows;
+                const int pg = A.P.page_of(it.b, slot >> A.P.page_log2);
+                return pg < 0 ? A.n_rows : (int)A.P.row(pg, it.h, slot & (A.P.page() - 1));
+            };
+            int r0 = locate(0), r1 = locate(1), r2 = locate(2);
+            for (int i = 0; i < ahead && i < n && ok; ++i) load(&tmK, i == 0 ? r0 : r1);
+            for (int i = 0; i < n && ok; ++i) {
+                const int r3 = locate(i + 3);
+                load(&tmV, r0);
+                if (ok && i + ahead < n) load(&tmK, ahead == 1 ? r1 : r2);
+                r0 = r1, r1 = r2, r2 = r3;
+            }
+        }
+        if (!ok && lane == 0)                                // copies in flight end before the CTA does
+            for (int i = 0; i < NST; ++i) {
+                if (filled || i < ring.slot) mbar_wait(&S->full[i], i < ring.slot ? ring.phase : ring.phase ^ 1);
+            }
+    } else if (warp == 9) {
+        // -------------------------------------------------------- issuer --
+        regs_down<kRegsOther>();
+        if (lane == 0) {
+            const Item &it = S->role[9].it;
+            constexpr uint32_t idS = tc::idesc_bf16(kRowsTile, BN, false, false);
+            constexpr uint32_t idO = tc::idesc_bf16(kRowsTile, D, false, true);
+            Ring<NST> ring;
+            uint32_t units = 0, steps[2] = {0, 0};           // q_ready, p_ready phases
+            bool ok = true;
+            auto tile = [&](const Ring<NST> &x) { return smem_u32(sm + G::SM_KV + x.slot * G::TILE); };
+            auto arrived = [&](const Ring<NST> &x) { return wait_bar(&S->full[x.slot], x.phase, S, A.status, 92); };
+            auto release = [&]() {                           // once the products issued so far are done
+                tc::commit(&S->empty[ring.slot]);
+                ring.next();
+            };
+            auto issue_S = [&](int t, int qt, const Ring<NST> &x) {
+                const uint32_t sQ = smem_u32(sm + G::SM_Q + qt * G::TILE), sK = tile(x);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk >> 2) * (BN * 128) + (kk & 3) * 32;
+                    tc::mma_ss(tmem + t * BN, tc::smem_desc(sQ + o, 16, 1024, tc::kSwizzle128B),
+                               tc::smem_desc(sK + o, 16, 1024, tc::kSwizzle128B), idS, kk > 0);
+                }
+                tc::commit(&S->s_full[t]);
+            };
+            auto issue_PV = [&](int t, const Ring<NST> &x, bool first) {
+                const uint32_t sV = tile(x);
+#pragma unroll
+                for (int kk = 0; kk < BN / 16; ++kk)
+                    tc::mma_ts(tmem + G::COL_O + t * D, tmem + t * BN + kk * 8,
+                               tc::smem_desc(sV + kk * 2048, BN * 128, 1024, tc::kSwizzle128B), idO,
+                               (!first || kk > 0) ? 1u : 0u);
+            };
+            auto p_wait = [&](int t) {
+                const bool r = wait_bar(&S->p_ready[t], steps[t] & 1, S, A.status, 93);
+                ++steps[t];
+                tc::fence_after();
+                return r;
+            };
+            while (ok && S->role[9].walk.next(A.P, A.W, S->role[9].it)) {
+                const int n = it.t_hi - it.t_lo;
+                ok = wait_bar(&S->q_ready, units & 1, S, A.status, 94);
+                ++units;
+                tc::fence_after();
+                if (it.rows > kRowsTile) {
+                    // the streams are two row tiles on the same keys
+                    ok = ok && arrived(ring);
+                    if (!ok) break;
+                    issue_S(0, 0, ring);
+                    issue_S(1, 1, ring);
+                    release();
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        const Ring<NST> k = ring.after();    // K_{j+1}, after V_j
+                        ok = arrived(ring) && (!more || arrived(k)) && p_wait(0);
+                        if (!ok) break;
+                        issue_PV(0, ring, j == 0);
+                        if (more) issue_S(0, 0, k);
+                        else tc::commit(&S->o_full[0]);
+                        ok = p_wait(1);
+                        if (!ok) break;
+                        issue_PV(1, ring, j == 0);
+                        release();
+                        if (more) {
+                            issue_S(1, 1, ring);
+                            release();
+                        } else {
+                            tc::commit(&S->o_full[1]);
+                        }
+                    }
+                } else {
+                    // the streams take the key tiles of one row tile in turn
+                    for (int t = 0; t < 2 && t < n && ok; ++t) {
+                        ok = arrived(ring);
+                        if (!ok) break;
+                        issue_S(t, 0, ring);
+                        release();
+                    }
+                    for (int j = 0; j < n && ok; ++j) {
+                        const int t = j & 1;
+                        ok = arrived(ring) && p_wait(t);
+                        if (!ok) break;
+                        issue_PV(t, ring, j < 2);
+                        release();
+                        if (j + 2 < n) {
+                            ok = arrived(ring);
+                            if (!ok) break;
+                            issue_S(t, 0, ring);
+                            release();
+                        } else {
+                            tc::commit(&S->o_full[t]);
+                        }
+                    }
+                }
+            }
+        }
+    } else {
+        // ------------------------------------------------------- softmax --
+        regs_up<kRegsSoftmax>();
+        const Item &it = S->role[warp].it;
+        const int t = warp >> 2;                             // stream
+        const int r = threadIdx.x & 127;                     // row of the stream's tile
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + t * BN;
+        uint32_t steps = 0, units[2] = {0, 0}, met = 0;      // s_full, o_full and meet phases
+        uint32_t item = 0;                                   // ring items of the parts before this one
+        bool ok = true;
+        auto meet = [&](int where) {                         // both softmax groups
+            mbar_arrive(&S->meet);
+            const bool r = wait_warp(&S->meet, met & 1, S, A.status, where);
+            ++met;
+            return r;
+        };
+        // the streams' (m, l) where the second row tile's Q would be
+        float2 *ml_x = reinterpret_cast<float2 *>(sm + G::SM_Q + G::TILE);
+        if (threadIdx.x == 0) A.parts.desc[blockIdx.x].parts = 0;
+        while (ok && step(S, warp, A)) {
+            const int n = it.t_hi - it.t_lo, len = it.ctx + it.n;
+            const bool big = it.rows > kRowsTile;
+            const int row0 = it.mt * 256;
+            auto out_row = [&](int rr) {                     // row of q, out and ml_out
+                const int R = row0 + rr;
+                return (size_t)(it.tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G;
+            };
+            {
+                // Q: big, the stream's tile; else each group half of the one tile
+                constexpr int CH = D / 8, RP = 128 / CH;     // 16-byte chunks per row, rows per pass
+                const int c = r % CH, q0 = r / CH;
+                uint8_t *sQ = sm + G::SM_Q + (big ? t * G::TILE : 0);
+                const int lo = big ? 0 : t * 64, cnt = big ? 128 : 64, base = big ? t * 128 : 0;
+#pragma unroll 4
+                for (int i = q0; i < cnt; i += RP) {
+                    const int rr = lo + i;
+                    uint4 x = make_uint4(0, 0, 0, 0);
+                    if (base + rr < it.rows)
+                        x = *reinterpret_cast<const uint4 *>(A.q + out_row(base + rr) * D + c * 8);
+                    *reinterpret_cast<uint4 *>(sQ + (c >> 3) * (BN * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x;
+                }
+                fence_async_smem();
+                tc::fence_before();
+                mbar_arrive(&S->q_ready);
+                __syncwarp();
+            }
+            const int R = (big ? t * 128 : 0) + r;           // row within the unit
+            const bool valid = R < it.rows;
+            const int kmax = valid ? it.ctx + (row0 + R) / A.W.G : -1;
+            // keys every row of the tile sees
+            const int kall = it.ctx + (row0 + (big ? t * 128 : 0)) / A.W.G;
+            float m = kNegBig, l = 0.f;
+            const int mine = big ? n : (n + 1 - t) / 2;      // this stream's steps
+            for (int j = 0; j < mine; ++j) {
+                const int i = big ? j : 2 * j + t;           // key tile of the part
+                const int key0 = (it.t_lo + i) * BN;
+                ok = wait_warp(&S->s_full[t], steps & 1, S, A.status, 95);
+                ++steps;
+                if (!ok) break;
+                tc::fence_after();
+                uint32_t u[4][32];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) tc::ld32(tS + h * 32, u[h]);
+                tc::ld_wait();
+                if (key0 + BN - 1 > kall) {
+#pragma unroll
+                    for (int h = 0; h < 4; ++h)
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            if (key0 + h * 32 + c > kmax) u[h][c] = 0xff800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    mx[h] = __uint_as_float(u[h][0]);
+#pragma unroll
+                    for (int c = 1; c < 32; ++c) mx[h] = fmaxf(mx[h], __uint_as_float(u[h][c]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                float alpha = 1.f;
+                if ((top - m) * A.sl2 > kLazy) {
+                    alpha = ex2((m - top) * A.sl2);
+                    m = top;
+                }
+                // the stream's previous O += P V came before this S in the issue
+                // order, so it is complete
+                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+                    l *= alpha;
+#pragma unroll
+                    for (int h = 0; h < D / 32; ++h) {
+                        uint32_t o[32];
+                        const uint32_t tO = tmem + lanes + G::COL_O + t * D + h * 32;
+                        tc::ld32(tO, o);
+                        tc::ld_wait();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                        tc::st32(tO, o);
+                    }
+                }
+                const float2 sc = make_float2(A.sl2, A.sl2), nm = make_float2(-m * A.sl2, -m * A.sl2);
+                float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int h = 2 * g + e / 16, c = 2 * (e % 16);
+                        const float2 x = fma2(make_float2(__uint_as_float(u[h][c]), __uint_as_float(u[h][c + 1])), sc, nm);
+                        const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                        sum[e & 1] = add2(sum[e & 1], p);
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+                        pk[e] = *reinterpret_cast<const uint32_t *>(&b);
+                    }
+                    tc::st32(tS + g * 32, pk);
+                }
+                const float2 s2 = add2(sum[0], sum[1]);
+                l += s2.x + s2.y;
+                if (i == n - 1 && key0 + BN > len && (!big || t == 0)) {
+                    // V rows of the last page past the sequence's end
+                    const uint32_t vi = item + 2u * n - 1;   // the part's last ring item
+                    ok = wait_warp(&S->full[vi % NST], (vi / NST) & 1, S, A.status, 96);
+                    if (!ok) break;
+                    uint8_t *sV = sm + G::SM_KV + (vi % NST) * G::TILE;
+                    const int page = A.P.page();
+                    const int z0 = len - key0, z1 = min(BN, (len + page - 1) / page * page - key0);
+                    for (int x = r; x < (z1 - z0) * (D / 8); x += 128) {
+                        const int row = z0 + x / (D / 8), c = x % (D / 8);
+                        *reinterpret_cast<uint4 *>(sV + (c >> 3) * (BN * 128) + row * 128 + (c & 7) * 16) =
+                            make_uint4(0, 0, 0, 0);
+                    }
+                    fence_async_smem();
+                    __syncwarp();
+                }
+                tc::st_wait();
+                tc::fence_before();
+                mbar_arrive(&S->p_ready[t]);
+            }
+            if (!ok) break;
+            // ------------------------------------------------ output of the part --
+            const size_t pr = A.parts.row(blockIdx.x, it.head ? 1 : 0, R);
+            auto finish = [&](float M, float L, float w0, float w1, int c0, int c1) {
+                // channels [c0, c1): w0 O_t (+ w1 O_1 of the merged streams)
+                const float inv = it.whole ? 1.f / L : 1.f;
+                const size_t row = valid ? out_row(R) : 0;
+#pragma unroll 1
+                for (int c = c0; c < c1; c += 32) {
+                    uint32_t o[32], o1[32];
+                    __syncwarp();
+                    tc::ld32(tmem + lanes + G::COL_O + (big ? t * D : 0) + c, o);
+                    if (!big && n > 1) tc::ld32(tmem + lanes + G::COL_O + D + c, o1);
+                    tc::ld_wait();
+                    float x[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        x[e] = __uint_as_float(o[e]) * w0;
+                        if (!big && n > 1) x[e] = fmaf(__uint_as_float(o1[e]), w1, x[e]);
+                    }
+                    if (valid && it.whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const __nv_bfloat162 b = __floats2bfloat162_rn(x[e + 2 * k] * inv, x[e + 2 * k + 1] * inv);
+                                w[k] = *reinterpret_cast<const uint32_t *>(&b);
+                            }
+                            *reinterpret_cast<uint4 *>(A.out + row * D + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                    } else if (valid) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>(A.parts.o + pr * D + c + e) =
+                                make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                    }
+                }
+                if (valid && c0 == 0) {
+                    if (!it.whole) A.parts.ml[pr] = make_float2(M, L);
+                    else if (A.ml_out) A.ml_out[row] = make_float2(M, inv);
+                }
+            };
+            if (big) {
+                ok = wait_warp(&S->o_full[t], units[t] & 1, S, A.status, 97);
+                ++units[0], ++units[1];
+                if (!ok) break;
+                tc::fence_after();
+                finish(m * A.sl2, l, 1.f, 0.f, 0, D);
+            } else {
+                ml_x[t * kRowsTile + r] = make_float2(m * A.sl2, l);
+                ok = wait_warp(&S->o_full[0], units[0] & 1, S, A.status, 98) &&
+                     (n == 1 || wait_warp(&S->o_full[1], units[1] & 1, S, A.status, 99));
+                ++units[0];
+                if (n > 1) ++units[1];
+                ok = ok && meet(100);
+                if (!ok) break;
+                tc::fence_after();
+                const float2 a = ml_x[r], b = ml_x[kRowsTile + r];
+                const float M = fmaxf(a.x, b.x), w0 = ex2(a.x - M), w1 = ex2(b.x - M);
+                finish(M, fmaf(a.y, w0, b.y * w1), w0, w1, t * (D / 2), (t + 1) * (D / 2));
+                tc::fence_before();
+                ok = meet(101);                              // O and the (m, l) are free again
+                if (!ok) break;
+                tc::fence_after();
+            }
+            if (!it.whole && it.head && threadIdx.x == 0) {
+                PartDesc &d = A.parts.desc[blockIdx.x];
+                d.parts = it.parts;
+                d.tok0 = it.tok0;
+                d.h = it.h;
+                d.row0 = row0;
+                d.rows = it.rows;
+            }
+            item += 2u * n;
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 9) {
+        __syncwarp();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float2 *ml,
+                   const Parts &parts, int32_t *status, cudaStream_t st)
+{
+    Params A;
+    A.P = P;
+    A.W = W;
+    A.q = (const __nv_bfloat16 *)q;
+    A.out = (__nv_bfloat16 *)out;
+    A.ml_out = ml;
+    A.parts = parts;
+    A.status = status;
+    A.Hq = Hq;
+    A.box_rows = std::min(1 << P.page_log2, BN);
+    A.n_rows = (P.n_pages * P.Hkv) << P.page_log2;
+    A.sl2 = std::max(sl2, 1e-30f);     // a masked score is -inf; times zero it would be NaN
+    CUtensorMap mk, mv;
+    const uint64_t bytes = (uint64_t)D * 2;
+    if (!tma_map_bf16_3d(&mk, P.k, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1) ||
+        !tma_map_bf16_3d(&mv, P.v, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1))
+        return cudaErrorInvalidValue;
+    auto kern = attn_tc_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(tc_ctas()), dim3(kThreads), Geom<D>::SMEM, st, mk, mv, A);
+}
+
+}  // namespace
+
+int tc_ctas() { return device_sm_count(); }
+
+cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+                    const Parts &parts, int32_t *status, cudaStream_t st)
+{
+    return d == 128 ? launch<128>(P, W, q, Hq, sl2, out, ml, parts, status, st)
+                    : launch<64>(P, W, q, Hq, sl2, out, ml, parts, status, st);
+}
+
+}  // namespace paged
+}  // namespace vc
