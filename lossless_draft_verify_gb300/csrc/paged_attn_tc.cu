@@ -9,9 +9,7 @@
 //   warp 8          producer: one TMA box per (page, 64 channels), each lane a
 //                   box, into a ring of 128-key K and V tiles;
 //   warp 9          issues the MMAs: S = Q K^T and O += P V, accumulators and
-//                   P (bf16, over S's columns) in tensor memory;
-//   warps 10, 11    idle: they complete the warpgroup whose registers go to
-//                   the softmax threads, which hold a row of 128 scores each.
+//                   P (bf16, over S's columns) in tensor memory.
 // The two streams keep the tensor cores busy in turn: while stream 0 takes the
 // exponentials of its S, stream 1's products run.  With more than 128 rows the
 // streams are the unit's two row tiles, sharing every K/V tile; with fewer they
@@ -36,7 +34,7 @@ namespace {
 
 constexpr int BN = 128;
 constexpr int kRowsTile = 128;
-constexpr int kThreads = 384;
+constexpr int kThreads = 320;
 constexpr int kSoftmax = 256;
 constexpr float kLazy = 8.f;
 
@@ -76,12 +74,6 @@ struct Params {
     int Hq, box_rows, n_rows;      // n_rows: rows of the pool's tensor map
     float sl2;
 };
-
-// The launch gives 384 x 168 registers; the softmax warpgroups take 224 each,
-// the third keeps 56: 2 x 128 x 224 + 128 x 56 = 384 x 168.
-constexpr int kRegsSoftmax = 224, kRegsOther = 56;
-template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
-template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
 
 __device__ __forceinline__ float ex2(float x)
 {
@@ -172,13 +164,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tc::fence_after();
     pdl_trigger();
     const uint32_t tmem = S->tmem;
-    if (warp < 10 && lane == 0) S->role[warp].walk.start(A.P, A.W, S->piece);
+    if (lane == 0) S->role[warp].walk.start(A.P, A.W, S->piece);
 
-    if (warp >= 10) {
-        regs_down<kRegsOther>();
-    } else if (warp == 8) {
+    if (warp == 8) {
         // ------------------------------------------------------- producer --
-        regs_down<kRegsOther>();
         const Item &it = S->role[warp].it;
         if (lane == 0) {
             tc::prefetch_tmap(&tmK);
@@ -229,7 +218,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             }
     } else if (warp == 9) {
         // -------------------------------------------------------- issuer --
-        regs_down<kRegsOther>();
         if (lane == 0) {
             const Item &it = S->role[9].it;
             constexpr uint32_t idS = tc::idesc_bf16(kRowsTile, BN, false, false);
@@ -326,7 +314,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
     } else {
         // ------------------------------------------------------- softmax --
-        regs_up<kRegsSoftmax>();
         const Item &it = S->role[warp].it;
         const int t = warp >> 2;                             // stream
         const int r = threadIdx.x & 127;                     // row of the stream's tile
@@ -385,25 +372,34 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 ++steps;
                 if (!ok) break;
                 tc::fence_after();
-                uint32_t u[4][32];
+                const bool cut = key0 + BN - 1 > kall;       // some row does not see all keys
+                // a score chunk: 32 keys of the row, those it does not see at -inf
+                auto chunk = [&](int h, uint32_t (&u)[32]) {
+                    if (!cut) return;
 #pragma unroll
-                for (int h = 0; h < 4; ++h) tc::ld32(tS + h * 32, u[h]);
-                tc::ld_wait();
-                if (key0 + BN - 1 > kall) {
-#pragma unroll
-                    for (int h = 0; h < 4; ++h)
-#pragma unroll
-                        for (int c = 0; c < 32; ++c)
-                            if (key0 + h * 32 + c > kmax) u[h][c] = 0xff800000u;
-                }
-                float mx[4];
+                    for (int c = 0; c < 32; ++c)
+                        if (key0 + h * 32 + c > kmax) u[c] = 0xff800000u;
+                };
+                // the scores are read twice, 32 at a time: holding all 128 would spill
+                uint32_t u[2][32];
+                float top = kNegBig;
+                tc::ld32(tS, u[0]);
 #pragma unroll
                 for (int h = 0; h < 4; ++h) {
-                    mx[h] = __uint_as_float(u[h][0]);
+                    tc::ld_wait();
+                    if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
+                    uint32_t (&x)[32] = u[h & 1];
+                    chunk(h, x);
+                    float a = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+                    float b = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
 #pragma unroll
-                    for (int c = 1; c < 32; ++c) mx[h] = fmaxf(mx[h], __uint_as_float(u[h][c]));
+                    for (int c = 4; c < 32; c += 4) {
+                        a = fmaxf(a, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
+                        b = fmaxf(b, fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])));
+                    }
+                    top = fmaxf(top, fmaxf(a, b));
                 }
-                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                tc::ld32(tS, u[0]);
                 float alpha = 1.f;
                 if ((top - m) * A.sl2 > kLazy) {
                     alpha = ex2((m - top) * A.sl2);
@@ -427,18 +423,22 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 const float2 sc = make_float2(A.sl2, A.sl2), nm = make_float2(-m * A.sl2, -m * A.sl2);
                 float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                    uint32_t pk[32];
+                for (int h = 0; h < 4; ++h) {
+                    tc::ld_wait();
+                    if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
+                    uint32_t (&v)[32] = u[h & 1];
+                    chunk(h, v);
+                    uint32_t pk[16];
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) {
-                        const int h = 2 * g + e / 16, c = 2 * (e % 16);
-                        const float2 x = fma2(make_float2(__uint_as_float(u[h][c]), __uint_as_float(u[h][c + 1])), sc, nm);
+                    for (int e = 0; e < 16; ++e) {
+                        const float2 x = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc, nm);
                         const float2 p = make_float2(ex2(x.x), ex2(x.y));
                         sum[e & 1] = add2(sum[e & 1], p);
                         const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
                         pk[e] = *reinterpret_cast<const uint32_t *>(&b);
                     }
-                    tc::st32(tS + g * 32, pk);
+                    // P's columns 16 h .. lie over scores already read
+                    tc::st16(tS + h * 16, pk);
                 }
                 const float2 s2 = add2(sum[0], sum[1]);
                 l += s2.x + s2.y;
