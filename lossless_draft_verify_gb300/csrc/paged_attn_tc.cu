@@ -380,66 +380,61 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     for (int c = 0; c < 32; ++c)
                         if (key0 + h * 32 + c > kmax) u[c] = 0xff800000u;
                 };
-                // the scores are read twice, 32 at a time: holding all 128 would spill
-                uint32_t u[2][32];
-                float top = kNegBig;
-                tc::ld32(tS, u[0]);
+                // Exponentials against the running maximum as it stands, the
+                // tile's maximum in the same pass.  Where it has grown by more
+                // than 2^8 (a first tile, and rarely after it) O is rescaled
+                // and the pass repeated; P is stored once it holds.
+                uint32_t pk[64];
+                float2 sum[2];
+                for (;;) {
+                    const float2 sc = make_float2(A.sl2, A.sl2), nm = make_float2(-m * A.sl2, -m * A.sl2);
+                    sum[0] = sum[1] = make_float2(0.f, 0.f);
+                    float top[2] = {kNegBig, kNegBig};
+                    uint32_t u[2][32];
+                    tc::ld32(tS, u[0]);
 #pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    tc::ld_wait();
-                    if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
-                    uint32_t (&x)[32] = u[h & 1];
-                    chunk(h, x);
-                    float a = fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
-                    float b = fmaxf(__uint_as_float(x[2]), __uint_as_float(x[3]));
-#pragma unroll
-                    for (int c = 4; c < 32; c += 4) {
-                        a = fmaxf(a, fmaxf(__uint_as_float(x[c]), __uint_as_float(x[c + 1])));
-                        b = fmaxf(b, fmaxf(__uint_as_float(x[c + 2]), __uint_as_float(x[c + 3])));
-                    }
-                    top = fmaxf(top, fmaxf(a, b));
-                }
-                tc::ld32(tS, u[0]);
-                float alpha = 1.f;
-                if ((top - m) * A.sl2 > kLazy) {
-                    alpha = ex2((m - top) * A.sl2);
-                    m = top;
-                }
-                // the stream's previous O += P V came before this S in the issue
-                // order, so it is complete
-                if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-                    l *= alpha;
-#pragma unroll
-                    for (int h = 0; h < D / 32; ++h) {
-                        uint32_t o[32];
-                        const uint32_t tO = tmem + lanes + G::COL_O + t * D + h * 32;
-                        tc::ld32(tO, o);
+                    for (int h = 0; h < 4; ++h) {
                         tc::ld_wait();
+                        if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
+                        uint32_t (&v)[32] = u[h & 1];
+                        chunk(h, v);
 #pragma unroll
-                        for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
-                        tc::st32(tO, o);
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 s = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
+                            top[e & 1] = fmaxf(top[e & 1], fmaxf(s.x, s.y));
+                            const float2 x = fma2(s, sc, nm);
+                            const float2 p = make_float2(ex2(x.x), ex2(x.y));
+                            sum[e & 1] = add2(sum[e & 1], p);
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
+                            pk[16 * h + e] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                    }
+                    const float mx = fmaxf(top[0], top[1]);
+                    const bool grown = (mx - m) * A.sl2 > kLazy;
+                    if (!__any_sync(0xffffffffu, grown)) break;
+                    float alpha = 1.f;
+                    if (grown) {
+                        alpha = ex2((m - mx) * A.sl2);
+                        m = mx;
+                    }
+                    l *= alpha;
+                    // the stream's previous O += P V came before this S in the
+                    // issue order, so it is complete
+                    if (j > 0) {
+#pragma unroll 1
+                        for (int h = 0; h < D; h += 32) {
+                            uint32_t o[32];
+                            const uint32_t tO = tmem + lanes + G::COL_O + t * D + h;
+                            tc::ld32(tO, o);
+                            tc::ld_wait();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) o[c] = __float_as_uint(__uint_as_float(o[c]) * alpha);
+                            tc::st32(tO, o);
+                        }
                     }
                 }
-                const float2 sc = make_float2(A.sl2, A.sl2), nm = make_float2(-m * A.sl2, -m * A.sl2);
-                float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-#pragma unroll
-                for (int h = 0; h < 4; ++h) {
-                    tc::ld_wait();
-                    if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
-                    uint32_t (&v)[32] = u[h & 1];
-                    chunk(h, v);
-                    uint32_t pk[16];
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) {
-                        const float2 x = fma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), sc, nm);
-                        const float2 p = make_float2(ex2(x.x), ex2(x.y));
-                        sum[e & 1] = add2(sum[e & 1], p);
-                        const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
-                        pk[e] = *reinterpret_cast<const uint32_t *>(&b);
-                    }
-                    // P's columns 16 h .. lie over scores already read
-                    tc::st16(tS + h * 16, pk);
-                }
+                tc::st32(tS, reinterpret_cast<uint32_t (&)[32]>(pk[0]));
+                tc::st32(tS + 32, reinterpret_cast<uint32_t (&)[32]>(pk[32]));
                 const float2 s2 = add2(sum[0], sum[1]);
                 l += s2.x + s2.y;
                 if (i == n - 1 && key0 + BN > len && (!big || t == 0)) {
