@@ -781,8 +781,8 @@ vc_status vc_gemm_ex(const void *x, const void *w, const void *resid, void *out,
  * (that sequence is treated as having no tokens).
  *
  * Supported: d in {64, 128}, page in {16, 32, 64, 128, 256}, any Hq that is a
- * multiple of Hkv; fewer than 2^31 slots n_pages * Hkv * page, and T * Hq <=
- * 2^30.
+ * multiple of Hkv with Hq / Hkv <= 128; fewer than 2^31 slots n_pages * Hkv *
+ * page, and T * Hq <= 2^30.
  */
 #define VC_PAGED_BAD_PAGE 1
 #define VC_PAGED_BAD_LENGTH 2

@@ -284,22 +284,64 @@ struct Parts {
     }
 };
 
+// ----- pieces of the tensor-core kernels ----------------------------------------------
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// A place in a ring of N buffers and the parity of its current round.
+template <int N>
+struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++slot == N) slot = 0, phase ^= 1;
+    }
+    __device__ __forceinline__ Ring after() const
+    {
+        Ring r = *this;
+        r.next();
+        return r;
+    }
+};
+
+// A bounded wait by one thread: on a timeout it is reported and the CTA's
+// other roles, whose waits then run out too, leave as well.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, int32_t *status, int where)
+{
+    if (mbar_wait(bar, parity)) return true;
+    report_timeout(status, where);
+    return false;
+}
+// The same by a whole warp, which stays together.
+__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_t *status, int where)
+{
+    return __all_sync(0xffffffffu, wait_bar(bar, parity, status, where));
+}
+
 // ----- launchers ----------------------------------------------------------------------
 // paged_attn_simt.cu: fp32 on the CUDA cores
 int simt_rows(int T, int G);
 int simt_ctas();
-template <typename T>
-cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                       const Parts &parts, cudaStream_t st);
-template <typename T>
-cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float2 *ml,
+cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float *lse,
                       float *scores, int scores_stride, cudaStream_t st);
 
 // paged_attn_tc.cu: bf16 on the tensor cores, row tiles of 256
 constexpr int kTcRows = 256;
 int tc_ctas();
-cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                     const Parts &parts, int32_t *status, cudaStream_t st);
+
+// paged_mass_tc.cu: scores += the attention weight of every slot, lse (log2
+// domain) of every row given
+cudaError_t mass_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float *lse,
+                    float *scores, int scores_stride, int32_t *status, cudaStream_t st);
 
 // paged_attn.cu: attention, with scores != null also the attention mass
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, bool mass);

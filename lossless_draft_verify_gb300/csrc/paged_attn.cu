@@ -14,7 +14,7 @@ constexpr int kMergeWarps = 8;
 
 template <typename T, int D>
 __global__ void __launch_bounds__(32 * kMergeWarps)
-merge_kernel(Parts parts, int G, int Hq, T *__restrict__ out, float2 *__restrict__ ml_out)
+merge_kernel(Parts parts, int G, int Hq, T *__restrict__ out, float *__restrict__ lse_out)
 {
     pdl_wait();
     pdl_trigger();
@@ -53,7 +53,7 @@ merge_kernel(Parts parts, int G, int Hq, T *__restrict__ out, float2 *__restrict
         T *o = out + row * D + V * lane;
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = Elem<T>::from_f(acc[e] * inv);
-        if (ml_out && lane == 0) ml_out[row] = make_float2(M, inv);
+        if (lse_out && lane == 0) lse_out[row] = M + log2f(L);
     }
 }
 
@@ -62,7 +62,7 @@ struct WsLayout {
     int rows_cap, n_cta;
 };
 
-// [status | desc | partial (m, l) | partial o | (m, 1/l) of every row]
+// [status | desc | partial (m, l) | partial o | lse of every row]
 WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, bool with_rows)
 {
     WsLayout w;
@@ -74,17 +74,17 @@ WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, bool with_rows)
     w.ml = w.desc + align256((size_t)w.n_cta * sizeof(PartDesc));
     w.o = w.ml + align256(n * sizeof(float2));
     w.rows = w.o + align256(n * d * sizeof(float));
-    w.bytes = w.rows + (with_rows ? align256((size_t)T * Hq * sizeof(float2)) : 0);
+    w.bytes = w.rows + (with_rows ? align256((size_t)T * Hq * sizeof(float)) : 0);
     return w;
 }
 
 template <typename T>
-cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq, void *out, float2 *ml,
+cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq, void *out, float *lse,
                   cudaStream_t st)
 {
     const dim3 grid(n_cta, cdiv(rows, kMergeWarps));
-    return d == 128 ? launch_pdl(merge_kernel<T, 128>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, ml)
-                    : launch_pdl(merge_kernel<T, 64>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, ml);
+    return d == 128 ? launch_pdl(merge_kernel<T, 128>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, lse)
+                    : launch_pdl(merge_kernel<T, 64>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, lse);
 }
 
 template <typename T>
@@ -93,13 +93,14 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
 {
     const WsLayout w = layout(dt, d, W.T, W.G, Hq, scores != nullptr);
     Parts parts = {(PartDesc *)(ws + w.desc), (float2 *)(ws + w.ml), (float *)(ws + w.o), w.rows_cap};
-    float2 *ml = scores ? (float2 *)(ws + w.rows) : nullptr;
+    float *lse = scores ? (float *)(ws + w.rows) : nullptr;
     cudaError_t e;
-    if constexpr (std::is_same_v<T, float>) e = attn_simt<T>(P, W, d, q, Hq, sl2, out, ml, parts, st);
-    else e = attn_tc(P, W, d, q, Hq, sl2, out, ml, parts, (int32_t *)ws, st);
-    if (e == cudaSuccess) e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, ml, st);
-    if (e == cudaSuccess && scores) e = mass_simt<T>(P, W, d, q, Hq, sl2, ml, scores, scores_stride, st);
-    return e;
+    if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
+    else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, parts, (int32_t *)ws, st);
+    if (e == cudaSuccess) e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
+    if (e != cudaSuccess || !scores) return e;
+    if constexpr (std::is_same_v<T, float>) return mass_simt(P, W, d, q, Hq, sl2, lse, scores, scores_stride, st);
+    else return mass_tc(P, W, d, q, Hq, sl2, lse, scores, scores_stride, (int32_t *)ws, st);
 }
 
 }  // namespace

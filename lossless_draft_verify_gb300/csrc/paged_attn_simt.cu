@@ -13,46 +13,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// 16 bytes of a K, V or q row as fp32
-template <typename T> struct Chunk;
-template <> struct Chunk<float> {
-    static constexpr int N = 4;
-    static __device__ __forceinline__ void load(const float *p, float *o)
-    {
-        const float4 x = *reinterpret_cast<const float4 *>(p);
-        o[0] = x.x, o[1] = x.y, o[2] = x.z, o[3] = x.w;
-    }
-};
-template <> struct Chunk<__nv_bfloat16> {
-    static constexpr int N = 8;
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float *o)
-    {
-        const uint4 x = *reinterpret_cast<const uint4 *>(p);
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[2 * i] = bf16_lo(w[i]), o[2 * i + 1] = bf16_hi(w[i]);
-    }
-};
-
 // rows [0, n_rows) of a tile into shared memory (pitch floats apart); row r at
 // src(r), null: zeros
-template <typename T, int D, typename F>
+template <int D, typename F>
 __device__ __forceinline__ void load_rows(float *dst, int pitch, int n_rows, F src)
 {
-    constexpr int N = Chunk<T>::N, C = D / N;
-    for (int i = threadIdx.x; i < n_rows * C; i += kThreads) {
-        const int r = i / C, c = (i % C) * N;
-        float x[N];
-        const T *p = src(r);
-        if (p) {
-            Chunk<T>::load(p + c, x);
-        } else {
-#pragma unroll
-            for (int e = 0; e < N; ++e) x[e] = 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < N; e += 4)
-            *reinterpret_cast<float4 *>(dst + r * pitch + c + e) = make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+    for (int i = threadIdx.x; i < n_rows * (D / 4); i += kThreads) {
+        const int r = i / (D / 4), c = (i % (D / 4)) * 4;
+        const float *p = src(r);
+        *reinterpret_cast<float4 *>(dst + r * pitch + c) =
+            p ? *reinterpret_cast<const float4 *>(p + c) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
 }
 
@@ -65,10 +35,10 @@ struct Geom {
 // One CTA per piece of the batch's work (paged.cuh).  256 threads as 16 x 16:
 // thread (ty, tx) holds rows ty * RT .. + RT - 1 against keys tx + 16 j, and
 // the same rows' outputs at channels 4 tx + 64 j.
-template <typename T, int D, int BM, int BN>
+template <int D, int BM, int BN>
 __global__ void __launch_bounds__(kThreads)
-attn_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale_log2, T *__restrict__ out,
-                 float2 *__restrict__ ml_out, Parts parts)
+attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float scale_log2, float *__restrict__ out,
+                 float *__restrict__ lse_out, Parts parts)
 {
     constexpr int RT = BM / 16, KT = BN / 16, CT = D / 64;
     using G = Geom<D, BM, BN>;
@@ -81,7 +51,7 @@ attn_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
     if (threadIdx.x < 32) find_piece<BM, BN>(P, W, blockIdx.x, gridDim.x, &piece);
     __syncthreads();
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const T *pk = (const T *)P.k, *pv = (const T *)P.v;
+    const float *pk = (const float *)P.k, *pv = (const float *)P.v;
     Walk<BM, BN> walk;
     walk.start(P, W, piece);
     if (threadIdx.x == 0) parts.desc[blockIdx.x].parts = 0;
@@ -93,7 +63,7 @@ attn_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
             return ((size_t)(it.tok0 + R / W.G) * Hq + it.h * W.G + R % W.G) * D;
         };
         __syncthreads();
-        load_rows<T, D>(sQ, G::PQ, BM, [&](int r) { return r < it.rows ? q + token_row(r) : nullptr; });
+        load_rows<D>(sQ, G::PQ, BM, [&](int r) { return r < it.rows ? q + token_row(r) : nullptr; });
         float m[RT], l[RT], acc[RT][CT][4];
         int kmax[RT];
 #pragma unroll
@@ -113,12 +83,12 @@ attn_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
                 s_page[threadIdx.x] = slot < len ? P.page_of(it.b, slot >> P.page_log2) : -1;
             }
             __syncthreads();
-            auto slot_row = [&](const T *base, int r) -> const T * {
+            auto slot_row = [&](const float *base, int r) -> const float * {
                 const int pg = s_page[r >> 4], slot = key0 + r;
                 return pg >= 0 && slot < len ? base + P.row(pg, it.h, slot & (P.page() - 1)) * D : nullptr;
             };
-            load_rows<T, D>(sK, G::PQ, BN, [&](int r) { return slot_row(pk, r); });
-            load_rows<T, D>(sV, D, BN, [&](int r) { return slot_row(pv, r); });
+            load_rows<D>(sK, G::PQ, BN, [&](int r) { return slot_row(pk, r); });
+            load_rows<D>(sV, D, BN, [&](int r) { return slot_row(pv, r); });
             __syncthreads();
             float s[RT][KT];
 #pragma unroll
@@ -198,13 +168,13 @@ attn_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
             const int r = ty * RT + i;
             if (r >= it.rows) continue;
             if (it.whole) {
-                T *o = out + token_row(r);
+                float *o = out + token_row(r);
                 const float inv = 1.f / l[i];
 #pragma unroll
                 for (int j = 0; j < CT; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) o[4 * tx + 64 * j + e] = Elem<T>::from_f(acc[i][j][e] * inv);
-                if (ml_out && tx == 0) ml_out[token_row(r) / D] = make_float2(m[i], inv);
+                    *reinterpret_cast<float4 *>(o + 4 * tx + 64 * j) = make_float4(
+                        acc[i][j][0] * inv, acc[i][j][1] * inv, acc[i][j][2] * inv, acc[i][j][3] * inv);
+                if (lse_out && tx == 0) lse_out[token_row(r) / D] = m[i] + log2f(l[i]);
             } else {
                 const size_t pr = parts.row(blockIdx.x, it.head ? 1 : 0, r);
 #pragma unroll
@@ -227,23 +197,23 @@ attn_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
 
 // ----- attention mass ---------------------------------------------------------------
 // scores[b][h][slot] += sum over the rows that see the slot of p, with every
-// row's final maximum and 1 / sum.  One CTA per (b, h, 64-key tile), the
+// row's final maximum and sum, as lse = maximum + log2(sum).  One CTA per (b, h, 64-key tile), the
 // sequence's rows in tiles of 64; every slot is written by one thread, in an
 // order that the lengths fix.
-template <typename T, int D>
+template <int D>
 __global__ void __launch_bounds__(kThreads)
-mass_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale_log2,
-                 const float2 *__restrict__ ml, float *__restrict__ scores, int scores_stride)
+mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float scale_log2,
+                 const float *__restrict__ lse, float *__restrict__ scores, int scores_stride)
 {
     constexpr int BM = 64, BN = 64, PQ = D + 4;
     extern __shared__ __align__(16) float smf[];
     float *sQ = smf, *sK = sQ + BM * PQ, *sSum = sK + BN * PQ;      // sSum [16][BN]
-    __shared__ float2 sML[BM];
+    __shared__ float s_lse[BM];
     __shared__ int s_page[BN / 16];
     pdl_wait();
     pdl_trigger();
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
-    const T *pk = (const T *)P.k;
+    const float *pk = (const float *)P.k;
     for (long u = blockIdx.x; u < (long)P.B * P.Hkv; u += gridDim.x) {
         const int b = (int)(u / P.Hkv), h = (int)(u % P.Hkv);
         const Seq s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
@@ -256,7 +226,7 @@ mass_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
                 s_page[threadIdx.x] = slot < len ? P.page_of(b, slot >> P.page_log2) : -1;
             }
             __syncthreads();
-            load_rows<T, D>(sK, PQ, BN, [&](int r) -> const T * {
+            load_rows<D>(sK, PQ, BN, [&](int r) -> const float * {
                 const int pg = s_page[r >> 4], slot = key0 + r;
                 return pg >= 0 && slot < len ? pk + P.row(pg, h, slot & (P.page() - 1)) * D : nullptr;
             });
@@ -270,10 +240,10 @@ mass_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
                     const long R = r0 + r;
                     return (size_t)(s.tok0 + R / W.G) * Hq + h * W.G + R % W.G;
                 };
-                load_rows<T, D>(sQ, PQ, BM,
+                load_rows<D>(sQ, PQ, BM,
                                 [&](int r) { return r0 + r < rows ? q + token_row(r) * D : nullptr; });
                 if (threadIdx.x < BM)
-                    sML[threadIdx.x] = r0 + threadIdx.x < rows ? ml[token_row(threadIdx.x)] : make_float2(0.f, 0.f);
+                    s_lse[threadIdx.x] = r0 + threadIdx.x < rows ? lse[token_row(threadIdx.x)] : 0.f;
                 __syncthreads();
                 float a4[4][4];
 #pragma unroll
@@ -301,10 +271,10 @@ mass_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
                 for (int i = 0; i < 4; ++i) {
                     const long R = r0 + ty * 4 + i;
                     const int kmax = R < rows ? s.ctx + (int)(R / W.G) : -1;
-                    const float2 mi = sML[ty * 4 + i];
+                    const float e = s_lse[ty * 4 + i];
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (key0 + tx + 16 * j <= kmax) sum[j] += exp2f(a4[i][j] * scale_log2 - mi.x) * mi.y;
+                        if (key0 + tx + 16 * j <= kmax) sum[j] += exp2f(a4[i][j] * scale_log2 - e);
                 }
             }
             __syncthreads();
@@ -321,29 +291,29 @@ mass_simt_kernel(Pool P, WorkDim W, const T *__restrict__ q, int Hq, float scale
     }
 }
 
-template <typename T, int D, int BM, int BN>
-cudaError_t launch_attn(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float2 *ml,
+template <int D, int BM, int BN>
+cudaError_t launch_attn(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
                         const Parts &parts, int n_cta, cudaStream_t st)
 {
-    auto kern = attn_simt_kernel<T, D, BM, BN>;
+    auto kern = attn_simt_kernel<D, BM, BN>;
     constexpr int smem = Geom<D, BM, BN>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(n_cta), dim3(kThreads), smem, st, P, W, (const T *)q, Hq, sl2, (T *)out, ml, parts);
+    return launch_pdl(kern, dim3(n_cta), dim3(kThreads), smem, st, P, W, (const float *)q, Hq, sl2, (float *)out, lse, parts);
 }
 
-template <typename T, int D>
-cudaError_t launch_mass(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, const float2 *ml,
+template <int D>
+cudaError_t launch_mass(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, const float *lse,
                         float *scores, int scores_stride, cudaStream_t st)
 {
-    auto kern = mass_simt_kernel<T, D>;
+    auto kern = mass_simt_kernel<D>;
     constexpr int smem = (2 * 64 * (D + 4) + 16 * 64) * 4;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // about six CTAs per SM over the units; a CTA strides over its unit's key tiles
     const int units = (int)std::min<long>((long)P.B * P.Hkv, 1 << 20);
     const int per_unit = std::max(1, std::min(6 * device_sm_count() / units, 65535));
-    return launch_pdl(kern, dim3(units, per_unit), dim3(kThreads), smem, st, P, W, (const T *)q, Hq, sl2, ml, scores,
+    return launch_pdl(kern, dim3(units, per_unit), dim3(kThreads), smem, st, P, W, (const float *)q, Hq, sl2, lse, scores,
                       scores_stride);
 }
 
@@ -353,34 +323,23 @@ cudaError_t launch_mass(const Pool &P, const WorkDim &W, const void *q, int Hq, 
 int simt_rows(int T, int G) { return (long)T * G <= 16 ? 16 : 64; }
 int simt_ctas() { return 2 * device_sm_count(); }
 
-template <typename T>
-cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                       const Parts &parts, cudaStream_t st)
 {
     const int n = simt_ctas();
     if (simt_rows(W.T, W.G) == 16)
-        return d == 128 ? launch_attn<T, 128, 16, 64>(P, W, q, Hq, sl2, out, ml, parts, n, st)
-                        : launch_attn<T, 64, 16, 64>(P, W, q, Hq, sl2, out, ml, parts, n, st);
-    return d == 128 ? launch_attn<T, 128, 64, 32>(P, W, q, Hq, sl2, out, ml, parts, n, st)
-                    : launch_attn<T, 64, 64, 32>(P, W, q, Hq, sl2, out, ml, parts, n, st);
+        return d == 128 ? launch_attn<128, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st)
+                        : launch_attn<64, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st);
+    return d == 128 ? launch_attn<128, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)
+                    : launch_attn<64, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st);
 }
 
-template <typename T>
-cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float2 *ml,
+cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float *lse,
                       float *scores, int scores_stride, cudaStream_t st)
 {
-    return d == 128 ? launch_mass<T, 128>(P, W, q, Hq, sl2, ml, scores, scores_stride, st)
-                    : launch_mass<T, 64>(P, W, q, Hq, sl2, ml, scores, scores_stride, st);
+    return d == 128 ? launch_mass<128>(P, W, q, Hq, sl2, lse, scores, scores_stride, st)
+                    : launch_mass<64>(P, W, q, Hq, sl2, lse, scores, scores_stride, st);
 }
-
-template cudaError_t attn_simt<float>(const Pool &, const WorkDim &, int, const void *, int, float, void *, float2 *,
-                                      const Parts &, cudaStream_t);
-template cudaError_t attn_simt<__nv_bfloat16>(const Pool &, const WorkDim &, int, const void *, int, float, void *,
-                                              float2 *, const Parts &, cudaStream_t);
-template cudaError_t mass_simt<float>(const Pool &, const WorkDim &, int, const void *, int, float, const float2 *,
-                                      float *, int, cudaStream_t);
-template cudaError_t mass_simt<__nv_bfloat16>(const Pool &, const WorkDim &, int, const void *, int, float,
-                                              const float2 *, float *, int, cudaStream_t);
 
 }  // namespace paged
 }  // namespace vc

@@ -54,7 +54,6 @@ struct Shared {
     uint64_t full[10], empty[10];
     uint64_t q_ready, s_full[2], p_ready[2], o_full[2], meet;
     uint32_t tmem;
-    int32_t abort_flag;
     Piece piece;
     struct {
         Walk<256, BN> walk;
@@ -68,52 +67,15 @@ struct Params {
     WorkDim W;
     const __nv_bfloat16 *q;
     __nv_bfloat16 *out;
-    float2 *ml_out;
+    float *lse_out;
     Parts parts;
     int32_t *status;
     int Hq, box_rows, n_rows;      // n_rows: rows of the pool's tensor map
     float sl2;
 };
 
-__device__ __forceinline__ float ex2(float x)
-{
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, Shared *S, int32_t *status, int where)
-{
-    if (mbar_wait(bar, parity)) return true;
-    report_timeout(status, where);
-    atomicExch(&S->abort_flag, 1);
-    return false;
-}
-
-// The same by a whole warp, which stays together.
-__device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, Shared *S, int32_t *status, int where)
-{
-    return __all_sync(0xffffffffu, wait_bar(bar, parity, S, status, where));
-}
-
-// A place in the ring of K and V tiles; items are taken in the order in which
-// the products need them: K_0 (K_1), then V_i, K_{i + ahead}.
-template <int NST>
-struct Ring {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next()
-    {
-        if (++slot == NST) slot = 0, phase ^= 1;
-    }
-    __device__ __forceinline__ Ring after() const
-    {
-        Ring r = *this;
-        r.next();
-        return r;
-    }
-};
-
+// Items of the ring are taken in the order in which the products need them:
+// K_0 (K_1), then V_i, K_{i + ahead}.
 // The warp's next part; false at the end of the piece.
 __device__ __forceinline__ bool step(Shared *S, int warp, const Params &A)
 {
@@ -151,7 +113,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             mbar_init(&S->p_ready[t], 128);
             mbar_init(&S->o_full[t], 1);
         }
-        S->abort_flag = 0;
         fence_mbar_init();
     }
     if (warp == 9) {
@@ -180,7 +141,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         auto load = [&](const CUtensorMap *map, int row) {
             const int s = ring.slot;
             if (filled) {
-                if (lane == 0) ok = wait_bar(&S->empty[s], ring.phase ^ 1, S, A.status, 91);
+                if (lane == 0) ok = wait_bar(&S->empty[s], ring.phase ^ 1, A.status, 91);
                 ok = __shfl_sync(0xffffffffu, ok, 0);
                 if (!ok) return;
             }
@@ -226,7 +187,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             uint32_t units = 0, steps[2] = {0, 0};           // q_ready, p_ready phases
             bool ok = true;
             auto tile = [&](const Ring<NST> &x) { return smem_u32(sm + G::SM_KV + x.slot * G::TILE); };
-            auto arrived = [&](const Ring<NST> &x) { return wait_bar(&S->full[x.slot], x.phase, S, A.status, 92); };
+            auto arrived = [&](const Ring<NST> &x) { return wait_bar(&S->full[x.slot], x.phase, A.status, 92); };
             auto release = [&]() {                           // once the products issued so far are done
                 tc::commit(&S->empty[ring.slot]);
                 ring.next();
@@ -250,14 +211,14 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                                (!first || kk > 0) ? 1u : 0u);
             };
             auto p_wait = [&](int t) {
-                const bool r = wait_bar(&S->p_ready[t], steps[t] & 1, S, A.status, 93);
+                const bool r = wait_bar(&S->p_ready[t], steps[t] & 1, A.status, 93);
                 ++steps[t];
                 tc::fence_after();
                 return r;
             };
             while (ok && S->role[9].walk.next(A.P, A.W, S->role[9].it)) {
                 const int n = it.t_hi - it.t_lo;
-                ok = wait_bar(&S->q_ready, units & 1, S, A.status, 94);
+                ok = wait_bar(&S->q_ready, units & 1, A.status, 94);
                 ++units;
                 tc::fence_after();
                 if (it.rows > kRowsTile) {
@@ -324,7 +285,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         bool ok = true;
         auto meet = [&](int where) {                         // both softmax groups
             mbar_arrive(&S->meet);
-            const bool r = wait_warp(&S->meet, met & 1, S, A.status, where);
+            const bool r = wait_warp(&S->meet, met & 1, A.status, where);
             ++met;
             return r;
         };
@@ -335,7 +296,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const int n = it.t_hi - it.t_lo, len = it.ctx + it.n;
             const bool big = it.rows > kRowsTile;
             const int row0 = it.mt * 256;
-            auto out_row = [&](int rr) {                     // row of q, out and ml_out
+            auto out_row = [&](int rr) {                     // row of q, out and lse_out
                 const int R = row0 + rr;
                 return (size_t)(it.tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G;
             };
@@ -368,7 +329,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             for (int j = 0; j < mine; ++j) {
                 const int i = big ? j : 2 * j + t;           // key tile of the part
                 const int key0 = (it.t_lo + i) * BN;
-                ok = wait_warp(&S->s_full[t], steps & 1, S, A.status, 95);
+                ok = wait_warp(&S->s_full[t], steps & 1, A.status, 95);
                 ++steps;
                 if (!ok) break;
                 tc::fence_after();
@@ -440,7 +401,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 if (i == n - 1 && key0 + BN > len && (!big || t == 0)) {
                     // V rows of the last page past the sequence's end
                     const uint32_t vi = item + 2u * n - 1;   // the part's last ring item
-                    ok = wait_warp(&S->full[vi % NST], (vi / NST) & 1, S, A.status, 96);
+                    ok = wait_warp(&S->full[vi % NST], (vi / NST) & 1, A.status, 96);
                     if (!ok) break;
                     uint8_t *sV = sm + G::SM_KV + (vi % NST) * G::TILE;
                     const int page = A.P.page();
@@ -497,19 +458,19 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 }
                 if (valid && c0 == 0) {
                     if (!it.whole) A.parts.ml[pr] = make_float2(M, L);
-                    else if (A.ml_out) A.ml_out[row] = make_float2(M, inv);
+                    else if (A.lse_out) A.lse_out[row] = M + log2f(L);
                 }
             };
             if (big) {
-                ok = wait_warp(&S->o_full[t], units[t] & 1, S, A.status, 97);
+                ok = wait_warp(&S->o_full[t], units[t] & 1, A.status, 97);
                 ++units[0], ++units[1];
                 if (!ok) break;
                 tc::fence_after();
                 finish(m * A.sl2, l, 1.f, 0.f, 0, D);
             } else {
                 ml_x[t * kRowsTile + r] = make_float2(m * A.sl2, l);
-                ok = wait_warp(&S->o_full[0], units[0] & 1, S, A.status, 98) &&
-                     (n == 1 || wait_warp(&S->o_full[1], units[1] & 1, S, A.status, 99));
+                ok = wait_warp(&S->o_full[0], units[0] & 1, A.status, 98) &&
+                     (n == 1 || wait_warp(&S->o_full[1], units[1] & 1, A.status, 99));
                 ++units[0];
                 if (n > 1) ++units[1];
                 ok = ok && meet(100);
@@ -544,7 +505,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 }
 
 template <int D>
-cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float2 *ml,
+cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
                    const Parts &parts, int32_t *status, cudaStream_t st)
 {
     Params A;
@@ -552,7 +513,7 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     A.W = W;
     A.q = (const __nv_bfloat16 *)q;
     A.out = (__nv_bfloat16 *)out;
-    A.ml_out = ml;
+    A.lse_out = lse;
     A.parts = parts;
     A.status = status;
     A.Hq = Hq;
@@ -574,11 +535,11 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
 
 int tc_ctas() { return device_sm_count(); }
 
-cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float2 *ml,
+cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                     const Parts &parts, int32_t *status, cudaStream_t st)
 {
-    return d == 128 ? launch<128>(P, W, q, Hq, sl2, out, ml, parts, status, st)
-                    : launch<64>(P, W, q, Hq, sl2, out, ml, parts, status, st);
+    return d == 128 ? launch<128>(P, W, q, Hq, sl2, out, lse, parts, status, st)
+                    : launch<64>(P, W, q, Hq, sl2, out, lse, parts, status, st);
 }
 
 }  // namespace paged

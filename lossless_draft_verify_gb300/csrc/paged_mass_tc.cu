@@ -1,0 +1,421 @@
+// paged_mass_tc.cu -- the attention weight every slot of a paged bf16 cache
+// receives from a ragged batch of chunks, on the tensor cores:
+//
+//   scores[b][h][j] += sum over the rows r = (i, g) that see slot j of
+//       2^(scale' q_r . k_j - lse_r),   j <= ctx + i, lse from the attention.
+//
+// The product is taken transposed, S^T = K Q^T: a key is a row of the
+// accumulator, so one thread holds all of a key's weights for 128 query rows
+// and sums them without any exchange; every slot is owned by one thread and
+// its sum has a fixed order.  Four key tiles of 128 stay in shared memory while the
+// sequence's row tiles pass (a row tile is floor(128 / G) queries of the G
+// heads, one TMA box), so K is read from HBM once and a row tile from L2 once
+// per 512 keys.  With one row tile (decoding) this is a stream of K, bound by
+// HBM; with many the exponentials bound it.
+//   warps 0-3, 4-7  sums of the even and odd key tiles of a group;
+//   warp 8          producer; warp 9 issues the MMAs (four accumulators).
+#include "paged.cuh"
+#include "tcgen05.cuh"
+
+namespace vc {
+namespace paged {
+namespace {
+
+constexpr int BN = 128;          // keys per tile
+constexpr int kGroup = 4;        // key tiles of a group
+constexpr int kThreads = 320;
+constexpr int kQStages = 2;
+
+template <int D>
+struct Geom {
+    static constexpr int HALVES = D / 64;
+    static constexpr int TILE = BN * D * 2;
+    static constexpr int STAGES = kGroup * (128 / D);
+    static constexpr int SM_Q = 0;
+    static constexpr int SM_K = kQStages * TILE;
+    static constexpr int SM_X = SM_K + STAGES * TILE;
+    static constexpr int SMEM = SM_X + 8 * 512 + 1024;
+};
+
+// A CTA's share: groups, in the order sequence, head, group, each with the
+// cost 4 row tiles + 1; a group belongs to the CTA in whose part of the total
+// it begins.
+struct MassWalk {
+    int b, h, g;                 // next group
+    int groups, mt, rt;          // of the sequence: key groups, row tiles, rows per row tile
+    Seq s;
+    long at, end;                // cost at the next group's beginning, end of the share
+
+    static __device__ __forceinline__ long cost(int mt) { return 4l * mt + 1; }
+    __device__ __forceinline__ void shape(const Pool &P, const WorkDim &W, int b_)
+    {
+        b = b_;
+        s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
+        rt = BN / W.G * W.G;
+        mt = (int)(((long)s.n * W.G + rt - 1) / rt);
+        groups = mt > 0 ? (s.ctx + s.n + BN * kGroup - 1) / (BN * kGroup) : 0;
+    }
+};
+
+struct MassItem {
+    int b, h, key0, tiles;       // key tiles of the group
+    int tok0, ctx, len, mt0, mt; // row tiles mt0 .. mt - 1 see the group
+    long rows;
+};
+
+struct Shared {
+    uint64_t k_full[2 * kGroup], k_empty[2 * kGroup], q_full[kQStages], q_empty[kQStages], s_full[4], s_free[4];
+    uint32_t tmem;
+    MassWalk start;
+};
+
+struct Params {
+    Pool P;
+    WorkDim W;
+    const float *lse;
+    float *scores;
+    int32_t *status;
+    int Hq, scores_stride, box_rows, n_rows, q_box;   // q_box: queries per row tile box
+    float sl2;
+};
+
+// One warp finds where the CTA's share begins.
+__device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, MassWalk *out)
+{
+    const int lane = threadIdx.x & 31;
+    long total = 0;
+    MassWalk w;
+    for (int b0 = 0; b0 < A.P.B; b0 += 32) {
+        long c = 0;
+        if (b0 + lane < A.P.B) {
+            w.shape(A.P, A.W, b0 + lane);
+            c = (long)w.groups * A.P.Hkv * MassWalk::cost(w.mt);
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+        total += c;
+    }
+    const long per = (total + n_cta - 1) / n_cta, lo = per * cta, hi = lmin(total, lo + per);
+    if (lane == 0) out->at = out->end = 0;
+    __syncwarp();
+    if (lo >= hi) return;
+    long before = 0;
+    for (int b0 = 0; b0 < A.P.B; b0 += 32) {
+        long c = 0;
+        if (b0 + lane < A.P.B) {
+            w.shape(A.P, A.W, b0 + lane);
+            c = (long)w.groups * A.P.Hkv * MassWalk::cost(w.mt);
+        }
+        long incl = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long up = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += up;
+        }
+        const long start = before + incl - c;
+        if (c > 0 && start <= lo && lo < start + c) {
+            // the first group that begins at lo or later (it may be the next sequence's first)
+            const long cg = MassWalk::cost(w.mt), x = (lo - start + cg - 1) / cg;
+            w.h = (int)(x / w.groups);
+            w.g = (int)(x % w.groups);
+            w.at = start + x * cg;
+            w.end = hi;
+            *out = w;
+        }
+        before += __shfl_sync(0xffffffffu, incl, 31);
+    }
+}
+
+__device__ __forceinline__ bool next_group(MassWalk &w, const Params &A, MassItem &it)
+{
+    while (w.at < w.end) {
+        if (w.g >= w.groups) {
+            w.g = 0;
+            ++w.h;
+        }
+        if (w.groups == 0 || w.h >= A.P.Hkv) {
+            if (w.b + 1 >= A.P.B) return false;
+            w.shape(A.P, A.W, w.b + 1);
+            w.h = w.g = 0;
+            continue;
+        }
+        it.b = w.b;
+        it.h = w.h;
+        it.key0 = w.g * BN * kGroup;
+        it.tok0 = w.s.tok0;
+        it.ctx = w.s.ctx;
+        it.len = w.s.ctx + w.s.n;
+        it.tiles = min(kGroup, (it.len - it.key0 + BN - 1) / BN);
+        it.rows = (long)w.s.n * A.W.G;
+        it.mt0 = (int)(lmax(it.key0 - w.s.ctx, 0) * A.W.G / w.rt);
+        it.mt = w.mt;
+        w.at += MassWalk::cost(w.mt);
+        ++w.g;
+        return true;
+    }
+    return false;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmQ, Params A)
+{
+    using G = Geom<D>;
+    constexpr int NST = G::STAGES;
+    extern __shared__ __align__(1024) uint8_t sm[];
+    float *s_lse = reinterpret_cast<float *>(sm + G::SM_X);  // [8 warps][128]
+    Shared *S = reinterpret_cast<Shared *>(sm + G::SM_X + 8 * 512);
+    static_assert(sizeof(Shared) <= 1024, "shared block");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    pdl_wait();
+    if (smem_u32(sm) & 1023u) {                              // never expected: the swizzled tiles need it
+        if (threadIdx.x == 0) report_timeout(A.status, 110);
+        return;
+    }
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < NST; ++i) {
+            mbar_init(&S->k_full[i], 1);
+            mbar_init(&S->k_empty[i], 1);
+        }
+        for (int i = 0; i < kQStages; ++i) {
+            mbar_init(&S->q_full[i], 1);
+            mbar_init(&S->q_empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&S->s_full[i], 1);
+            mbar_init(&S->s_free[i], 4);                     // the warps of a group of sums
+        }
+        fence_mbar_init();
+    }
+    if (warp == 9) {
+        tc::tmem_alloc(&S->tmem, 512);
+        tc::tmem_relinquish();
+    }
+    if (warp == 8) find_share(A, blockIdx.x, gridDim.x, &S->start);
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    pdl_trigger();
+    const uint32_t tmem = S->tmem;
+    const int rt = BN / A.W.G * A.W.G;                       // rows of a row tile
+    MassWalk walk = S->start;
+    MassItem it;
+
+    if (warp == 8) {
+        // ------------------------------------------------------- producer --
+        const int boxes = BN / A.box_rows * G::HALVES;
+        const int bp = lane / G::HALVES, half = lane % G::HALVES;
+        const uint32_t q_bytes = (uint32_t)A.q_box * A.W.G * D * 2;
+        Ring<NST> kr;
+        Ring<kQStages> qr;
+        bool ok = true, k_round = false, q_round = false;
+        auto load_q = [&](int mt) {
+            if (q_round) {
+                if (lane == 0) ok = wait_bar(&S->q_empty[qr.slot], qr.phase ^ 1, A.status, 111);
+                ok = __shfl_sync(0xffffffffu, ok, 0);
+                if (!ok) return;
+            }
+            if (lane == 0) {
+                uint8_t *dst = sm + G::SM_Q + qr.slot * G::TILE;
+                mbar_arrive_expect_tx(&S->q_full[qr.slot], q_bytes);
+#pragma unroll
+                for (int x = 0; x < G::HALVES; ++x)
+                    tc::tma_load_3d(dst + x * (BN * 128), &tmQ, x * 64, it.h * A.W.G, it.tok0 + mt * (BN / A.W.G),
+                                    &S->q_full[qr.slot]);
+            }
+            qr.next();
+            q_round = q_round || qr.slot == 0;
+        };
+        while (ok && next_group(walk, A, it)) {
+            load_q(it.mt0);
+            for (int k = 0; k < it.tiles && ok; ++k) {
+                const int slot = it.key0 + k * BN + bp * A.box_rows;
+                int row = A.n_rows;                          // outside the map: zeros
+                if (lane < boxes && slot < it.len) {
+                    const int pg = A.P.page_of(it.b, slot >> A.P.page_log2);
+                    if (pg >= 0) row = (int)A.P.row(pg, it.h, slot & (A.P.page() - 1));
+                }
+                if (k_round) {
+                    if (lane == 0) ok = wait_bar(&S->k_empty[kr.slot], kr.phase ^ 1, A.status, 112);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&S->k_full[kr.slot], G::TILE);
+                __syncwarp();
+                if (lane < boxes)
+                    tc::tma_load_3d(sm + G::SM_K + kr.slot * G::TILE + half * (BN * 128) + bp * A.box_rows * 128, &tmK,
+                                    half * 64, row, 0, &S->k_full[kr.slot]);
+                kr.next();
+                k_round = k_round || kr.slot == 0;
+            }
+            for (int q = it.mt0 + 1; q < it.mt && ok; ++q) load_q(q);
+        }
+        if (!ok && lane == 0) {                              // copies in flight end before the CTA does
+            for (int i = 0; i < NST; ++i)
+                if (k_round || i < kr.slot) mbar_wait(&S->k_full[i], i < kr.slot ? kr.phase : kr.phase ^ 1);
+            for (int i = 0; i < kQStages; ++i)
+                if (q_round || i < qr.slot) mbar_wait(&S->q_full[i], i < qr.slot ? qr.phase : qr.phase ^ 1);
+        }
+    } else if (warp == 9) {
+        // -------------------------------------------------------- issuer --
+        if (lane == 0) {
+            Ring<NST> k0;                                    // the group's first key tile
+            Ring<kQStages> qr;
+            Ring<2> sr[2];                                   // accumulators of the two groups of sums
+            bool ok = true, s_round[2] = {false, false};
+            while (ok && next_group(walk, A, it)) {
+                Ring<NST> kr = k0;
+                for (int q = it.mt0; q < it.mt && ok; ++q) {
+                    ok = wait_bar(&S->q_full[qr.slot], qr.phase, A.status, 113);
+                    if (!ok) break;
+                    const int cols = (int)lmin(rt, it.rows - (long)q * rt);
+                    const uint32_t id = tc::idesc_bf16(BN, (cols + 15) / 16 * 16, false, false);
+                    const uint32_t sQ = smem_u32(sm + G::SM_Q + qr.slot * G::TILE);
+                    kr = k0;
+                    for (int k = 0; k < it.tiles; ++k) {
+                        const int w = k & 1;
+                        Ring<2> &a = sr[w];
+                        ok = wait_bar(&S->k_full[kr.slot], kr.phase, A.status, 114) &&
+                             (!s_round[w] || wait_bar(&S->s_free[2 * w + a.slot], a.phase ^ 1, A.status, 115));
+                        if (!ok) break;
+                        tc::fence_after();
+                        const uint32_t sK = smem_u32(sm + G::SM_K + kr.slot * G::TILE);
+#pragma unroll
+                        for (int kk = 0; kk < D / 16; ++kk) {
+                            const uint32_t o = (kk >> 2) * (BN * 128) + (kk & 3) * 32;
+                            tc::mma_ss(tmem + (2 * w + a.slot) * BN, tc::smem_desc(sK + o, 16, 1024, tc::kSwizzle128B),
+                                       tc::smem_desc(sQ + o, 16, 1024, tc::kSwizzle128B), id, kk > 0);
+                        }
+                        tc::commit(&S->s_full[2 * w + a.slot]);
+                        a.next();
+                        s_round[w] = s_round[w] || a.slot == 0;
+                        if (q == it.mt - 1) tc::commit(&S->k_empty[kr.slot]);
+                        kr.next();
+                    }
+                    tc::commit(&S->q_empty[qr.slot]);
+                    qr.next();
+                }
+                k0 = kr;
+            }
+        }
+    } else {
+        // ---------------------------------------------------------- sums --
+        const int w = warp >> 2, wq = warp & 3;
+        const uint32_t lanes = (uint32_t)(wq * 32) << 16;
+        float *my_lse = s_lse + warp * BN;
+        Ring<2> sr;
+        bool ok = true;
+        while (ok && next_group(walk, A, it)) {
+            float sum[kGroup / 2];
+#pragma unroll
+            for (int i = 0; i < kGroup / 2; ++i) sum[i] = 0.f;
+            for (int q = it.mt0; q < it.mt && ok; ++q) {
+                const int cols = (int)lmin(rt, it.rows - (long)q * rt);
+                // lse of the tile's rows, a copy per warp
+                __syncwarp();
+                for (int c = lane; c < BN; c += 32) {
+                    const int R = q * rt + c;
+                    my_lse[c] = c < cols ? A.lse[(size_t)(it.tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G] : 0.f;
+                }
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < kGroup / 2; ++i) {
+                    const int k = 2 * i + w;
+                    if (k >= it.tiles || !ok) continue;
+                    ok = wait_warp(&S->s_full[2 * w + sr.slot], sr.phase, A.status, 116);
+                    if (!ok) continue;
+                    tc::fence_after();
+                    const int tile0 = it.key0 + k * BN, key = tile0 + wq * 32 + lane;
+                    // columns [lo, cols) see the key; [lo_all, cols) every key of the tile
+                    const int lo = (int)lmin(lmax((long)(key - it.ctx) * A.W.G - (long)q * rt, 0), BN);
+                    const int lo_all = (int)lmin(lmax((long)(tile0 + BN - 1 - it.ctx) * A.W.G - (long)q * rt, 0), BN);
+                    float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                    const float2 sc = make_float2(A.sl2, A.sl2);
+                    for (int c0 = 0; c0 < cols; c0 += 32) {
+                        uint32_t u[32];
+                        __syncwarp();
+                        tc::ld32(tmem + lanes + (2 * w + sr.slot) * BN + c0, u);
+                        tc::ld_wait();
+                        if (c0 >= lo_all && c0 + 32 <= cols) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 4) {
+                                const float4 e = *reinterpret_cast<const float4 *>(my_lse + c0 + c);
+                                const float2 x = fma2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sc,
+                                                      make_float2(-e.x, -e.y));
+                                const float2 y = fma2(make_float2(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])),
+                                                      sc, make_float2(-e.z, -e.w));
+                                acc[0] = add2(acc[0], make_float2(ex2(x.x), ex2(x.y)));
+                                acc[1] = add2(acc[1], make_float2(ex2(y.x), ex2(y.y)));
+                            }
+                        } else {
+                            // columns past the rows hold whatever was there: chosen, not multiplied away
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) {
+                                const float p = ex2(fmaf(__uint_as_float(u[c]), A.sl2, -my_lse[c0 + c]));
+                                if (c0 + c >= lo && c0 + c < cols) acc[0].x += p;
+                            }
+                        }
+                    }
+                    sum[i] += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                    tc::fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&S->s_free[2 * w + sr.slot]);
+                    sr.next();
+                }
+            }
+            if (!ok) break;
+            float *dst = A.scores + ((size_t)it.b * A.P.Hkv + it.h) * A.scores_stride;
+#pragma unroll
+            for (int i = 0; i < kGroup / 2; ++i) {
+                const int key = it.key0 + (2 * i + w) * BN + wq * 32 + lane;
+                if (key < it.len) dst[key] += sum[i];
+            }
+        }
+    }
+    tc::fence_before();
+    __syncthreads();
+    tc::fence_after();
+    if (warp == 9) {
+        __syncwarp();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D>
+cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, const float *lse, float *scores,
+                   int scores_stride, int32_t *status, cudaStream_t st)
+{
+    Params A;
+    A.P = P;
+    A.W = W;
+    A.lse = lse;
+    A.scores = scores;
+    A.status = status;
+    A.Hq = Hq;
+    A.scores_stride = scores_stride;
+    A.box_rows = std::min(1 << P.page_log2, BN);
+    A.n_rows = (P.n_pages * P.Hkv) << P.page_log2;
+    A.q_box = std::min(BN / W.G, W.T);
+    A.sl2 = sl2;
+    CUtensorMap mk, mq;
+    const uint64_t bytes = (uint64_t)D * 2;
+    if (!tma_map_bf16_3d(&mk, P.k, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1) ||
+        !tma_map_bf16_3d(&mq, q, D, Hq, W.T, bytes, bytes * Hq, 64, W.G, A.q_box))
+        return cudaErrorInvalidValue;
+    auto kern = mass_tc_kernel<D>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3(device_sm_count()), dim3(kThreads), Geom<D>::SMEM, st, mk, mq, A);
+}
+
+}  // namespace
+
+cudaError_t mass_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float *lse,
+                    float *scores, int scores_stride, int32_t *status, cudaStream_t st)
+{
+    return d == 128 ? launch<128>(P, W, q, Hq, sl2, lse, scores, scores_stride, status, st)
+                    : launch<64>(P, W, q, Hq, sl2, lse, scores, scores_stride, status, st);
+}
+
+}  // namespace paged
+}  // namespace vc

@@ -428,7 +428,10 @@ bool paged_heads_ok(const vc_paged_cache *c, int T, int Hq)
     return T >= 0 && Hq > 0 && Hq % c->Hkv == 0;
 }
 
-bool paged_rows_ok(int T, int Hq) { return (int64_t)T * Hq <= (1 << 30); }
+bool paged_rows_ok(const vc_paged_cache *c, int T, int Hq)
+{
+    return (int64_t)T * Hq <= (1 << 30) && Hq / c->Hkv <= 128;
+}
 
 paged::Pool paged_pool(const vc_paged_cache *c)
 {
@@ -448,7 +451,7 @@ paged::Pool paged_pool(const vc_paged_cache *c)
 
 size_t paged_attn_ws(const vc_paged_cache *c, int T, int Hq, bool mass)
 {
-    if (!paged_ok(c) || !paged_supported(c) || !paged_heads_ok(c, T, Hq) || !paged_rows_ok(T, Hq)) return 0;
+    if (!paged_ok(c) || !paged_supported(c) || !paged_heads_ok(c, T, Hq) || !paged_rows_ok(c, T, Hq)) return 0;
     return paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, mass);
 }
 
@@ -459,7 +462,7 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t 
     if (!paged_ok(c) || !q || !q_start || !ctx_len || !out || !ws || !paged_heads_ok(c, T, Hq)) return VC_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
     if (!(sm_scale >= 0.f) || sm_scale > FLT_MAX) return VC_ERR_INVALID;
-    if (!paged_supported(c) || !paged_rows_ok(T, Hq)) return VC_ERR_UNSUPPORTED;
+    if (!paged_supported(c) || !paged_rows_ok(c, T, Hq)) return VC_ERR_UNSUPPORTED;
     if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
     if (ws_bytes < paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, scores != nullptr)) return VC_ERR_INVALID;
     if (T == 0) return VC_OK;
@@ -502,7 +505,7 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
     if (!paged_heads_ok(cache, T, Hq) || (q_gain == nullptr) != (k_gain == nullptr)) return VC_ERR_INVALID;
     if (!(eps >= 0.f) || !aligned(qkv, 16) || !aligned(q_out, 16)) return VC_ERR_INVALID;
     if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > cache->d) return VC_ERR_INVALID;
-    if (!paged_supported(cache) || !paged_rows_ok(T, Hq)) return VC_ERR_UNSUPPORTED;
+    if (!paged_supported(cache) || !paged_rows_ok(cache, T, Hq)) return VC_ERR_UNSUPPORTED;
     if (T == 0) return VC_OK;
     return cuda_status(paged::append(paged_pool(cache), cache->dt, cache->d, qkv, q_gain, k_gain, eps, *rope, positions,
                                      q_start, ctx_len, T, Hq, q_out, stream));

@@ -71,7 +71,7 @@ def test_bad_arguments_are_refused(vc):
     at = [A, c, A, A, 4, 4, 1.0, A, A, need, None]
     for i, x, want in [(0, None, 1), (0, A + 8, 1), (2, None, 1), (3, None, 1), (4, -1, 1), (5, 0, 1), (5, 5, 1),
                        (6, -1.0, 1), (6, math.nan, 1), (6, math.inf, 1), (7, None, 1), (7, A + 4, 1), (8, None, 1),
-                       (8, A + 16, 1), (9, need - 1, 1), (4, 1 << 29, 2)]:
+                       (8, A + 16, 1), (9, need - 1, 1), (4, 1 << 29, 2), (5, 258, 2)]:
         a = list(at)
         a[i] = x
         assert L.vc_paged_attn(*a) == want, (i, x)
