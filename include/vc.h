@@ -817,7 +817,7 @@ vc_status vc_rope_init_freqs(vc_rope *rope, int rotary_dim, const double *inv_fr
  * vc_paged_append -- the chunk's q, k and v on their way to attention: qkv
  * [T][(Hq + 2 Hkv) d] (the rows of a q | k | v projection) in cache->dt.
  * Every q head goes to q_out [T][Hq][d], every k and v head into the pages at
- * its token's slot.  With q_gain and k_gain ([d] each, cache->dt; both or
+ * its token's slot; all 16-byte aligned.  With q_gain and k_gain ([d] each, cache->dt; both or
  * neither NULL) each q and k head is first normalised,
  *   x / sqrt(mean(x^2) + eps) * gain.
  * Then q and k are rotated at positions[row] (device int32 [T]; NULL: the

@@ -6,11 +6,13 @@
 // ascending).  A cluster of eight CTAs takes one (sequence, head): an
 // MSB-first radix select (11 + 11 + 10 bits of an order-preserving integer
 // image of the scores) with one histogram per CTA in shared memory, summed
-// over the cluster through distributed shared memory, finds the threshold;
-// counts exchanged the same way give every CTA the place of its first kept
-// slot, and an ordered block scan writes the kept slots and their scores.  The
-// scores are read once per pass, from L2 after the first.  A second kernel moves the rows:
-// one read and one write of every kept row, which is what bounds the call.
+// over the cluster through distributed shared memory, finds the threshold.
+// Every warp owns a run of consecutive slots; its counts above and at the
+// threshold, prefixed over warps and CTAs, give the place of its first kept
+// slot, and ballots order the rest.  The scores are read once per pass, eight
+// loads in flight per thread, from L2 after the first.  A second kernel moves
+// the rows: one read and one write of every kept row, which is what bounds the
+// call.
 #include <cooperative_groups.h>
 
 #include "paged.cuh"
@@ -51,32 +53,33 @@ __device__ __forceinline__ int src_tokens(const Pool &S, const int32_t *src_len,
     return 0;
 }
 
-// inclusive scan over the block's threads
-__device__ __forceinline__ int block_scan(int v, int *warp_sums)
+constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 8;                              // scores a thread has in flight
+
+// f(index, score, in range) for the slots of [lo, hi) that fall to the caller,
+// one of `stride`; all lanes of a warp run alike.
+template <typename F>
+__device__ __forceinline__ void for_scores(const float *__restrict__ sc, int lo, int hi, int at, int stride, F f)
 {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int i0 = lo; i0 < hi; i0 += stride * kBatch) {
+        float x[kBatch];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int up = __shfl_up_sync(0xffffffffu, v, o);
-        if (lane >= o) v += up;
+        for (int e = 0; e < kBatch; ++e) {
+            const int i = i0 + e * stride + at;
+            x[e] = i < hi ? sc[i] : 0.f;
+        }
+#pragma unroll
+        for (int e = 0; e < kBatch; ++e) f(i0 + e * stride + at, x[e], i0 + e * stride + at < hi);
     }
-    __syncthreads();
-    if (lane == 31) warp_sums[warp] = v;
-    __syncthreads();
-    int before = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w)
-        if (w < warp) before += warp_sums[w];
-    return v + before;
 }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 select_kernel(Pool S, EvictParams E)
 {
     __shared__ int hist[kBins];
-    __shared__ int warp_sums[kThreads / 32];
+    __shared__ int warp_sums[kWarps];
     __shared__ int s_digit, s_above;
-    __shared__ int s_count[2];                         // this CTA's slots above / at the threshold
+    __shared__ int2 s_count[kWarps + 1];               // slots above / at the threshold: by warp, of the CTA
     cg::cluster_group cluster = cg::this_cluster();
     pdl_wait();
     pdl_trigger();
@@ -89,9 +92,10 @@ select_kernel(Pool S, EvictParams E)
     int32_t *kept = E.kept_idx + (size_t)unit * E.kept_stride;
     float *sc_out = E.scores_out ? E.scores_out + (size_t)unit * E.out_stride : nullptr;
     if (unit % S.Hkv == 0 && rank == 0 && threadIdx.x == 0) E.dst_len[b] = keep;
-    // this CTA's candidates [lo, hi), a multiple of the block size but for the last
-    const int seg = cdiv(cdiv(cand, kCluster), kThreads) * kThreads;
-    const int lo = min(cand, rank * seg), hi = min(cand, lo + seg);
+    // the CTA's candidates [lo, hi), in runs of `run` slots per warp
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int run = cdiv(cdiv(cand, kCluster * kWarps), 32) * 32;
+    const int lo = (int)min((long)cand, (long)rank * run * kWarps), hi = (int)min((long)cand, lo + (long)run * kWarps);
 
     uint32_t prefix = 0;
     int remaining = top;                               // still to be taken among keys that match the prefix
@@ -103,10 +107,11 @@ select_kernel(Pool S, EvictParams E)
             shift -= width;
             for (int i = threadIdx.x; i < bins; i += kThreads) hist[i] = 0;
             __syncthreads();
-            for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-                const uint32_t key = score_key(sc[i]);
-                if (pass == 0 || (key >> (shift + width)) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
-            }
+            for_scores(sc, lo, hi, threadIdx.x, kThreads, [&](int, float x, bool on) {
+                const uint32_t key = score_key(x);
+                if (on && (pass == 0 || (key >> (shift + width)) == prefix))
+                    atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+            });
             cluster.sync();
             // totals from the highest digit down, kBins / kThreads digits per thread
             constexpr int PER = kBins / kThreads;
@@ -121,7 +126,15 @@ select_kernel(Pool S, EvictParams E)
                 cnt[e] = c;
                 sum += c;
             }
-            const int incl = block_scan(sum, warp_sums);
+            int incl = sum;                            // inclusive over the block's threads
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += up;
+            }
+            if (lane == 31) warp_sums[warp] = incl;
+            __syncthreads();
+            for (int w = 0; w < warp; ++w) incl += warp_sums[w];
             int above = incl - sum;
             if (above < remaining && remaining <= incl) {
 #pragma unroll
@@ -141,53 +154,44 @@ select_kernel(Pool S, EvictParams E)
     // prefix is now the threshold key; of the slots that hold it the first
     // `remaining` are kept.  top = 0 keeps none, top = cand all.
     const bool none = top == 0, all = top == cand;
-    int above = 0, at = 0;
-    for (int i = lo + threadIdx.x; i < hi; i += kThreads) {
-        const uint32_t key = score_key(sc[i]);
-        above += all || (!none && key > prefix);
-        at += !all && !none && key == prefix;
+    const int wlo = min(hi, lo + warp * run), whi = min(hi, wlo + run);
+    int2 mine = make_int2(0, 0);                       // kept for sure, tied
+    if (!none) {
+        for_scores(sc, wlo, whi, lane, 32, [&](int, float x, bool on) {
+            const uint32_t key = score_key(x);
+            mine.x += __popc(__ballot_sync(0xffffffffu, on && (all || key > prefix)));
+            mine.y += __popc(__ballot_sync(0xffffffffu, on && !all && key == prefix));
+        });
     }
-    if (threadIdx.x < 2) s_count[threadIdx.x] = 0;
+    if (lane == 0) s_count[warp] = mine;
     __syncthreads();
-    above = (int)__reduce_add_sync(0xffffffffu, (unsigned)above);
-    at = (int)__reduce_add_sync(0xffffffffu, (unsigned)at);
-    if ((threadIdx.x & 31) == 0) {
-        atomicAdd(&s_count[0], above);
-        atomicAdd(&s_count[1], at);
+    if (threadIdx.x == 0) {
+        int2 sum = make_int2(0, 0);
+        for (int w = 0; w < kWarps; ++w) sum.x += s_count[w].x, sum.y += s_count[w].y;
+        s_count[kWarps] = sum;
     }
     cluster.sync();
-    int above_before = 0, at_before = 0;
+    int2 before = make_int2(0, 0);
     for (int r = 0; r < rank; ++r) {
-        above_before += *cluster.map_shared_rank(&s_count[0], r);
-        at_before += *cluster.map_shared_rank(&s_count[1], r);
+        const int2 c = *cluster.map_shared_rank(&s_count[kWarps], r);
+        before.x += c.x, before.y += c.y;
     }
-    // ordered write: kept slots above the threshold and the first `remaining` at it
-    int base = above_before + min(at_before, remaining), at_base = at_before;
-    for (int i0 = lo; i0 < hi; i0 += kThreads) {
-        const int i = i0 + threadIdx.x;
-        const float s = i < hi ? sc[i] : 0.f;
-        const uint32_t key = score_key(s);
-        const bool gt = i < hi && (all || (!none && key > prefix));
-        const bool eq = i < hi && !all && !none && key == prefix;
-        // both counts in one scan: at most kThreads of each
-        const int incl = block_scan((gt ? 1 : 0) | (eq ? 1 << 16 : 0), warp_sums);
-        const int gt_i = incl & 0xffff, eq_i = incl >> 16;
-        const int eq_room = max(0, remaining - at_base);           // ties this step may still keep
-        const int eq_kept = min(eq_i, eq_room);
-        if (gt || (eq && eq_i <= eq_room)) {
-            const int j = base + gt_i + eq_kept - 1;
-            kept[j] = i;
-            if (sc_out) sc_out[j] = s;
-        }
-        // totals of the step
-        __syncthreads();
-        if (threadIdx.x == kThreads - 1) {
-            s_digit = gt_i + eq_kept;
-            s_above = eq_i;
-        }
-        __syncthreads();
-        base += s_digit;
-        at_base += s_above;
+    for (int w = 0; w < warp; ++w) before.x += s_count[w].x, before.y += s_count[w].y;
+    if (mine.x + mine.y > 0) {
+        // a tied slot is kept while fewer than `remaining` ties precede it
+        for_scores(sc, wlo, whi, lane, 32, [&](int i, float x, bool on) {
+            const uint32_t key = score_key(x), below = (1u << lane) - 1;
+            const bool gt = on && (all || key > prefix), eq = on && !all && key == prefix;
+            const unsigned m_gt = __ballot_sync(0xffffffffu, gt), m_eq = __ballot_sync(0xffffffffu, eq);
+            const int ties = before.y + __popc(m_eq & below);
+            if (gt || (eq && ties < remaining)) {
+                const int j = before.x + __popc(m_gt & below) + min(ties, remaining);
+                kept[j] = i;
+                if (sc_out) sc_out[j] = x;
+            }
+            before.x += __popc(m_gt);
+            before.y += __popc(m_eq);
+        });
     }
     for (int i = rank * kThreads + threadIdx.x; i < recent; i += kCluster * kThreads) {
         kept[top + i] = cand + i;

@@ -503,7 +503,8 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
 {
     if (!paged_ok(cache) || !qkv || !rope || !q_start || !ctx_len || !q_out) return VC_ERR_INVALID;
     if (!paged_heads_ok(cache, T, Hq) || (q_gain == nullptr) != (k_gain == nullptr)) return VC_ERR_INVALID;
-    if (!(eps >= 0.f) || !aligned(qkv, 16) || !aligned(q_out, 16)) return VC_ERR_INVALID;
+    if (!(eps >= 0.f) || !aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16) || !aligned(k_gain, 16))
+        return VC_ERR_INVALID;
     if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > cache->d) return VC_ERR_INVALID;
     if (!paged_supported(cache) || !paged_rows_ok(cache, T, Hq)) return VC_ERR_UNSUPPORTED;
     if (T == 0) return VC_OK;
