@@ -5,13 +5,16 @@
 // Selection is exact: the kept set is the largest by (score descending, slot
 // ascending).  A cluster of eight CTAs takes one (sequence, head): an
 // MSB-first radix select (11 + 11 + 10 bits of an order-preserving integer
-// image of the scores) with one histogram per CTA in shared memory, summed
-// over the cluster through distributed shared memory, finds the threshold.
+// image of the scores) with one histogram per CTA in shared memory finds the
+// threshold; each CTA adds up an eighth of the digits over the cluster through
+// distributed shared memory, and the one that holds the searched digit tells
+// the others.
 // Every warp owns a run of consecutive slots; its counts above and at the
 // threshold, prefixed over warps and CTAs, give the place of its first kept
-// slot, and ballots order the rest.  The scores are read once per pass, eight
-// loads in flight per thread, from L2 after the first.  A second kernel moves
-// the rows: one read and one write of every kept row, which is what bounds the
+// slot, and ballots order the rest.  The scores are read from memory once, eight
+// loads in flight per thread, and kept in shared memory for the further passes
+// (read again where a CTA has more than 16384).  A second kernel moves the
+// rows: one read and one write of every kept row, which is what bounds the
 // call.
 #include <cooperative_groups.h>
 
@@ -26,6 +29,7 @@ namespace {
 constexpr int kCluster = 8;
 constexpr int kThreads = 512;
 constexpr int kBins = 2048;
+constexpr int kCache = 16384;                          // scores a CTA keeps: 64 KB, two CTAs per SM
 
 // larger score -> larger key; -0 and +0 are one score, NaN is below every number
 __device__ __forceinline__ uint32_t score_key(float s)
@@ -40,7 +44,7 @@ struct EvictParams {
     const int32_t *src_len;
     int32_t *dst_len, *kept_idx;
     float *scores_out;
-    int scores_stride, kept_stride, out_stride;
+    int scores_stride, kept_stride, out_stride, cache;
     long top, recent;
 };
 
@@ -59,7 +63,7 @@ constexpr int kBatch = 8;                              // scores a thread has in
 // f(index, score, in range) for the slots of [lo, hi) that fall to the caller,
 // one of `stride`; all lanes of a warp run alike.
 template <typename F>
-__device__ __forceinline__ void for_scores(const float *__restrict__ sc, int lo, int hi, int at, int stride, F f)
+__device__ __forceinline__ void for_scores(const float *sc, int lo, int hi, int at, int stride, F f)
 {
     for (int i0 = lo; i0 < hi; i0 += stride * kBatch) {
         float x[kBatch];
@@ -78,7 +82,9 @@ select_kernel(Pool S, EvictParams E)
 {
     __shared__ int hist[kBins];
     __shared__ int warp_sums[kWarps];
+    __shared__ int s_slice[kCluster];                  // the CTAs' totals of their digits, of this pass
     __shared__ int s_digit, s_above;
+    extern __shared__ float cache[];
     __shared__ int2 s_count[kWarps + 1];               // slots above / at the threshold: by warp, of the CTA
     cg::cluster_group cluster = cg::this_cluster();
     pdl_wait();
@@ -99,34 +105,35 @@ select_kernel(Pool S, EvictParams E)
 
     uint32_t prefix = 0;
     int remaining = top;                               // still to be taken among keys that match the prefix
+    const float *src = sc;
     if (top > 0 && top < cand) {
+        const bool keep_scores = hi - lo <= E.cache;
         int shift = 32;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            const int width = pass == 2 ? 10 : 11, bins = 1 << width;
+            const int width = pass == 2 ? 10 : 11, bins = 1 << width, part = bins / kCluster;
             shift -= width;
             for (int i = threadIdx.x; i < bins; i += kThreads) hist[i] = 0;
             __syncthreads();
-            for_scores(sc, lo, hi, threadIdx.x, kThreads, [&](int, float x, bool on) {
+            for_scores(src, lo, hi, threadIdx.x, kThreads, [&](int i, float x, bool on) {
                 const uint32_t key = score_key(x);
+                if (on && pass == 0 && keep_scores) cache[i - lo] = x;
                 if (on && (pass == 0 || (key >> (shift + width)) == prefix))
                     atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
             });
+            if (keep_scores) src = cache - lo;
             cluster.sync();
-            // totals from the highest digit down, kBins / kThreads digits per thread
-            constexpr int PER = kBins / kThreads;
-            int cnt[PER], sum = 0;
+            // This CTA's digits, from the highest down: rank 0 has the highest
+            // part of them.  Two threads per digit, four histograms each.
+            const int dgt = bins - 1 - (rank * part + (int)threadIdx.x / 2);
+            int cnt = 0;
+            if ((int)threadIdx.x < 2 * part) {
 #pragma unroll
-            for (int e = 0; e < PER; ++e) {
-                const int dgt = bins - 1 - (threadIdx.x * PER + e);
-                int c = 0;
-                if (dgt >= 0)
-#pragma unroll
-                    for (int r = 0; r < kCluster; ++r) c += *cluster.map_shared_rank(&hist[dgt], r);
-                cnt[e] = c;
-                sum += c;
+                for (int r = 0; r < kCluster / 2; ++r)
+                    cnt += *cluster.map_shared_rank(&hist[dgt], (threadIdx.x & 1) * (kCluster / 2) + r);
             }
-            int incl = sum;                            // inclusive over the block's threads
+            cnt += __shfl_xor_sync(0xffffffffu, cnt, 1);
+            int incl = threadIdx.x & 1 ? 0 : cnt;      // inclusive over the digits from the highest
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int up = __shfl_up_sync(0xffffffffu, incl, o);
@@ -135,18 +142,18 @@ select_kernel(Pool S, EvictParams E)
             if (lane == 31) warp_sums[warp] = incl;
             __syncthreads();
             for (int w = 0; w < warp; ++w) incl += warp_sums[w];
-            int above = incl - sum;
-            if (above < remaining && remaining <= incl) {
-#pragma unroll
-                for (int e = 0; e < PER; ++e) {
-                    if (above < remaining && remaining <= above + cnt[e]) {
-                        s_digit = bins - 1 - (threadIdx.x * PER + e);
-                        s_above = above;
-                    }
-                    above += cnt[e];
+            if (threadIdx.x == kThreads - 1)
+                for (int r = 0; r < kCluster; ++r) *cluster.map_shared_rank(&s_slice[rank], r) = incl;
+            cluster.sync();
+            int above = 0;                             // keys with digits of lower ranks
+            for (int r = 0; r < rank; ++r) above += s_slice[r];
+            const int before = above + incl - cnt;
+            if (!(threadIdx.x & 1) && (int)threadIdx.x < 2 * part && before < remaining && remaining <= before + cnt)
+                for (int r = 0; r < kCluster; ++r) {
+                    *cluster.map_shared_rank(&s_digit, r) = dgt;
+                    *cluster.map_shared_rank(&s_above, r) = before;
                 }
-            }
-            cluster.sync();                            // the histograms have been read; s_digit is visible
+            cluster.sync();                            // the digit has arrived, the histograms have been read
             prefix = (prefix << width) | (uint32_t)s_digit;
             remaining -= s_above;
         }
@@ -157,7 +164,7 @@ select_kernel(Pool S, EvictParams E)
     const int wlo = min(hi, lo + warp * run), whi = min(hi, wlo + run);
     int2 mine = make_int2(0, 0);                       // kept for sure, tied
     if (!none) {
-        for_scores(sc, wlo, whi, lane, 32, [&](int, float x, bool on) {
+        for_scores(src, wlo, whi, lane, 32, [&](int, float x, bool on) {
             const uint32_t key = score_key(x);
             mine.x += __popc(__ballot_sync(0xffffffffu, on && (all || key > prefix)));
             mine.y += __popc(__ballot_sync(0xffffffffu, on && !all && key == prefix));
@@ -179,7 +186,7 @@ select_kernel(Pool S, EvictParams E)
     for (int w = 0; w < warp; ++w) before.x += s_count[w].x, before.y += s_count[w].y;
     if (mine.x + mine.y > 0) {
         // a tied slot is kept while fewer than `remaining` ties precede it
-        for_scores(sc, wlo, whi, lane, 32, [&](int i, float x, bool on) {
+        for_scores(src, wlo, whi, lane, 32, [&](int i, float x, bool on) {
             const uint32_t key = score_key(x), below = (1u << lane) - 1;
             const bool gt = on && (all || key > prefix), eq = on && !all && key == prefix;
             const unsigned m_gt = __ballot_sync(0xffffffffu, gt), m_eq = __ballot_sync(0xffffffffu, eq);
@@ -262,7 +269,11 @@ cudaError_t evict(const Pool &S, const Pool &Dp, int row_bytes, const float *sco
     E.top = top;
     E.recent = recent;
     const int units = S.B * S.Hkv;
-    cudaError_t e = launch_pdl(select_kernel, dim3(units * kCluster), dim3(kThreads), 0, st, S, E);
+    const long cap = (long)S.max_blocks << S.page_log2, runs = cdiv(cap, kCluster * kWarps * 32) * 32l * kWarps;
+    E.cache = (int)std::min<long>(kCache, runs);
+    cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCache * 4);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(select_kernel, dim3(units * kCluster), dim3(kThreads), E.cache * 4, st, S, E);
     if (e != cudaSuccess) return e;
     // about 12 CTAs per SM, none without a row to move
     const long most = std::min<long>((long)S.max_blocks << S.page_log2, top + recent);
