@@ -867,7 +867,7 @@ vc_status vc_paged_attn_h2o(const void *q, const vc_paged_cache *cache, const in
  * shortened sequences; src's can then be freed, and pages shared with other
  * sequences stay intact).  dst_len[b] = n_b (device int32 [B], not src_len);
  * kept_idx[u * kept_stride + j] = the slot that went to slot j of unit u;
- * scores_out, unless NULL: its score at [u * scores_out_stride + j], the
+ * scores_out, unless NULL: its score (a zero without sign) at [u * scores_out_stride + j], the
  * accumulated scores of the shortened cache.  Entries and rows from n_b on are left
  * as they are.
  * scores as in vc_paged_attn_h2o.  src and dst agree in B, Hkv, d and dt; dst's

@@ -11,7 +11,7 @@
 // the others.
 // Every warp owns a run of consecutive slots; its counts above and at the
 // threshold, prefixed over warps and CTAs, give the place of its first kept
-// slot, and ballots order the rest.  The scores are read from memory once, eight
+// slot, and ballots order the rest.  The scores are read from memory once, 16
 // loads in flight per thread, and kept in shared memory for the further passes
 // (read again where a CTA has more than 16384).  A second kernel moves the
 // rows: one read and one write of every kept row, which is what bounds the
@@ -31,12 +31,16 @@ constexpr int kThreads = 512;
 constexpr int kBins = 2048;
 constexpr int kCache = 16384;                          // scores a CTA keeps: 64 KB, two CTAs per SM
 
-// larger score -> larger key; -0 and +0 are one score, NaN is below every number
-__device__ __forceinline__ uint32_t score_key(float s)
+// One pattern per score: -0 as +0, every NaN as the all-ones one.
+__device__ __forceinline__ uint32_t score_bits(float s)
 {
-    if (s != s) return 0u;
     const uint32_t u = s == 0.f ? 0u : __float_as_uint(s);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    return s != s ? 0xffffffffu : u;
+}
+// larger score -> larger key; NaN, the lowest, is 0
+__device__ __forceinline__ uint32_t score_key(uint32_t bits)
+{
+    return bits ^ ((uint32_t)((int32_t)bits >> 31) | 0x80000000u);
 }
 
 struct EvictParams {
@@ -58,22 +62,27 @@ __device__ __forceinline__ int src_tokens(const Pool &S, const int32_t *src_len,
 }
 
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 8;                              // scores a thread has in flight
-
-// f(index, score, in range) for the slots of [lo, hi) that fall to the caller,
-// one of `stride`; all lanes of a warp run alike.
-template <typename F>
-__device__ __forceinline__ void for_scores(const float *sc, int lo, int hi, int at, int stride, F f)
+// f(slot, bits, in range) for the slots of [lo, hi) that fall to the caller,
+// `at` and every `stride`th from there on; all lanes of a warp run alike.  16
+// loads are in flight per thread.
+template <typename L, typename F>
+__device__ __forceinline__ void for_scores(int lo, int hi, int at, int stride, L load, F f)
 {
-    for (int i0 = lo; i0 < hi; i0 += stride * kBatch) {
-        float x[kBatch];
+    constexpr int N = 16;
+    int i = lo + at;
+    for (; i - at + stride * N <= hi; i += stride * N) {
+        uint32_t x[N];
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) {
-            const int i = i0 + e * stride + at;
-            x[e] = i < hi ? sc[i] : 0.f;
-        }
+        for (int e = 0; e < N; ++e) x[e] = load(i + e * stride);
 #pragma unroll
-        for (int e = 0; e < kBatch; ++e) f(i0 + e * stride + at, x[e], i0 + e * stride + at < hi);
+        for (int e = 0; e < N; ++e) f(i + e * stride, x[e], true);
+    }
+    for (; i - at < hi; i += stride * 4) {
+        uint32_t x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = i + e * stride < hi ? load(i + e * stride) : 0u;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f(i + e * stride, x[e], i + e * stride < hi);
     }
 }
 
@@ -84,7 +93,7 @@ select_kernel(Pool S, EvictParams E)
     __shared__ int warp_sums[kWarps];
     __shared__ int s_slice[kCluster];                  // the CTAs' totals of their digits, of this pass
     __shared__ int s_digit, s_above;
-    extern __shared__ float cache[];
+    extern __shared__ uint32_t cache[];
     __shared__ int2 s_count[kWarps + 1];               // slots above / at the threshold: by warp, of the CTA
     cg::cluster_group cluster = cg::this_cluster();
     pdl_wait();
@@ -105,9 +114,11 @@ select_kernel(Pool S, EvictParams E)
 
     uint32_t prefix = 0;
     int remaining = top;                               // still to be taken among keys that match the prefix
-    const float *src = sc;
+    auto from_memory = [&](int i) { return score_bits(sc[i]); };
+    auto from_cache = [&](int i) { return cache[i - lo]; };
+    bool cached = false;
     if (top > 0 && top < cand) {
-        const bool keep_scores = hi - lo <= E.cache;
+        const bool fits = hi - lo <= E.cache;
         int shift = 32;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
@@ -115,13 +126,18 @@ select_kernel(Pool S, EvictParams E)
             shift -= width;
             for (int i = threadIdx.x; i < bins; i += kThreads) hist[i] = 0;
             __syncthreads();
-            for_scores(src, lo, hi, threadIdx.x, kThreads, [&](int i, float x, bool on) {
-                const uint32_t key = score_key(x);
-                if (on && pass == 0 && keep_scores) cache[i - lo] = x;
-                if (on && (pass == 0 || (key >> (shift + width)) == prefix))
-                    atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
-            });
-            if (keep_scores) src = cache - lo;
+            auto add = [&](int, uint32_t bits, bool on) {
+                const uint32_t key = score_key(bits);
+                if (on && (key >> (shift + width)) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1);
+            };
+            if (pass == 0)
+                for_scores(lo, hi, threadIdx.x, kThreads, from_memory, [&](int i, uint32_t bits, bool on) {
+                    if (on && fits) cache[i - lo] = bits;
+                    if (on) atomicAdd(&hist[score_key(bits) >> 21], 1);
+                });
+            else if (cached) for_scores(lo, hi, threadIdx.x, kThreads, from_cache, add);
+            else for_scores(lo, hi, threadIdx.x, kThreads, from_memory, add);
+            cached = fits;
             cluster.sync();
             // This CTA's digits, from the highest down: rank 0 has the highest
             // part of them.  Two threads per digit, four histograms each.
@@ -163,13 +179,13 @@ select_kernel(Pool S, EvictParams E)
     const bool none = top == 0, all = top == cand;
     const int wlo = min(hi, lo + warp * run), whi = min(hi, wlo + run);
     int2 mine = make_int2(0, 0);                       // kept for sure, tied
-    if (!none) {
-        for_scores(src, wlo, whi, lane, 32, [&](int, float x, bool on) {
-            const uint32_t key = score_key(x);
-            mine.x += __popc(__ballot_sync(0xffffffffu, on && (all || key > prefix)));
-            mine.y += __popc(__ballot_sync(0xffffffffu, on && !all && key == prefix));
-        });
-    }
+    auto tally = [&](int, uint32_t bits, bool on) {
+        const uint32_t key = score_key(bits);
+        mine.x += __popc(__ballot_sync(0xffffffffu, on && (all || key > prefix)));
+        mine.y += __popc(__ballot_sync(0xffffffffu, on && !all && key == prefix));
+    };
+    if (cached) for_scores(wlo, whi, lane, 32, from_cache, tally);
+    else if (!none) for_scores(wlo, whi, lane, 32, from_memory, tally);
     if (lane == 0) s_count[warp] = mine;
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -186,19 +202,21 @@ select_kernel(Pool S, EvictParams E)
     for (int w = 0; w < warp; ++w) before.x += s_count[w].x, before.y += s_count[w].y;
     if (mine.x + mine.y > 0) {
         // a tied slot is kept while fewer than `remaining` ties precede it
-        for_scores(src, wlo, whi, lane, 32, [&](int i, float x, bool on) {
-            const uint32_t key = score_key(x), below = (1u << lane) - 1;
+        auto write = [&](int i, uint32_t bits, bool on) {
+            const uint32_t key = score_key(bits), below = (1u << lane) - 1;
             const bool gt = on && (all || key > prefix), eq = on && !all && key == prefix;
             const unsigned m_gt = __ballot_sync(0xffffffffu, gt), m_eq = __ballot_sync(0xffffffffu, eq);
             const int ties = before.y + __popc(m_eq & below);
             if (gt || (eq && ties < remaining)) {
                 const int j = before.x + __popc(m_gt & below) + min(ties, remaining);
                 kept[j] = i;
-                if (sc_out) sc_out[j] = x;
+                if (sc_out) sc_out[j] = __uint_as_float(bits);
             }
             before.x += __popc(m_gt);
             before.y += __popc(m_eq);
-        });
+        };
+        if (cached) for_scores(wlo, whi, lane, 32, from_cache, write);
+        else for_scores(wlo, whi, lane, 32, from_memory, write);
     }
     for (int i = rank * kThreads + threadIdx.x; i < recent; i += kCluster * kThreads) {
         kept[top + i] = cand + i;
