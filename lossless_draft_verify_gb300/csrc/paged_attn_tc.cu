@@ -25,6 +25,8 @@
 // V rows past the sequence's end may hold any bits and 0 * NaN is not 0: those
 // that share the last page with tokens are cleared in shared memory, further
 // pages are not read (their boxes lie outside the map and fill with zeros).
+#include <type_traits>
+
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
@@ -179,97 +181,106 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             }
     } else if (warp == 9) {
         // -------------------------------------------------------- issuer --
-        if (lane == 0) {
-            const Item &it = S->role[9].it;
-            constexpr uint32_t idS = tc::idesc_bf16(kRowsTile, BN, false, false);
-            constexpr uint32_t idO = tc::idesc_bf16(kRowsTile, D, false, true);
-            Ring<NST> ring;
-            uint32_t units = 0, steps[2] = {0, 0};           // q_ready, p_ready phases
-            bool ok = true;
-            auto tile = [&](const Ring<NST> &x) { return smem_u32(sm + G::SM_KV + x.slot * G::TILE); };
-            auto arrived = [&](const Ring<NST> &x) { return wait_bar(&S->full[x.slot], x.phase, A.status, 92); };
-            auto release = [&]() {                           // once the products issued so far are done
-                tc::commit(&S->empty[ring.slot]);
-                ring.next();
-            };
-            auto issue_S = [&](int t, int qt, const Ring<NST> &x) {
-                const uint32_t sQ = smem_u32(sm + G::SM_Q + qt * G::TILE), sK = tile(x);
+        // The warp runs as one and an elected thread issues: operands that are
+        // the same for the whole warp then stay in uniform registers.  All
+        // tensor memory is this CTA's, so its addresses are constants.
+        const Item &it = S->role[warp].it;
+        constexpr uint32_t idS = tc::idesc_bf16(kRowsTile, BN, false, false);
+        constexpr uint32_t idO = tc::idesc_bf16(kRowsTile, D, false, true);
+        constexpr uint32_t hi = tc::desc_hi(1024, tc::kSwizzle128B), HALF = BN * 128 >> 4;
+        const uint32_t kv_lo = tc::desc_lo(smem_u32(sm + G::SM_KV), BN * 128), q_lo = tc::desc_lo(smem_u32(sm), 16);
+        Ring<NST> ring;
+        uint32_t units = 0, ready[2] = {0, 0};               // q_ready, p_ready phases
+        bool ok = tmem == 0;
+        if (!ok) report_timeout(A.status, 89);               // never expected
+        auto arrived = [&](const Ring<NST> &x) { return wait_warp(&S->full[x.slot], x.phase, A.status, 92); };
+        auto release = [&]() {                               // once the products issued so far are done
+            if (tc::elect()) tc::commit(&S->empty[ring.slot]);
+            ring.next();
+        };
+        // S of stream T: row tile QT against a K tile
+        auto issue_S = [&](auto T, auto QT, int slot) {
+            const uint32_t a = q_lo + QT * (G::TILE >> 4), k = kv_lo + slot * (G::TILE >> 4);
+            if (tc::elect()) {
+                tc::mma_ss2<false>(T * BN, a, hi, k, hi, idS);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk >> 2) * (BN * 128) + (kk & 3) * 32;
-                    tc::mma_ss(tmem + t * BN, tc::smem_desc(sQ + o, 16, 1024, tc::kSwizzle128B),
-                               tc::smem_desc(sK + o, 16, 1024, tc::kSwizzle128B), idS, kk > 0);
-                }
-                tc::commit(&S->s_full[t]);
-            };
-            auto issue_PV = [&](int t, const Ring<NST> &x, bool first) {
-                const uint32_t sV = tile(x);
+                for (int kk = 1; kk < D / 16; ++kk)
+                    tc::mma_ss2<true>(T * BN, a + (kk >> 2) * HALF + (kk & 3) * 2, hi, k + (kk >> 2) * HALF + (kk & 3) * 2,
+                                      hi, idS);
+                tc::commit(&S->s_full[T]);
+            }
+        };
+        auto issue_PV = [&](auto T, int slot, bool first, bool last) {
+            constexpr uint32_t d = G::COL_O + T * D, p = T * BN;
+            const uint32_t v = kv_lo + slot * (G::TILE >> 4);
+            if (tc::elect()) {
+                tc::mma_ts2(d, p, v, hi, idO, first ? 0u : 1u);
 #pragma unroll
-                for (int kk = 0; kk < BN / 16; ++kk)
-                    tc::mma_ts(tmem + G::COL_O + t * D, tmem + t * BN + kk * 8,
-                               tc::smem_desc(sV + kk * 2048, BN * 128, 1024, tc::kSwizzle128B), idO,
-                               (!first || kk > 0) ? 1u : 0u);
-            };
-            auto p_wait = [&](int t) {
-                const bool r = wait_bar(&S->p_ready[t], steps[t] & 1, A.status, 93);
-                ++steps[t];
-                tc::fence_after();
-                return r;
-            };
-            while (ok && S->role[9].walk.next(A.P, A.W, S->role[9].it)) {
-                const int n = it.t_hi - it.t_lo;
-                ok = wait_bar(&S->q_ready, units & 1, A.status, 94);
-                ++units;
-                tc::fence_after();
-                if (it.rows > kRowsTile) {
-                    // the streams are two row tiles on the same keys
-                    ok = ok && arrived(ring);
+                for (int kk = 1; kk < BN / 16; ++kk) tc::mma_ts2(d, p + kk * 8, v + kk * (2048 >> 4), hi, idO, 1u);
+                if (last) tc::commit(&S->o_full[T]);
+            }
+        };
+        using C0 = std::integral_constant<int, 0>;
+        using C1 = std::integral_constant<int, 1>;
+        auto p_wait = [&](auto T) {
+            const bool r = wait_warp(&S->p_ready[T], ready[T] & 1, A.status, 93);
+            ++ready[T];
+            tc::fence_after();
+            return r;
+        };
+        while (ok && step(S, warp, A)) {
+            const int n = it.t_hi - it.t_lo;
+            ok = wait_warp(&S->q_ready, units & 1, A.status, 94);
+            ++units;
+            tc::fence_after();
+            ok = ok && arrived(ring);
+            if (!ok) break;
+            if (it.rows > kRowsTile) {
+                // the streams are two row tiles on the same keys
+                issue_S(C0{}, C0{}, ring.slot);
+                issue_S(C1{}, C1{}, ring.slot);
+                release();
+                for (int j = 0; j < n; ++j) {
+                    const bool more = j + 1 < n;
+                    const Ring<NST> k = ring.after();        // K_{j+1}, after V_j
+                    ok = arrived(ring) && (!more || arrived(k)) && p_wait(C0{});
                     if (!ok) break;
-                    issue_S(0, 0, ring);
-                    issue_S(1, 1, ring);
+                    issue_PV(C0{}, ring.slot, j == 0, !more);
+                    if (more) issue_S(C0{}, C0{}, k.slot);
+                    ok = p_wait(C1{});
+                    if (!ok) break;
+                    issue_PV(C1{}, ring.slot, j == 0, !more);
                     release();
-                    for (int j = 0; j < n; ++j) {
-                        const bool more = j + 1 < n;
-                        const Ring<NST> k = ring.after();    // K_{j+1}, after V_j
-                        ok = arrived(ring) && (!more || arrived(k)) && p_wait(0);
-                        if (!ok) break;
-                        issue_PV(0, ring, j == 0);
-                        if (more) issue_S(0, 0, k);
-                        else tc::commit(&S->o_full[0]);
-                        ok = p_wait(1);
-                        if (!ok) break;
-                        issue_PV(1, ring, j == 0);
+                    if (more) {
+                        issue_S(C1{}, C1{}, ring.slot);
                         release();
-                        if (more) {
-                            issue_S(1, 1, ring);
-                            release();
-                        } else {
-                            tc::commit(&S->o_full[1]);
-                        }
                     }
-                } else {
-                    // the streams take the key tiles of one row tile in turn
-                    for (int t = 0; t < 2 && t < n && ok; ++t) {
+                }
+            } else {
+                // the streams take the key tiles of one row tile in turn
+                issue_S(C0{}, C0{}, ring.slot);
+                release();
+                if (n > 1) {
+                    ok = arrived(ring);
+                    if (!ok) break;
+                    issue_S(C1{}, C0{}, ring.slot);
+                    release();
+                }
+                auto one = [&](auto T, int j) {
+                    ok = arrived(ring) && p_wait(T);
+                    if (!ok) return;
+                    issue_PV(T, ring.slot, j < 2, j + 2 >= n);
+                    release();
+                    if (j + 2 < n) {
                         ok = arrived(ring);
-                        if (!ok) break;
-                        issue_S(t, 0, ring);
+                        if (!ok) return;
+                        issue_S(T, C0{}, ring.slot);
                         release();
                     }
-                    for (int j = 0; j < n && ok; ++j) {
-                        const int t = j & 1;
-                        ok = arrived(ring) && p_wait(t);
-                        if (!ok) break;
-                        issue_PV(t, ring, j < 2);
-                        release();
-                        if (j + 2 < n) {
-                            ok = arrived(ring);
-                            if (!ok) break;
-                            issue_S(t, 0, ring);
-                            release();
-                        } else {
-                            tc::commit(&S->o_full[t]);
-                        }
-                    }
+                };
+                for (int j = 0; j < n && ok; j += 2) {
+                    one(C0{}, j);
+                    if (ok && j + 1 < n) one(C1{}, j + 1);
                 }
             }
         }

@@ -357,6 +357,7 @@ def test_evict_reports_what_does_not_fit():
     n = torch.zeros(3, dtype=torch.int32, device="cuda")
     kept = torch.zeros(3, 2, 20, dtype=torch.int32, device="cuda")
     scores = torch.rand(3, 2, src.slots, device="cuda")
+    scores[0, :, 32:36] = 2.0                               # kept, on the page whose number is bad
     bt.block_table[0, 2] = -9
     vc.vc_paged_evict(scores, src, torch.tensor([100, 60, src.slots + 1], dtype=torch.int32, device="cuda"), 15, 5,
                       dst, n, kept)
