@@ -36,7 +36,8 @@ namespace {
 
 constexpr int BN = 128;
 constexpr int kRowsTile = 128;
-constexpr int kThreads = 320;
+constexpr int kThreads = 352;
+constexpr int kProducer = 8, kIssuer = 9, kProducer2 = 10;     // warps
 constexpr int kSoftmax = 256;
 constexpr float kLazy = 8.f;
 
@@ -61,7 +62,7 @@ struct Shared {
         Walk<256, BN> walk;
         Item it;
         bool more;
-    } role[10];        // each warp's walk through the piece: in registers it would make the softmax threads spill
+    } role[11];        // each warp's walk through the piece: in registers it would make the softmax threads spill
 };
 
 struct Params {
@@ -117,11 +118,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == kIssuer) {
         tc::tmem_alloc(&S->tmem, 512);
         tc::tmem_relinquish();
     }
-    if (warp == 8) find_piece<256, BN>(A.P, A.W, blockIdx.x, gridDim.x, &S->piece);
+    if (warp == kProducer) find_piece<256, BN>(A.P, A.W, blockIdx.x, gridDim.x, &S->piece);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -129,15 +130,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const uint32_t tmem = S->tmem;
     if (lane == 0) S->role[warp].walk.start(A.P, A.W, S->piece);
 
-    if (warp == 8) {
+    if (warp == kProducer || warp == kProducer2) {
         // ------------------------------------------------------- producer --
         const Item &it = S->role[warp].it;
         if (lane == 0) {
             tc::prefetch_tmap(&tmK);
             tc::prefetch_tmap(&tmV);
         }
-        const int boxes = BN / A.box_rows * G::HALVES;       // per tile, at most 16
-        const int bp = lane / G::HALVES, half = lane % G::HALVES;
+        // the two warps share a tile's boxes (at most 16), one to a lane
+        const int boxes = BN / A.box_rows * G::HALVES, mine = (boxes + 1) / 2;
+        const int box = (warp == kProducer2 ? mine : 0) + lane, bp = box / G::HALVES, half = box % G::HALVES;
+        const bool on = lane < mine && box < boxes;
         Ring<NST> ring;
         bool ok = true, filled = false;                      // filled: the ring has been round once
         auto load = [&](const CUtensorMap *map, int row) {
@@ -148,9 +151,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 if (!ok) return;
             }
             uint8_t *dst = sm + G::SM_KV + s * G::TILE;
-            if (lane == 0) mbar_arrive_expect_tx(&S->full[s], G::TILE);
+            // (the other warp's boxes may land first: the phase ends with this arrival and all bytes)
+            if (lane == 0 && warp == kProducer) mbar_arrive_expect_tx(&S->full[s], G::TILE);
             __syncwarp();
-            if (lane < boxes)
+            if (on)
                 tc::tma_load_3d(dst + half * (BN * 128) + bp * A.box_rows * 128, map, half * 64, row, 0, &S->full[s]);
             ring.next();
             filled = filled || ring.slot == 0;
@@ -158,28 +162,38 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         while (ok && step(S, warp, A)) {
             const int n = it.t_hi - it.t_lo, len = it.ctx + it.n;
             const int ahead = it.rows > kRowsTile ? 1 : 2;
-            // row of the lane's box of key tile i; past the sequence's end or
-            // through a bad page number: outside the map
-            auto locate = [&](int i) {
+            // the lane's box of key tile i: its table entry is read some tiles
+            // before it is looked at
+            auto entry = [&](int i) {
                 const int slot = (it.t_lo + i) * BN + bp * A.box_rows;
-                if (lane >= boxes || i >= n || slot >= len) return A.n_rows;
-                const int pg = A.P.page_of(it.b, slot >> A.P.page_log2);
-                return pg < 0 ? A.n_rows : (int)A.P.row(pg, it.h, slot & (A.P.page() - 1));
+                return on && i < n && slot < len
+                           ? A.P.table[(size_t)it.b * A.P.max_blocks + (slot >> A.P.page_log2)] : 0;
             };
-            int r0 = locate(0), r1 = locate(1), r2 = locate(2);
-            for (int i = 0; i < ahead && i < n && ok; ++i) load(&tmK, i == 0 ? r0 : r1);
+            // past the sequence's end or through a bad page number: a row
+            // outside the map, which fills with zeros
+            auto row = [&](int i, int page) {
+                const int slot = (it.t_lo + i) * BN + bp * A.box_rows;
+                if (!on || slot >= len) return A.n_rows;
+                if ((unsigned)page < (unsigned)A.P.n_pages)
+                    return (int)A.P.row(page, it.h, slot & (A.P.page() - 1));
+                set_flag(A.P.status, VC_PAGED_BAD_PAGE);
+                return A.n_rows;
+            };
+            int e0 = entry(0), e1 = entry(1), e2 = entry(2);
+            load(&tmK, row(0, e0));
+            if (ok && ahead == 2 && n > 1) load(&tmK, row(1, e1));
             for (int i = 0; i < n && ok; ++i) {
-                const int r3 = locate(i + 3);
-                load(&tmV, r0);
-                if (ok && i + ahead < n) load(&tmK, ahead == 1 ? r1 : r2);
-                r0 = r1, r1 = r2, r2 = r3;
+                const int e3 = entry(i + 3);
+                load(&tmV, row(i, e0));
+                if (ok && i + ahead < n) load(&tmK, row(i + ahead, ahead == 1 ? e1 : e2));
+                e0 = e1, e1 = e2, e2 = e3;
             }
         }
         if (!ok && lane == 0)                                // copies in flight end before the CTA does
             for (int i = 0; i < NST; ++i) {
                 if (filled || i < ring.slot) mbar_wait(&S->full[i], i < ring.slot ? ring.phase : ring.phase ^ 1);
             }
-    } else if (warp == 9) {
+    } else if (warp == kIssuer) {
         // -------------------------------------------------------- issuer --
         // The warp runs as one and an elected thread issues: operands that are
         // the same for the whole warp then stay in uniform registers.  All
@@ -337,7 +351,36 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const int kall = it.ctx + (row0 + (big ? t * 128 : 0)) / A.W.G;
             float m = kNegBig, l = 0.f;
             const int mine = big ? n : (n + 1 - t) / 2;      // this stream's steps
-            for (int j = 0; j < mine; ++j) {
+            // V rows of the last page past the sequence's end, before the product
+            // with key tile i (big: stream 0's comes first)
+            auto zero_tail = [&](int i) {
+                const int key0 = (it.t_lo + i) * BN;
+                if (i != n - 1 || key0 + BN <= len || (big && t == 1)) return;
+                const uint32_t vi = item + 2u * n - 1;       // the part's last ring item
+                ok = wait_warp(&S->full[vi % NST], (vi / NST) & 1, A.status, 96);
+                uint8_t *sV = sm + G::SM_KV + (vi % NST) * G::TILE;
+                const int page = A.P.page();
+                const int z0 = len - key0, z1 = ok ? min(BN, (len + page - 1) / page * page - key0) : 0;
+                for (int x = r; x < (z1 - z0) * (D / 8); x += 128) {
+                    const int row = z0 + x / (D / 8), c = x % (D / 8);
+                    *reinterpret_cast<uint4 *>(sV + (c >> 3) * (BN * 128) + row * 128 + (c & 7) * 16) =
+                        make_uint4(0, 0, 0, 0);
+                }
+                fence_async_smem();
+                __syncwarp();
+            };
+            // a warp without a row of the unit (most, where a token decodes)
+            // keeps the barriers' count; the P it leaves makes rows of O that
+            // nobody reads
+            const bool live = __any_sync(0xffffffffu, valid);
+            for (int j = 0; j < mine && !live; ++j) {
+                ok = wait_warp(&S->s_full[t], steps & 1, A.status, 95);
+                ++steps;
+                if (!ok) break;
+                zero_tail(big ? j : 2 * j + t);
+                mbar_arrive(&S->p_ready[t]);
+            }
+            for (int j = 0; j < mine && live; ++j) {
                 const int i = big ? j : 2 * j + t;           // key tile of the part
                 const int key0 = (it.t_lo + i) * BN;
                 ok = wait_warp(&S->s_full[t], steps & 1, A.status, 95);
@@ -409,22 +452,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 tc::st32(tS + 32, reinterpret_cast<uint32_t (&)[32]>(pk[32]));
                 const float2 s2 = add2(sum[0], sum[1]);
                 l += s2.x + s2.y;
-                if (i == n - 1 && key0 + BN > len && (!big || t == 0)) {
-                    // V rows of the last page past the sequence's end
-                    const uint32_t vi = item + 2u * n - 1;   // the part's last ring item
-                    ok = wait_warp(&S->full[vi % NST], (vi / NST) & 1, A.status, 96);
-                    if (!ok) break;
-                    uint8_t *sV = sm + G::SM_KV + (vi % NST) * G::TILE;
-                    const int page = A.P.page();
-                    const int z0 = len - key0, z1 = min(BN, (len + page - 1) / page * page - key0);
-                    for (int x = r; x < (z1 - z0) * (D / 8); x += 128) {
-                        const int row = z0 + x / (D / 8), c = x % (D / 8);
-                        *reinterpret_cast<uint4 *>(sV + (c >> 3) * (BN * 128) + row * 128 + (c & 7) * 16) =
-                            make_uint4(0, 0, 0, 0);
-                    }
-                    fence_async_smem();
-                    __syncwarp();
-                }
+                zero_tail(i);
+                if (!ok) break;
                 tc::st_wait();
                 tc::fence_before();
                 mbar_arrive(&S->p_ready[t]);
@@ -437,7 +466,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 const float inv = it.whole ? 1.f / L : 1.f;
                 const size_t row = valid ? out_row(R) : 0;
 #pragma unroll 1
-                for (int c = c0; c < c1; c += 32) {
+                for (int c = c0; c < c1 && live; c += 32) {
                     uint32_t o[32], o1[32];
                     __syncwarp();
                     tc::ld32(tmem + lanes + G::COL_O + (big ? t * D : 0) + c, o);
@@ -509,7 +538,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 9) {
+    if (warp == kIssuer) {
         __syncwarp();
         tc::tmem_dealloc(tmem, 512);
     }
