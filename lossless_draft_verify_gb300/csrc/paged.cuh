@@ -60,27 +60,39 @@ struct Seq {
     int tok0, n, ctx;
 };
 
-__host__ __device__ __forceinline__ Seq load_seq(const Pool &P, const int32_t *__restrict__ q_start,
-                                        const int32_t *__restrict__ ctx_len, int T, int b)
+struct RawSeq {
+    int start, end, ctx;
+};
+
+__host__ __device__ __forceinline__ RawSeq raw_seq(const int32_t *__restrict__ q_start,
+                                                   const int32_t *__restrict__ ctx_len, int b)
 {
-    Seq s;
-    s.tok0 = q_start[b];
-    const int end = q_start[b + 1];
-    s.ctx = ctx_len[b];
-    s.n = end - s.tok0;
-    const bool ok = s.tok0 >= 0 && end >= s.tok0 && end <= T && s.ctx >= 0 && (long)s.ctx + s.n <= P.capacity();
+    return RawSeq{q_start[b], q_start[b + 1], ctx_len[b]};
+}
+
+__host__ __device__ __forceinline__ Seq check_seq(const Pool &P, const RawSeq &r, int T)
+{
+    const bool ok = r.start >= 0 && r.end >= r.start && r.end <= T && r.ctx >= 0 &&
+                    (long)r.ctx + (r.end - r.start) <= P.capacity();
     if (!ok) {
         set_flag(P.status, VC_PAGED_BAD_LENGTH);
-        s.tok0 = s.n = s.ctx = 0;
+        return Seq{0, 0, 0};
     }
-    return s;
+    return Seq{r.start, r.end - r.start, r.ctx};
+}
+
+__host__ __device__ __forceinline__ Seq load_seq(const Pool &P, const int32_t *__restrict__ q_start,
+                                                 const int32_t *__restrict__ ctx_len, int T, int b)
+{
+    return check_seq(P, raw_seq(q_start, ctx_len, b), T);
 }
 
 // ----- division of the attention work ----------------------------------------
 // A unit is (sequence b, kv head h, row tile mt): BM consecutive rows of the
 // n * G (query, head of the group) rows that share a kv head, row = i * G + g.
 // It takes the key tiles (BN keys) its last query can see.  The units of a
-// batch, laid end to end with kUnitCost extra tiles each (loading Q, writing
+// batch, laid end to end by cost (a tile's, twice as much where more than half
+// of a 256-row tile's rows are there, and kUnitCost for loading Q and writing
 // the output), are cut into equal pieces, one per CTA: a piece may begin and
 // end inside a unit, whose partial results are then merged.  One long sequence
 // and many short ones thus fill the GPU alike, and the division depends on the
@@ -88,10 +100,20 @@ __host__ __device__ __forceinline__ Seq load_seq(const Pool &P, const int32_t *_
 struct WorkDim {
     const int32_t *q_start, *ctx_len;
     int T, G;
-    int min_tiles;     // a piece is at least this long
+    int min_piece;     // a piece costs at least this much
 };
 
-constexpr int kUnitCost = 2;
+// Measured on a batch of nine sequences (chunks of 1 to 700 over up to 20000
+// tokens, 28/4 heads, pages of 16): 806 us at 2, 745 at 4, 606 at 9,
+// 505 at 16, 502 at 20; a decode step of 16 x 32768 tokens 313 us at 2, 323 at
+// 16, 331 at 28.
+constexpr int kUnitCost = 16;
+// A piece costs at least this much (eight more tiles per CTA cost a lone short
+// sequence more than the merge of its parts).
+constexpr int kMinPiece = 10;
+// A unit of at most this cost is never cut: merging its parts would take longer
+// than it does.  It belongs to the CTA in whose piece its middle lies.
+constexpr int kWhole = 4 + kUnitCost;
 
 // What one CTA has to do: from unit (b, h, mt), cost offset `off` within it,
 // `len` cost units on.  Written to shared memory by one warp, read by all.
@@ -113,6 +135,14 @@ struct Units {
         const long last = lmin((long)s.n * G, (long)(mt + 1) * BM) - 1;    // last row of the tile
         return (s.ctx + (int)(last / G) + 1 + BN - 1) / BN;
     }
+    static __host__ __device__ __forceinline__ int weight(const Seq &s, int G, int mt)
+    {
+        return BM == 256 && (long)s.n * G - (long)mt * BM > BM / 2 ? 2 : 1;
+    }
+    static __host__ __device__ __forceinline__ int cost(const Seq &s, int G, int mt)
+    {
+        return tiles(s, G, mt) * weight(s, G, mt) + kUnitCost;
+    }
     static __host__ __device__ __forceinline__ int mtiles(const Seq &s, int G)
     {
         return (int)(((long)s.n * G + BM - 1) / BM);
@@ -121,7 +151,7 @@ struct Units {
     {
         long c = 0;
         const int m = mtiles(s, G);
-        for (int i = 0; i < m; ++i) c += tiles(s, G, i) + kUnitCost;
+        for (int i = 0; i < m; ++i) c += cost(s, G, i);
         return c;
     }
     // head, row tile and offset of cost unit x of a sequence (hc: head_cost)
@@ -131,7 +161,7 @@ struct Units {
         x -= out.h * hc;
         int mt = 0;
         for (;;) {
-            const int t = tiles(s, G, mt) + kUnitCost;
+            const int t = cost(s, G, mt);
             if (x < t) break;
             x -= t;
             ++mt;
@@ -141,49 +171,61 @@ struct Units {
     }
 };
 
+// By one warp, 32 sequences at a time, the next ones' lengths being read under
+// the arithmetic.  A first round (lo < 0) adds up the costs and keeps those of
+// the first 32 chunks of 32 sequences, one per lane, so that the second one,
+// which finds the sequence that holds the piece's beginning, can go straight to
+// its chunk.  One loop serves both: code that runs once is paid for in
+// instruction fetches.
 template <int BM, int BN>
 __device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int cta, int n_cta, Piece *out)
 {
     using U = Units<BM, BN>;
-    const int lane = threadIdx.x & 31;
-    long total = 0;
-    for (int b0 = 0; b0 < P.B; b0 += 32) {
-        long c = 0;
-        if (b0 + lane < P.B) c = U::head_cost(load_seq(P, W.q_start, W.ctx_len, W.T, b0 + lane), W.G) * P.Hkv;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-        total += c;
-    }
-    const long per = piece_len(total, n_cta, W.min_tiles);
-    const long lo = per * cta, hi = lmin(total, lo + per);
-    if (lo >= hi) {
-        if (lane == 0) out->len = 0;
-        return;
-    }
-    long before = 0;
-    for (int b0 = 0; b0 < P.B; b0 += 32) {
-        long hc = 0;
-        Seq s = {0, 0, 0};
-        if (b0 + lane < P.B) {
-            s = load_seq(P, W.q_start, W.ctx_len, W.T, b0 + lane);
-            hc = U::head_cost(s, W.G);
-        }
-        const long c = hc * P.Hkv;
-        long incl = c;
+    const int lane = threadIdx.x & 31, chunks = (P.B + 31) / 32;
+    auto fetch = [&](int c) {
+        const int b = 32 * c + lane;
+        return b < P.B ? raw_seq(W.q_start, W.ctx_len, b) : RawSeq{0, 0, 0};
+    };
+    if (lane == 0) out->len = 0;
+    long lo = -1, hi = 0, per = 0, before = 0, chunk = 0;
+    int c = 0;
+    RawSeq next = fetch(0);
+#pragma unroll 1
+    for (;;) {
+        const Seq s = check_seq(P, next, W.T);
+        if (c + 1 < chunks) next = fetch(c + 1);
+        const long hc = U::head_cost(s, W.G), x = hc * P.Hkv;
+        long incl = x;                               // inclusive over the lanes
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        const long start = before + incl - c;
-        if (c > 0 && start <= lo && lo < start + c) {
-            U::place(s, W.G, hc, lo - start, *out);
-            out->b = b0 + lane;
-            out->len = hi - lo;
-            out->per = per;
+        const long sum = __shfl_sync(0xffffffffu, incl, 31), start = before + incl - x;
+        if (lo >= 0) {
+            const bool here = start <= lo && lo < start + x;
+            if (here) {
+                U::place(s, W.G, hc, lo - start, *out);
+                out->b = 32 * c + lane;
+                out->per = per;
+                out->len = hi - lo;
+            }
+            if (__any_sync(0xffffffffu, here)) break;
+        } else if (c == lane) {
+            chunk = before + sum;                    // the running total
         }
-        before += __shfl_sync(0xffffffffu, incl, 31);
+        before += sum;
+        if (++c < chunks) continue;
+        if (lo >= 0) break;                          // not reached: lo lies below the total
+        per = piece_len(before, n_cta, W.min_piece);
+        lo = per * cta;
+        hi = lmin(before, lo + per);
+        if (lo >= hi) break;
+        c = __popc(__ballot_sync(0xffffffffu, lane < chunks && chunk <= lo));   // chunks that end at or before lo
+        before = c ? __shfl_sync(0xffffffffu, chunk, c - 1) : 0;
+        next = fetch(c);
     }
+    __syncwarp();
 }
 
 // One unit, or the part of it that falls to this CTA.
@@ -223,9 +265,10 @@ struct Walk {
     __host__ __device__ __forceinline__ bool next(const Pool &P, const WorkDim &W, Item &it)
     {
         while (left > 0) {
-            const int nt = U::tiles(s, W.G, mt), cost = nt + kUnitCost;
+            const int cost = U::cost(s, W.G, mt), weight = U::weight(s, W.G, mt);
             const long take = lmin(left, (long)cost - off);
-            const long a = off, e = off + take;
+            const bool uncut = cost <= kWhole, mine = !uncut || (off <= cost / 2 && cost / 2 < off + take);
+            const long a = uncut ? 0 : off, e = uncut ? cost : off + take;
             it.b = b;
             it.h = h;
             it.mt = mt;
@@ -234,10 +277,9 @@ struct Walk {
             it.ctx = s.ctx;
             it.rows = (int)lmin((long)BM, (long)s.n * W.G - (long)mt * BM);
             // the unit's first kUnitCost cost units carry no tile
-            it.t_lo = (int)lmax(a - kUnitCost, 0);
-            it.t_hi = (int)lmax(e - kUnitCost, 0);
-            // the first part with tiles is the CTA holding cost unit kUnitCost
-            const bool starts = a <= kUnitCost, ends = e == cost;
+            it.t_lo = (int)(lmax(a - kUnitCost, 0) / weight);
+            it.t_hi = (int)(lmax(e - kUnitCost, 0) / weight);
+            const bool starts = it.t_lo == 0, ends = e == cost;
             it.head = starts;
             it.whole = starts && ends;
             it.parts = 0;
@@ -256,7 +298,7 @@ struct Walk {
                     if (m == 0) left = 0;
                 }
             }
-            if (it.t_hi > it.t_lo) return true;
+            if (mine && it.t_hi > it.t_lo) return true;
         }
         return false;
     }
@@ -325,6 +367,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_
 
 // ----- launchers ----------------------------------------------------------------------
 // paged_attn_simt.cu: fp32 on the CUDA cores
+constexpr int kSimtKeys = 32;      // the smallest key tile of its variants
 int simt_rows(int T, int G);
 int simt_ctas();
 cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
@@ -333,7 +376,7 @@ cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int
                       float *scores, int scores_stride, cudaStream_t st);
 
 // paged_attn_tc.cu: bf16 on the tensor cores, row tiles of 256
-constexpr int kTcRows = 256;
+constexpr int kTcRows = 256, kTcKeys = 128;
 int tc_ctas();
 cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                     const Parts &parts, int32_t *status, cudaStream_t st);

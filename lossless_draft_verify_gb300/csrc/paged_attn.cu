@@ -97,7 +97,11 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     cudaError_t e;
     if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
     else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, parts, (int32_t *)ws, st);
-    if (e == cudaSuccess) e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
+    // no unit is cut where the block table cannot hold a sequence long enough
+    constexpr int tile = std::is_same_v<T, float> ? kSimtKeys : kTcKeys, weight = std::is_same_v<T, float> ? 1 : 2;
+    const long cap = (long)P.max_blocks << P.page_log2;
+    if (e == cudaSuccess && (cap + tile - 1) / tile * weight + kUnitCost > kWhole)
+        e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
     if (e != cudaSuccess || !scores) return e;
     if constexpr (std::is_same_v<T, float>) return mass_simt(P, W, d, q, Hq, sl2, lse, scores, scores_stride, st);
     else return mass_tc(P, W, d, q, Hq, sl2, lse, scores, scores_stride, (int32_t *)ws, st);
@@ -118,7 +122,7 @@ cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t
     W.ctx_len = ctx_len;
     W.T = T;
     W.G = Hq / P.Hkv;
-    W.min_tiles = 4 + kUnitCost;
+    W.min_piece = kMinPiece;
     const float sl2 = sm_scale * kLog2e;
     return dt == VC_BF16 ? run<__nv_bfloat16>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st)
                          : run<float>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st);

@@ -153,7 +153,8 @@ using namespace vc::paged;
 #define NEED(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); std::exit(1); } } while (0)
 
 // every key tile of every unit falls to one CTA; a shared unit's parts sit in
-// consecutive CTAs, the first in slot 1, the others in slot 0, no slot twice
+// consecutive CTAs, the first in slot 1, the others in slot 0, no slot twice;
+// small units are not shared
 template <int BM, int BN> void division(std::mt19937 &r)
 {
     const int B = 1 + r() % 12, G = 1 + r() % 9, Hkv = 1 + r() % 5, n_cta = r() % 2 ? 152 : 304, mode = r() % 4;
@@ -169,12 +170,12 @@ template <int BM, int BN> void division(std::mt19937 &r)
     int32_t status = 0;
     Pool P{};
     P.status = &status, P.B = B, P.Hkv = Hkv, P.page_log2 = 4, P.n_pages = 1, P.max_blocks = 1 << 20;
-    WorkDim W{qs.data(), cl.data(), T, G, (int)(1 + r() % 12)};
+    WorkDim W{qs.data(), cl.data(), T, G, (int)(2 + r() % 12)};
     using U = Units<BM, BN>;
     auto seq = [&](int b) { return load_seq(P, W.q_start, W.ctx_len, T, b); };
     long total = 0;
     for (int b = 0; b < B; ++b) total += U::head_cost(seq(b), G) * Hkv;
-    const long per = piece_len(total, n_cta, W.min_tiles);
+    const long per = piece_len(total, n_cta, W.min_piece);
     std::map<std::tuple<int, int, int>, std::vector<std::array<int, 5>>> got;
     for (int c = 0; c < n_cta; ++c) {
         Piece p{};
@@ -217,6 +218,7 @@ template <int BM, int BN> void division(std::mt19937 &r)
                     if (v.size() > 1) NEED(v[i][3] == (i == 0) && v[i][2] == v[0][2] + (int)i);
                 }
                 if (v.size() > 1) NEED(v[0][4] == (int)v.size());
+                if (U::cost(seq(b), G, m) <= kWhole) NEED(v.size() == 1);
                 NEED(at == U::tiles(seq(b), G, m));
             }
     NEED(units == (long)got.size() && status == 0);
