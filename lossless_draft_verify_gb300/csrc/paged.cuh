@@ -100,20 +100,23 @@ __host__ __device__ __forceinline__ Seq load_seq(const Pool &P, const int32_t *_
 struct WorkDim {
     const int32_t *q_start, *ctx_len;
     int T, G;
-    int min_piece;     // a piece costs at least this much
 };
 
-// Measured on a batch of nine sequences (chunks of 1 to 700 over up to 20000
-// tokens, 28/4 heads, pages of 16): 806 us at 2, 745 at 4, 606 at 9,
-// 505 at 16, 502 at 20; a decode step of 16 x 32768 tokens 313 us at 2, 323 at
-// 16, 331 at 28.
-constexpr int kUnitCost = 16;
-// A piece costs at least this much (eight more tiles per CTA cost a lone short
-// sequence more than the merge of its parts).
-constexpr int kMinPiece = 10;
-// A unit of at most this cost is never cut: merging its parts would take longer
-// than it does.  It belongs to the CTA in whose piece its middle lies.
-constexpr int kWhole = 4 + kUnitCost;
+// A unit of at most kWhole is never cut: merging its parts would take longer
+// than it does.  It belongs to the CTA in whose piece its middle lies.  A piece
+// costs at least kMinPiece.
+// Measured with the tensor-core kernel (row tiles of 256) on a batch of nine
+// sequences (chunks of 1 to 700 over up to 20000 tokens, 28/4 heads, pages of
+// 16): 806 us at kUnitCost 2, 745 at 4, 606 at 9, 505 at 16, 502 at 20; a decode
+// step of 16 x 32768 tokens 313 us at 2, 323 at 16, 331 at 28.  The CUDA-core
+// kernels' tiles take longer and their units less: four sequences of 17 tokens
+// at most over 2000 in fp32 25.6 us with 1, 2, 3 and 34.4 with 4, 6, 8.
+template <int BM>
+struct Cost {
+    static constexpr int kUnitCost = BM == 256 ? 16 : 1;
+    static constexpr int kMinPiece = BM == 256 ? 10 : 2;
+    static constexpr int kWhole = BM == 256 ? 20 : 3;
+};
 
 // What one CTA has to do: from unit (b, h, mt), cost offset `off` within it,
 // `len` cost units on.  Written to shared memory by one warp, read by all.
@@ -129,7 +132,8 @@ __host__ __device__ inline long piece_len(long total, int n_cta, int min_len)
 }
 
 template <int BM, int BN>
-struct Units {
+struct Units : Cost<BM> {
+    using Cost<BM>::kUnitCost;
     static __host__ __device__ __forceinline__ int tiles(const Seq &s, int G, int mt)
     {
         const long last = lmin((long)s.n * G, (long)(mt + 1) * BM) - 1;    // last row of the tile
@@ -217,7 +221,7 @@ __device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int 
         before += sum;
         if (++c < chunks) continue;
         if (lo >= 0) break;                          // not reached: lo lies below the total
-        per = piece_len(before, n_cta, W.min_piece);
+        per = piece_len(before, n_cta, U::kMinPiece);
         lo = per * cta;
         hi = lmin(before, lo + per);
         if (lo >= hi) break;
@@ -267,7 +271,7 @@ struct Walk {
         while (left > 0) {
             const int cost = U::cost(s, W.G, mt), weight = U::weight(s, W.G, mt);
             const long take = lmin(left, (long)cost - off);
-            const bool uncut = cost <= kWhole, mine = !uncut || (off <= cost / 2 && cost / 2 < off + take);
+            const bool uncut = cost <= U::kWhole, mine = !uncut || (off <= cost / 2 && cost / 2 < off + take);
             const long a = uncut ? 0 : off, e = uncut ? cost : off + take;
             it.b = b;
             it.h = h;
@@ -277,8 +281,8 @@ struct Walk {
             it.ctx = s.ctx;
             it.rows = (int)lmin((long)BM, (long)s.n * W.G - (long)mt * BM);
             // the unit's first kUnitCost cost units carry no tile
-            it.t_lo = (int)(lmax(a - kUnitCost, 0) / weight);
-            it.t_hi = (int)(lmax(e - kUnitCost, 0) / weight);
+            it.t_lo = (int)(lmax(a - U::kUnitCost, 0) / weight);
+            it.t_hi = (int)(lmax(e - U::kUnitCost, 0) / weight);
             const bool starts = it.t_lo == 0, ends = e == cost;
             it.head = starts;
             it.whole = starts && ends;
@@ -368,7 +372,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_
 // ----- launchers ----------------------------------------------------------------------
 // paged_attn_simt.cu: fp32 on the CUDA cores
 constexpr int kSimtKeys = 32;      // the smallest key tile of its variants
-int simt_rows(int T, int G);
+int simt_rows(int T, int G, int B);
 int simt_ctas();
 cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                       const Parts &parts, cudaStream_t st);
@@ -387,7 +391,7 @@ cudaError_t mass_tc(const Pool &P, const WorkDim &W, int d, const void *q, int H
                     float *scores, int scores_stride, int32_t *status, cudaStream_t st);
 
 // paged_attn.cu: attention, with scores != null also the attention mass
-size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, bool mass);
+size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, bool mass);
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
                  int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st);
 

@@ -63,11 +63,11 @@ struct WsLayout {
 };
 
 // [status | desc | partial (m, l) | partial o | lse of every row]
-WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, bool with_rows)
+WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, bool with_rows)
 {
     WsLayout w;
     w.n_cta = dt == VC_BF16 ? tc_ctas() : simt_ctas();
-    const long unit = dt == VC_BF16 ? kTcRows : simt_rows(T, G);
+    const long unit = dt == VC_BF16 ? kTcRows : simt_rows(T, G, B);
     w.rows_cap = (int)std::min<long>(unit, (long)T * G);
     const size_t n = (size_t)w.n_cta * 2 * w.rows_cap;
     w.desc = kStatusBytes;
@@ -91,7 +91,7 @@ template <typename T>
 cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void *q, int Hq, float sl2, void *out,
                 float *scores, int scores_stride, uint8_t *ws, cudaStream_t st)
 {
-    const WsLayout w = layout(dt, d, W.T, W.G, Hq, scores != nullptr);
+    const WsLayout w = layout(dt, d, W.T, W.G, Hq, P.B, scores != nullptr);
     Parts parts = {(PartDesc *)(ws + w.desc), (float2 *)(ws + w.ml), (float *)(ws + w.o), w.rows_cap};
     float *lse = scores ? (float *)(ws + w.rows) : nullptr;
     cudaError_t e;
@@ -100,7 +100,8 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     // no unit is cut where the block table cannot hold a sequence long enough
     constexpr int tile = std::is_same_v<T, float> ? kSimtKeys : kTcKeys, weight = std::is_same_v<T, float> ? 1 : 2;
     const long cap = (long)P.max_blocks << P.page_log2;
-    if (e == cudaSuccess && (cap + tile - 1) / tile * weight + kUnitCost > kWhole)
+    using C = Cost<std::is_same_v<T, float> ? 64 : kTcRows>;
+    if (e == cudaSuccess && (cap + tile - 1) / tile * weight + C::kUnitCost > C::kWhole)
         e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
     if (e != cudaSuccess || !scores) return e;
     if constexpr (std::is_same_v<T, float>) return mass_simt(P, W, d, q, Hq, sl2, lse, scores, scores_stride, st);
@@ -109,9 +110,9 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
 
 }  // namespace
 
-size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, bool mass)
+size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, bool mass)
 {
-    return layout(dt, d, T, Hq / Hkv, Hq, mass).bytes;
+    return layout(dt, d, T, Hq / Hkv, Hq, B, mass).bytes;
 }
 
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
@@ -122,7 +123,6 @@ cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t
     W.ctx_len = ctx_len;
     W.T = T;
     W.G = Hq / P.Hkv;
-    W.min_piece = kMinPiece;
     const float sl2 = sm_scale * kLog2e;
     return dt == VC_BF16 ? run<__nv_bfloat16>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st)
                          : run<float>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st);

@@ -319,15 +319,16 @@ cudaError_t launch_mass(const Pool &P, const WorkDim &W, const void *q, int Hq, 
 
 }  // namespace
 
-// rows a CTA holds: 64, or 16 when no unit of the batch can have more
-int simt_rows(int T, int G) { return (long)T * G <= 16 ? 16 : 64; }
+// rows a CTA holds: 16 where the batch has no more per sequence on average
+// (decoding), else 64
+int simt_rows(int T, int G, int B) { return (long)T * G <= 16l * B ? 16 : 64; }
 int simt_ctas() { return 2 * device_sm_count(); }
 
 cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                       const Parts &parts, cudaStream_t st)
 {
     const int n = simt_ctas();
-    if (simt_rows(W.T, W.G) == 16)
+    if (simt_rows(W.T, W.G, P.B) == 16)
         return d == 128 ? launch_attn<128, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st)
                         : launch_attn<64, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st);
     return d == 128 ? launch_attn<128, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)

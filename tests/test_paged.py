@@ -170,12 +170,12 @@ template <int BM, int BN> void division(std::mt19937 &r)
     int32_t status = 0;
     Pool P{};
     P.status = &status, P.B = B, P.Hkv = Hkv, P.page_log2 = 4, P.n_pages = 1, P.max_blocks = 1 << 20;
-    WorkDim W{qs.data(), cl.data(), T, G, (int)(2 + r() % 12)};
+    WorkDim W{qs.data(), cl.data(), T, G};
     using U = Units<BM, BN>;
     auto seq = [&](int b) { return load_seq(P, W.q_start, W.ctx_len, T, b); };
     long total = 0;
     for (int b = 0; b < B; ++b) total += U::head_cost(seq(b), G) * Hkv;
-    const long per = piece_len(total, n_cta, W.min_piece);
+    const long per = piece_len(total, n_cta, U::kMinPiece);
     std::map<std::tuple<int, int, int>, std::vector<std::array<int, 5>>> got;
     for (int c = 0; c < n_cta; ++c) {
         Piece p{};
@@ -218,7 +218,7 @@ template <int BM, int BN> void division(std::mt19937 &r)
                     if (v.size() > 1) NEED(v[i][3] == (i == 0) && v[i][2] == v[0][2] + (int)i);
                 }
                 if (v.size() > 1) NEED(v[0][4] == (int)v.size());
-                if (U::cost(seq(b), G, m) <= kWhole) NEED(v.size() == 1);
+                if (U::cost(seq(b), G, m) <= U::kWhole) NEED(v.size() == 1);
                 NEED(at == U::tiles(seq(b), G, m));
             }
     NEED(units == (long)got.size() && status == 0);
