@@ -382,8 +382,10 @@ cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int
 // paged_attn_tc.cu: bf16 on the tensor cores, row tiles of 256
 constexpr int kTcRows = 256, kTcKeys = 128;
 int tc_ctas();
+// s_out (or null): the scores of every row, s_stride apart (a multiple of 128,
+// at least the table's slots), in the log2 domain
 cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
-                    const Parts &parts, int32_t *status, cudaStream_t st);
+                    float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st);
 
 // paged_mass_tc.cu: scores += the attention weight of every slot, lse (log2
 // domain) of every row given
@@ -391,7 +393,7 @@ cudaError_t mass_tc(const Pool &P, const WorkDim &W, int d, const void *q, int H
                     float *scores, int scores_stride, int32_t *status, cudaStream_t st);
 
 // paged_attn.cu: attention, with scores != null also the attention mass
-size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, bool mass);
+size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass);
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
                  int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st);
 

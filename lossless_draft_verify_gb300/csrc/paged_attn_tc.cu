@@ -22,6 +22,10 @@
 // the second product (half a step of bf16 per weight, the type the matrix unit
 // takes), out once.
 //
+// With STORE the scores are written out too (fp32, log2 domain), for the
+// attention mass of a batch of few rows: G scores of 4 bytes per key and kv head
+// beside 4 d bytes of K and V, instead of a second read of K.
+//
 // V rows past the sequence's end may hold any bits and 0 * NaN is not 0: those
 // that share the last page with tokens are cleared in shared memory, further
 // pages are not read (their boxes lie outside the map and fill with zeros).
@@ -73,6 +77,8 @@ struct Params {
     float *lse_out;
     Parts parts;
     int32_t *status;
+    float *s_out;                  // STORE: scores of row r of q at s_out + r * s_stride
+    long s_stride;
     int Hq, box_rows, n_rows;      // n_rows: rows of the pool's tensor map
     float sl2;
 };
@@ -89,7 +95,7 @@ __device__ __forceinline__ bool step(Shared *S, int warp, const Params &A)
     return x.more;
 }
 
-template <int D>
+template <int D, bool STORE>
 __global__ void __launch_bounds__(kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Params A)
 {
@@ -349,6 +355,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const int kmax = valid ? it.ctx + (row0 + R) / A.W.G : -1;
             // keys every row of the tile sees
             const int kall = it.ctx + (row0 + (big ? t * 128 : 0)) / A.W.G;
+            float *s_row = STORE && valid ? A.s_out + (long)out_row(R) * A.s_stride : nullptr;
             float m = kNegBig, l = 0.f;
             const int mine = big ? n : (n + 1 - t) / 2;      // this stream's steps
             // V rows of the last page past the sequence's end, before the product
@@ -412,6 +419,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         tc::ld_wait();
                         if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
                         uint32_t (&v)[32] = u[h & 1];
+                        if constexpr (STORE) {
+                            if (valid) {
+                                float *dst = s_row + key0 + h * 32;
+#pragma unroll
+                                for (int c = 0; c < 32; c += 4)
+                                    *reinterpret_cast<float4 *>(dst + c) = make_float4(
+                                        __uint_as_float(v[c]) * A.sl2, __uint_as_float(v[c + 1]) * A.sl2,
+                                        __uint_as_float(v[c + 2]) * A.sl2, __uint_as_float(v[c + 3]) * A.sl2);
+                            }
+                            __syncwarp();
+                        }
                         chunk(h, v);
 #pragma unroll
                         for (int e = 0; e < 16; ++e) {
@@ -544,9 +562,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
 }
 
-template <int D>
+template <int D, bool STORE>
 cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
-                   const Parts &parts, int32_t *status, cudaStream_t st)
+                   float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st)
 {
     Params A;
     A.P = P;
@@ -556,6 +574,8 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     A.lse_out = lse;
     A.parts = parts;
     A.status = status;
+    A.s_out = s_out;
+    A.s_stride = s_stride;
     A.Hq = Hq;
     A.box_rows = std::min(1 << P.page_log2, BN);
     A.n_rows = (P.n_pages * P.Hkv) << P.page_log2;
@@ -565,7 +585,7 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     if (!tma_map_bf16_3d(&mk, P.k, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1) ||
         !tma_map_bf16_3d(&mv, P.v, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1))
         return cudaErrorInvalidValue;
-    auto kern = attn_tc_kernel<D>;
+    auto kern = attn_tc_kernel<D, STORE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::SMEM);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(tc_ctas()), dim3(kThreads), Geom<D>::SMEM, st, mk, mv, A);
@@ -576,10 +596,13 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
 int tc_ctas() { return device_sm_count(); }
 
 cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
-                    const Parts &parts, int32_t *status, cudaStream_t st)
+                    float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st)
 {
-    return d == 128 ? launch<128>(P, W, q, Hq, sl2, out, lse, parts, status, st)
-                    : launch<64>(P, W, q, Hq, sl2, out, lse, parts, status, st);
+    if (s_out)
+        return d == 128 ? launch<128, true>(P, W, q, Hq, sl2, out, lse, s_out, s_stride, parts, status, st)
+                        : launch<64, true>(P, W, q, Hq, sl2, out, lse, s_out, s_stride, parts, status, st);
+    return d == 128 ? launch<128, false>(P, W, q, Hq, sl2, out, lse, nullptr, 0, parts, status, st)
+                    : launch<64, false>(P, W, q, Hq, sl2, out, lse, nullptr, 0, parts, status, st);
 }
 
 }  // namespace paged

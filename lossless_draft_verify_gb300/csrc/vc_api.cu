@@ -452,7 +452,7 @@ paged::Pool paged_pool(const vc_paged_cache *c)
 size_t paged_attn_ws(const vc_paged_cache *c, int T, int Hq, bool mass)
 {
     if (!paged_ok(c) || !paged_supported(c) || !paged_heads_ok(c, T, Hq) || !paged_rows_ok(c, T, Hq)) return 0;
-    return paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, mass);
+    return paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page, mass);
 }
 
 vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t *q_start, const int32_t *ctx_len,
@@ -464,7 +464,8 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t 
     if (!(sm_scale >= 0.f) || sm_scale > FLT_MAX) return VC_ERR_INVALID;
     if (!paged_supported(c) || !paged_rows_ok(c, T, Hq)) return VC_ERR_UNSUPPORTED;
     if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
-    if (ws_bytes < paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, scores != nullptr)) return VC_ERR_INVALID;
+    if (ws_bytes < paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page,
+                                     scores != nullptr)) return VC_ERR_INVALID;
     if (T == 0) return VC_OK;
     return cuda_status(paged::attn(paged_pool(c), c->dt, c->d, q, q_start, ctx_len, T, Hq, sm_scale, out, scores,
                                    scores_stride, ws, stream));
