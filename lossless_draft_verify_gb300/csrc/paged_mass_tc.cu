@@ -12,8 +12,10 @@
 // heads, one TMA box), so K is read from HBM once and a row tile from L2 once
 // per 512 keys.  With one row tile (decoding) this is a stream of K, bound by
 // HBM; with many the exponentials bound it.
-//   warps 0-3, 4-7  sums of the even and odd key tiles of a group;
-//   warp 8          producer; warp 9 issues the MMAs (four accumulators).
+//   warps 0-15      sums, four warps to a key tile of the group (and to one of
+//                   four accumulators): enough of them that the exponentials,
+//                   16 a clock and SM, are always fed;
+//   warp 16         producer; warp 17 issues the MMAs.
 #include "paged.cuh"
 #include "tcgen05.cuh"
 
@@ -23,7 +25,8 @@ namespace {
 
 constexpr int BN = 128;          // keys per tile
 constexpr int kGroup = 4;        // key tiles of a group
-constexpr int kThreads = 320;
+constexpr int kThreads = 576;
+constexpr int kProducer = 16, kIssuer = 17;     // warps
 constexpr int kQStages = 2;
 
 template <int D>
@@ -34,7 +37,7 @@ struct Geom {
     static constexpr int SM_Q = 0;
     static constexpr int SM_K = kQStages * TILE;
     static constexpr int SM_X = SM_K + STAGES * TILE;
-    static constexpr int SMEM = SM_X + 8 * 512 + 1024;
+    static constexpr int SMEM = SM_X + 16 * 512 + 1024;
 };
 
 // A CTA's share: groups, in the order sequence, head, group, each with the
@@ -163,8 +166,8 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     using G = Geom<D>;
     constexpr int NST = G::STAGES;
     extern __shared__ __align__(1024) uint8_t sm[];
-    float *s_lse = reinterpret_cast<float *>(sm + G::SM_X);  // [8 warps][128]
-    Shared *S = reinterpret_cast<Shared *>(sm + G::SM_X + 8 * 512);
+    float *s_lse = reinterpret_cast<float *>(sm + G::SM_X);  // [16 warps][128]
+    Shared *S = reinterpret_cast<Shared *>(sm + G::SM_X + 16 * 512);
     static_assert(sizeof(Shared) <= 1024, "shared block");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
@@ -187,11 +190,11 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         }
         fence_mbar_init();
     }
-    if (warp == 9) {
+    if (warp == kIssuer) {
         tc::tmem_alloc(&S->tmem, 512);
         tc::tmem_relinquish();
     }
-    if (warp == 8) find_share(A, blockIdx.x, gridDim.x, &S->start);
+    if (warp == kProducer) find_share(A, blockIdx.x, gridDim.x, &S->start);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
@@ -201,7 +204,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     MassWalk walk = S->start;
     MassItem it;
 
-    if (warp == 8) {
+    if (warp == kProducer) {
         // ------------------------------------------------------- producer --
         const int boxes = BN / A.box_rows * G::HALVES;
         const int bp = lane / G::HALVES, half = lane % G::HALVES;
@@ -256,126 +259,131 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             for (int i = 0; i < kQStages; ++i)
                 if (q_round || i < qr.slot) mbar_wait(&S->q_full[i], i < qr.slot ? qr.phase : qr.phase ^ 1);
         }
-    } else if (warp == 9) {
+    } else if (warp == kIssuer) {
         // -------------------------------------------------------- issuer --
-        if (lane == 0) {
-            Ring<NST> k0;                                    // the group's first key tile
-            Ring<kQStages> qr;
-            Ring<2> sr[2];                                   // accumulators of the two groups of sums
-            bool ok = true, s_round[2] = {false, false};
-            while (ok && next_group(walk, A, it)) {
-                Ring<NST> kr = k0;
-                for (int q = it.mt0; q < it.mt && ok; ++q) {
-                    ok = wait_bar(&S->q_full[qr.slot], qr.phase, A.status, 113);
-                    if (!ok) break;
-                    const int cols = (int)lmin(rt, it.rows - (long)q * rt);
-                    const uint32_t id = tc::idesc_bf16(BN, (cols + 15) / 16 * 16, false, false);
-                    const uint32_t sQ = smem_u32(sm + G::SM_Q + qr.slot * G::TILE);
-                    kr = k0;
-                    for (int k = 0; k < it.tiles; ++k) {
-                        const int w = k & 1;
-                        Ring<2> &a = sr[w];
-                        ok = wait_bar(&S->k_full[kr.slot], kr.phase, A.status, 114) &&
-                             (!s_round[w] || wait_bar(&S->s_free[2 * w + a.slot], a.phase ^ 1, A.status, 115));
-                        if (!ok) break;
-                        tc::fence_after();
-                        const uint32_t sK = smem_u32(sm + G::SM_K + kr.slot * G::TILE);
+        // The warp runs as one and an elected thread issues: operands that are
+        // the same for the whole warp then stay in uniform registers.  All
+        // tensor memory is this CTA's, so its addresses are constants.
+        constexpr uint32_t hi = tc::desc_hi(1024, tc::kSwizzle128B), HALF = BN * 128 >> 4;
+        const uint32_t k_lo = tc::desc_lo(smem_u32(sm + G::SM_K), 16), q_lo = tc::desc_lo(smem_u32(sm + G::SM_Q), 16);
+        Ring<NST> k0;                                        // the group's first key tile
+        Ring<kQStages> qr;
+        uint32_t used[kGroup] = {};                          // rounds of each key tile's accumulator
+        bool ok = tmem == 0;
+        if (!ok) report_timeout(A.status, 109);              // never expected
+        while (ok && next_group(walk, A, it)) {
+            Ring<NST> kr = k0;
+            for (int q = it.mt0; q < it.mt && ok; ++q) {
+                ok = wait_warp(&S->q_full[qr.slot], qr.phase, A.status, 113);
+                if (!ok) break;
+                const int cols = (int)lmin(rt, it.rows - (long)q * rt);
+                const uint32_t id = tc::idesc_bf16(BN, (cols + 15) / 16 * 16, false, false);
+                const uint32_t bq = q_lo + qr.slot * (G::TILE >> 4);
+                kr = k0;
 #pragma unroll
-                        for (int kk = 0; kk < D / 16; ++kk) {
-                            const uint32_t o = (kk >> 2) * (BN * 128) + (kk & 3) * 32;
-                            tc::mma_ss(tmem + (2 * w + a.slot) * BN, tc::smem_desc(sK + o, 16, 1024, tc::kSwizzle128B),
-                                       tc::smem_desc(sQ + o, 16, 1024, tc::kSwizzle128B), id, kk > 0);
-                        }
-                        tc::commit(&S->s_full[2 * w + a.slot]);
-                        a.next();
-                        s_round[w] = s_round[w] || a.slot == 0;
+                for (int k = 0; k < kGroup; ++k) {
+                    if (k >= it.tiles) break;
+                    ok = wait_warp(&S->k_full[kr.slot], kr.phase, A.status, 114) &&
+                         (used[k] == 0 || wait_warp(&S->s_free[k], (used[k] - 1) & 1, A.status, 115));
+                    if (!ok) break;
+                    tc::fence_after();
+                    const uint32_t ak = k_lo + kr.slot * (G::TILE >> 4), d = k * BN;
+                    if (tc::elect()) {
+                        tc::mma_ss2<false>(d, ak, hi, bq, hi, id);
+#pragma unroll
+                        for (int kk = 1; kk < D / 16; ++kk)
+                            tc::mma_ss2<true>(d, ak + (kk >> 2) * HALF + (kk & 3) * 2, hi,
+                                              bq + (kk >> 2) * HALF + (kk & 3) * 2, hi, id);
+                        tc::commit(&S->s_full[k]);
                         if (q == it.mt - 1) tc::commit(&S->k_empty[kr.slot]);
-                        kr.next();
                     }
-                    tc::commit(&S->q_empty[qr.slot]);
-                    qr.next();
+                    ++used[k];
+                    kr.next();
                 }
-                k0 = kr;
+                if (ok && tc::elect()) tc::commit(&S->q_empty[qr.slot]);
+                qr.next();
             }
+            k0 = kr;
         }
     } else {
         // ---------------------------------------------------------- sums --
-        const int w = warp >> 2, wq = warp & 3;
+        const int k = warp >> 2, wq = warp & 3;              // the warp's key tile of the group
         const uint32_t lanes = (uint32_t)(wq * 32) << 16;
         float *my_lse = s_lse + warp * BN;
-        Ring<2> sr;
+        uint32_t used = 0;
         bool ok = true;
         while (ok && next_group(walk, A, it)) {
-            float sum[kGroup / 2];
+            if (k >= it.tiles) continue;
+            const int tile0 = it.key0 + k * BN, key = tile0 + wq * 32 + lane;
+            float sum = 0.f;
+            // lse of a row tile, four rows per lane, on its way a tile ahead
+            float next[4];
+            auto fetch = [&](int q) {
 #pragma unroll
-            for (int i = 0; i < kGroup / 2; ++i) sum[i] = 0.f;
+                for (int x = 0; x < 4; ++x) {
+                    const int c = lane + 32 * x;
+                    const long R = (long)q * rt + c;
+                    next[x] = c < rt && R < it.rows
+                                  ? A.lse[(size_t)(it.tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G] : 0.f;
+                }
+            };
+            fetch(it.mt0);
             for (int q = it.mt0; q < it.mt && ok; ++q) {
                 const int cols = (int)lmin(rt, it.rows - (long)q * rt);
-                // lse of the tile's rows, a copy per warp
-                __syncwarp();
-                for (int c = lane; c < BN; c += 32) {
-                    const int R = q * rt + c;
-                    my_lse[c] = c < cols ? A.lse[(size_t)(it.tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G] : 0.f;
-                }
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < kGroup / 2; ++i) {
-                    const int k = 2 * i + w;
-                    if (k >= it.tiles || !ok) continue;
-                    ok = wait_warp(&S->s_full[2 * w + sr.slot], sr.phase, A.status, 116);
-                    if (!ok) continue;
-                    tc::fence_after();
-                    const int tile0 = it.key0 + k * BN, key = tile0 + wq * 32 + lane;
-                    // columns [lo, cols) see the key; [lo_all, cols) every key of the tile
-                    const int lo = (int)lmin(lmax((long)(key - it.ctx) * A.W.G - (long)q * rt, 0), BN);
-                    const int lo_all = (int)lmin(lmax((long)(tile0 + BN - 1 - it.ctx) * A.W.G - (long)q * rt, 0), BN);
-                    float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
-                    const float2 sc = make_float2(A.sl2, A.sl2);
-                    for (int c0 = 0; c0 < cols; c0 += 32) {
-                        uint32_t u[32];
-                        __syncwarp();
-                        tc::ld32(tmem + lanes + (2 * w + sr.slot) * BN + c0, u);
-                        tc::ld_wait();
-                        if (c0 >= lo_all && c0 + 32 <= cols) {
+                for (int x = 0; x < 4; ++x) my_lse[lane + 32 * x] = next[x];
+                __syncwarp();
+                if (q + 1 < it.mt) fetch(q + 1);
+                ok = wait_warp(&S->s_full[k], used & 1, A.status, 116);
+                ++used;
+                if (!ok) break;
+                tc::fence_after();
+                // columns [lo, cols) see the key; [lo_all, cols) every key of the tile
+                const int lo = (int)lmin(lmax((long)(key - it.ctx) * A.W.G - (long)q * rt, 0), BN);
+                const int lo_all = (int)lmin(lmax((long)(tile0 + BN - 1 - it.ctx) * A.W.G - (long)q * rt, 0), BN);
+                float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
+                const float2 sc = make_float2(A.sl2, A.sl2);
+                const uint32_t tS = tmem + lanes + k * BN;
+#pragma unroll 1
+                for (int c0 = 0; c0 < cols; c0 += 32) {
+                    uint32_t v[32];
+                    tc::ld32(tS + c0, v);
+                    tc::ld_wait();
+                    if (c0 >= lo_all && c0 + 32 <= cols) {
 #pragma unroll
-                            for (int c = 0; c < 32; c += 4) {
-                                const float4 e = *reinterpret_cast<const float4 *>(my_lse + c0 + c);
-                                const float2 x = fma2(make_float2(__uint_as_float(u[c]), __uint_as_float(u[c + 1])), sc,
-                                                      make_float2(-e.x, -e.y));
-                                const float2 y = fma2(make_float2(__uint_as_float(u[c + 2]), __uint_as_float(u[c + 3])),
-                                                      sc, make_float2(-e.z, -e.w));
-                                acc[0] = add2(acc[0], make_float2(ex2(x.x), ex2(x.y)));
-                                acc[1] = add2(acc[1], make_float2(ex2(y.x), ex2(y.y)));
-                            }
-                        } else {
-                            // columns past the rows hold whatever was there: chosen, not multiplied away
-#pragma unroll
-                            for (int c = 0; c < 32; ++c) {
-                                const float p = ex2(fmaf(__uint_as_float(u[c]), A.sl2, -my_lse[c0 + c]));
-                                if (c0 + c >= lo && c0 + c < cols) acc[0].x += p;
-                            }
+                        for (int c = 0; c < 32; c += 4) {
+                            const float4 e = *reinterpret_cast<const float4 *>(my_lse + c0 + c);
+                            const float2 x = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc,
+                                                  make_float2(-e.x, -e.y));
+                            const float2 y = fma2(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
+                                                  sc, make_float2(-e.z, -e.w));
+                            acc[0] = add2(acc[0], make_float2(ex2(x.x), ex2(x.y)));
+                            acc[1] = add2(acc[1], make_float2(ex2(y.x), ex2(y.y)));
                         }
+                    } else {
+                        // columns past the rows hold whatever was there: chosen, not multiplied away
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            const float p = ex2(fmaf(__uint_as_float(v[c]), A.sl2, -my_lse[c0 + c]));
+                            if (c0 + c >= lo && c0 + c < cols) acc[0].x += p;
+                        }
+                        __syncwarp();
                     }
-                    sum[i] += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-                    tc::fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&S->s_free[2 * w + sr.slot]);
-                    sr.next();
                 }
+                sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+                tc::fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&S->s_free[k]);
             }
             if (!ok) break;
-            float *dst = A.scores + ((size_t)it.b * A.P.Hkv + it.h) * A.scores_stride;
-#pragma unroll
-            for (int i = 0; i < kGroup / 2; ++i) {
-                const int key = it.key0 + (2 * i + w) * BN + wq * 32 + lane;
-                if (key < it.len) dst[key] += sum[i];
-            }
+            if (key < it.len) A.scores[((size_t)it.b * A.P.Hkv + it.h) * A.scores_stride + key] += sum;
         }
     }
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
-    if (warp == 9) {
+    if (warp == kIssuer) {
         __syncwarp();
         tc::tmem_dealloc(tmem, 512);
     }
