@@ -781,8 +781,9 @@ vc_status vc_gemm_ex(const void *x, const void *w, const void *resid, void *out,
  * (that sequence is treated as having no tokens).
  *
  * Supported: d in {64, 128}, page in {16, 32, 64, 128, 256}, any Hq that is a
- * multiple of Hkv with Hq / Hkv <= 128; fewer than 2^31 slots n_pages * Hkv *
- * page, and T * Hq <= 2^30.
+ * multiple of Hkv with Hq / Hkv <= 128 and Hq + 2 Hkv <= 2^20; fewer than 2^31
+ * slots n_pages * Hkv * page and max_blocks * page, and T * Hq <= 2^30.  No
+ * output overlaps an input of its call.
  */
 #define VC_PAGED_BAD_PAGE 1
 #define VC_PAGED_BAD_LENGTH 2
@@ -836,6 +837,8 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
  * q, out: device [T][Hq][d] in cache->dt, 16-byte aligned.  bf16 caches run on
  * the tensor cores (fp32 accumulation, the softmax weights rounded to bf16),
  * fp32 caches on the CUDA cores in fp32.  sm_scale: finite, not negative.
+ * The order of a row's sums, and so its last bits, depends on the lengths of
+ * the whole batch (unlike vc_decoder_forward's).
  */
 size_t vc_paged_attn_workspace_bytes(const vc_paged_cache *cache, int T, int Hq);
 vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_t *q_start, const int32_t *ctx_len,
@@ -849,7 +852,9 @@ vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_
  *       heads of h that see j of softmax_j(q . k_j * sm_scale),
  * with every row's final maximum and sum, in fp32, each slot summed in an order
  * fixed by the lengths.  scores: device fp32, scores_stride >= max_blocks *
- * page.  Sequences without rows keep their scores.
+ * page.  Sequences without rows keep their scores.  The workspace of a bf16
+ * batch with T * Hq <= 16 * B * Hkv (decoding) also holds the scores of its
+ * rows, 4 bytes per query head and table slot.
  */
 size_t vc_paged_attn_h2o_workspace_bytes(const vc_paged_cache *cache, int T, int Hq);
 vc_status vc_paged_attn_h2o(const void *q, const vc_paged_cache *cache, const int32_t *q_start,

@@ -11,10 +11,13 @@
 // sequence's row tiles pass (a row tile is floor(128 / G) queries of the G
 // heads, one TMA box), so K is read from HBM once and a row tile from L2 once
 // per 512 keys.  With one row tile (decoding) this is a stream of K, bound by
-// HBM; with many the exponentials bound it.
-//   warps 0-15      sums, four warps to a key tile of the group (and to one of
-//                   four accumulators): enough of them that the exponentials,
-//                   16 a clock and SM, are always fed;
+// HBM; with many the sums' arithmetic is the bound.  Groups of two or one tile,
+// for a finer division, cost more than they give (471 and 656 us against 404
+// and 583): each row tile is then on its way for fewer products.
+//   warps 0-15      sums, four warps to a key tile of the group and to one of
+//                   four accumulators (two sets of four, each with every other
+//                   tile: 454 against 404 us for two 512-token chunks over
+//                   16000 tokens with their attention);
 //   warp 16         producer; warp 17 issues the MMAs.
 #include "paged.cuh"
 #include "tcgen05.cuh"

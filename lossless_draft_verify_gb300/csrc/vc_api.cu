@@ -430,7 +430,7 @@ bool paged_heads_ok(const vc_paged_cache *c, int T, int Hq)
 
 bool paged_rows_ok(const vc_paged_cache *c, int T, int Hq)
 {
-    return (int64_t)T * Hq <= (1 << 30) && Hq / c->Hkv <= 128;
+    return (int64_t)T * Hq <= (1 << 30) && Hq / c->Hkv <= 128 && (int64_t)Hq + 2ll * c->Hkv <= (1 << 20);
 }
 
 paged::Pool paged_pool(const vc_paged_cache *c)
@@ -460,7 +460,7 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t 
                           size_t ws_bytes, cudaStream_t stream)
 {
     if (!paged_ok(c) || !q || !q_start || !ctx_len || !out || !ws || !paged_heads_ok(c, T, Hq)) return VC_ERR_INVALID;
-    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
+    if (q == out || !aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
     if (!(sm_scale >= 0.f) || sm_scale > FLT_MAX) return VC_ERR_INVALID;
     if (!paged_supported(c) || !paged_rows_ok(c, T, Hq)) return VC_ERR_UNSUPPORTED;
     if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
@@ -504,7 +504,7 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
 {
     if (!paged_ok(cache) || !qkv || !rope || !q_start || !ctx_len || !q_out) return VC_ERR_INVALID;
     if (!paged_heads_ok(cache, T, Hq) || (q_gain == nullptr) != (k_gain == nullptr)) return VC_ERR_INVALID;
-    if (!(eps >= 0.f) || !aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16) || !aligned(k_gain, 16))
+    if (!(eps >= 0.f) || eps > FLT_MAX || qkv == q_out || !aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16) || !aligned(k_gain, 16))
         return VC_ERR_INVALID;
     if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > cache->d) return VC_ERR_INVALID;
     if (!paged_supported(cache) || !paged_rows_ok(cache, T, Hq)) return VC_ERR_UNSUPPORTED;

@@ -799,6 +799,10 @@ class PagedCache:
             if t is not None and (t.device != self.device or not t.is_contiguous()):
                 raise ValueError("tensors must be contiguous and on the pool's device")
 
+    def _on_gpu(self):
+        if self.device.type != "cuda":
+            raise ValueError(f"the pool is on {self.device}, not on a GPU")
+
     def _check_batch(self, q_start, ctx_len):
         if q_start.dtype != torch.int32 or ctx_len.dtype != torch.int32:
             raise TypeError("q_start and ctx_len are int32")
@@ -836,6 +840,7 @@ def vc_paged_append(qkv, cache: PagedCache, q_start, ctx_len, q_out, rope: Rope,
             raise TypeError("qkv, q_out and the gains have the cache's dtype, the gains d entries")
     if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
         raise TypeError("positions is int32 [T]")
+    cache._on_gpu()
     _check(load().vc_paged_append(qkv.data_ptr(), _ptr(q_gain), _ptr(k_gain), float(eps), ctypes.byref(rope),
                                   _ptr(positions), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
                                   ctypes.byref(cache.c), q_out.data_ptr(), _stream(stream)), "vc_paged_append")
@@ -863,6 +868,7 @@ def vc_paged_attn(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, 
     """Causal attention of the batch's chunks over the pages: q, out [T][Hq][d],
     q_start int32 [B + 1], ctx_len int32 [B]."""
     T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws)
+    cache._on_gpu()
     _check(load().vc_paged_attn(q.data_ptr(), ctypes.byref(cache.c), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
                                 float(sm_scale), out.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
            "vc_paged_attn")
@@ -875,6 +881,7 @@ def vc_paged_attn_h2o(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, o
     T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores)
     if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (cache.B, cache.Hkv):
         raise ValueError(f"scores is fp32 [{cache.B}][{cache.Hkv}][slots]")
+    cache._on_gpu()
     _check(load().vc_paged_attn_h2o(q.data_ptr(), ctypes.byref(cache.c), q_start.data_ptr(), ctx_len.data_ptr(), T,
                                     Hq, float(sm_scale), out.data_ptr(), scores.data_ptr(), scores.shape[2], ws.ptr,
                                     ws.nbytes, _stream(stream)), "vc_paged_attn_h2o")
@@ -893,6 +900,7 @@ def vc_paged_evict(scores, src: PagedCache, src_len, keep_top: int, keep_recent:
     for t in (src_len, dst_len):
         if t.dtype != torch.int32 or t.shape != (src.B,):
             raise ValueError(f"src_len and dst_len are int32 [{src.B}]")
+    src._on_gpu()
     _check(load().vc_paged_evict(scores.data_ptr(), scores.shape[2], ctypes.byref(src.c), src_len.data_ptr(),
                                  DropCfg(int(keep_top), int(keep_recent)), ctypes.byref(dst.c), dst_len.data_ptr(),
                                  kept_idx.data_ptr(), kept_idx.shape[2], _ptr(scores_out),

@@ -43,9 +43,9 @@ def test_bad_caches_are_refused(vc, kw, want):
     L = vc.load()
     c = _cache(vc, **kw)
     rope = vc.vc_rope_init(64, 1e4)
-    assert L.vc_paged_append(A, None, None, 1e-6, rope, None, A, A, 4, 4, c, A, None) == want
-    assert L.vc_paged_attn(A, c, A, A, 4, 4, 1.0, A, A, BIG, None) == want
-    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A, A, 1 << 30, A, BIG, None) == want
+    assert L.vc_paged_append(A, None, None, 1e-6, rope, None, A, A, 4, 4, c, A + 64, None) == want
+    assert L.vc_paged_attn(A, c, A, A, 4, 4, 1.0, A + 64, A, BIG, None) == want
+    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A + 64, A, 1 << 30, A, BIG, None) == want
     assert L.vc_paged_attn_workspace_bytes(c, 4, 4) == 0 == L.vc_paged_attn_h2o_workspace_bytes(c, 4, 4)
     good = _cache(vc, **{k: v for k, v in kw.items() if k in ("B", "Hkv", "d", "dt")})
     for s, t in ((c, good), (good, c)):
@@ -56,9 +56,10 @@ def test_bad_arguments_are_refused(vc):
     L = vc.load()
     c = _cache(vc)
     rope = vc.vc_rope_init(128, 1e4)
-    app = [A, None, None, 1e-6, rope, None, A, A, 4, 4, c, A, None]
+    app = [A, None, None, 1e-6, rope, None, A, A, 4, 4, c, A + 4096, None]
     for i, x, want in [(0, None, 1), (0, A + 2, 1), (1, A, 1), (2, A, 1), (3, -1.0, 1), (3, math.nan, 1), (6, None, 1),
-                       (7, None, 1), (8, -1, 1), (9, 0, 1), (9, 3, 1), (11, None, 1), (8, 1 << 29, 2)]:
+                       (7, None, 1), (8, -1, 1), (9, 0, 1), (9, 3, 1), (11, None, 1), (11, A, 1), (3, math.inf, 1),
+                       (8, 1 << 29, 2)]:
         a = list(app)
         a[i] = x
         assert L.vc_paged_append(*a) == want, (i, x)
@@ -68,18 +69,18 @@ def test_bad_arguments_are_refused(vc):
     need = L.vc_paged_attn_workspace_bytes(c, 4, 4)
     need2 = L.vc_paged_attn_h2o_workspace_bytes(c, 4, 4)
     assert 0 < need < need2
-    at = [A, c, A, A, 4, 4, 1.0, A, A, need, None]
+    at = [A, c, A, A, 4, 4, 1.0, A + 4096, A, need, None]
     for i, x, want in [(0, None, 1), (0, A + 8, 1), (2, None, 1), (3, None, 1), (4, -1, 1), (5, 0, 1), (5, 5, 1),
                        (6, -1.0, 1), (6, math.nan, 1), (6, math.inf, 1), (7, None, 1), (7, A + 4, 1), (8, None, 1),
-                       (8, A + 16, 1), (9, need - 1, 1), (4, 1 << 29, 2), (5, 258, 2)]:
+                       (8, A + 16, 1), (9, need - 1, 1), (4, 1 << 29, 2), (5, 258, 2), (7, A, 1)]:
         a = list(at)
         a[i] = x
         assert L.vc_paged_attn(*a) == want, (i, x)
-    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A, None, 256, A, need2, None) == 1
-    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A, A, 255, A, need2, None) == 1      # fewer scores than slots
-    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A, A, 256, A, need2 - 1, None) == 1
+    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A + 64, None, 256, A, need2, None) == 1
+    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A + 64, A, 255, A, need2, None) == 1      # fewer scores than slots
+    assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, 1.0, A + 64, A, 256, A, need2 - 1, None) == 1
     # no rows: nothing to do, nothing enqueued
-    assert L.vc_paged_attn(A, c, A, A, 0, 4, 1.0, A, A, BIG, None) == 0
+    assert L.vc_paged_attn(A, c, A, A, 0, 4, 1.0, A + 64, A, BIG, None) == 0
     assert L.vc_paged_append(*app[:8], 0, *app[9:]) == 0
     ev = [A, 256, c, A, vc.DropCfg(20, 10), c, A + 64, A, 30, A + 128, 30, None]
     for i, x in [(0, None), (1, 255), (3, None), (4, vc.DropCfg(-1, 0)), (4, vc.DropCfg(0, -1)), (6, None), (6, A),
@@ -136,6 +137,8 @@ def test_the_binding_refuses(vc):
     with pytest.raises(TypeError):
         vc.vc_paged_append(torch.zeros(3, 8 * 64), c, st, ctx, q, vc.vc_rope_init(64, 1e4),
                            positions=torch.zeros(3))
+    with pytest.raises(ValueError, match="not on a GPU"):
+        vc.vc_paged_attn(q, c, st, ctx, 1.0, q.clone(), ws)
     with pytest.raises(ValueError):
         vc.vc_paged_evict(torch.zeros(1, 2, 32), c, ctx, 1, 1, c, torch.zeros(2, **i32), torch.zeros(1, 2, 2, **i32))
 
