@@ -142,6 +142,95 @@ def test_attention_repeats_and_rides_in_a_graph():
     assert vc.vc_poll_status(ws) == 0
 
 
+def test_two_graphs_share_a_workspace():
+    """Nothing of a call stays in the workspace: two captured batches of other
+    shapes replay in turn on one."""
+    vc = lib()
+    jobs, need = [], 0
+    for ns, cs, Hq in (([1, 1, 1], [3000, 77, 900], 8), ([60, 200], [500, 40], 4)):
+        bt = Batch(ns, cs, 2, 128, 32, BF, seed=len(jobs))
+        cache = _cache(vc, bt)
+        q = bt.randn(bt.T, Hq, 128)
+        need = max(need, vc.vc_paged_attn_h2o_workspace_bytes(cache, bt.T, Hq))
+        jobs.append((bt, cache, q, torch.empty_like(q), torch.zeros(bt.B, 2, cache.slots, device="cuda")))
+    ws = vc.Workspace(need)
+    graphs = []
+    for bt, cache, q, out, scores in jobs:
+        _attn(vc, bt, q, 0.1, True, scores.clone(), cache, ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], capture_error_mode="thread_local"):
+            vc.vc_paged_attn_h2o(q, cache, bt.q_start, bt.ctx, 0.1, out, scores, ws)
+    for _ in range(2):
+        for (bt, cache, q, out, scores), g in zip(jobs, graphs):
+            out.fill_(7.0), scores.zero_()
+            g.replay()
+    torch.cuda.synchronize()
+    for bt, cache, q, out, scores in jobs:
+        mass, mtol = _compare(bt, q, out, 0.1)
+        close(scores, mass, mtol, "scores")
+    assert vc.vc_poll_status(ws) == 0
+
+
+def test_sixteen_byte_alignment_is_enough():
+    vc = lib()
+    bt = Batch([9, 2], [300, 77], 2, 64, 16, BF, seed=6)
+
+    def shifted(t):
+        x = torch.zeros(t.numel() + 8, dtype=t.dtype, device="cuda")[8:].view(t.shape)
+        return x.copy_(t)
+    q = shifted(bt.randn(bt.T, 4, 64))
+    bt.k, bt.v = shifted(bt.k), shifted(bt.v)
+    scores = torch.zeros(bt.B, 2, bt.width * 16, device="cuda")
+    out = _attn(vc, bt, q, 0.2, True, scores, out=shifted(torch.full_like(q, 7.0)))
+    mass, mtol = _compare(bt, q, out, 0.2)
+    close(scores, mass, mtol, "scores")
+    bt = Batch([9, 2], [300, 77], 2, 64, 16, BF, seed=6)
+    qkv, qo = shifted(bt.randn(bt.T, 8 * 64)), shifted(torch.zeros(bt.T, 4, 64, dtype=BF, device="cuda"))
+    vc.vc_paged_append(qkv, _cache(vc, bt), bt.q_start, bt.ctx, qo, vc.vc_rope_init(64, 1e4))
+    y, _, tol = paged_ref.append(bt, qkv, 4, [1e4 ** (-j / 32) for j in range(32)],
+                                 [c + i for n, c in zip(bt.ns, bt.cs) for i in range(n)], None, None, 0.0)
+    close(qo, y[:, :4], tol[:, :4], "q")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_pools_past_two_to_the_31_elements(dtype):
+    """Pages whose elements lie past 2^31: every operator gives what it gives
+    on a small pool, bit for bit."""
+    vc = lib()
+    Hkv, page, d = 8, 256, 128
+    small = Batch([3, 1], [600, 255], Hkv, d, page, dtype, seed=7, width=4)
+    n_big = 2 ** 31 // (Hkv * page * d) + 20
+    shift = n_big - small.n_pages
+    big_k = torch.empty(n_big, Hkv, page, d, dtype=dtype, device="cuda")
+    big_v = torch.empty_like(big_k)
+    big_k[shift:], big_v[shift:] = small.k, small.v
+    table = torch.where(small.block_table >= 0, small.block_table + shift, small.block_table)
+    q = small.randn(small.T, 16, d)
+    qkv = small.randn(small.T, (16 + 2 * Hkv) * d)
+    rope = vc.vc_rope_init(d, 1e4)
+    got = []
+    for k, v, tab in ((small.k, small.v, small.block_table), (big_k, big_v, table)):
+        cache = vc.PagedCache(k, v, tab)
+        ws = vc.Workspace(vc.vc_paged_attn_h2o_workspace_bytes(cache, small.T, 16))
+        out, qo = torch.empty_like(q), torch.empty_like(q)
+        scores = torch.zeros(2, Hkv, cache.slots, device="cuda")
+        vc.vc_paged_append(qkv, cache, small.q_start, small.ctx, qo, rope)
+        vc.vc_paged_attn_h2o(q, cache, small.q_start, small.ctx, 0.1, out, scores, ws)
+        # eviction into two pages that no table names
+        spare = [p for p in range(small.n_pages) if not (small.block_table == p).any()][:2]
+        off = 0 if k is small.k else shift
+        dst = vc.PagedCache(k, v, torch.tensor([[spare[0] + off], [spare[1] + off]], dtype=torch.int32, device="cuda"))
+        n, kept = torch.zeros(2, dtype=torch.int32, device="cuda"), torch.zeros(2, Hkv, 90, dtype=torch.int32,
+                                                                                device="cuda")
+        vc.vc_paged_evict(scores, cache, (small.ctx + torch.tensor([3, 1], device="cuda")).int(), 70, 20, dst, n, kept)
+        torch.cuda.synchronize()
+        assert int(cache.status) == int(dst.status) == 0 and vc.vc_poll_status(ws) == 0
+        rows = k[dst.block_table[:, 0].long(), :, :90]
+        got.append((out, qo, scores, n, kept, rows.clone(), v[dst.block_table[:, 0].long(), :, :90].clone()))
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+
+
 def test_two_calls_at_once_on_two_streams():
     vc = lib()
     jobs = []
