@@ -134,23 +134,22 @@ __host__ __device__ inline long piece_len(long total, int n_cta, int min_len)
 template <int BM, int BN>
 struct Units : Cost<BM> {
     using Cost<BM>::kUnitCost;
+    // 32-bit arithmetic: a sequence has at most 2^30 rows
     static __host__ __device__ __forceinline__ int tiles(const Seq &s, int G, int mt)
     {
-        const long last = lmin((long)s.n * G, (long)(mt + 1) * BM) - 1;    // last row of the tile
-        return (s.ctx + (int)(last / G) + 1 + BN - 1) / BN;
+        const unsigned rows = (unsigned)s.n * G, end = ((unsigned)mt + 1) * BM;
+        const unsigned last = (rows < end ? rows : end) - 1;              // last row of the tile
+        return (int)((s.ctx + last / (unsigned)G + 1 + BN - 1) / BN);
     }
     static __host__ __device__ __forceinline__ int weight(const Seq &s, int G, int mt)
     {
-        return BM == 256 && (long)s.n * G - (long)mt * BM > BM / 2 ? 2 : 1;
+        return BM == 256 && s.n * G - mt * BM > BM / 2 ? 2 : 1;
     }
     static __host__ __device__ __forceinline__ int cost(const Seq &s, int G, int mt)
     {
         return tiles(s, G, mt) * weight(s, G, mt) + kUnitCost;
     }
-    static __host__ __device__ __forceinline__ int mtiles(const Seq &s, int G)
-    {
-        return (int)(((long)s.n * G + BM - 1) / BM);
-    }
+    static __host__ __device__ __forceinline__ int mtiles(const Seq &s, int G) { return (s.n * G + BM - 1) / BM; }
     static __host__ __device__ __forceinline__ long head_cost(const Seq &s, int G)
     {
         long c = 0;

@@ -345,13 +345,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 const int c = r % CH, q0 = r / CH;
                 uint8_t *sQ = sm + G::SM_Q + (big ? t * G::TILE : 0);
                 const int lo = big ? 0 : t * 64, cnt = big ? 128 : 64, base = big ? t * 128 : 0;
-#pragma unroll 4
-                for (int i = q0; i < cnt; i += RP) {
-                    const int rr = lo + i;
-                    uint4 x = make_uint4(0, 0, 0, 0);
-                    if (base + rr < it.rows)
-                        x = *reinterpret_cast<const uint4 *>(A.q + out_row(base + rr) * D + c * 8);
-                    *reinterpret_cast<uint4 *>(sQ + (c >> 3) * (BN * 128) + rr * 128 + (((c & 7) ^ (rr & 7)) << 4)) = x;
+#pragma unroll 1
+                for (int i0 = q0; i0 < cnt; i0 += 8 * RP) {
+                    uint4 x[8];                              // eight loads in flight
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = lo + i0 + e * RP;
+                        x[e] = make_uint4(0, 0, 0, 0);
+                        if (i0 + e * RP < cnt && base + rr < it.rows)
+                            x[e] = *reinterpret_cast<const uint4 *>(A.q + out_row(base + rr) * D + c * 8);
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int rr = lo + i0 + e * RP;
+                        if (i0 + e * RP < cnt)
+                            *reinterpret_cast<uint4 *>(sQ + (c >> 3) * (BN * 128) + rr * 128 +
+                                                       (((c & 7) ^ (rr & 7)) << 4)) = x[e];
+                    }
                 }
                 fence_async_smem();
                 tc::fence_before();
