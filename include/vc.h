@@ -836,7 +836,8 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
  * 0 .. ctx_len[b] + i, query head hq reading kv head hq / (Hq / Hkv).
  * q, out: device [T][Hq][d] in cache->dt, 16-byte aligned.  bf16 caches run on
  * the tensor cores (fp32 accumulation, the softmax weights rounded to bf16),
- * fp32 caches on the CUDA cores in fp32.  sm_scale: finite, not negative.
+ * fp32 caches on the CUDA cores in fp32.  sm_scale: finite, not negative, at
+ * most 1e8; products q . k lie within +-1e30.
  * The order of a row's sums, and so its last bits, depends on the lengths of
  * the whole batch (unlike vc_decoder_forward's).
  */

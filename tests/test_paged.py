@@ -109,6 +109,15 @@ def test_rope_tables(vc):
     assert got.turn[0] == 0 and got.turn[1] == 3 << 62 and got.rotary_dim == 16
 
 
+def test_a_scale_past_the_range_is_refused(vc):
+    L = vc.load()
+    c = _cache(vc)
+    for scale, want in ((1.01e8, 2), (3e38, 2)):
+        assert L.vc_paged_attn(A, c, A, A, 4, 4, scale, A + 4096, A, BIG, None) == want
+        assert L.vc_paged_attn_h2o(A, c, A, A, 4, 4, scale, A + 4096, A, 256, A, BIG, None) == want
+    assert L.vc_paged_attn(A, c, A, A, 0, 4, 1e8, A + 4096, A, BIG, None) == 0
+
+
 def test_the_binding_refuses(vc):
     k = torch.zeros(4, 2, 16, 64)
     tab = torch.zeros(1, 2, dtype=torch.int32)
