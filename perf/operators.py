@@ -287,7 +287,10 @@ def _evict(s):
     c = s["case"]
     if own:
         from lossless_draft_verify_gb300 import vc
-        vc.vc_paged_evict(s["scores"], s["cache"], s["ctx"], c["top"], c["recent"], s["cache2"], s["len2"], s["kept"],
+        # no more than the longest sequence has: what the outputs have room for
+        recent = min(c["recent"], s["max_len"])
+        top = min(c["top"], s["max_len"] - recent)
+        vc.vc_paged_evict(s["scores"], s["cache"], s["ctx"], top, recent, s["cache2"], s["len2"], s["kept"],
                           scores_out=s["scores2"])
         return s["kept"], s["len2"], s["k2"], s["v2"], s["scores2"]
     B, Hkv, page, most = c["B"], c["Hkv"], c["page"], s["most"]
