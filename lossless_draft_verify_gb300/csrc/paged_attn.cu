@@ -74,17 +74,24 @@ sum_kernel(Pool P, WorkDim W, const float *__restrict__ s_in, long s_stride, con
     if (s.n == 0 || j >= len) return;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     // rows before the first that sees slot j contribute nothing
-    const long first = lmax(j - s.ctx, 0) * W.G, rows = (long)s.n * W.G;
+    int i = max(j - s.ctx, 0), g = 0;
+    size_t row = (size_t)(s.tok0 + i) * Hq + h * W.G;
+    const int left = (s.n - i) * W.G;
 #pragma unroll 4
-    for (long r = first; r < rows; ++r) {
-        const size_t row = (size_t)(s.tok0 + r / W.G) * Hq + h * W.G + r % W.G;
+    for (int r = 0; r < left; ++r) {
         const float4 x = *reinterpret_cast<const float4 *>(s_in + row * s_stride + j);
         const float e = lse[row];
-        const int last = s.ctx + (int)(r / W.G) - j;       // slots up to j + last are seen
+        const int last = s.ctx + i - j;                    // slots up to j + last are seen
         sum[0] += ex2(x.x - e);
         if (last >= 1) sum[1] += ex2(x.y - e);
         if (last >= 2) sum[2] += ex2(x.z - e);
         if (last >= 3) sum[3] += ex2(x.w - e);
+        ++row;
+        if (++g == W.G) {
+            g = 0;
+            ++i;
+            row += Hq - W.G;
+        }
     }
     float *dst = scores + (size_t)u * scores_stride + j;
 #pragma unroll

@@ -11,13 +11,17 @@
 // sequence's row tiles pass (a row tile is floor(128 / G) queries of the G
 // heads, one TMA box), so K is read from HBM once and a row tile from L2 once
 // per 512 keys.  With one row tile (decoding) this is a stream of K, bound by
-// HBM; with many the sums' arithmetic is the bound.  Groups of two or one tile,
-// for a finer division, cost more than they give (471 and 656 us against 404
-// and 583): each row tile is then on its way for fewer products.
+// HBM; with many by the sums' arithmetic and waits: 150 us after the 222 of the
+// attention for two 512-token chunks over 16000 tokens, 32/8 heads, the
+// tensor cores busy a third of it.  Shares are counted in key tiles, not groups:
+// a prompt of 2048 over 8000 tokens 462 us with its attention against 528, eight
+// of 512 109 against 124, four chunks of 300 over 4000 tokens 258 against 237.
+// Groups of two or one tile at most cost more than they give (471 and 656 us
+// against 404 and 583 before), and so do accumulators in two halves, the second
+// product under the first one's sums (414 against 370).
 //   warps 0-15      sums, four warps to a key tile of the group and to one of
 //                   four accumulators (two sets of four, each with every other
-//                   tile: 454 against 404 us for two 512-token chunks over
-//                   16000 tokens with their attention);
+//                   tile: 454 against 404 us, before, for the two chunks above);
 //   warp 16         producer; warp 17 issues the MMAs.
 #include "paged.cuh"
 #include "tcgen05.cuh"
@@ -43,14 +47,14 @@ struct Geom {
     static constexpr int SMEM = SM_X + 16 * 512 + 1024;
 };
 
-// A CTA's share: groups, in the order sequence, head, group, each with the
-// cost 4 row tiles + 1; a group belongs to the CTA in whose part of the total
-// it begins.
+// A CTA's share: key tiles, in the order sequence, head, tile, each with the
+// cost 4 row tiles + 1; a tile belongs to the CTA in whose part of the total it
+// begins.  The tiles of a head in a share are taken in groups of like size.
 struct MassWalk {
-    int b, h, g;                 // next group
-    int groups, mt, rt;          // of the sequence: key groups, row tiles, rows per row tile
+    int b, h, t;                 // next key tile
+    int nt, mt, rt;              // of the sequence: key tiles, row tiles, rows per row tile
     Seq s;
-    long at, end;                // cost at the next group's beginning, end of the share
+    long at, end;                // cost at the next tile's beginning, end of the share
 
     static __device__ __forceinline__ long cost(int mt) { return 4l * mt + 1; }
     __device__ __forceinline__ void shape(const Pool &P, const WorkDim &W, int b_)
@@ -58,15 +62,15 @@ struct MassWalk {
         b = b_;
         s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
         rt = BN / W.G * W.G;
-        mt = (int)(((long)s.n * W.G + rt - 1) / rt);
-        groups = mt > 0 ? (s.ctx + s.n + BN * kGroup - 1) / (BN * kGroup) : 0;
+        mt = (s.n * W.G + rt - 1) / rt;
+        nt = mt > 0 ? (s.ctx + s.n + BN - 1) / BN : 0;
     }
 };
 
 struct MassItem {
     int b, h, key0, tiles;       // key tiles of the group
     int tok0, ctx, len, mt0, mt; // row tiles mt0 .. mt - 1 see the group
-    long rows;
+    int rows;
 };
 
 struct Shared {
@@ -95,7 +99,7 @@ __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, 
         long c = 0;
         if (b0 + lane < A.P.B) {
             w.shape(A.P, A.W, b0 + lane);
-            c = (long)w.groups * A.P.Hkv * MassWalk::cost(w.mt);
+            c = (long)w.nt * A.P.Hkv * MassWalk::cost(w.mt);
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
@@ -110,7 +114,7 @@ __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, 
         long c = 0;
         if (b0 + lane < A.P.B) {
             w.shape(A.P, A.W, b0 + lane);
-            c = (long)w.groups * A.P.Hkv * MassWalk::cost(w.mt);
+            c = (long)w.nt * A.P.Hkv * MassWalk::cost(w.mt);
         }
         long incl = c;
 #pragma unroll
@@ -120,10 +124,10 @@ __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, 
         }
         const long start = before + incl - c;
         if (c > 0 && start <= lo && lo < start + c) {
-            // the first group that begins at lo or later (it may be the next sequence's first)
+            // the first tile that begins at lo or later (it may be the next sequence's first)
             const long cg = MassWalk::cost(w.mt), x = (lo - start + cg - 1) / cg;
-            w.h = (int)(x / w.groups);
-            w.g = (int)(x % w.groups);
+            w.h = (int)(x / w.nt);
+            w.t = (int)(x % w.nt);
             w.at = start + x * cg;
             w.end = hi;
             *out = w;
@@ -135,28 +139,30 @@ __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, 
 __device__ __forceinline__ bool next_group(MassWalk &w, const Params &A, MassItem &it)
 {
     while (w.at < w.end) {
-        if (w.g >= w.groups) {
-            w.g = 0;
+        if (w.t >= w.nt) {
+            w.t = 0;
             ++w.h;
         }
-        if (w.groups == 0 || w.h >= A.P.Hkv) {
+        if (w.nt == 0 || w.h >= A.P.Hkv) {
             if (w.b + 1 >= A.P.B) return false;
             w.shape(A.P, A.W, w.b + 1);
-            w.h = w.g = 0;
+            w.h = w.t = 0;
             continue;
         }
         it.b = w.b;
         it.h = w.h;
-        it.key0 = w.g * BN * kGroup;
+        it.key0 = w.t * BN;
         it.tok0 = w.s.tok0;
         it.ctx = w.s.ctx;
         it.len = w.s.ctx + w.s.n;
-        it.tiles = min(kGroup, (it.len - it.key0 + BN - 1) / BN);
-        it.rows = (long)w.s.n * A.W.G;
+        const long c = MassWalk::cost(w.mt);
+        const int left = (int)lmin(w.nt - w.t, (w.end - w.at + c - 1) / c);
+        it.tiles = cdiv(left, cdiv(left, kGroup));
+        it.rows = w.s.n * A.W.G;
         it.mt0 = (int)(lmax(it.key0 - w.s.ctx, 0) * A.W.G / w.rt);
         it.mt = w.mt;
-        w.at += MassWalk::cost(w.mt);
-        ++w.g;
+        w.at += it.tiles * c;
+        w.t += it.tiles;
         return true;
     }
     return false;
@@ -169,7 +175,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     using G = Geom<D>;
     constexpr int NST = G::STAGES;
     extern __shared__ __align__(1024) uint8_t sm[];
-    float *s_lse = reinterpret_cast<float *>(sm + G::SM_X);  // [16 warps][128]
+    float *s_lse = reinterpret_cast<float *>(sm + G::SM_X);  // [16 warps][128]: -lse
     Shared *S = reinterpret_cast<Shared *>(sm + G::SM_X + 16 * 512);
     static_assert(sizeof(Shared) <= 1024, "shared block");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -279,7 +285,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             for (int q = it.mt0; q < it.mt && ok; ++q) {
                 ok = wait_warp(&S->q_full[qr.slot], qr.phase, A.status, 113);
                 if (!ok) break;
-                const int cols = (int)lmin(rt, it.rows - (long)q * rt);
+                const int cols = min(rt, it.rows - q * rt);
                 const uint32_t id = tc::idesc_bf16(BN, (cols + 15) / 16 * 16, false, false);
                 const uint32_t bq = q_lo + qr.slot * (G::TILE >> 4);
                 kr = k0;
@@ -315,27 +321,30 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         float *my_lse = s_lse + warp * BN;
         uint32_t used = 0;
         bool ok = true;
+        int off[4];                                          // lse of the lane's rows in a row tile
+#pragma unroll
+        for (int x = 0; x < 4; ++x) off[x] = (lane + 32 * x) / A.W.G * A.Hq + (lane + 32 * x) % A.W.G;
         while (ok && next_group(walk, A, it)) {
             if (k >= it.tiles) continue;
             const int tile0 = it.key0 + k * BN, key = tile0 + wq * 32 + lane;
             float sum = 0.f;
             // lse of a row tile, four rows per lane, on its way a tile ahead
             float next[4];
+            const float *lse = A.lse + (size_t)it.tok0 * A.Hq + it.h * A.W.G;
             auto fetch = [&](int q) {
+                const float *p = lse + (size_t)q * (rt / A.W.G) * A.Hq;
 #pragma unroll
                 for (int x = 0; x < 4; ++x) {
                     const int c = lane + 32 * x;
-                    const long R = (long)q * rt + c;
-                    next[x] = c < rt && R < it.rows
-                                  ? A.lse[(size_t)(it.tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G] : 0.f;
+                    next[x] = c < rt && q * rt + c < it.rows ? p[off[x]] : 0.f;
                 }
             };
             fetch(it.mt0);
             for (int q = it.mt0; q < it.mt && ok; ++q) {
-                const int cols = (int)lmin(rt, it.rows - (long)q * rt);
+                const int cols = min(rt, it.rows - q * rt);
                 __syncwarp();
 #pragma unroll
-                for (int x = 0; x < 4; ++x) my_lse[lane + 32 * x] = next[x];
+                for (int x = 0; x < 4; ++x) my_lse[lane + 32 * x] = -next[x];
                 __syncwarp();
                 if (q + 1 < it.mt) fetch(q + 1);
                 ok = wait_warp(&S->s_full[k], used & 1, A.status, 116);
@@ -343,8 +352,8 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 if (!ok) break;
                 tc::fence_after();
                 // columns [lo, cols) see the key; [lo_all, cols) every key of the tile
-                const int lo = (int)lmin(lmax((long)(key - it.ctx) * A.W.G - (long)q * rt, 0), BN);
-                const int lo_all = (int)lmin(lmax((long)(tile0 + BN - 1 - it.ctx) * A.W.G - (long)q * rt, 0), BN);
+                const int lo = min(max(max(key - it.ctx, 0) * A.W.G - q * rt, 0), BN);
+                const int lo_all = min(max(max(tile0 + BN - 1 - it.ctx, 0) * A.W.G - q * rt, 0), BN);
                 float2 acc[2] = {{0.f, 0.f}, {0.f, 0.f}};
                 const float2 sc = make_float2(A.sl2, A.sl2);
                 const uint32_t tS = tmem + lanes + k * BN;
@@ -358,9 +367,9 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         for (int c = 0; c < 32; c += 4) {
                             const float4 e = *reinterpret_cast<const float4 *>(my_lse + c0 + c);
                             const float2 x = fma2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc,
-                                                  make_float2(-e.x, -e.y));
+                                                  make_float2(e.x, e.y));
                             const float2 y = fma2(make_float2(__uint_as_float(v[c + 2]), __uint_as_float(v[c + 3])),
-                                                  sc, make_float2(-e.z, -e.w));
+                                                  sc, make_float2(e.z, e.w));
                             acc[0] = add2(acc[0], make_float2(ex2(x.x), ex2(x.y)));
                             acc[1] = add2(acc[1], make_float2(ex2(y.x), ex2(y.y)));
                         }
@@ -368,7 +377,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         // columns past the rows hold whatever was there: chosen, not multiplied away
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
-                            const float p = ex2(fmaf(__uint_as_float(v[c]), A.sl2, -my_lse[c0 + c]));
+                            const float p = ex2(fmaf(__uint_as_float(v[c]), A.sl2, my_lse[c0 + c]));
                             if (c0 + c >= lo && c0 + c < cols) acc[0].x += p;
                         }
                         __syncwarp();
