@@ -785,6 +785,10 @@ class PagedCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.c = PagedCacheC(k.data_ptr(), v.data_ptr(), block_table.data_ptr(), self.status.data_ptr(), self.B,
                              self.Hkv, self.d, self.page, self.n_pages, self.max_blocks, _dt(k))
+        # what every call needs, made once (a call's checks are most of its host time)
+        self.ref = ctypes.byref(self.c)
+        self._index = self.device.index if self.device.type == "cuda" else None
+        self._starts, self._lens, self._units = torch.Size((self.B + 1,)), torch.Size((self.B,)), (self.B, self.Hkv)
 
     @property
     def slots(self) -> int:
@@ -793,20 +797,25 @@ class PagedCache:
 
     def _check(self, *tensors):
         """Contiguous tensors on the pool's device, which is the current one."""
-        if self.device.type == "cuda" and self.device.index != torch.cuda.current_device():
+        if self._index is not None and self._index != torch._C._cuda_getDevice():
             raise ValueError(f"the pool is on {self.device}, the current device is {torch.cuda.current_device()}")
+        device = self.device
         for t in tensors:
-            if t is not None and (t.device != self.device or not t.is_contiguous()):
+            if t is not None and (t.device != device or not t.is_contiguous()):
                 raise ValueError("tensors must be contiguous and on the pool's device")
 
     def _on_gpu(self):
-        if self.device.type != "cuda":
+        if self._index is None:
             raise ValueError(f"the pool is on {self.device}, not on a GPU")
+
+    def _stream(self, stream) -> int:
+        """The stream's handle, or that of the pool's device's current one."""
+        return torch._C._cuda_getCurrentRawStream(self._index) if stream is None else stream.cuda_stream
 
     def _check_batch(self, q_start, ctx_len):
         if q_start.dtype != torch.int32 or ctx_len.dtype != torch.int32:
             raise TypeError("q_start and ctx_len are int32")
-        if q_start.shape != (self.B + 1,) or ctx_len.shape != (self.B,):
+        if q_start.shape != self._starts or ctx_len.shape != self._lens:
             raise ValueError(f"q_start [{self.B + 1}] and ctx_len [{self.B}] expected")
 
 
@@ -831,37 +840,40 @@ def vc_paged_append(qkv, cache: PagedCache, q_start, ctx_len, q_out, rope: Rope,
     per-head RMS norm (q_gain, k_gain [d]; both or neither) and rotation at
     positions int32 [T] (None: the tokens' slots)."""
     T, Hq, d = q_out.shape
+    dtype = cache.dtype
     cache._check(qkv, q_start, ctx_len, q_out, positions, q_gain, k_gain)
     cache._check_batch(q_start, ctx_len)
     if d != cache.d or qkv.numel() != T * (Hq + 2 * cache.Hkv) * d:
         raise ValueError(f"qkv {tuple(qkv.shape)} and q_out {tuple(q_out.shape)} do not fit {cache.Hkv} kv heads")
-    for t, n in ((qkv, None), (q_out, None), (q_gain, d), (k_gain, d)):
-        if t is not None and (t.dtype != cache.dtype or (n is not None and t.numel() != n)):
-            raise TypeError("qkv, q_out and the gains have the cache's dtype, the gains d entries")
+    if (qkv.dtype != dtype or q_out.dtype != dtype
+            or (q_gain is not None and (q_gain.dtype != dtype or q_gain.numel() != d))
+            or (k_gain is not None and (k_gain.dtype != dtype or k_gain.numel() != d))):
+        raise TypeError("qkv, q_out and the gains have the cache's dtype, the gains d entries")
     if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
         raise TypeError("positions is int32 [T]")
     cache._on_gpu()
     _check(load().vc_paged_append(qkv.data_ptr(), _ptr(q_gain), _ptr(k_gain), float(eps), ctypes.byref(rope),
-                                  _ptr(positions), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
-                                  ctypes.byref(cache.c), q_out.data_ptr(), _stream(stream)), "vc_paged_append")
+                                  _ptr(positions), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq, cache.ref,
+                                  q_out.data_ptr(), cache._stream(stream)), "vc_paged_append")
 
 
 def vc_paged_attn_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
-    return int(load().vc_paged_attn_workspace_bytes(ctypes.byref(cache.c), T, Hq))
+    return int(load().vc_paged_attn_workspace_bytes(cache.ref, T, Hq))
 
 
 def vc_paged_attn_h2o_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
-    return int(load().vc_paged_attn_h2o_workspace_bytes(ctypes.byref(cache.c), T, Hq))
+    return int(load().vc_paged_attn_h2o_workspace_bytes(cache.ref, T, Hq))
 
 
 def _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores=None):
     cache._check(q, q_start, ctx_len, out, ws.buf, scores)
     cache._check_batch(q_start, ctx_len)
-    if q.dim() != 3 or q.shape != out.shape or q.shape[2] != cache.d:
+    shape = q.shape
+    if len(shape) != 3 or shape != out.shape or shape[2] != cache.d:
         raise ValueError(f"q and out [T][Hq][{cache.d}] expected")
     if q.dtype != cache.dtype or out.dtype != cache.dtype:
         raise TypeError("q and out have the cache's dtype")
-    return q.shape[0], q.shape[1]
+    return shape[0], shape[1]
 
 
 def vc_paged_attn(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, ws: Workspace, stream=None):
@@ -869,8 +881,8 @@ def vc_paged_attn(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, 
     q_start int32 [B + 1], ctx_len int32 [B]."""
     T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws)
     cache._on_gpu()
-    _check(load().vc_paged_attn(q.data_ptr(), ctypes.byref(cache.c), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
-                                float(sm_scale), out.data_ptr(), ws.ptr, ws.nbytes, _stream(stream)),
+    _check(load().vc_paged_attn(q.data_ptr(), cache.ref, q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
+                                float(sm_scale), out.data_ptr(), ws.ptr, ws.nbytes, cache._stream(stream)),
            "vc_paged_attn")
 
 
@@ -879,12 +891,12 @@ def vc_paged_attn_h2o(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, o
     """vc_paged_attn that adds every cached token's attention weight to scores
     fp32 [B][Hkv][S], S >= the cache's slots."""
     T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores)
-    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (cache.B, cache.Hkv):
+    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != cache._units:
         raise ValueError(f"scores is fp32 [{cache.B}][{cache.Hkv}][slots]")
     cache._on_gpu()
-    _check(load().vc_paged_attn_h2o(q.data_ptr(), ctypes.byref(cache.c), q_start.data_ptr(), ctx_len.data_ptr(), T,
+    _check(load().vc_paged_attn_h2o(q.data_ptr(), cache.ref, q_start.data_ptr(), ctx_len.data_ptr(), T,
                                     Hq, float(sm_scale), out.data_ptr(), scores.data_ptr(), scores.shape[2], ws.ptr,
-                                    ws.nbytes, _stream(stream)), "vc_paged_attn_h2o")
+                                    ws.nbytes, cache._stream(stream)), "vc_paged_attn_h2o")
 
 
 def vc_paged_evict(scores, src: PagedCache, src_len, keep_top: int, keep_recent: int, dst: PagedCache, dst_len,
@@ -893,16 +905,16 @@ def vc_paged_evict(scores, src: PagedCache, src_len, keep_top: int, keep_recent:
     (sequence, kv head) of src, into dst's pages: scores fp32 [B][Hkv][S],
     kept_idx int32 [B][Hkv][n], scores_out fp32 [B][Hkv][n] or None."""
     src._check(scores, src_len, dst.k, dst_len, kept_idx, scores_out)
-    for t, dt, shape in ((scores, torch.float32, (src.B, src.Hkv)), (kept_idx, torch.int32, (src.B, src.Hkv)),
-                         (scores_out, torch.float32, (src.B, src.Hkv))):
-        if t is not None and (t.dtype != dt or t.dim() != 3 or t.shape[:2] != shape):
+    units = src._units
+    for t, dt in ((scores, torch.float32), (kept_idx, torch.int32), (scores_out, torch.float32)):
+        if t is not None and (t.dtype != dt or t.dim() != 3 or t.shape[:2] != units):
             raise ValueError(f"scores, kept_idx and scores_out are [{src.B}][{src.Hkv}][..], fp32, int32 and fp32")
     for t in (src_len, dst_len):
-        if t.dtype != torch.int32 or t.shape != (src.B,):
+        if t.dtype != torch.int32 or t.shape != src._lens:
             raise ValueError(f"src_len and dst_len are int32 [{src.B}]")
     src._on_gpu()
-    _check(load().vc_paged_evict(scores.data_ptr(), scores.shape[2], ctypes.byref(src.c), src_len.data_ptr(),
-                                 DropCfg(int(keep_top), int(keep_recent)), ctypes.byref(dst.c), dst_len.data_ptr(),
+    _check(load().vc_paged_evict(scores.data_ptr(), scores.shape[2], src.ref, src_len.data_ptr(),
+                                 DropCfg(int(keep_top), int(keep_recent)), dst.ref, dst_len.data_ptr(),
                                  kept_idx.data_ptr(), kept_idx.shape[2], _ptr(scores_out),
-                                 scores_out.shape[2] if scores_out is not None else 0, _stream(stream)),
+                                 scores_out.shape[2] if scores_out is not None else 0, src._stream(stream)),
            "vc_paged_evict")
