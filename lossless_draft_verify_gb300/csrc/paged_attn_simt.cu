@@ -33,12 +33,32 @@ __device__ __forceinline__ void load_rows(float *dst, int pitch, int n_rows, F s
 template <int D, int BM, int BN>
 struct Geom {
     static constexpr int PQ = D + 4, PP = BN + 4;      // pitches: rows 4 banks apart
-    static constexpr int SMEM = (BM * PQ + BN * PQ + BN * D + BM * PP) * 4;
+    static constexpr int STAGE = BN * PQ + BN * D;     // a key tile's K and V
+    static constexpr int SMEM = (BM * PQ + 2 * STAGE + BM * PP) * 4;
 };
+
+// 16 bytes to shared memory, zeros where !on (src is then not read)
+__device__ __forceinline__ void copy16(float *dst, const float *src, bool on)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+                 :: "r"(smem_u32(dst)), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(float *dst, const float *src, bool on)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;"
+                 :: "r"(smem_u32(dst)), "l"(src), "r"(on ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
 // One CTA per piece of the batch's work (paged.cuh).  256 threads as 16 x 16:
 // thread (ty, tx) holds rows ty * RT .. + RT - 1 against keys tx + 16 j, and
-// the same rows' outputs at channels 4 tx + 64 j.
+// the same rows' outputs at channels 4 tx + 64 j.  Products are taken two
+// channels at a time (half the instructions).  Bound by shared memory's reads and
+// the instructions around them: four chunks of 300 over 2000 tokens, 16/4 heads
+// of 128, 572 us, 37 TFLOP/s (674 with one stage and single products, 821 and 725
+// with tiles of 64 keys or 8 rows per thread, for which fewer warps fit); a token of
+// 8 sequences over 4000, 32/8 heads, 159 us, 1.7 TB/s (252 with one stage).
 template <int D, int BM, int BN>
 __global__ void __launch_bounds__(kThreads)
 attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float scale_log2, float *__restrict__ out,
@@ -47,9 +67,8 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
     constexpr int RT = BM / 16, KT = BN / 16, CT = D / 64;
     using G = Geom<D, BM, BN>;
     extern __shared__ __align__(16) float smf[];
-    float *sQ = smf, *sK = sQ + BM * G::PQ, *sV = sK + BN * G::PQ, *sP = sV + BN * D;
+    float *sQ = smf, *sKV = sQ + BM * G::PQ, *sP = sKV + 2 * G::STAGE;
     __shared__ Piece piece;
-    __shared__ int s_page[BN / 16];
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x < 32) find_piece<BM, BN>(P, W, blockIdx.x, gridDim.x, &piece);
@@ -68,7 +87,8 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
         };
         __syncthreads();
         load_rows<D>(sQ, G::PQ, BM, [&](int r) { return r < it.rows ? q + token_row(r) : nullptr; });
-        float m[RT], l[RT], acc[RT][CT][4];
+        float m[RT], l[RT];
+        float2 acc[RT][CT][2];
         int kmax[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -77,28 +97,49 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
             const int r = ty * RT + i;
             kmax[i] = r < it.rows ? it.ctx + (row0 + r) / W.G : -1;
 #pragma unroll
-            for (int j = 0; j < CT; ++j) acc[i][j][0] = acc[i][j][1] = acc[i][j][2] = acc[i][j][3] = 0.f;
+            for (int j = 0; j < CT; ++j) acc[i][j][0] = acc[i][j][1] = make_float2(0.f, 0.f);
         }
+        // Key tiles pass through two stages: a tile is on its way while the one
+        // before it is computed with, its page numbers are read a tile earlier.
+        constexpr int CH = D / 4, RP = kThreads / CH, NR = BN / RP;
+        const int c4 = (int)threadIdx.x % CH * 4, r0 = threadIdx.x / CH;
+        int pages[NR];
+        auto look_up = [&](int t) {
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                const int slot = t * BN + r0 + x * RP;
+                pages[x] = t < it.t_hi && slot < len ? P.page_of(it.b, slot >> P.page_log2) : -1;
+            }
+        };
+        auto fetch = [&](int t) {
+            float *k = sKV + (t & 1) * G::STAGE, *v = k + BN * G::PQ;
+#pragma unroll
+            for (int x = 0; x < NR; ++x) {
+                const int r = r0 + x * RP, slot = t * BN + r;
+                const bool on = pages[x] >= 0;
+                const size_t at = on ? P.row(pages[x], it.h, slot & (P.page() - 1)) * D + c4 : 0;
+                copy16(k + r * G::PQ + c4, pk + at, on);
+                copy16(v + r * D + c4, pv + at, on);
+            }
+            copy_commit();
+        };
+        look_up(it.t_lo);
+        fetch(it.t_lo);
+        look_up(it.t_lo + 1);
         for (int t = it.t_lo; t < it.t_hi; ++t) {
             const int key0 = t * BN;
+            const float *sK = sKV + (t & 1) * G::STAGE, *sV = sK + BN * G::PQ;
+            copy_wait();
             __syncthreads();
-            if (threadIdx.x < BN / 16) {
-                const int slot = key0 + threadIdx.x * 16;
-                s_page[threadIdx.x] = slot < len ? P.page_of(it.b, slot >> P.page_log2) : -1;
+            if (t + 1 < it.t_hi) {
+                fetch(t + 1);
+                look_up(t + 2);
             }
-            __syncthreads();
-            auto slot_row = [&](const float *base, int r) -> const float * {
-                const int pg = s_page[r >> 4], slot = key0 + r;
-                return pg >= 0 && slot < len ? base + P.row(pg, it.h, slot & (P.page() - 1)) * D : nullptr;
-            };
-            load_rows<D>(sK, G::PQ, BN, [&](int r) { return slot_row(pk, r); });
-            load_rows<D>(sV, D, BN, [&](int r) { return slot_row(pv, r); });
-            __syncthreads();
-            float s[RT][KT];
+            float2 s2[RT][KT];                         // even and odd channels
 #pragma unroll
             for (int i = 0; i < RT; ++i)
 #pragma unroll
-                for (int j = 0; j < KT; ++j) s[i][j] = 0.f;
+                for (int j = 0; j < KT; ++j) s2[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
             for (int c = 0; c < D; c += 4) {
                 float4 a[RT], b[KT];
@@ -111,19 +152,17 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
                 for (int i = 0; i < RT; ++i)
 #pragma unroll
                     for (int j = 0; j < KT; ++j) {
-                        s[i][j] = fmaf(a[i].x, b[j].x, s[i][j]);
-                        s[i][j] = fmaf(a[i].y, b[j].y, s[i][j]);
-                        s[i][j] = fmaf(a[i].z, b[j].z, s[i][j]);
-                        s[i][j] = fmaf(a[i].w, b[j].w, s[i][j]);
+                        s2[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(b[j].x, b[j].y), s2[i][j]);
+                        s2[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(b[j].z, b[j].w), s2[i][j]);
                     }
             }
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
-                float mx = kNegBig;
+                float s[KT], mx = kNegBig;
 #pragma unroll
                 for (int j = 0; j < KT; ++j) {
-                    s[i][j] = key0 + tx + 16 * j <= kmax[i] ? s[i][j] * scale_log2 : -INFINITY;
-                    mx = fmaxf(mx, s[i][j]);
+                    s[j] = key0 + tx + 16 * j <= kmax[i] ? (s2[i][j].x + s2[i][j].y) * scale_log2 : -INFINITY;
+                    mx = fmaxf(mx, s[j]);
                 }
 #pragma unroll
                 for (int o = 1; o < 16; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
@@ -132,7 +171,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
                 float sum = 0.f;
 #pragma unroll
                 for (int j = 0; j < KT; ++j) {
-                    const float p = exp2f(s[i][j] - mn);
+                    const float p = exp2f(s[j] - mn);
                     sum += p;
                     sP[(ty * RT + i) * G::PP + tx + 16 * j] = p;
                 }
@@ -140,7 +179,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
 #pragma unroll
                 for (int j = 0; j < CT; ++j)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[i][j][e] *= alpha;
+                    for (int e = 0; e < 2; ++e) acc[i][j][e] = mul2(acc[i][j][e], make_float2(alpha, alpha));
             }
             __syncwarp();                              // a row's 16 threads are in one warp
 #pragma unroll 2
@@ -157,10 +196,8 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
 #pragma unroll
                         for (int i = 0; i < RT; ++i) {
                             const float w = kk == 0 ? p[i].x : kk == 1 ? p[i].y : kk == 2 ? p[i].z : p[i].w;
-                            acc[i][j][0] = fmaf(w, v.x, acc[i][j][0]);
-                            acc[i][j][1] = fmaf(w, v.y, acc[i][j][1]);
-                            acc[i][j][2] = fmaf(w, v.z, acc[i][j][2]);
-                            acc[i][j][3] = fmaf(w, v.w, acc[i][j][3]);
+                            acc[i][j][0] = fma2(make_float2(w, w), make_float2(v.x, v.y), acc[i][j][0]);
+                            acc[i][j][1] = fma2(make_float2(w, w), make_float2(v.z, v.w), acc[i][j][1]);
                         }
                     }
             }
@@ -177,14 +214,14 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
 #pragma unroll
                 for (int j = 0; j < CT; ++j)
                     *reinterpret_cast<float4 *>(o + 4 * tx + 64 * j) = make_float4(
-                        acc[i][j][0] * inv, acc[i][j][1] * inv, acc[i][j][2] * inv, acc[i][j][3] * inv);
+                        acc[i][j][0].x * inv, acc[i][j][0].y * inv, acc[i][j][1].x * inv, acc[i][j][1].y * inv);
                 if (lse_out && tx == 0) lse_out[token_row(r) / D] = m[i] + log2f(l[i]);
             } else {
                 const size_t pr = parts.row(blockIdx.x, it.head ? 1 : 0, r);
 #pragma unroll
                 for (int j = 0; j < CT; ++j)
                     *reinterpret_cast<float4 *>(parts.o + pr * D + 4 * tx + 64 * j) =
-                        make_float4(acc[i][j][0], acc[i][j][1], acc[i][j][2], acc[i][j][3]);
+                        make_float4(acc[i][j][0].x, acc[i][j][0].y, acc[i][j][1].x, acc[i][j][1].y);
                 if (tx == 0) parts.ml[pr] = make_float2(m[i], l[i]);
             }
         }
@@ -201,9 +238,10 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
 
 // Where the key tiles that the block table can hold are fewer than three per SM
 // and the sequences have this many rows on average, a cluster shares a tile's
-// rows.  16/4 heads of 128: one prompt of 900 211 against 783 us with one CTA per
-// tile, 8 prompts of 600 (320 tiles) 769 against 907, 4 chunks of 300 over 2000
-// tokens (576 tiles) 1260 against 1058.
+// rows.  16/4 heads of 128, with the attention, before the tiles had two stages:
+// one prompt of 900 211 against 783 us with one CTA per tile, 8 prompts of 600 (320
+// tiles) 769 against 907, 4 chunks of 300 over 2000 tokens (576 tiles) 1260 against
+// 1058.  With them 185, 635 and 875.
 constexpr long kSplitRows = 1024;
 
 // ----- attention mass ---------------------------------------------------------------
@@ -219,8 +257,8 @@ mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
 {
     constexpr int BM = 64, BN = 64, PQ = D + 4;
     extern __shared__ __align__(16) float smf[];
-    float *sQ = smf, *sK = sQ + BM * PQ, *sSum = sK + BN * PQ;      // sSum [16][BN]
-    __shared__ float s_lse[BM], s_tot[BN];
+    float *sQs = smf, *sK = sQs + 2 * BM * PQ, *sSum = sK + BN * PQ;      // sSum [16][BN]
+    __shared__ float s_lse[2][BM], s_tot[BN];
     __shared__ int s_page[BN / 16];
     pdl_wait();
     pdl_trigger();
@@ -246,22 +284,41 @@ mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
             const int rows = s.n * G;
             // rows before the first one that sees the tile's first key contribute nothing
             const int first = max(key0 - s.ctx, 0) * G / BM * BM;
-            for (int r0 = first + (int)blockIdx.z * BM; r0 < rows; r0 += Z * BM) {
+            // Row tiles pass through two stages, as the attention's key tiles do.
+            constexpr int CH = D / 4, RP = kThreads / CH;
+            const int c4 = (int)threadIdx.x % CH * 4, tr = threadIdx.x / CH;
+            const int di = RP / G, dg = RP - di * G;
+            auto fetch = [&](int r0, int stage) {
+                int i = (r0 + tr) / G, g = r0 + tr - i * G;
+#pragma unroll
+                for (int x = 0; x < BM / RP; ++x) {
+                    const int r = tr + x * RP;
+                    const bool on = r0 + r < rows;
+                    const size_t at = on ? ((size_t)(s.tok0 + i) * Hq + h * G + g) * D + c4 : 0;
+                    copy16(sQs + (stage * BM + r) * PQ + c4, q + at, on);
+                    i += di, g += dg;
+                    if (g >= G) g -= G, ++i;
+                }
+                if (threadIdx.x < BM) {
+                    const int R = r0 + threadIdx.x, t = R / G;
+                    const bool on = R < rows;
+                    copy4(&s_lse[stage][threadIdx.x],
+                          lse + (on ? (size_t)(s.tok0 + t) * Hq + h * G + (R - t * G) : 0), on);
+                }
+                copy_commit();
+            };
+            int stage = 0, r0 = first + (int)blockIdx.z * BM;
+            if (r0 < rows) fetch(r0, 0);
+            for (; r0 < rows; r0 += Z * BM, stage ^= 1) {
+                copy_wait();
                 __syncthreads();
-                auto token_row = [&](int r) {
-                    const int R = r0 + r, i = R / G;
-                    return (size_t)(s.tok0 + i) * Hq + h * G + (R - i * G);
-                };
-                load_rows<D>(sQ, PQ, BM,
-                                [&](int r) { return r0 + r < rows ? q + token_row(r) * D : nullptr; });
-                if (threadIdx.x < BM)
-                    s_lse[threadIdx.x] = r0 + threadIdx.x < rows ? lse[token_row(threadIdx.x)] : 0.f;
-                __syncthreads();
-                float a4[4][4];
+                if (r0 + Z * BM < rows) fetch(r0 + Z * BM, stage ^ 1);
+                const float *sQ = sQs + stage * BM * PQ;
+                float2 a4[4][4];                       // even and odd channels
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) a4[i][j] = 0.f;
+                    for (int j = 0; j < 4; ++j) a4[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
                 for (int c = 0; c < D; c += 4) {
                     float4 a[4], k4[4];
@@ -273,20 +330,19 @@ mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
                     for (int i = 0; i < 4; ++i)
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
-                            a4[i][j] = fmaf(a[i].x, k4[j].x, a4[i][j]);
-                            a4[i][j] = fmaf(a[i].y, k4[j].y, a4[i][j]);
-                            a4[i][j] = fmaf(a[i].z, k4[j].z, a4[i][j]);
-                            a4[i][j] = fmaf(a[i].w, k4[j].w, a4[i][j]);
+                            a4[i][j] = fma2(make_float2(a[i].x, a[i].y), make_float2(k4[j].x, k4[j].y), a4[i][j]);
+                            a4[i][j] = fma2(make_float2(a[i].z, a[i].w), make_float2(k4[j].z, k4[j].w), a4[i][j]);
                         }
                 }
+                int tok = (r0 + ty * 4) / G, g = r0 + ty * 4 - tok * G;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int R = r0 + ty * 4 + i;
-                    const int kmax = R < rows ? s.ctx + R / G : -1;
-                    const float e = s_lse[ty * 4 + i];
+                    const int kmax = r0 + ty * 4 + i < rows ? s.ctx + tok : -1;
+                    const float e = s_lse[stage][ty * 4 + i];
+                    if (++g == G) g = 0, ++tok;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (key0 + tx + 16 * j <= kmax) sum[j] += exp2f(a4[i][j] * scale_log2 - e);
+                        if (key0 + tx + 16 * j <= kmax) sum[j] += exp2f((a4[i][j].x + a4[i][j].y) * scale_log2 - e);
                 }
             }
             __syncthreads();
@@ -331,7 +387,7 @@ cudaError_t launch_mass(const Pool &P, const WorkDim &W, const void *q, int Hq, 
                         float *scores, int scores_stride, cudaStream_t st)
 {
     auto kern = mass_simt_kernel<D, Z>;
-    constexpr int smem = (2 * 64 * (D + 4) + 16 * 64) * 4;
+    constexpr int smem = (3 * 64 * (D + 4) + 16 * 64) * 4;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     // about six CTAs per SM over the units; a cluster strides over its unit's key tiles
@@ -363,7 +419,7 @@ cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int
 {
     const int n = simt_ctas();
     if (simt_rows(W.T, W.G, P.B) == 16)
-        return d == 128 ? launch_attn<128, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st)
+        return d == 128 ? launch_attn<128, 16, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)
                         : launch_attn<64, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st);
     return d == 128 ? launch_attn<128, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)
                     : launch_attn<64, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st);
