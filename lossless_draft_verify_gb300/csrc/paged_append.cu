@@ -20,11 +20,16 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T> struct Row8;      // 8 consecutive channels, in pairs
+template <typename T> struct Row8;      // 8 consecutive channels: as read, and in pairs
 template <> struct Row8<float> {
-    static __device__ __forceinline__ void load(const float *p, float2 (&x)[4])
+    uint4 a, b;
+    __device__ __forceinline__ void load(const float *p)
     {
-        const uint4 a = ldg_stream(p), b = ldg_stream(p + 4);
+        a = ldg_stream(p);
+        b = ldg_stream(p + 4);
+    }
+    __device__ __forceinline__ void get(float2 (&x)[4]) const
+    {
         x[0] = make_float2(__uint_as_float(a.x), __uint_as_float(a.y));
         x[1] = make_float2(__uint_as_float(a.z), __uint_as_float(a.w));
         x[2] = make_float2(__uint_as_float(b.x), __uint_as_float(b.y));
@@ -37,9 +42,10 @@ template <> struct Row8<float> {
     }
 };
 template <> struct Row8<__nv_bfloat16> {
-    static __device__ __forceinline__ void load(const __nv_bfloat16 *p, float2 (&x)[4])
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = ldg_stream(p); }
+    __device__ __forceinline__ void get(float2 (&x)[4]) const
     {
-        const uint4 a = ldg_stream(p);
         const uint32_t w[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) x[i] = make_float2(bf16_lo(w[i]), bf16_hi(w[i]));
@@ -76,10 +82,11 @@ struct AppendParams {
 };
 
 // TPB tokens per CTA; blockIdx.y takes its share of the heads.  A lane group
-// has NB heads in flight, the first ones already while the tokens' sequences,
-// pages and angles are looked up (a second head in flight per group lowers the
-// occupancy: 30.2 against 23.7 us at 4670 tokens).
-template <typename E, int D, int TPB, int NB>
+// keeps its next head in flight, as read: the first one while the tokens'
+// sequences, pages and angles are looked up, each other one under the arithmetic
+// of the one before (22.9 us at 4670 tokens when it is read after it, 20.2 and
+// 21.5 with two and three in flight).
+template <typename E, int D, int TPB>
 __global__ void __launch_bounds__(kThreads, 4)
 append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
 {
@@ -98,19 +105,16 @@ append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
     const bool rot = l < rl;
     const int c0 = 8 * (rot ? l : 2 * rl + 2 * (l - rl)), c1 = rot ? c0 + half : c0 + 8;
     const E *qkv = (const E *)A.qkv + (size_t)t0 * heads * D;
-    float2 x0[NB][4] = {}, x1[NB][4] = {};
-    auto load = [&](int i0) {
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const int i = i0 + n * gridDim.y * GROUPS + g;
-            if (i < items) {
-                Row8<E>::load(qkv + (size_t)i * D + c0, x0[n]);
-                Row8<E>::load(qkv + (size_t)i * D + c1, x1[n]);
-            }
+    const int stride = gridDim.y * GROUPS;
+    Row8<E> r0 = {}, r1 = {};
+    int i0 = blockIdx.y * GROUPS;
+    auto load = [&](int i) {
+        if (i < items) {
+            r0.load(qkv + (size_t)i * D + c0);
+            r1.load(qkv + (size_t)i * D + c1);
         }
     };
-    int i0 = blockIdx.y * GROUPS;
-    load(i0);
+    load(i0 + g);
     if (A.q_gain)
         for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
             const int c = i % D;
@@ -161,61 +165,59 @@ append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
         s_sin[t][j / 8 * 12 + j % 8] = sn;
     }
     __syncthreads();
-    const int stride = gridDim.y * GROUPS, p0 = c0 / 8 * 12, p1 = c1 / 8 * 12;
+    const int p0 = c0 / 8 * 12, p1 = c1 / 8 * 12;
     int t = (i0 + g) / heads, hh = (i0 + g) % heads;       // the lane group's token and head
-    for (;;) {
+    for (; i0 < items; i0 += stride) {
+        float2 x0[4], x1[4];
+        r0.get(x0);
+        r1.get(x1);
+        load(i0 + stride + g);
+        const bool on = t < TPB && i0 + g < items && s_page[t] != -2;
+        const bool is_v = hh >= A.Hq + A.P.Hkv;
+        if (A.q_gain) {
+            float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int n = 0; n < NB; ++n) {
-            const bool on = t < TPB && i0 + n * stride + g < items && s_page[t] != -2;
-            const bool is_v = hh >= A.Hq + A.P.Hkv;
-            if (A.q_gain) {
-                float2 ss = make_float2(0.f, 0.f);
+            for (int e = 0; e < 4; ++e) ss = fma2(x0[e], x0[e], fma2(x1[e], x1[e], ss));
+            float sum = ss.x + ss.y;                   // unread rows sum garbage, which nobody uses
 #pragma unroll
-                for (int e = 0; e < 4; ++e) ss = fma2(x0[n][e], x0[n][e], fma2(x1[n][e], x1[n][e], ss));
-                float sum = ss.x + ss.y;                   // unread rows sum garbage, which nobody uses
-#pragma unroll
-                for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-                if (on && !is_v) {
-                    const float inv = rsqrtf(sum * (1.f / D) + A.eps);
-                    const float *gain = s_gain[hh < A.Hq ? 0 : 1];
-                    const float2 inv2 = make_float2(inv, inv);
-                    float2 g0[4], g1[4];
-                    lds8(gain + p0, g0);
-                    lds8(gain + p1, g1);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        x0[n][e] = mul2(mul2(x0[n][e], inv2), g0[e]);
-                        x1[n][e] = mul2(mul2(x1[n][e], inv2), g1[e]);
-                    }
-                }
-            }
-            if (on && rot && !is_v) {
-                float2 c[4], s[4];
-                lds8(s_cos[t] + p0, c);
-                lds8(s_sin[t] + p0, s);
+            for (int o = LANES / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+            if (on && !is_v) {
+                const float inv = rsqrtf(sum * (1.f / D) + A.eps);
+                const float *gain = s_gain[hh < A.Hq ? 0 : 1];
+                const float2 inv2 = make_float2(inv, inv);
+                float2 g0[4], g1[4];
+                lds8(gain + p0, g0);
+                lds8(gain + p1, g1);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 a = x0[n][e], b = x1[n][e];
-                    x0[n][e] = sub2(mul2(a, c[e]), mul2(b, s[e]));
-                    x1[n][e] = fma2(a, s[e], mul2(b, c[e]));
+                    x0[e] = mul2(mul2(x0[e], inv2), g0[e]);
+                    x1[e] = mul2(mul2(x1[e], inv2), g1[e]);
                 }
             }
-            if (on && (hh < A.Hq || s_page[t] >= 0)) {     // a page outside the pool: nothing is written
-                E *dst;
-                if (hh < A.Hq) {
-                    dst = (E *)A.q_out + ((size_t)(t0 + t) * A.Hq + hh) * D;
-                } else {
-                    const int h = is_v ? hh - A.Hq - A.P.Hkv : hh - A.Hq;
-                    dst = (E *)(is_v ? A.P.v : A.P.k) + A.P.row(s_page[t], h, s_slot[t]) * D;
-                }
-                Row8<E>::store(dst + c0, x0[n]);
-                Row8<E>::store(dst + c1, x1[n]);
-            }
-            for (hh += stride; hh >= heads; hh -= heads) ++t;
         }
-        i0 += NB * stride;
-        if (i0 >= items) break;
-        load(i0);
+        if (on && rot && !is_v) {
+            float2 c[4], s[4];
+            lds8(s_cos[t] + p0, c);
+            lds8(s_sin[t] + p0, s);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 a = x0[e], b = x1[e];
+                x0[e] = sub2(mul2(a, c[e]), mul2(b, s[e]));
+                x1[e] = fma2(a, s[e], mul2(b, c[e]));
+            }
+        }
+        if (on && (hh < A.Hq || s_page[t] >= 0)) {     // a page outside the pool: nothing is written
+            E *dst;
+            if (hh < A.Hq) {
+                dst = (E *)A.q_out + ((size_t)(t0 + t) * A.Hq + hh) * D;
+            } else {
+                const int h = is_v ? hh - A.Hq - A.P.Hkv : hh - A.Hq;
+                dst = (E *)(is_v ? A.P.v : A.P.k) + A.P.row(s_page[t], h, s_slot[t]) * D;
+            }
+            Row8<E>::store(dst + c0, x0);
+            Row8<E>::store(dst + c1, x1);
+        }
+        for (hh += stride; hh >= heads; hh -= heads) ++t;
     }
 }
 
@@ -226,11 +228,11 @@ cudaError_t launch(const AppendParams &A, const vc_rope &rope, cudaStream_t st)
     // Few tokens: one per CTA, its heads over several CTAs, one head per lane
     // group; many: four per CTA, which share the look-ups and the sines.  32/8
     // heads of 128 in bf16: 16 tokens 3.3 against 6.9 us, 600 tokens 6.8 against
-    // 7.0, 2400 tokens 21.1 against 10.5, 4670 tokens 44.0 against 22.9 (115 MB,
-    // 74% of the measured copy rate).
+    // 7.0, 2400 tokens 21.1 against 10.5, 4670 tokens 44.0 against 22.9, and 19.5
+    // with the next head in flight (115 MB, 87% of the measured copy rate).
     if (A.T <= 4 * device_sm_count())
-        return launch_pdl(append_kernel<E, D, 1, 1>, dim3(A.T, cdiv(heads, groups)), dim3(kThreads), 0, st, A, rope);
-    return launch_pdl(append_kernel<E, D, 4, 1>, dim3(cdiv(A.T, 4)), dim3(kThreads), 0, st, A, rope);
+        return launch_pdl(append_kernel<E, D, 1>, dim3(A.T, cdiv(heads, groups)), dim3(kThreads), 0, st, A, rope);
+    return launch_pdl(append_kernel<E, D, 4>, dim3(cdiv(A.T, 4)), dim3(kThreads), 0, st, A, rope);
 }
 
 }  // namespace
