@@ -3,12 +3,13 @@
 // best-scored older ones move, in ascending order, to other pages.
 //
 // Selection is exact: the kept set is the largest by (score descending, slot
-// ascending).  A cluster of eight CTAs takes one (sequence, head): an
+// ascending).  One CTA, or a cluster of eight, takes one (sequence, head): an
 // MSB-first radix select (11 + 11 + 10 bits of an order-preserving integer
 // image of the scores) with one histogram per CTA in shared memory finds the
-// threshold; each CTA adds up an eighth of the digits over the cluster through
+// threshold; in a cluster each CTA adds up an eighth of the digits through
 // distributed shared memory, and the one that holds the searched digit tells
-// the others.
+// the others (all digits in every CTA, for one barrier a pass instead of three,
+// takes longer: 90 against 62 us for 128 units of 4000 tokens).
 // Every warp owns a run of consecutive slots; its counts above and at the
 // threshold, prefixed over warps and CTAs, give the place of its first kept
 // slot, and ballots order the rest.  The scores are read from memory once, 16
@@ -86,19 +87,24 @@ __device__ __forceinline__ void for_scores(int lo, int hi, int at, int stride, L
     }
 }
 
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+template <int Z>
+__global__ void __cluster_dims__(Z, 1, 1) __launch_bounds__(kThreads)
 select_kernel(Pool S, EvictParams E)
 {
-    __shared__ int hist[kBins];
+    __shared__ __align__(16) int hist[kBins];
     __shared__ int warp_sums[kWarps];
-    __shared__ int s_slice[kCluster];                  // the CTAs' totals of their digits, of this pass
+    __shared__ int s_slice[Z];                         // the CTAs' totals of their digits, of this pass
     __shared__ int s_digit, s_above;
     extern __shared__ uint32_t cache[];
     __shared__ int2 s_count[kWarps + 1];               // slots above / at the threshold: by warp, of the CTA
     cg::cluster_group cluster = cg::this_cluster();
+    auto sync_all = [&] {
+        if constexpr (Z == 1) __syncthreads();
+        else cluster.sync();
+    };
     pdl_wait();
     pdl_trigger();
-    const int unit = blockIdx.x / kCluster, rank = (int)cluster.block_rank();
+    const int unit = blockIdx.x / Z, rank = (int)(blockIdx.x % Z);
     const int b = unit / S.Hkv;
     const int L = src_tokens(S, E.src_len, b);
     const int recent = (int)min(E.recent, (long)L), cand = L - recent;
@@ -109,7 +115,7 @@ select_kernel(Pool S, EvictParams E)
     if (unit % S.Hkv == 0 && rank == 0 && threadIdx.x == 0) E.dst_len[b] = keep;
     // the CTA's candidates [lo, hi), in runs of `run` slots per warp
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int run = cdiv(cdiv(cand, kCluster * kWarps), 32) * 32;
+    const int run = cdiv(cdiv(cand, Z * kWarps), 32) * 32;
     const int lo = (int)min((long)cand, (long)rank * run * kWarps), hi = (int)min((long)cand, lo + (long)run * kWarps);
 
     uint32_t prefix = 0;
@@ -122,7 +128,7 @@ select_kernel(Pool S, EvictParams E)
         int shift = 32;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
-            const int width = pass == 2 ? 10 : 11, bins = 1 << width, part = bins / kCluster;
+            const int width = pass == 2 ? 10 : 11, bins = 1 << width, part = bins / Z;
             shift -= width;
             for (int i = threadIdx.x; i < bins; i += kThreads) hist[i] = 0;
             __syncthreads();
@@ -138,38 +144,64 @@ select_kernel(Pool S, EvictParams E)
             else if (cached) for_scores(lo, hi, threadIdx.x, kThreads, from_cache, add);
             else for_scores(lo, hi, threadIdx.x, kThreads, from_memory, add);
             cached = fits;
-            cluster.sync();
-            // This CTA's digits, from the highest down: rank 0 has the highest
-            // part of them.  Two threads per digit, four histograms each.
-            const int dgt = bins - 1 - (rank * part + (int)threadIdx.x / 2);
-            int cnt = 0;
-            if ((int)threadIdx.x < 2 * part) {
+            sync_all();
+            if constexpr (Z == 1) {
+                // four digits per thread, from the highest down
+                const int dgt = bins - 4 - 4 * (int)threadIdx.x;
+                int4 cnt = make_int4(0, 0, 0, 0);
+                if (dgt >= 0) cnt = *reinterpret_cast<const int4 *>(&hist[dgt]);
+                const int all4 = cnt.x + cnt.y + cnt.z + cnt.w;
+                int incl = all4;
 #pragma unroll
-                for (int r = 0; r < kCluster / 2; ++r)
-                    cnt += *cluster.map_shared_rank(&hist[dgt], (threadIdx.x & 1) * (kCluster / 2) + r);
-            }
-            cnt += __shfl_xor_sync(0xffffffffu, cnt, 1);
-            int incl = threadIdx.x & 1 ? 0 : cnt;      // inclusive over the digits from the highest
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int up = __shfl_up_sync(0xffffffffu, incl, o);
-                if (lane >= o) incl += up;
-            }
-            if (lane == 31) warp_sums[warp] = incl;
-            __syncthreads();
-            for (int w = 0; w < warp; ++w) incl += warp_sums[w];
-            if (threadIdx.x == kThreads - 1)
-                for (int r = 0; r < kCluster; ++r) *cluster.map_shared_rank(&s_slice[rank], r) = incl;
-            cluster.sync();
-            int above = 0;                             // keys with digits of lower ranks
-            for (int r = 0; r < rank; ++r) above += s_slice[r];
-            const int before = above + incl - cnt;
-            if (!(threadIdx.x & 1) && (int)threadIdx.x < 2 * part && before < remaining && remaining <= before + cnt)
-                for (int r = 0; r < kCluster; ++r) {
-                    *cluster.map_shared_rank(&s_digit, r) = dgt;
-                    *cluster.map_shared_rank(&s_above, r) = before;
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
                 }
-            cluster.sync();                            // the digit has arrived, the histograms have been read
+                if (lane == 31) warp_sums[warp] = incl;
+                __syncthreads();
+                for (int w = 0; w < warp; ++w) incl += warp_sums[w];
+                int before = incl - all4;
+                if (before < remaining && remaining <= incl) {
+                    const int by[4] = {cnt.w, cnt.z, cnt.y, cnt.x};
+                    int e = 0;
+                    while (e < 3 && remaining > before + by[e]) before += by[e++];
+                    s_digit = dgt + 3 - e;
+                    s_above = before;
+                }
+                __syncthreads();
+            } else {
+                // This CTA's digits, from the highest down: rank 0 has the highest
+                // part of them.  Two threads per digit, four histograms each.
+                const int dgt = bins - 1 - (rank * part + (int)threadIdx.x / 2);
+                int cnt = 0;
+                if ((int)threadIdx.x < 2 * part) {
+#pragma unroll
+                    for (int r = 0; r < Z / 2; ++r)
+                        cnt += *cluster.map_shared_rank(&hist[dgt], (threadIdx.x & 1) * (Z / 2) + r);
+                }
+                cnt += __shfl_xor_sync(0xffffffffu, cnt, 1);
+                int incl = threadIdx.x & 1 ? 0 : cnt;      // inclusive over the digits from the highest
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int up = __shfl_up_sync(0xffffffffu, incl, o);
+                    if (lane >= o) incl += up;
+                }
+                if (lane == 31) warp_sums[warp] = incl;
+                __syncthreads();
+                for (int w = 0; w < warp; ++w) incl += warp_sums[w];
+                if (threadIdx.x == kThreads - 1)
+                    for (int r = 0; r < Z; ++r) *cluster.map_shared_rank(&s_slice[rank], r) = incl;
+                cluster.sync();
+                int above = 0;                             // keys with digits of lower ranks
+                for (int r = 0; r < rank; ++r) above += s_slice[r];
+                const int before = above + incl - cnt;
+                if (!(threadIdx.x & 1) && (int)threadIdx.x < 2 * part && before < remaining && remaining <= before + cnt)
+                    for (int r = 0; r < Z; ++r) {
+                        *cluster.map_shared_rank(&s_digit, r) = dgt;
+                        *cluster.map_shared_rank(&s_above, r) = before;
+                    }
+                cluster.sync();                            // the digit has arrived, the histograms have been read
+            }
             prefix = (prefix << width) | (uint32_t)s_digit;
             remaining -= s_above;
         }
@@ -193,7 +225,7 @@ select_kernel(Pool S, EvictParams E)
         for (int w = 0; w < kWarps; ++w) sum.x += s_count[w].x, sum.y += s_count[w].y;
         s_count[kWarps] = sum;
     }
-    cluster.sync();
+    sync_all();
     int2 before = make_int2(0, 0);
     for (int r = 0; r < rank; ++r) {
         const int2 c = *cluster.map_shared_rank(&s_count[kWarps], r);
@@ -218,11 +250,11 @@ select_kernel(Pool S, EvictParams E)
         if (cached) for_scores(wlo, whi, lane, 32, from_cache, write);
         else for_scores(wlo, whi, lane, 32, from_memory, write);
     }
-    for (int i = rank * kThreads + threadIdx.x; i < recent; i += kCluster * kThreads) {
+    for (int i = rank * kThreads + threadIdx.x; i < recent; i += Z * kThreads) {
         kept[top + i] = cand + i;
         if (sc_out) sc_out[top + i] = sc[cand + i];
     }
-    cluster.sync();                                    // no CTA leaves while its counts may be read
+    sync_all();                                        // no CTA leaves while its counts may be read
 }
 
 // Rows of kept slots from the source pages to the destination's.  16 bytes per
@@ -269,6 +301,17 @@ move_kernel(Pool S, Pool Dp, EvictParams E, int row_bytes, int blocks_per_unit)
     }
 }
 
+template <int Z>
+cudaError_t select(const Pool &S, EvictParams E, int units, long cap, cudaStream_t st)
+{
+    auto kern = select_kernel<Z>;
+    const long runs = cdiv(cap, Z * kWarps * 32) * 32l * kWarps;       // a CTA's share of the largest sequence
+    E.cache = (int)std::min<long>(kCache, runs);
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kCache * 4);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(kern, dim3((unsigned)units * Z), dim3(kThreads), E.cache * 4, st, S, E);
+}
+
 }  // namespace
 
 cudaError_t evict(const Pool &S, const Pool &Dp, int row_bytes, const float *scores, int scores_stride,
@@ -287,14 +330,14 @@ cudaError_t evict(const Pool &S, const Pool &Dp, int row_bytes, const float *sco
     E.top = top;
     E.recent = recent;
     const int units = S.B * S.Hkv;
-    const long cap = (long)S.max_blocks << S.page_log2, runs = cdiv(cap, kCluster * kWarps * 32) * 32l * kWarps;
-    E.cache = (int)std::min<long>(kCache, runs);
-    cudaError_t e = cudaFuncSetAttribute(select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kCache * 4);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(select_kernel, dim3(units * kCluster), dim3(kThreads), E.cache * 4, st, S, E);
+    const long cap = (long)S.max_blocks << S.page_log2;
+    // A table that one CTA's shared memory covers needs no cluster: the tokens of
+    // 256 (sequence, head) units, 1000 each, 42 us with the moves against 127, of 128
+    // units of 16000 29 against 64; of 8 units of 16000 18 against 16.
+    cudaError_t e = cap <= kCache ? select<1>(S, E, units, cap, st) : select<kCluster>(S, E, units, cap, st);
     if (e != cudaSuccess) return e;
     // about 12 CTAs per SM, none without a row to move
-    const long most = std::min<long>((long)S.max_blocks << S.page_log2, top + recent);
+    const long most = std::min<long>(cap, top + recent);
     const int per = kMoveThreads / (row_bytes / 16) * kRows;
     const int bpu = (int)std::max<long>(1, std::min<long>(cdiv(most, per), cdiv(12l * device_sm_count(), units)));
     return launch_pdl(move_kernel, dim3((unsigned)units * bpu), dim3(kMoveThreads), 0, st, S, Dp, E, row_bytes, bpu);

@@ -437,6 +437,23 @@ def test_evict_all_equal_scores():
     _evict(vc, bt, torch.full((2, 2, bt.width * 16), math.nan, device="cuda"), 100, 20, 32)
 
 
+@pytest.mark.parametrize("lens,top,recent,slots", [
+    ([16384, 16000], 700, 65, 16384), ([16385, 5], 700, 65, 16400), ([700, 0, 64], 20, 10, 16400),
+    ([5000, 4097, 4096], 900, 65, 40000), ([140000, 3], 5000, 100, 140000), ([20000], 19990, 5, 20000)])
+def test_evict_where_the_selection_changes_form(lens, top, recent, slots):
+    """One CTA per unit up to 16384 slots of the table, a cluster beyond, which
+    keeps up to 131072 scores on chip: ties, signed zeros and NaN on each side."""
+    vc = lib()
+    page = 16
+    bt = Batch([0] * len(lens), lens, 2, 64, page, BF, seed=slots % 97, width=-(-slots // page))
+    assert slots <= bt.width * page < slots + page
+    g = torch.Generator().manual_seed(slots % 89)
+    sc = (torch.randn(bt.B, 2, bt.width * page, generator=g) * 4).round() / 4
+    sc = sc * torch.where(torch.rand(sc.shape, generator=g) < 0.5, 1.0, -1.0)
+    sc[torch.rand(sc.shape, generator=g) < 0.02] = math.nan
+    _evict(vc, bt, sc.cuda(), top, recent, 32)
+
+
 def test_evict_reports_what_does_not_fit():
     vc = lib()
     bt = Batch([0] * 3, [100, 60, 50], 2, 64, 16, BF, seed=4)
