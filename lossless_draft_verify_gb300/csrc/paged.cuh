@@ -110,7 +110,8 @@ struct WorkDim {
 // 16): 806 us at kUnitCost 2, 745 at 4, 606 at 9, 505 at 16, 502 at 20; a decode
 // step of 16 x 32768 tokens 313 us at 2, 323 at 16, 331 at 28.  The CUDA-core
 // kernels' tiles take longer and their units less: four sequences of 17 tokens
-// at most over 2000 in fp32 25.6 us with 1, 2, 3 and 34.4 with 4, 6, 8.
+// at most over 2000 in fp32 25.6 us with 1, 2, 3 and 34.4 with 4, 6, 8 (with one
+// stage for the key tiles; 22.5 now).
 template <int BM>
 struct Cost {
     static constexpr int kUnitCost = BM == 256 ? 16 : 1;

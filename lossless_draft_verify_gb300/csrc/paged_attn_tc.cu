@@ -19,7 +19,8 @@
 // take the key tiles alternately for the same rows and are merged at the end,
 // so that a short unit, which HBM bounds, has both softmax groups on it.
 // Measured: a decode step of 16 x 32768 tokens, 32/8 heads, 318 us = 6.75 TB/s;
-// 2048 tokens over 30000 780 to 802 us = 1.30 to 1.33 PFLOP/s at the power limit.
+// 2048 tokens over 30000 786 to 794 us = 1.32 PFLOP/s at the power limit (720 in a
+// short run below it, 779 with one load of Q at a time per thread).
 // A stream's chain S, softmax, P V bounds the latter: 64-key steps with S twice
 // buffered (950 us), two threads per row (824 us) and the first half's product
 // under the second's exponentials (802 us) do not shorten it.
