@@ -7,18 +7,20 @@
 // The product is taken transposed, S^T = K Q^T: a key is a row of the
 // accumulator, so one thread holds all of a key's weights for 128 query rows
 // and sums them without any exchange; every slot is owned by one thread and
-// its sum has a fixed order.  Four key tiles of 128 stay in shared memory while the
-// sequence's row tiles pass (a row tile is floor(128 / G) queries of the G
-// heads, one TMA box), so K is read from HBM once and a row tile from L2 once
-// per 512 keys.  With one row tile (decoding) this is a stream of K, bound by
-// HBM; with many by the sums' arithmetic and waits: 150 us after the 222 of the
-// attention for two 512-token chunks over 16000 tokens, 32/8 heads, the
-// tensor cores busy a third of it.  Shares are counted in key tiles, not groups:
-// a prompt of 2048 over 8000 tokens 462 us with its attention against 528, eight
-// of 512 109 against 124, four chunks of 300 over 4000 tokens 258 against 237.
-// Groups of two or one tile at most cost more than they give (471 and 656 us
-// against 404 and 583 before), and so do accumulators in two halves, the second
-// product under the first one's sums (414 against 370).
+// its sum has a fixed order.  A group of up to four key tiles of 128 stays in
+// shared memory while the sequence's row tiles pass (a row tile is floor(128 / G)
+// queries of the G heads, one TMA box), so K is read from HBM once and a row tile
+// from L2 once per group.  With one row tile (decoding) this is a stream of K,
+// bound by HBM; with many by the sums' arithmetic and waits: about 150 us after
+// the 222 of the attention for two 512-token chunks over 16000 tokens, 32/8
+// heads, the tensor cores busy a third of it.
+// A batch's groups all have the size that leaves the busiest CTA the least: with
+// 512 tokens over 8000 122 us (with the attention) against 127 with shares cut at
+// any key tile, four chunks of 300 over 4000, 7 query heads to each of 8, 240 against 259, a prompt
+// of 2048 over 8000 484 against 461, and 528 with groups of four.  Groups of two or
+// one everywhere cost more than they give (471 and 656 us against 404 and 583), and
+// so do accumulators in two halves, the second product under the first one's sums
+// (414 against 370).
 //   warps 0-15      sums, four warps to a key tile of the group and to one of
 //                   four accumulators (two sets of four, each with every other
 //                   tile: 454 against 404 us, before, for the two chunks above);
@@ -47,16 +49,18 @@ struct Geom {
     static constexpr int SMEM = SM_X + 16 * 512 + 1024;
 };
 
-// A CTA's share: key tiles, in the order sequence, head, tile, each with the
-// cost 4 row tiles + 1; a tile belongs to the CTA in whose part of the total it
-// begins.  The tiles of a head in a share are taken in groups of like size.
+// A CTA's share: groups of up to `size` key tiles, in the order sequence, head,
+// group, each with the cost 4 row tiles + 1; a group belongs to the CTA in whose
+// part of the total it begins.
 struct MassWalk {
-    int b, h, t;                 // next key tile
+    int b, h, g;                 // next group
     int nt, mt, rt;              // of the sequence: key tiles, row tiles, rows per row tile
+    int size;
     Seq s;
-    long at, end;                // cost at the next tile's beginning, end of the share
+    long at, end;                // cost at the next group's beginning, end of the share
 
     static __device__ __forceinline__ long cost(int mt) { return 4l * mt + 1; }
+    __device__ __forceinline__ int groups(int k) const { return (nt + k - 1) / k; }
     __device__ __forceinline__ void shape(const Pool &P, const WorkDim &W, int b_)
     {
         b = b_;
@@ -89,21 +93,52 @@ struct Params {
     float sl2;
 };
 
-// One warp finds where the CTA's share begins.
+// One warp finds where the CTA's share begins.  First the size of the groups: a
+// round of a group of k tiles (a row tile's products and sums) takes about
+// 0.7 + 0.4 k us, and the CTA with the most groups is the last one.
 __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, MassWalk *out)
 {
     const int lane = threadIdx.x & 31;
-    long total = 0;
     MassWalk w;
+    auto take = [&](int b0) {                          // the lane's sequence of 32
+        if (b0 == 0 || b0 + lane >= A.P.B) w.nt = 0;
+        if (b0 + lane < A.P.B) w.shape(A.P, A.W, b0 + lane);
+    };
+    float n[kGroup] = {}, c[kGroup] = {};              // groups, rounds
     for (int b0 = 0; b0 < A.P.B; b0 += 32) {
-        long c = 0;
-        if (b0 + lane < A.P.B) {
-            w.shape(A.P, A.W, b0 + lane);
-            c = (long)w.nt * A.P.Hkv * MassWalk::cost(w.mt);
-        }
+        take(b0);
+        if (w.nt == 0) continue;
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
-        total += c;
+        for (int k = 0; k < kGroup; ++k) {
+            const float x = (float)w.groups(k + 1) * A.P.Hkv;
+            n[k] += x;
+            c[k] += x * w.mt;
+        }
+    }
+    int size = 1;
+    float best = 0.f;
+#pragma unroll
+    for (int k = 0; k < kGroup; ++k) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+            n[k] += __shfl_xor_sync(0xffffffffu, n[k], o);
+            c[k] += __shfl_xor_sync(0xffffffffu, c[k], o);
+        }
+        const float t = n[k] > 0.f ? ceilf(n[k] / n_cta) * (c[k] / n[k]) * (7 + 4 * (k + 1)) : 0.f;
+        if (k == 0 || t <= best) {
+            best = t;
+            size = k + 1;
+        }
+    }
+    const bool few = A.P.B <= 32;                      // the lanes still hold them
+    auto of = [&] { return w.nt > 0 ? (long)w.groups(size) * A.P.Hkv * MassWalk::cost(w.mt) : 0l; };
+    long total = 0;
+    for (int b0 = 0; b0 < A.P.B; b0 += 32) {
+        if (!few) take(b0);
+        long x = of();
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        total += x;
     }
     const long per = (total + n_cta - 1) / n_cta, lo = per * cta, hi = lmin(total, lo + per);
     if (lane == 0) out->at = out->end = 0;
@@ -111,25 +146,23 @@ __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, 
     if (lo >= hi) return;
     long before = 0;
     for (int b0 = 0; b0 < A.P.B; b0 += 32) {
-        long c = 0;
-        if (b0 + lane < A.P.B) {
-            w.shape(A.P, A.W, b0 + lane);
-            c = (long)w.nt * A.P.Hkv * MassWalk::cost(w.mt);
-        }
-        long incl = c;
+        if (!few) take(b0);
+        const long x = of();
+        long incl = x;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const long up = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += up;
         }
-        const long start = before + incl - c;
-        if (c > 0 && start <= lo && lo < start + c) {
-            // the first tile that begins at lo or later (it may be the next sequence's first)
-            const long cg = MassWalk::cost(w.mt), x = (lo - start + cg - 1) / cg;
-            w.h = (int)(x / w.nt);
-            w.t = (int)(x % w.nt);
-            w.at = start + x * cg;
+        const long start = before + incl - x;
+        if (x > 0 && start <= lo && lo < start + x) {
+            // the first group that begins at lo or later (it may be the next sequence's first)
+            const long cg = MassWalk::cost(w.mt), i = (lo - start + cg - 1) / cg;
+            w.h = (int)(i / w.groups(size));
+            w.g = (int)(i % w.groups(size));
+            w.at = start + i * cg;
             w.end = hi;
+            w.size = size;
             *out = w;
         }
         before += __shfl_sync(0xffffffffu, incl, 31);
@@ -139,30 +172,28 @@ __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, 
 __device__ __forceinline__ bool next_group(MassWalk &w, const Params &A, MassItem &it)
 {
     while (w.at < w.end) {
-        if (w.t >= w.nt) {
-            w.t = 0;
+        if (w.g * w.size >= w.nt) {
+            w.g = 0;
             ++w.h;
         }
         if (w.nt == 0 || w.h >= A.P.Hkv) {
             if (w.b + 1 >= A.P.B) return false;
             w.shape(A.P, A.W, w.b + 1);
-            w.h = w.t = 0;
+            w.h = w.g = 0;
             continue;
         }
         it.b = w.b;
         it.h = w.h;
-        it.key0 = w.t * BN;
+        it.key0 = w.g * w.size * BN;
         it.tok0 = w.s.tok0;
         it.ctx = w.s.ctx;
         it.len = w.s.ctx + w.s.n;
-        const long c = MassWalk::cost(w.mt);
-        const int left = (int)lmin(w.nt - w.t, (w.end - w.at + c - 1) / c);
-        it.tiles = cdiv(left, cdiv(left, kGroup));
+        it.tiles = min(w.size, w.nt - w.g * w.size);
         it.rows = w.s.n * A.W.G;
         it.mt0 = (int)(lmax(it.key0 - w.s.ctx, 0) * A.W.G / w.rt);
         it.mt = w.mt;
-        w.at += it.tiles * c;
-        w.t += it.tiles;
+        w.at += MassWalk::cost(w.mt);
+        ++w.g;
         return true;
     }
     return false;
