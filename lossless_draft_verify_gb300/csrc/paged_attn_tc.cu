@@ -52,6 +52,7 @@ constexpr int kRowsTile = 128;
 constexpr int kThreads = 352;
 constexpr int kProducer = 8, kIssuer = 9, kProducer2 = 10;     // warps
 constexpr int kSoftmax = 256;
+constexpr int kSharedBytes = 3 << 10;                          // barriers, the roles' walks
 constexpr float kLazy = 8.f;
 
 template <int D>
@@ -62,7 +63,7 @@ struct Geom {
     static constexpr int SM_Q = 0;
     static constexpr int SM_KV = 2 * TILE;
     static constexpr int SM_BAR = SM_KV + STAGES * TILE;
-    static constexpr int SMEM = SM_BAR + 3072;
+    static constexpr int SMEM = SM_BAR + kSharedBytes;
     static constexpr uint32_t COL_O = 256;                   // S0 | S1 | O0 | O1
 };
 
@@ -112,7 +113,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     constexpr int NST = G::STAGES;
     extern __shared__ __align__(1024) uint8_t sm[];
     Shared *S = reinterpret_cast<Shared *>(sm + G::SM_BAR);
-    static_assert(sizeof(Shared) <= 3072, "shared block");
+    static_assert(sizeof(Shared) <= kSharedBytes, "shared block");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     if (smem_u32(sm) & 1023u) {                              // never expected: the swizzled tiles need it

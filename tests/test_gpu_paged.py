@@ -93,6 +93,27 @@ def test_attention_mass(case, dtype):
         assert torch.equal(scores[b, :, untouched:], before[b, :, untouched:])
 
 
+# row tiles of a batch in groups of one, two, three and four key tiles; more
+# sequences than a warp has lanes
+MASS = [([20], [c], 32, 8) for c in (2300, 4000, 6000, 9000)] + [
+    ([20 + i % 7 for i in range(40)], [(37 * i) % 500 for i in range(40)], 4, 2),
+    ([30 * (i % 3) for i in range(70)], [(53 * i) % 300 for i in range(70)], 8, 8)]
+
+
+@pytest.mark.parametrize("case", range(len(MASS)))
+def test_mass_of_many_key_tiles_and_sequences(case):
+    vc = lib()
+    ns, cs, Hq, Hkv = MASS[case]
+    bt = Batch(ns, cs, Hkv, 64, 64, BF, seed=200 + case)
+    q = bt.randn(bt.T, Hq, 64, scale=1.5)
+    scores = torch.zeros(bt.B, Hkv, bt.width * 64, device="cuda")
+    out = _attn(vc, bt, q, 0.125, True, scores)
+    mass, mtol = _compare(bt, q, out, 0.125)
+    close(scores, mass, mtol, "scores")
+    for b in range(bt.B):
+        assert (scores[b, :, bt.lens[b] if bt.ns[b] else 0:] == 0).all()
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("scale,peak", [(0.0, 1.0), (0.3, 6.0), (1.0, 4.0)])
 def test_attention_scales(dtype, scale, peak):
