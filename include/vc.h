@@ -837,7 +837,9 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
  * q, out: device [T][Hq][d] in cache->dt, 16-byte aligned.  bf16 caches run on
  * the tensor cores (fp32 accumulation, the softmax weights rounded to bf16),
  * fp32 caches on the CUDA cores in fp32.  sm_scale: finite, not negative, at
- * most 1e8; products q . k lie within +-1e30.
+ * most 1e8; products q . k lie within +-1e30.  Scores are fp32: a row's weights
+ * are off by some 2^-23 times its largest |q . k * sm_scale|, so that far above
+ * 10^6 only equal scores and much smaller ones are told apart.
  * The order of a row's sums, and so its last bits, depends on the lengths of
  * the whole batch (unlike vc_decoder_forward's).
  */
@@ -852,7 +854,9 @@ vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_
  *   scores[u * scores_stride + j] += sum over the chunk's rows and the query
  *       heads of h that see j of softmax_j(q . k_j * sm_scale),
  * with every row's final maximum and sum, in fp32, each slot summed in an order
- * fixed by the lengths.  scores: device fp32, scores_stride >= max_blocks *
+ * fixed by the lengths.  No weight is above one, but where a row's scores are far
+ * above 10^6 its weights need not sum to one: the logarithm of their sum is lost
+ * beside the maximum.  scores: device fp32, scores_stride >= max_blocks *
  * page.  Sequences without rows keep their scores.  The workspace of a bf16
  * batch with T * Hq <= 16 * B * Hkv (decoding) also holds the scores of its
  * rows, 4 bytes per query head and table slot.

@@ -12,7 +12,12 @@ namespace vc {
 namespace paged {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNegBig = -1.0e30f;
+// Below every score in the log2 domain (products within 1e30, times a scale of
+// at most 1e8 and log2 e: 1.44e38), and its distance to the largest is finite.
+// A row that has seen no key has it as its maximum.
+constexpr float kLowest = -1.5e38f;
+// the same for products not yet scaled
+constexpr float kLowestProduct = -1.0e30f;
 
 __host__ __device__ inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 

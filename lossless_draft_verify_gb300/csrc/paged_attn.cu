@@ -22,7 +22,7 @@ merge_kernel(Parts parts, int G, int Hq, T *__restrict__ out, float *__restrict_
     const PartDesc d = parts.desc[c];
     if (d.parts == 0) return;
     for (int r = blockIdx.y * kMergeWarps + (threadIdx.x >> 5); r < d.rows; r += gridDim.y * kMergeWarps) {
-        float M = kNegBig;
+        float M = kLowest;
         for (int p = lane; p < d.parts; p += 32) M = fmaxf(M, parts.ml[parts.row(c + p, p == 0 ? 1 : 0, r)].x);
         M = warp_max(M);
         constexpr int V = D / 32;

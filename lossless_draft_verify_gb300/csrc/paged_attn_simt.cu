@@ -92,7 +92,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
         int kmax[RT];
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
-            m[i] = kNegBig;
+            m[i] = kLowest;
             l[i] = 0.f;
             const int r = ty * RT + i;
             kmax[i] = r < it.rows ? it.ctx + (row0 + r) / W.G : -1;
@@ -158,7 +158,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
             }
 #pragma unroll
             for (int i = 0; i < RT; ++i) {
-                float s[KT], mx = kNegBig;
+                float s[KT], mx = kLowest;
 #pragma unroll
                 for (int j = 0; j < KT; ++j) {
                     s[j] = key0 + tx + 16 * j <= kmax[i] ? (s2[i][j].x + s2[i][j].y) * scale_log2 : -INFINITY;
@@ -342,7 +342,8 @@ mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
                     if (++g == G) g = 0, ++tok;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        if (key0 + tx + 16 * j <= kmax) sum[j] += exp2f((a4[i][j].x + a4[i][j].y) * scale_log2 - e);
+                        if (key0 + tx + 16 * j <= kmax)        // the score rounded as for the row's maximum
+                            sum[j] += exp2f(__fsub_rn(__fmul_rn(a4[i][j].x + a4[i][j].y, scale_log2), e));
                 }
             }
             __syncthreads();

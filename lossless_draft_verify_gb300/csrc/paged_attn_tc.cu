@@ -53,7 +53,7 @@ constexpr int kThreads = 352;
 constexpr int kProducer = 8, kIssuer = 9, kProducer2 = 10;     // warps
 constexpr int kSoftmax = 256;
 constexpr int kSharedBytes = 3 << 10;                          // barriers, the roles' walks
-constexpr float kLazy = 8.f;
+constexpr float kLazy = 8.f;                                   // log2 domain
 
 template <int D>
 struct Geom {
@@ -376,7 +376,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             // keys every row of the tile sees
             const int kall = it.ctx + (row0 + (big ? t * 128 : 0)) / A.W.G;
             float *s_row = STORE && valid ? A.s_out + (long)out_row(R) * A.s_stride : nullptr;
-            float m = kNegBig, l = 0.f;
+            // m: of the products; with STORE, which scales them anyway, of the scores
+            constexpr float kFloor = STORE ? kLowest : kLowestProduct;
+            const float unit = STORE ? 1.f : A.sl2;          // m * unit: log2 domain
+            float m = kFloor, l = 0.f;
             const int mine = big ? n : (n + 1 - t) / 2;      // this stream's steps
             // V rows of the last page past the sequence's end, before the product
             // with key tile i (big: stream 0's comes first)
@@ -429,9 +432,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 uint32_t pk[64];
                 float2 sum[2];
                 for (;;) {
-                    const float2 sc = make_float2(A.sl2, A.sl2), nm = make_float2(-m * A.sl2, -m * A.sl2);
+                    const float2 sc = make_float2(A.sl2, A.sl2), nm = make_float2(-m, -m);
                     sum[0] = sum[1] = make_float2(0.f, 0.f);
-                    float top[2] = {kNegBig, kNegBig};
+                    float top[2] = {kFloor, kFloor};
                     uint32_t u[2][32];
                     tc::ld32(tS, u[0]);
 #pragma unroll
@@ -440,13 +443,17 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
                         uint32_t (&v)[32] = u[h & 1];
                         if constexpr (STORE) {
+#pragma unroll
+                            for (int c = 0; c < 32; c += 2) {
+                                const float2 s = mul2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc);
+                                v[c] = __float_as_uint(s.x);
+                                v[c + 1] = __float_as_uint(s.y);
+                            }
                             if (valid) {
                                 float *dst = s_row + key0 + h * 32;
 #pragma unroll
                                 for (int c = 0; c < 32; c += 4)
-                                    *reinterpret_cast<float4 *>(dst + c) = make_float4(
-                                        __uint_as_float(v[c]) * A.sl2, __uint_as_float(v[c + 1]) * A.sl2,
-                                        __uint_as_float(v[c + 2]) * A.sl2, __uint_as_float(v[c + 3]) * A.sl2);
+                                    *reinterpret_cast<uint4 *>(dst + c) = make_uint4(v[c], v[c + 1], v[c + 2], v[c + 3]);
                             }
                             __syncwarp();
                         }
@@ -455,7 +462,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         for (int e = 0; e < 16; ++e) {
                             const float2 s = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
                             top[e & 1] = fmaxf(top[e & 1], fmaxf(s.x, s.y));
-                            const float2 x = fma2(s, sc, nm);
+                            // the difference first: zero at the maximum however large the
+                            // scores, where an fma would leave the rounding of m * scale
+                            const float2 x = STORE ? add2(s, nm) : mul2(add2(s, nm), sc);
                             const float2 p = make_float2(ex2(x.x), ex2(x.y));
                             sum[e & 1] = add2(sum[e & 1], p);
                             const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
@@ -463,11 +472,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         }
                     }
                     const float mx = fmaxf(top[0], top[1]);
-                    const bool grown = (mx - m) * A.sl2 > kLazy;
+                    const bool grown = (mx - m) * unit > kLazy;
                     if (!__any_sync(0xffffffffu, grown)) break;
                     float alpha = 1.f;
                     if (grown) {
-                        alpha = ex2((m - mx) * A.sl2);
+                        alpha = ex2((m - mx) * unit);
                         m = mx;
                     }
                     l *= alpha;
@@ -544,9 +553,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 ++units[0], ++units[1];
                 if (!ok) break;
                 tc::fence_after();
-                finish(m * A.sl2, l, 1.f, 0.f, 0, D);
+                finish(m * unit, l, 1.f, 0.f, 0, D);
             } else {
-                ml_x[t * kRowsTile + r] = make_float2(m * A.sl2, l);
+                ml_x[t * kRowsTile + r] = make_float2(m * unit, l);
                 ok = wait_warp(&S->o_full[0], units[0] & 1, A.status, 98) &&
                      (n == 1 || wait_warp(&S->o_full[1], units[1] & 1, A.status, 99));
                 ++units[0];

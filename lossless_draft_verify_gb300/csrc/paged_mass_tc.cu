@@ -4,6 +4,11 @@
 //   scores[b][h][j] += sum over the rows r = (i, g) that see slot j of
 //       2^(scale' q_r . k_j - lse_r),   j <= ctx + i, lse from the attention.
 //
+// One fma gives the exponent where no |lse| of a row tile is above 2^20 (it is
+// then off by 2^-5, lse's rounding, at most).  Above, the scaled score is rounded
+// first, as it was for the row's maximum, so that no weight exceeds one whatever
+// the scores' size (in every tile: 395 against 382 us for the two chunks below).
+//
 // The product is taken transposed, S^T = K Q^T: a key is a row of the
 // accumulator, so one thread holds all of a key's weights for 128 query rows
 // and sums them without any exchange; every slot is owned by one thread and
@@ -376,6 +381,8 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 __syncwarp();
 #pragma unroll
                 for (int x = 0; x < 4; ++x) my_lse[lane + 32 * x] = -next[x];
+                const bool large = __any_sync(0xffffffffu, fmaxf(fmaxf(fabsf(next[0]), fabsf(next[1])),
+                                                                 fmaxf(fabsf(next[2]), fabsf(next[3]))) > 0x1p20f);
                 __syncwarp();
                 if (q + 1 < it.mt) fetch(q + 1);
                 ok = wait_warp(&S->s_full[k], used & 1, A.status, 116);
@@ -393,7 +400,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     uint32_t v[32];
                     tc::ld32(tS + c0, v);
                     tc::ld_wait();
-                    if (c0 >= lo_all && c0 + 32 <= cols) {
+                    if (c0 >= lo_all && c0 + 32 <= cols && !large) {
 #pragma unroll
                         for (int c = 0; c < 32; c += 4) {
                             const float4 e = *reinterpret_cast<const float4 *>(my_lse + c0 + c);
@@ -408,7 +415,7 @@ mass_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         // columns past the rows hold whatever was there: chosen, not multiplied away
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
-                            const float p = ex2(fmaf(__uint_as_float(v[c]), A.sl2, my_lse[c0 + c]));
+                            const float p = ex2(__fadd_rn(__fmul_rn(__uint_as_float(v[c]), A.sl2), my_lse[c0 + c]));
                             if (c0 + c >= lo && c0 + c < cols) acc[0].x += p;
                         }
                         __syncwarp();

@@ -463,7 +463,7 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t 
     if (q == out || !aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
     if (!(sm_scale >= 0.f) || sm_scale > FLT_MAX) return VC_ERR_INVALID;
     if (!paged_supported(c) || !paged_rows_ok(c, T, Hq)) return VC_ERR_UNSUPPORTED;
-    // an empty row's maximum, -1e30, stays finite when it is scaled
+    // scores of products up to 1e30, and their differences, stay finite in the log2 domain
     if (sm_scale > 1e8f) return VC_ERR_UNSUPPORTED;
     if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
     if (ws_bytes < paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page,

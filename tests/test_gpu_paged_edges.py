@@ -1,0 +1,68 @@
+"""Paged-cache operators on the GPU at the edges of what they accept: scores far
+outside the usual range, tables much wider than their sequences, batches of
+more sequences than a warp keeps."""
+import pytest
+import torch
+
+import paged_ref
+from helpers import lib
+from paged_ref import U_F32, Batch, close, half_step
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _call(vc, bt, q, scale, scores=None):
+    cache = vc.PagedCache(bt.k, bt.v, bt.block_table)
+    out = torch.full_like(q, 7.0)
+    T, Hq, _ = q.shape
+    if scores is None:
+        ws = vc.Workspace(vc.vc_paged_attn_workspace_bytes(cache, T, Hq))
+        vc.vc_paged_attn(q, cache, bt.q_start, bt.ctx, scale, out, ws)
+    else:
+        ws = vc.Workspace(vc.vc_paged_attn_h2o_workspace_bytes(cache, T, Hq))
+        vc.vc_paged_attn_h2o(q, cache, bt.q_start, bt.ctx, scale, out, scores, ws)
+    assert vc.vc_poll_status(ws) == 0 and int(cache.status) == 0
+    return out
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("power,scale", [(41, 1e8), (0, 1e8), (20, 1.0)])
+@pytest.mark.parametrize("ns,cs", [([1, 1, 1], [30, 200, 9000]), ([3, 40, 2], [60, 9000, 170])])
+def test_scores_of_any_size(dtype, sign, power, scale, ns, cs):
+    """Products up to 1e25 at a scale of 1e8, all of one sign, in whole units
+    (short contexts) and cut ones (9000 tokens): equal largest scores share the
+    weight, all others are too far below to count.  One channel of q and k is
+    set, so every product is exact, and equal products give equal scores.  The
+    weights are then exactly one before the division; what is left is the sum
+    over the values (at most twice (L + 16) half steps of fp32) and the output's
+    rounding."""
+    vc = lib()
+    page, d, G = 16, 64, 2
+    bt = Batch(ns, cs, 1, d, page, dtype, seed=1)
+    key = torch.where(torch.isnan(bt.k), bt.k, torch.zeros_like(bt.k))
+    for b in range(bt.B):
+        for s in range(bt.lens[b]):
+            key[bt.table[b][s // page], 0, s % page, 0] = (1.375 if s % 3 == 0 else 1.625) * 2.0 ** power
+    bt.k = key
+    q = torch.zeros(bt.T, G, d, dtype=dtype, device="cuda")
+    q[:, :, 0] = sign * 1.6875 * 2.0 ** power
+    slots = bt.width * page
+    scores = torch.zeros(bt.B, 1, slots, device="cuda")
+    outs = [_call(vc, bt, q, scale), _call(vc, bt, q, scale, scores)]
+    assert torch.equal(*outs)
+    for b in range(bt.B):
+        k, v = bt.rows(bt.k, b, 0)[:, 0] * sign, bt.rows(bt.v, b, 0)
+        best = torch.zeros(slots, dtype=torch.bool)
+        for i in range(ns[b]):
+            n = cs[b] + i + 1
+            tie = k[:n] == k[:n].max()
+            want = v[:n][tie].mean(0).expand(G, d)
+            tol = 2 * (n + 16) * U_F32 * v[:n][tie].abs().mean(0) + half_step(dtype) * want.abs() * 1.01
+            close(outs[0][bt.start[b] + i], want, tol, f"row {i} of sequence {b}")
+            best[:n] |= tie
+        got = scores[b, 0].cpu()
+        assert torch.isfinite(got).all() and (got[~best] == 0).all() and (got[best] > 0).all()
+        assert got.max() <= ns[b] * G * (1 + (ns[b] * G + 16) * U_F32)
