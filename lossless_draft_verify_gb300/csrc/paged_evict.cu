@@ -252,7 +252,7 @@ select_kernel(Pool S, EvictParams E)
     }
     for (int i = rank * kThreads + threadIdx.x; i < recent; i += Z * kThreads) {
         kept[top + i] = cand + i;
-        if (sc_out) sc_out[top + i] = sc[cand + i];
+        if (sc_out) sc_out[top + i] = __uint_as_float(score_bits(sc[cand + i]));
     }
     sync_all();                                        // no CTA leaves while its counts may be read
 }

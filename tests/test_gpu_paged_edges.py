@@ -66,3 +66,30 @@ def test_scores_of_any_size(dtype, sign, power, scale, ns, cs):
         got = scores[b, 0].cpu()
         assert torch.isfinite(got).all() and (got[~best] == 0).all() and (got[best] > 0).all()
         assert got.max() <= ns[b] * G * (1 + (ns[b] * G + 16) * U_F32)
+
+
+@pytest.mark.parametrize("top,recent,slots", [(20, 10, 128), (0, 60, 128), (500, 30, 128), (20, 70, 17000)])
+def test_evicted_scores_have_no_negative_zero(top, recent, slots):
+    """Zeros of both signs among the chosen and among the newest slots: the
+    scores that come out are zeros without sign."""
+    vc = lib()
+    page, lens = 16, [100, 7]
+    bt = Batch([0, 0], lens, 2, 64, page, BF, seed=3, width=-(-slots // page))
+    src = vc.PagedCache(bt.k, bt.v, bt.block_table)
+    scores = torch.zeros(2, 2, src.slots, device="cuda")
+    scores[..., ::2] = -0.0
+    n = min(top + recent, src.slots)
+    blocks = -(-n // page)
+    k2 = torch.zeros(2 * blocks, 2, page, 64, dtype=BF, device="cuda")
+    dst = vc.PagedCache(k2, k2.clone(), torch.arange(2 * blocks, dtype=torch.int32, device="cuda").view(2, blocks))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n2, kept = torch.zeros(2, **i32), torch.zeros(2, 2, n, **i32)
+    out = torch.full((2, 2, n), 5.0, device="cuda")
+    vc.vc_paged_evict(scores, src, torch.tensor(lens, **i32), top, recent, dst, n2, kept, scores_out=out)
+    torch.cuda.synchronize()
+    for b in range(2):
+        m = int(n2[b])
+        assert m == min(top, max(lens[b] - recent, 0)) + min(recent, lens[b])
+        for h in range(2):
+            assert kept[b, h, :m].tolist() == paged_ref.evict(scores[b, h].tolist(), lens[b], top, recent)
+        assert (out[b, :, :m].view(torch.int32) == 0).all() and (out[b, :, m:] == 5.0).all()
