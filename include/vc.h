@@ -771,7 +771,9 @@ vc_status vc_gemm_ex(const void *x, const void *w, const void *resid, void *out,
  * sequence b owns rows q_start[b] .. q_start[b+1] - 1 (device int32 [B + 1],
  * ascending, q_start[B] <= T), its chunk, possibly none.  ctx_len (device int32 [B]):
  * tokens cached before the chunk; row i of the chunk is slot ctx_len[b] + i.
- * Rows before q_start[0] or from q_start[B] on are left as they are.
+ * Rows before q_start[0] or from q_start[B] on are left as they are.  With
+ * T = 0 nothing is enqueued (no length is looked at), and the arrays of T rows
+ * may be NULL.
  *
  * Errors on the device go to *status (one word, not cleared by the library):
  * VC_PAGED_BAD_PAGE, a table entry outside [0, n_pages) (nothing is read or

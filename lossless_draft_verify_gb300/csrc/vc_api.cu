@@ -459,8 +459,9 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t 
                           int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws,
                           size_t ws_bytes, cudaStream_t stream)
 {
-    if (!paged_ok(c) || !q || !q_start || !ctx_len || !out || !ws || !paged_heads_ok(c, T, Hq)) return VC_ERR_INVALID;
-    if (q == out || !aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
+    if (!paged_ok(c) || !q_start || !ctx_len || !ws || !paged_heads_ok(c, T, Hq)) return VC_ERR_INVALID;
+    if (T > 0 && (!q || !out || q == out)) return VC_ERR_INVALID;      // an empty batch's may be null
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
     if (!(sm_scale >= 0.f) || sm_scale > FLT_MAX) return VC_ERR_INVALID;
     if (!paged_supported(c) || !paged_rows_ok(c, T, Hq)) return VC_ERR_UNSUPPORTED;
     // scores of products up to 1e30, and their differences, stay finite in the log2 domain
@@ -504,9 +505,11 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
                           const int32_t *positions, const int32_t *q_start, const int32_t *ctx_len, int T, int Hq,
                           const vc_paged_cache *cache, void *q_out, cudaStream_t stream)
 {
-    if (!paged_ok(cache) || !qkv || !rope || !q_start || !ctx_len || !q_out) return VC_ERR_INVALID;
+    if (!paged_ok(cache) || !rope || !q_start || !ctx_len) return VC_ERR_INVALID;
+    if (T > 0 && (!qkv || !q_out || qkv == q_out)) return VC_ERR_INVALID;
     if (!paged_heads_ok(cache, T, Hq) || (q_gain == nullptr) != (k_gain == nullptr)) return VC_ERR_INVALID;
-    if (!(eps >= 0.f) || eps > FLT_MAX || qkv == q_out || !aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16) || !aligned(k_gain, 16))
+    if (!(eps >= 0.f) || eps > FLT_MAX || !aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16) ||
+        !aligned(k_gain, 16))
         return VC_ERR_INVALID;
     if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > cache->d) return VC_ERR_INVALID;
     if (!paged_supported(cache) || !paged_rows_ok(cache, T, Hq)) return VC_ERR_UNSUPPORTED;

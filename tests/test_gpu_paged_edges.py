@@ -93,3 +93,23 @@ def test_evicted_scores_have_no_negative_zero(top, recent, slots):
         for h in range(2):
             assert kept[b, h, :m].tolist() == paged_ref.evict(scores[b, h].tolist(), lens[b], top, recent)
         assert (out[b, :, :m].view(torch.int32) == 0).all() and (out[b, :, m:] == 5.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_an_empty_batch(dtype):
+    """Tensors of no rows: every call returns without touching anything."""
+    vc = lib()
+    bt = Batch([0, 0], [30, 7], 2, 64, 16, dtype, seed=4)
+    cache = vc.PagedCache(bt.k, bt.v, bt.block_table)
+    k0 = bt.k.clone()
+    q = torch.empty(0, 4, 64, dtype=dtype, device="cuda")
+    scores = torch.rand(2, 2, cache.slots, device="cuda")
+    before = scores.clone()
+    ws = vc.Workspace(vc.vc_paged_attn_h2o_workspace_bytes(cache, 0, 4))
+    vc.vc_paged_append(torch.empty(0, 8 * 64, dtype=dtype, device="cuda"), cache, bt.q_start, bt.ctx,
+                       torch.empty_like(q), vc.vc_rope_init(64, 1e4))
+    vc.vc_paged_attn(q, cache, bt.q_start, bt.ctx, 0.1, torch.empty_like(q), ws)
+    vc.vc_paged_attn_h2o(q, cache, bt.q_start, bt.ctx, 0.1, torch.empty_like(q), scores, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(scores, before) and int(cache.status) == 0 and vc.vc_poll_status(ws) == 0
+    assert torch.equal(torch.nan_to_num(bt.k.float(), nan=3.0), torch.nan_to_num(k0.float(), nan=3.0))
