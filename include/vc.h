@@ -884,7 +884,8 @@ vc_status vc_paged_attn_h2o(const void *q, const vc_paged_cache *cache, const in
  * as they are.
  * scores as in vc_paged_attn_h2o.  src and dst agree in B, Hkv, d and dt; dst's
  * max_blocks * dst's page, kept_stride and scores_out_stride are each at least
- * min(keep_top + keep_recent, src's max_blocks * page).
+ * min(keep_top + keep_recent, src's max_blocks * page); where that is 0, kept_idx
+ * may be NULL.
  */
 vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_cache *src, const int32_t *src_len,
                          vc_drop_cfg cfg, const vc_paged_cache *dst, int32_t *dst_len, int32_t *kept_idx,

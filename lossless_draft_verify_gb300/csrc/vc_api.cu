@@ -547,7 +547,7 @@ vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_
                          vc_drop_cfg cfg, const vc_paged_cache *dst, int32_t *dst_len, int32_t *kept_idx,
                          int kept_stride, float *scores_out, int scores_out_stride, cudaStream_t stream)
 {
-    if (!scores || !paged_ok(src) || !paged_ok(dst) || !src_len || !dst_len || !kept_idx) return VC_ERR_INVALID;
+    if (!scores || !paged_ok(src) || !paged_ok(dst) || !src_len || !dst_len) return VC_ERR_INVALID;
     if (src_len == dst_len || scores == scores_out) return VC_ERR_INVALID;
     if (src->B != dst->B || src->Hkv != dst->Hkv || src->d != dst->d || src->dt != dst->dt) return VC_ERR_INVALID;
     if (cfg.keep_top < 0 || cfg.keep_recent < 0) return VC_ERR_INVALID;
@@ -556,6 +556,7 @@ vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_
     // neither count can matter past the capacity (and the sum stays in range)
     const int64_t top = cfg.keep_top < cap ? cfg.keep_top : cap, recent = cfg.keep_recent < cap ? cfg.keep_recent : cap;
     const int64_t most = top + recent < cap ? top + recent : cap;
+    if (!kept_idx && most > 0) return VC_ERR_INVALID;
     if (scores_stride < cap || kept_stride < most || (scores_out && scores_out_stride < most) ||
         (int64_t)dst->max_blocks * dst->page < most)
         return VC_ERR_INVALID;

@@ -113,3 +113,20 @@ def test_an_empty_batch(dtype):
     torch.cuda.synchronize()
     assert torch.equal(scores, before) and int(cache.status) == 0 and vc.vc_poll_status(ws) == 0
     assert torch.equal(torch.nan_to_num(bt.k.float(), nan=3.0), torch.nan_to_num(k0.float(), nan=3.0))
+
+
+def test_an_eviction_that_keeps_nothing():
+    """keep_top = keep_recent = 0 with outputs of no entries: the lengths become
+    zero and no page is written."""
+    vc = lib()
+    bt = Batch([0, 0], [30, 7], 2, 64, 16, BF, seed=4)
+    src = vc.PagedCache(bt.k, bt.v, bt.block_table)
+    k2 = torch.full((2, 2, 16, 64), 7.0, dtype=BF, device="cuda")
+    dst = vc.PagedCache(k2, k2.clone(), torch.tensor([[0], [1]], dtype=torch.int32, device="cuda"))
+    i32 = dict(dtype=torch.int32, device="cuda")
+    n = torch.full((2,), -5, **i32)
+    vc.vc_paged_evict(torch.rand(2, 2, src.slots, device="cuda"), src, torch.tensor(bt.lens, **i32), 0, 0, dst, n,
+                      torch.empty(2, 2, 0, **i32), scores_out=torch.empty(2, 2, 0, device="cuda"))
+    torch.cuda.synchronize()
+    assert n.tolist() == [0, 0] and int(src.status) == int(dst.status) == 0
+    assert (dst.k == 7.0).all() and (dst.v == 7.0).all()
