@@ -784,7 +784,7 @@ vc_status vc_gemm_ex(const void *x, const void *w, const void *resid, void *out,
  *
  * Supported: d in {64, 128}, page in {16, 32, 64, 128, 256}, any Hq that is a
  * multiple of Hkv with Hq / Hkv <= 128 and Hq + 2 Hkv <= 2^20; fewer than 2^31
- * slots n_pages * Hkv * page and max_blocks * page, and T * Hq <= 2^30.  No
+ * slots n_pages * Hkv * page, max_blocks * page <= 2^30 and T * Hq <= 2^30.  No
  * output overlaps an input of its call.
  */
 #define VC_PAGED_BAD_PAGE 1

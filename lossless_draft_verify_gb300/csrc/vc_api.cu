@@ -413,13 +413,14 @@ bool paged_ok(const vc_paged_cache *c)
     return aligned(c->k_pages, 16) && aligned(c->v_pages, 16) && aligned(c->block_table, 4) && aligned(c->status, 4);
 }
 
-// valid but not implemented: head sizes, page sizes, pools past 31-bit slot numbers
+// valid but not implemented: head sizes, page sizes, pools past 31-bit slot
+// numbers, sequences past 2^30 (kernels add a CTA's strides to a slot in 32 bits)
 bool paged_supported(const vc_paged_cache *c)
 {
     if (c->d != 64 && c->d != 128) return false;
     if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1))) return false;
     constexpr int64_t kMax = INT32_MAX;
-    return (int64_t)c->n_pages * c->page <= kMax / c->Hkv && c->max_blocks <= kMax / c->page &&
+    return (int64_t)c->n_pages * c->page <= kMax / c->Hkv && c->max_blocks <= (1 << 30) / c->page &&
            c->B <= kMax / 64 / c->Hkv;
 }
 

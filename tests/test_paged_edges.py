@@ -43,3 +43,21 @@ def test_a_batch_without_rows_needs_no_row_arrays(vc):
     assert L.vc_paged_attn(None, c, None, A, 0, 4, 1.0, None, A, ws, None) == 1
     assert L.vc_paged_attn(None, c, A, A, 0, 4, -1.0, None, A, ws, None) == 1
     assert L.vc_paged_attn_h2o(None, c, A, A, 0, 4, 1.0, None, None, 256, A, ws, None) == 1
+
+
+def test_tables_past_two_to_the_30_slots_are_refused(vc):
+    """Slots are 32-bit numbers that the kernels add tiles and strides to: the
+    eviction's last warp ran past 2^31 where a sequence came near it."""
+    L = vc.load()
+    rope = vc.vc_rope_init(64, 1e4)
+    for page, blocks in ((256, (1 << 23) - 1), (256, (1 << 22) + 1), (16, (1 << 26) + 1)):
+        c = _cache(vc, page=page, max_blocks=blocks)
+        assert L.vc_paged_append(A, None, None, 1e-6, rope, None, A, A, 0, 4, c, A + 4096, None) == 2
+        assert L.vc_paged_attn(A, c, A, A, 0, 4, 1.0, A + 4096, A, BIG, None) == 2
+        assert L.vc_paged_attn_h2o(A, c, A, A, 0, 4, 1.0, A + 4096, A, (1 << 31) - 1, A, BIG, None) == 2
+        assert L.vc_paged_attn_workspace_bytes(c, 4, 4) == 0 == L.vc_paged_attn_h2o_workspace_bytes(c, 4, 4)
+        for s, t in ((c, _cache(vc)), (_cache(vc), c)):
+            assert L.vc_paged_evict(A, (1 << 31) - 1, s, A, vc.DropCfg(4, 4), t, A + 64, A, 1 << 30, None, 0, None) == 2
+    c = _cache(vc, page=256, max_blocks=1 << 22)
+    assert L.vc_paged_attn(A, c, A, A, 0, 4, 1.0, A + 4096, A, BIG, None) == 0
+    assert L.vc_paged_attn_workspace_bytes(c, 4, 4) > 0
