@@ -861,7 +861,8 @@ vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_
  * beside the maximum.  scores: device fp32, scores_stride >= max_blocks *
  * page.  Sequences without rows keep their scores.  The workspace of a bf16
  * batch with T * Hq <= 16 * B * Hkv (decoding) also holds the scores of its
- * rows, 4 bytes per query head and table slot.
+ * rows, 4 bytes per query head and table slot, where that is 1 GiB at most;
+ * beyond it K is read a second time.
  */
 size_t vc_paged_attn_h2o_workspace_bytes(const vc_paged_cache *cache, int T, int Hq);
 vc_status vc_paged_attn_h2o(const void *q, const vc_paged_cache *cache, const int32_t *q_start,

@@ -109,6 +109,12 @@ struct WsLayout {
 // The scores of a bf16 batch are stored, for the mass, where it has 16 rows per
 // sequence and kv head at most on average.  Decode step of 16 x 32768 tokens,
 // 32/8 heads: 524 us with a second pass over K, 371 us with stored scores.
+// They are sized by the table, which is as wide as the longest sequence a server
+// allows: past kStoredMost bytes (a decode step of 256 sequences, 32 heads, 32768
+// table slots) the memory is saved at the price of the second pass: full tables at
+// the bound 5.39 ms, just past it 7.34 ms.
+constexpr size_t kStoredMost = size_t(1) << 30;
+
 WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool with_rows)
 {
     WsLayout w;
@@ -121,7 +127,9 @@ WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool 
     w.o = w.ml + align256(n * sizeof(float2));
     w.rows = w.o + align256(n * d * sizeof(float));
     w.stored = w.rows + (with_rows ? align256((size_t)T * Hq * sizeof(float)) : 0);
-    w.s_stride = with_rows && dt == VC_BF16 && (long)T * G <= 16l * B ? (cap + kTcKeys - 1) / kTcKeys * kTcKeys : 0;
+    w.s_stride = (cap + kTcKeys - 1) / kTcKeys * kTcKeys;
+    if (!with_rows || dt != VC_BF16 || (long)T * G > 16l * B || (size_t)T * Hq * w.s_stride * sizeof(float) > kStoredMost)
+        w.s_stride = 0;
     w.bytes = w.stored + align256((size_t)T * Hq * w.s_stride * sizeof(float));
     return w;
 }

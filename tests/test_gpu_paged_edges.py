@@ -130,3 +130,20 @@ def test_an_eviction_that_keeps_nothing():
     torch.cuda.synchronize()
     assert n.tolist() == [0, 0] and int(src.status) == int(dst.status) == 0
     assert (dst.k == 7.0).all() and (dst.v == 7.0).all()
+
+
+def test_mass_under_a_table_too_wide_for_stored_scores():
+    """A decode step whose scores, one per table slot, would take 2 GiB."""
+    vc = lib()
+    lens = [(173 * i) % 700 for i in range(16)]
+    bt = Batch([1] * 16, lens, 2, 64, 256, BF, seed=5, width=1 << 12)
+    cache = vc.PagedCache(bt.k, bt.v, bt.block_table)
+    assert vc.vc_paged_attn_h2o_workspace_bytes(cache, 16, 32) < 1 << 30
+    q = bt.randn(16, 32, 64, scale=1.5)
+    scores = torch.zeros(16, 2, bt.width * 256, device="cuda")
+    out = _call(vc, bt, q, 0.125, scores)
+    want, tol, mass, mtol = paged_ref.attn(bt, q, 0.125)
+    close(out, want, tol, "out")
+    close(scores, mass, mtol, "scores")
+    for b in range(16):
+        assert (scores[b, :, bt.lens[b]:] == 0).all()

@@ -61,3 +61,15 @@ def test_tables_past_two_to_the_30_slots_are_refused(vc):
     c = _cache(vc, page=256, max_blocks=1 << 22)
     assert L.vc_paged_attn(A, c, A, A, 0, 4, 1.0, A + 4096, A, BIG, None) == 0
     assert L.vc_paged_attn_workspace_bytes(c, 4, 4) > 0
+
+
+def test_the_mass_workspace_is_bounded(vc):
+    """Stored scores are sized by the table, which may be much wider than the
+    batch: past 1 GiB of them the call does without."""
+    L = vc.load()
+    for B, n, slots, stored in ((256, 1, 32768, 1 << 30), (256, 1, 131072, 0), (256, 4, 131072, 0), (1, 1, 1 << 23, 1 << 30),
+                                (1, 1, 1 << 24, 0), (16, 1, 32768, 1 << 26)):
+        c = _cache(vc, B=B, Hkv=8, max_blocks=slots // 64)
+        plain = L.vc_paged_attn_workspace_bytes(c, B * n, 32)
+        extra = L.vc_paged_attn_h2o_workspace_bytes(c, B * n, 32) - plain
+        assert stored <= extra <= stored + 4 * B * n * 32 + 512, (B, n, slots)
