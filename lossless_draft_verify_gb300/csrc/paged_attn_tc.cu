@@ -117,7 +117,10 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     if (smem_u32(sm) & 1023u) {                              // never expected: the swizzled tiles need it
-        if (threadIdx.x == 0) report_timeout(A.status, 90);
+        if (threadIdx.x == 0) {
+            report_timeout(A.status, 90);
+            A.parts.desc[blockIdx.x].parts = 0;              // the merge reads it
+        }
         return;
     }
     if (threadIdx.x == 0) {
