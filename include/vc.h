@@ -850,8 +850,8 @@ vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_
                         int T, int Hq, float sm_scale, void *out, void *ws, size_t ws_bytes, cudaStream_t stream);
 
 /*
- * vc_paged_attn_h2o -- vc_paged_attn that also accumulates the attention
- * weight every cached token receives: for kv unit u = b * Hkv + h and slot
+ * vc_paged_attn_h2o -- vc_paged_attn (the same bits in out) that also accumulates
+ * the attention weight every cached token receives: for kv unit u = b * Hkv + h and slot
  * j < ctx_len[b] + n_b,
  *   scores[u * scores_stride + j] += sum over the chunk's rows and the query
  *       heads of h that see j of softmax_j(q . k_j * sm_scale),

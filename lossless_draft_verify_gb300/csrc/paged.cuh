@@ -387,8 +387,8 @@ cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int
 // paged_attn_tc.cu: bf16 on the tensor cores, row tiles of 256
 constexpr int kTcRows = 256, kTcKeys = 128;
 int tc_ctas();
-// s_out (or null): the scores of every row, s_stride apart (a multiple of 128,
-// at least the table's slots), in the log2 domain
+// s_out (or null): the products q . k of every row, s_stride apart (a multiple
+// of 128, at least the table's slots)
 cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                     float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st);
 

@@ -58,13 +58,15 @@ merge_kernel(Parts parts, int G, int Hq, T *__restrict__ out, float *__restrict_
 }
 
 // scores[b][h][j] += sum over the sequence's rows that see slot j of 2^(s - lse),
-// from stored scores: four slots per thread, the rows one after another.  Bound
+// from stored products: four slots per thread, the rows one after another.  A
+// score is rounded before lse is subtracted, as for the row's maximum, so that no
+// weight exceeds one.  Bound
 // by HBM: 4 bytes per row and slot read, 8 per slot for the sums.
 constexpr int kSumThreads = 256, kSumSlots = 4 * kSumThreads;
 
 __global__ void __launch_bounds__(kSumThreads)
-sum_kernel(Pool P, WorkDim W, const float *__restrict__ s_in, long s_stride, const float *__restrict__ lse, int Hq,
-           float *__restrict__ scores, int scores_stride, int chunks)
+sum_kernel(Pool P, WorkDim W, const float *__restrict__ s_in, long s_stride, float sl2, const float *__restrict__ lse,
+           int Hq, float *__restrict__ scores, int scores_stride, int chunks)
 {
     pdl_wait();
     pdl_trigger();
@@ -81,11 +83,12 @@ sum_kernel(Pool P, WorkDim W, const float *__restrict__ s_in, long s_stride, con
     for (int r = 0; r < left; ++r) {
         const float4 x = *reinterpret_cast<const float4 *>(s_in + row * s_stride + j);
         const float e = lse[row];
+        auto weight = [&](float s) { return ex2(__fsub_rn(__fmul_rn(s, sl2), e)); };
         const int last = s.ctx + i - j;                    // slots up to j + last are seen
-        sum[0] += ex2(x.x - e);
-        if (last >= 1) sum[1] += ex2(x.y - e);
-        if (last >= 2) sum[2] += ex2(x.z - e);
-        if (last >= 3) sum[3] += ex2(x.w - e);
+        sum[0] += weight(x.x);
+        if (last >= 1) sum[1] += weight(x.y);
+        if (last >= 2) sum[2] += weight(x.z);
+        if (last >= 3) sum[3] += weight(x.w);
         ++row;
         if (++g == W.G) {
             g = 0;
@@ -102,7 +105,7 @@ sum_kernel(Pool P, WorkDim W, const float *__restrict__ s_in, long s_stride, con
 struct WsLayout {
     size_t desc, ml, o, rows, stored, bytes;
     int rows_cap, n_cta;
-    long s_stride;             // stored scores of a row; 0: not stored
+    long s_stride;             // stored products of a row; 0: not stored
 };
 
 // [status | desc | partial (m, l) | partial o | lse of every row | stored scores]
@@ -167,7 +170,7 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
         if (!stored) return mass_tc(P, W, d, q, Hq, sl2, lse, scores, scores_stride, (int32_t *)ws, st);
         const int chunks = cdiv(cap, kSumSlots);
         return launch_pdl(sum_kernel, dim3((unsigned)(P.B * P.Hkv) * chunks), dim3(kSumThreads), 0, st, P, W,
-                          (const float *)stored, w.s_stride, (const float *)lse, Hq, scores, scores_stride, chunks);
+                          (const float *)stored, w.s_stride, sl2, (const float *)lse, Hq, scores, scores_stride, chunks);
     }
 }
 

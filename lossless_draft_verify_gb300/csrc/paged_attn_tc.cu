@@ -31,8 +31,8 @@
 // the second product (half a step of bf16 per weight, the type the matrix unit
 // takes), out once.
 //
-// With STORE the scores are written out too (fp32, log2 domain), for the
-// attention mass of a batch of few rows: G scores of 4 bytes per key and kv head
+// With STORE the products q . k are written out too (fp32), for the attention
+// mass of a batch of few rows: G scores of 4 bytes per key and kv head
 // beside 4 d bytes of K and V, instead of a second read of K.
 //
 // V rows past the sequence's end may hold any bits and 0 * NaN is not 0: those
@@ -87,7 +87,7 @@ struct Params {
     float *lse_out;
     Parts parts;
     int32_t *status;
-    float *s_out;                  // STORE: scores of row r of q at s_out + r * s_stride
+    float *s_out;                  // STORE: products of row r of q at s_out + r * s_stride
     long s_stride;
     int Hq, box_rows, n_rows;      // n_rows: rows of the pool's tensor map
     float sl2;
@@ -379,10 +379,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             // keys every row of the tile sees
             const int kall = it.ctx + (row0 + (big ? t * 128 : 0)) / A.W.G;
             float *s_row = STORE && valid ? A.s_out + (long)out_row(R) * A.s_stride : nullptr;
-            // m: of the products; with STORE, which scales them anyway, of the scores
-            constexpr float kFloor = STORE ? kLowest : kLowestProduct;
-            const float unit = STORE ? 1.f : A.sl2;          // m * unit: log2 domain
-            float m = kFloor, l = 0.f;
+            float m = kLowestProduct, l = 0.f;               // m: of the products
             const int mine = big ? n : (n + 1 - t) / 2;      // this stream's steps
             // V rows of the last page past the sequence's end, before the product
             // with key tile i (big: stream 0's comes first)
@@ -437,7 +434,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 for (;;) {
                     const float2 sc = make_float2(A.sl2, A.sl2), nm = make_float2(-m, -m);
                     sum[0] = sum[1] = make_float2(0.f, 0.f);
-                    float top[2] = {kFloor, kFloor};
+                    float top[2] = {kLowestProduct, kLowestProduct};
                     uint32_t u[2][32];
                     tc::ld32(tS, u[0]);
 #pragma unroll
@@ -446,12 +443,6 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         if (h < 3) tc::ld32(tS + (h + 1) * 32, u[(h + 1) & 1]);
                         uint32_t (&v)[32] = u[h & 1];
                         if constexpr (STORE) {
-#pragma unroll
-                            for (int c = 0; c < 32; c += 2) {
-                                const float2 s = mul2(make_float2(__uint_as_float(v[c]), __uint_as_float(v[c + 1])), sc);
-                                v[c] = __float_as_uint(s.x);
-                                v[c + 1] = __float_as_uint(s.y);
-                            }
                             if (valid) {
                                 float *dst = s_row + key0 + h * 32;
 #pragma unroll
@@ -467,7 +458,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                             top[e & 1] = fmaxf(top[e & 1], fmaxf(s.x, s.y));
                             // the difference first: zero at the maximum however large the
                             // scores, where an fma would leave the rounding of m * scale
-                            const float2 x = STORE ? add2(s, nm) : mul2(add2(s, nm), sc);
+                            const float2 x = mul2(add2(s, nm), sc);
                             const float2 p = make_float2(ex2(x.x), ex2(x.y));
                             sum[e & 1] = add2(sum[e & 1], p);
                             const __nv_bfloat162 b = __floats2bfloat162_rn(p.x, p.y);
@@ -475,11 +466,11 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         }
                     }
                     const float mx = fmaxf(top[0], top[1]);
-                    const bool grown = (mx - m) * unit > kLazy;
+                    const bool grown = (mx - m) * A.sl2 > kLazy;
                     if (!__any_sync(0xffffffffu, grown)) break;
                     float alpha = 1.f;
                     if (grown) {
-                        alpha = ex2((m - mx) * unit);
+                        alpha = ex2((m - mx) * A.sl2);
                         m = mx;
                     }
                     l *= alpha;
@@ -556,9 +547,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 ++units[0], ++units[1];
                 if (!ok) break;
                 tc::fence_after();
-                finish(m * unit, l, 1.f, 0.f, 0, D);
+                finish(m * A.sl2, l, 1.f, 0.f, 0, D);
             } else {
-                ml_x[t * kRowsTile + r] = make_float2(m * unit, l);
+                ml_x[t * kRowsTile + r] = make_float2(m * A.sl2, l);
                 ok = wait_warp(&S->o_full[0], units[0] & 1, A.status, 98) &&
                      (n == 1 || wait_warp(&S->o_full[1], units[1] & 1, A.status, 99));
                 ++units[0];
@@ -611,7 +602,7 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     A.Hq = Hq;
     A.box_rows = std::min(1 << P.page_log2, BN);
     A.n_rows = (P.n_pages * P.Hkv) << P.page_log2;
-    A.sl2 = std::max(sl2, 1e-30f);     // a masked score is -inf; times zero it would be NaN
+    A.sl2 = std::max(sl2, 1e-38f);     // a masked product is -inf; times zero it would be NaN
     CUtensorMap mk, mv;
     const uint64_t bytes = (uint64_t)D * 2;
     if (!tma_map_bf16_3d(&mk, P.k, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1) ||

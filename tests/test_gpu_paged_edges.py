@@ -147,3 +147,16 @@ def test_mass_under_a_table_too_wide_for_stored_scores():
     close(scores, mass, mtol, "scores")
     for b in range(16):
         assert (scores[b, :, bt.lens[b]:] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ns,cs", [([1] * 5, [3000, 7, 0, 513, 90]), ([4, 0, 30, 150], [2000, 9, 600, 0])])
+def test_scores_change_no_bit_of_the_output(dtype, d, ns, cs):
+    """vc_paged_attn_h2o's output is vc_paged_attn's, with the scores stored (few
+    rows per sequence) and without."""
+    vc = lib()
+    bt = Batch(ns, cs, 2, d, 32, dtype, seed=9)
+    q = bt.randn(bt.T, 8, d, scale=2.0)
+    scores = torch.zeros(bt.B, 2, bt.width * 32, device="cuda")
+    assert torch.equal(_call(vc, bt, q, 0.1), _call(vc, bt, q, 0.1, scores))
