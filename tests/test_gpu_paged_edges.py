@@ -160,3 +160,82 @@ def test_scores_change_no_bit_of_the_output(dtype, d, ns, cs):
     q = bt.randn(bt.T, 8, d, scale=2.0)
     scores = torch.zeros(bt.B, 2, bt.width * 32, device="cuda")
     assert torch.equal(_call(vc, bt, q, 0.1), _call(vc, bt, q, 0.1, scores))
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("rows", [3, 40])
+def test_more_sequences_than_the_search_keeps(dtype, rows):
+    """2100 sequences: the search for a CTA's piece keeps the totals of the
+    first 1024 and goes on from there.  Runs of sequences without rows, and long
+    ones, around its 32- and 1024-sequence marks; few rows per sequence, whose
+    scores are stored, and many."""
+    vc = lib()
+    B = 2100
+    empty = set(range(28, 34)) | set(range(1000, 1030)) | set(range(1500, 1600)) | set(range(2090, 2100))
+    ns = [0 if i in empty else i % rows for i in range(B)]
+    cs = [(37 * i) % 150 for i in range(B)]
+    for b in (27, 34, 64, 999, 1031, 1057, 1700):
+        ns[b], cs[b] = 1 + b % 5, 1500 + b
+    bt = Batch(ns, cs, 1, 64, 32, dtype, seed=6, head_rows=1, tail_rows=2)
+    q = bt.randn(bt.T, 2, 64, scale=1.5)
+    scores = torch.zeros(B, 1, bt.width * 32, device="cuda")
+    out = _call(vc, bt, q, 0.125, scores)
+    assert torch.equal(out, _call(vc, bt, q, 0.125))
+    want, tol, mass, mtol = paged_ref.attn(bt, q, 0.125)
+    close(out[1:-2], want[1:-2], tol[1:-2], "out")
+    assert (out[0] == 7.0).all() and (out[-2:] == 7.0).all()
+    close(scores, mass, mtol, "scores")
+    for b in range(B):
+        assert (scores[b, :, bt.lens[b] if ns[b] else 0:] == 0).all()
+
+
+@pytest.mark.parametrize("ctx", [2300, 4000, 6000, 9000])
+def test_mass_of_many_key_tiles_at_heads_of_128(ctx):
+    """Groups of one, two, three and four key tiles of 128 channels."""
+    vc = lib()
+    bt = Batch([20], [ctx], 8, 128, 64, BF, seed=7)
+    q = bt.randn(bt.T, 32, 128, scale=1.5)
+    scores = torch.zeros(1, 8, bt.width * 64, device="cuda")
+    out = _call(vc, bt, q, 128 ** -0.5, scores)
+    want, tol, mass, mtol = paged_ref.attn(bt, q, 128 ** -0.5)
+    close(out, want, tol, "out")
+    close(scores, mass, mtol, "scores")
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ns,cs", [([1] * 6, [300, 0, 2000, 64, 5, 0]), ([30, 0, 7, 600], [100, 50, 900, 3])])
+def test_a_table_much_wider_than_its_sequences(dtype, ns, cs):
+    """Under a table for 131072 tokens every operator gives what it gives under one
+    of the sequences' own width, bit for bit."""
+    vc = lib()
+    page, d, Hq, Hkv = 32, 64, 4, 2
+    rope = vc.vc_rope_init(d, 1e4)
+    got = []
+    for width in (0, 131072 // page):
+        bt = Batch(ns, cs, Hkv, d, page, dtype, seed=8, width=width)
+        cache = vc.PagedCache(bt.k, bt.v, bt.block_table)
+        qkv = bt.randn(bt.T, (Hq + 2 * Hkv) * d)
+        q = torch.empty(bt.T, Hq, d, dtype=dtype, device="cuda")
+        vc.vc_paged_append(qkv, cache, bt.q_start, bt.ctx, q, rope)
+        scores = torch.zeros(bt.B, Hkv, cache.slots, device="cuda")
+        plain = _call(vc, bt, q, 0.125)
+        out = _call(vc, bt, q, 0.125, scores)
+        assert torch.equal(plain, out)
+        want, tol, mass, mtol = paged_ref.attn(bt, q, 0.125)
+        close(out, want, tol, "out")
+        close(scores, mass, mtol, "scores")
+        i32 = dict(dtype=torch.int32, device="cuda")
+        n2, kept = torch.zeros(bt.B, **i32), torch.full((bt.B, Hkv, 90), -1, **i32)
+        k2 = torch.zeros(3 * bt.B, Hkv, page, d, dtype=dtype, device="cuda")
+        dst = vc.PagedCache(k2, k2.clone(), torch.arange(3 * bt.B, **i32).view(bt.B, 3))
+        vc.vc_paged_evict(scores, cache, torch.tensor(bt.lens, **i32), 70, 20, dst, n2, kept)
+        torch.cuda.synchronize()
+        assert int(cache.status) == int(dst.status) == 0
+        w = max(bt.lens)
+        got.append((q, plain, out, scores[..., :w].clone(), n2, kept, dst.k, dst.v))
+        for b in range(bt.B):
+            for h in range(Hkv):
+                keep = paged_ref.evict(scores[b, h].tolist(), bt.lens[b], 70, 20)
+                assert kept[b, h, :len(keep)].tolist() == keep
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
