@@ -110,13 +110,14 @@ struct WorkDim {
 // A unit of at most kWhole is never cut: merging its parts would take longer
 // than it does.  It belongs to the CTA in whose piece its middle lies.  A piece
 // costs at least kMinPiece.
-// Measured with the tensor-core kernel (row tiles of 256) on a batch of nine
-// sequences (chunks of 1 to 700 over up to 20000 tokens, 28/4 heads, pages of
-// 16): 806 us at kUnitCost 2, 745 at 4, 606 at 9, 505 at 16, 502 at 20; a decode
-// step of 16 x 32768 tokens 313 us at 2, 323 at 16, 331 at 28.  The CUDA-core
-// kernels' tiles take longer and their units less: four sequences of 17 tokens
-// at most over 2000 in fp32 25.6 us with 1, 2, 3 and 34.4 with 4, 6, 8 (with one
-// stage for the key tiles; 22.5 now).
+// Single calls, inputs not in L2, at a kUnitCost of 2, 9, 16 and 24 for row tiles
+// of 256 (heads of 128): nine sequences (chunks of 1 to 700 over up to 20000
+// tokens, 28/4 heads, pages of 16) 682, 523, 494 and 493 us; a decode step of 16
+// x 32768 tokens 336, 334, 336 and 343, of 256 x 300 tokens 142, 142, 150 and 148;
+// 16 x 33 over 32768 400, 399, 400 and 410.  The CUDA-core kernels' tiles take
+// longer and their units less: at 1, 2, 4 and 8 a token of 8 sequences over 4000
+// takes 163, 162, 169 and 175 us, four chunks of 300 over 2000 578, 582, 585 and
+// 590, four chunks up to 17 over 2000 at most 27, 27, 27 and 25.
 template <int BM>
 struct Cost {
     static constexpr int kUnitCost = BM == 256 ? 16 : 1;

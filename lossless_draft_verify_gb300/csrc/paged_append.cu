@@ -5,8 +5,8 @@
 //   x' = x / sqrt(mean(x^2) + eps) * gain                  (optional)
 //   (x'_j, x'_{j + r/2}) turned by pos * w_j, j < r/2       (r = rotary_dim)
 //
-// Bound by HBM: every value is read once and written once, about ten
-// operations each.  A head's row is held by D/16 lanes, two 8-channel chunks
+// Every value is read once and written once, about ten operations each: its
+// floor is HBM's, what bounds it is latency (see launch).  A head's row is held by D/16 lanes, two 8-channel chunks
 // per lane chosen so that both halves of a rotated pair meet in one lane (no
 // exchange but the D/16-lane sum of squares).  Angles: w_j / 2 pi is kept as a
 // 64-bit fraction of a turn, so pos * w_j modulo one turn is an integer
@@ -84,8 +84,8 @@ struct AppendParams {
 // TPB tokens per CTA; blockIdx.y takes its share of the heads.  A lane group
 // keeps its next head in flight, as read: the first one while the tokens'
 // sequences, pages and angles are looked up, each other one under the arithmetic
-// of the one before (22.9 us at 4670 tokens when it is read after it, 20.2 and
-// 21.5 with two and three in flight).
+// of the one before (in a graph 19.5 us at 4670 tokens, 22.9 when it is read after
+// it, 20.2 and 21.5 with two and three in flight).
 template <typename E, int D, int TPB>
 __global__ void __launch_bounds__(kThreads, 4)
 append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
@@ -227,9 +227,12 @@ cudaError_t launch(const AppendParams &A, const vc_rope &rope, cudaStream_t st)
     const int heads = A.Hq + 2 * A.P.Hkv, groups = kThreads / (D / 16);
     // Few tokens: one per CTA, its heads over several CTAs, one head per lane
     // group; many: four per CTA, which share the look-ups and the sines.  32/8
-    // heads of 128 in bf16: 16 tokens 3.3 against 6.9 us, 600 tokens 6.8 against
-    // 7.0, 2400 tokens 21.1 against 10.5, 4670 tokens 44.0 against 22.9, and 19.5
-    // with the next head in flight (115 MB, 87% of the measured copy rate).
+    // heads of 128 in bf16, in a graph, one and four per CTA: 16 tokens 3.9 and 6.4
+    // us, 600 7.0 and 6.7, 1200 11.3 and 7.8, 2400 20.5 and 11.2, 4670 37.3 and 19.5.
+    // The last moves 115 MB, which about fills L2 from one replay to the next; with
+    // inputs that are not there the call takes 24.1 us, 70% of the measured copy
+    // rate: sequence, page and angles of four tokens are looked up before a CTA's
+    // first store, in two waves of CTAs.
     if (A.T <= 4 * device_sm_count())
         return launch_pdl(append_kernel<E, D, 1>, dim3(A.T, cdiv(heads, groups)), dim3(kThreads), 0, st, A, rope);
     return launch_pdl(append_kernel<E, D, 4>, dim3(cdiv(A.T, 4)), dim3(kThreads), 0, st, A, rope);

@@ -56,9 +56,8 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // the same rows' outputs at channels 4 tx + 64 j.  Products are taken two
 // channels at a time (half the instructions).  Bound by shared memory's reads and
 // the instructions around them: four chunks of 300 over 2000 tokens, 16/4 heads
-// of 128, 572 us, 37 TFLOP/s (674 with one stage and single products, 821 and 725
-// with tiles of 64 keys or 8 rows per thread, for which fewer warps fit); a token of
-// 8 sequences over 4000, 32/8 heads, 159 us, 1.7 TB/s (252 with one stage).
+// of 128, 572 us, 37 TFLOP/s (larger tiles leave room for fewer warps); a token of
+// 8 sequences over 4000, 32/8 heads, 157 us, 1.7 TB/s.
 template <int D, int BM, int BN>
 __global__ void __launch_bounds__(kThreads)
 attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float scale_log2, float *__restrict__ out,
@@ -238,10 +237,9 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
 
 // Where the key tiles that the block table can hold are fewer than three per SM
 // and the sequences have this many rows on average, a cluster shares a tile's
-// rows.  16/4 heads of 128, with the attention, before the tiles had two stages:
-// one prompt of 900 211 against 783 us with one CTA per tile, 8 prompts of 600 (320
-// tiles) 769 against 907, 4 chunks of 300 over 2000 tokens (576 tiles) 1260 against
-// 1058.  With them 185, 635 and 875.
+// rows.  16/4 heads of 128, with the attention, rows shared and one CTA per tile:
+// one prompt of 900 194 and 439 us, 8 prompts of 600 (320 tiles) 643 and 643, 4
+// chunks of 300 over 2000 tokens (576 tiles) 1039 and 883.
 constexpr long kSplitRows = 1024;
 
 // ----- attention mass ---------------------------------------------------------------

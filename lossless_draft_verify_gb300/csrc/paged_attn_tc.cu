@@ -18,12 +18,10 @@
 // streams are the unit's two row tiles, sharing every K/V tile; with fewer they
 // take the key tiles alternately for the same rows and are merged at the end,
 // so that a short unit, which HBM bounds, has both softmax groups on it.
-// Measured: a decode step of 16 x 32768 tokens, 32/8 heads, 318 us = 6.75 TB/s;
-// 2048 tokens over 30000 786 to 794 us = 1.32 PFLOP/s at the power limit (720 in a
-// short run below it, 779 with one load of Q at a time per thread).
-// A stream's chain S, softmax, P V bounds the latter: 64-key steps with S twice
-// buffered (950 us), two threads per row (824 us) and the first half's product
-// under the second's exponentials (802 us) do not shorten it.
+// Measured, 32/8 heads of 128: a decode step of 16 x 32768 tokens 318 us = 6.75
+// TB/s; 2048 tokens over 30000 785 to 805 us = 1.31 PFLOP/s at the power limit
+// (735 in a short run below it), bound by a stream's chain S, softmax, P V.  Heads
+// of 64: 204 us (5.3 TB/s) and 648.
 //
 // The running maximum is raised only when it grows by more than 2^8 (P and the
 // sum then stay within fp32 and bf16 range), so O is rarely rescaled; the sum
@@ -457,7 +455,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                             const float2 s = make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1]));
                             top[e & 1] = fmaxf(top[e & 1], fmaxf(s.x, s.y));
                             // the difference first: zero at the maximum however large the
-                            // scores, where an fma would leave the rounding of m * scale
+                            // scores, where an fma would leave the rounding of m * scale (and
+                            // take 1 to 2% less on prompts; the fma in warps without large
+                            // scores only takes 10% more)
                             const float2 x = mul2(add2(s, nm), sc);
                             const float2 p = make_float2(ex2(x.x), ex2(x.y));
                             sum[e & 1] = add2(sum[e & 1], p);

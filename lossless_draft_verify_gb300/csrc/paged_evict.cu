@@ -8,8 +8,7 @@
 // image of the scores) with one histogram per CTA in shared memory finds the
 // threshold; in a cluster each CTA adds up an eighth of the digits through
 // distributed shared memory, and the one that holds the searched digit tells
-// the others (all digits in every CTA, for one barrier a pass instead of three,
-// takes longer: 90 against 62 us for 128 units of 4000 tokens).
+// the others.
 // Every warp owns a run of consecutive slots; its counts above and at the
 // threshold, prefixed over warps and CTAs, give the place of its first kept
 // slot, and ballots order the rest.  The scores are read from memory once, 16
@@ -331,9 +330,10 @@ cudaError_t evict(const Pool &S, const Pool &Dp, int row_bytes, const float *sco
     E.recent = recent;
     const int units = S.B * S.Hkv;
     const long cap = (long)S.max_blocks << S.page_log2;
-    // A table that one CTA's shared memory covers needs no cluster: the tokens of
-    // 256 (sequence, head) units, 1000 each, 42 us with the moves against 127, of 128
-    // units of 16000 29 against 64; of 8 units of 16000 18 against 16.
+    // A table that one CTA's shared memory covers needs no cluster.  With the moves,
+    // in single calls, one CTA and a cluster: 256 (sequence, head) units of 1000
+    // tokens 46 and 132 us, 128 units of 16000 33 and 70, 8 units of 16000 25 and 23,
+    // of 2000 17 and 23.  A wider table takes the cluster whatever its sequences hold.
     cudaError_t e = cap <= kCache ? select<1>(S, E, units, cap, st) : select<kCluster>(S, E, units, cap, st);
     if (e != cudaSuccess) return e;
     // about 12 CTAs per SM, none without a row to move

@@ -7,7 +7,7 @@
 // One fma gives the exponent where no |lse| of a row tile is above 2^20 (it is
 // then off by 2^-5, lse's rounding, at most).  Above, the scaled score is rounded
 // first, as it was for the row's maximum, so that no weight exceeds one whatever
-// the scores' size (in every tile: 395 against 382 us for the two chunks below).
+// the scores' size (in every tile 3% more for the two chunks below).
 //
 // The product is taken transposed, S^T = K Q^T: a key is a row of the
 // accumulator, so one thread holds all of a key's weights for 128 query rows
@@ -16,19 +16,18 @@
 // shared memory while the sequence's row tiles pass (a row tile is floor(128 / G)
 // queries of the G heads, one TMA box), so K is read from HBM once and a row tile
 // from L2 once per group.  With one row tile (decoding) this is a stream of K,
-// bound by HBM; with many by the sums' arithmetic and waits: about 150 us after
-// the 222 of the attention for two 512-token chunks over 16000 tokens, 32/8
-// heads, the tensor cores busy a third of it.
-// A batch's groups all have the size that leaves the busiest CTA the least: with
-// 512 tokens over 8000 122 us (with the attention) against 127 with shares cut at
-// any key tile, four chunks of 300 over 4000, 7 query heads to each of 8, 240 against 259, a prompt
-// of 2048 over 8000 484 against 461, and 528 with groups of four.  Groups of two or
-// one everywhere cost more than they give (471 and 656 us against 404 and 583), and
-// so do accumulators in two halves, the second product under the first one's sums
-// (414 against 370).
+// bound by HBM; with many by the sums' arithmetic and waits: 156 us after the 230
+// of the attention for two 512-token chunks over 16000 tokens, 32/8 heads, the
+// tensor cores busy a third of it.
+// A batch's groups all have one size, chosen by an estimate (find_share).  With
+// the attention, in single calls, as chosen and with groups of 1, 2, 3, 4: two
+// chunks of 512 over 16000 387 us and 521, 406, 382, 384; 512 over 8000 131 and
+// 174, 144, 152, 131; 2048 over 8000 498 and 648, 534, 485, 532; four of 300 over
+// 4000, 7 query heads to each of 8, 247 and 350, 275, 265, 244; a fresh prompt of
+// 1500, 8/1 heads, 169 and 163, 181, 211, 254.  The last has 12 key tiles: work is
+// not divided over rows, so most SMs are idle there.
 //   warps 0-15      sums, four warps to a key tile of the group and to one of
-//                   four accumulators (two sets of four, each with every other
-//                   tile: 454 against 404 us, before, for the two chunks above);
+//                   four accumulators;
 //   warp 16         producer; warp 17 issues the MMAs.
 #include "paged.cuh"
 #include "tcgen05.cuh"
@@ -98,9 +97,11 @@ struct Params {
     float sl2;
 };
 
-// One warp finds where the CTA's share begins.  First the size of the groups: a
-// round of a group of k tiles (a row tile's products and sums) takes about
-// 0.7 + 0.4 k us, and the CTA with the most groups is the last one.
+// One warp finds where the CTA's share begins.  First the size of the groups, by
+// an estimate: a round of a group of k tiles (a row tile's products and sums)
+// takes about 0.7 + 0.4 k us, every group has the batch's average rounds (rows
+// that see none of a group's keys counted too), and the CTA with the most groups
+// is the last one.
 __device__ __forceinline__ void find_share(const Params &A, int cta, int n_cta, MassWalk *out)
 {
     const int lane = threadIdx.x & 31;
