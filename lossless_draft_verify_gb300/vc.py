@@ -770,7 +770,8 @@ def vc_swap_in_paced(dst: torch.Tensor, src_pinned: torch.Tensor, gbps: float, p
 class PagedCache:
     """A page pool and the block table of one batch (include/vc.h,
     vc_paged_cache): k, v [n_pages][Hkv][page][d], block_table int32
-    [B][max_blocks].  The tensors stay the caller's; several caches may name
+    [B][max_blocks].  The tensors stay the caller's, who fills them in place
+    (another table or pool needs another PagedCache); several caches may name
     one pool."""
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor):
