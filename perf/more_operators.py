@@ -1,0 +1,429 @@
+"""The 8-bit paged cache and attention over shared prefixes: what they compute,
+and the calls that reach them.
+
+A server drafts on a cache that costs half the memory and half the reads, and
+many of its sequences begin with the same tokens.  Four operators:
+
+  write   per-head RMS norm of queries and keys, position rotation, and the new
+          keys and values into 8-bit pages: e4m3 codes, one power-of-two scale
+          per (token, head), the smallest under which the row's largest value fits
+  read    cached tokens back from 8-bit pages, as packed rows
+  attn    causal attention of ragged chunks over 8-bit pages
+  shared  the same over 8-bit or full-precision pages, where the sequences of a
+          group share the pages of a prefix: one pass over it for all of them
+
+`run` computes them with elementary torch operations, or with `own` by the
+framework's entry points.
+"""
+import math
+import random
+
+import torch
+
+own = False
+
+EPS = 1e-6
+THETA = 500000.0
+
+
+# ------------------------------------------------------------------- cases --
+def listed():
+    dec = dict(Hq=32, Hkv=8, d=128, page=64, dtype="bf16")
+    return [
+        # one draft step of 16 sequences: a few hundred kB, launch latency counts
+        dict(name="write decode", op="write", B=16, n=1, ragged=0, ctx=500, pos0=30000, rotary=128, norm=True, **dec),
+        # prompts compressed as they are read in: 5 sequences, up to 3000 tokens each
+        dict(name="write prompts", op="write", B=5, n=3000, ragged=1, ctx=100, pos0=100000, rotary=128, norm=True,
+             **dec),
+        # drafted blocks of the fp32 model of the losslessness checks, read back for a comparison
+        dict(name="read fp32", op="read", B=4, n=65, ragged=3, ctx=300, Hkv=2, d=64, page=32, dtype="fp32"),
+        # four compressed sequences handed to another cache
+        dict(name="read long", op="read", B=4, n=32768, ragged=0, ctx=0, Hkv=8, d=128, page=64, dtype="bf16"),
+        # the shortest call: one sequence, one token, a short context
+        dict(name="attn one token", op="attn", B=1, n=1, ragged=0, ctx=200, Hq=8, Hkv=8, d=64, page=16, dtype="bf16"),
+        # a draft step of 16 sequences with 32k tokens each
+        dict(name="attn decode", op="attn", B=16, n=1, ragged=0, ctx=32768, **dec),
+        # a chunk of a long prompt over its compressed beginning
+        dict(name="attn prompt chunk", op="attn", B=1, n=2048, ragged=0, ctx=30000, **dec),
+        # a mixed batch of the fp32 model: drafted blocks over short contexts
+        dict(name="attn fp32", op="attn", B=4, n=17, ragged=3, ctx=2000, Hq=4, Hkv=2, d=64, page=32, dtype="fp32"),
+        # four chats with one instruction of 600 tokens, at their first words
+        dict(name="shared few", op="shared", B=4, groups=1, n=1, ragged=0, prefix=600, ctx=40, Hq=8, Hkv=8, d=64,
+             page=16, dtype="bf16", bits=16),
+        # a decode step of 32 conversations about one document of 32k tokens
+        dict(name="shared decode", op="shared", B=32, groups=1, n=1, ragged=5, prefix=32768, ctx=700, bits=16, **dec),
+        # verification of 16 drafts of 24 sequences in 3 groups of their own length, 7 query heads per kv head
+        dict(name="shared verify", op="shared", B=24, groups=3, n=17, ragged=6, prefix=16000, ctx=1500, Hq=28, Hkv=4,
+             d=128, page=16, dtype="bf16", bits=16),
+        # the draft step of the same over a compressed cache
+        dict(name="shared 8-bit", op="shared", B=32, groups=2, n=1, ragged=7, prefix=32000, ctx=2000, bits=8, **dec),
+    ]
+
+
+def _log(rng, lo, hi):
+    return max(lo, min(hi, int(round(math.exp(rng.uniform(math.log(lo), math.log(hi)))))))
+
+
+def draw(rng):
+    op = rng.choice(["write", "read", "attn", "attn", "shared", "shared"])
+    dtype = rng.choice(["bf16", "bf16", "bf16", "fp32"])
+    d = rng.choice([64, 128])
+    page = rng.choice([16, 32, 64, 128, 256])
+    Hkv = rng.choice([1, 2, 4, 8])
+    c = dict(op=op, dtype=dtype, d=d, page=page, Hkv=Hkv, ragged=rng.randrange(1, 1 << 20))
+    if op == "read":
+        n = _log(rng, 1, 32768)
+        c.update(n=n, B=_log(rng, 1, max(1, min(64, 4 * 32768 // n))), ctx=rng.randrange(0, 500))
+        return c
+    Hq = c["Hq"] = Hkv * rng.choice([1, 2, 3, 4, 7, 8])
+    if op == "write":
+        n = _log(rng, 1, 4000)
+        c.update(n=n, B=_log(rng, 1, max(1, min(64, 4000 // n))), ctx=rng.randrange(0, 300),
+                 pos0=_log(rng, 1, 1000000), rotary=rng.choice([d, d, d // 2]), norm=rng.random() < 0.7)
+        return c
+    n = _log(rng, 1, 1500) if op == "attn" else _log(rng, 1, 200)
+    ctx = _log(rng, 1, 30000) if op == "attn" else _log(rng, 1, 2000)
+    prefix = 0 if op == "attn" else _log(rng, 1, 30000)
+    most = 3e4 * 2048 * 32 * 128 / (8 if dtype == "fp32" else 1)       # rows x keys x channels of the largest
+    B = _log(rng, 1, 32)
+    while B > 1 and (B * n * (n + ctx + prefix) * Hq * d > most or B * (prefix + ctx + n) * Hkv > 16 * 32768 * 4):
+        B -= 1
+    while n > 1 and n * (n + ctx + prefix) * Hq * d > most:
+        n = n * 2 // 3
+    c.update(n=n, ctx=ctx, B=B)
+    if op == "shared":
+        c.update(prefix=prefix, groups=rng.randint(1, max(1, B // 2)), bits=rng.choice([16, 8]))
+    return c
+
+
+def _lengths(case):
+    """(chunk lengths, context lengths, [(first sequence, prefix)] of the groups) of the case's sequences."""
+    B, n, ctx = case["B"], case["n"], case["ctx"]
+    r = random.Random(case["ragged"])
+    if not case["ragged"]:
+        ns, cs = [n] * B, [ctx] * B
+    else:
+        ns = [r.randint(1, n) for _ in range(B)]
+        cs = [r.randint(0, ctx) for _ in range(B)]
+        if case["op"] == "attn" and B > 2:
+            ns[0], cs[1] = 1, 0                   # a decode step and a fresh prompt among the chunks
+        cs[-1] = ctx
+    if case["op"] != "shared":
+        return ns, cs, []
+    cut = sorted(r.sample(range(1, B), case["groups"] - 1)) if B > 1 else []
+    groups = [(b, case["prefix"] if i == 0 or not case["ragged"] else r.randint(1, case["prefix"]))
+              for i, b in enumerate([0] + cut)]
+    for (b, p), e in zip(groups, cut + [B]):
+        for i in range(b, e):
+            cs[i] += p                            # the context begins with the prefix
+    return ns, cs, groups
+
+
+def _shared_blocks(case, groups, b):
+    """Pages of sequence b's prefix that it shares: whole ones."""
+    return max([(g, p) for g, p in groups if g <= b])[1] // case["page"] if groups else 0
+
+
+def work(case):
+    e = 2 if case["dtype"] == "bf16" else 4
+    ns, cs, groups = _lengths(case)
+    d, Hkv, T = case["d"], case["Hkv"], sum(ns)
+    row8 = d + 1                                  # codes and a scale
+    if case["op"] == "write":
+        Hq = case["Hq"]
+        return {"bytes": T * ((Hq + 2 * Hkv) * d * e + Hq * d * e + 2 * Hkv * row8) + 4 * T,
+                "flops": 12 * T * (Hq + 2 * Hkv) * d}
+    if case["op"] == "read":
+        return {"bytes": 2 * T * Hkv * (row8 + d * e), "flops": 2 * T * Hkv * d}
+    Hq, L = case["Hq"], T + sum(cs)
+    rows = sum(n * c + n * (n + 1) // 2 for n, c in zip(ns, cs))
+    if groups:
+        ends = [b for b, _ in groups[1:]] + [case["B"]]
+        L -= sum((e2 - b - 1) * (p // case["page"]) * case["page"] for (b, p), e2 in zip(groups, ends))
+    kv = row8 if case.get("bits", 8) == 8 else d * e
+    return {"bytes": 2 * T * Hq * d * e + 2 * L * Hkv * kv, "flops": 4 * rows * Hq * d}
+
+
+# ------------------------------------------------------------------ inputs --
+def _pool(case, lens, groups, gen, spare=3):
+    """Pages in random order for sequences of `lens` tokens, the whole pages of
+    a group's prefix being those of its first sequence; table entries past a
+    sequence's last page are -1."""
+    page = case["page"]
+    blocks = [-(-L // page) for L in lens]
+    same = [_shared_blocks(case, groups, b) for b in range(len(lens))]
+    n_pages = sum(blocks) + spare
+    order = torch.randperm(n_pages, generator=gen, device="cuda", dtype=torch.int32)
+    table = torch.full((len(lens), max(max(blocks), 1)), -1, dtype=torch.int32, device="cuda")
+    at, first = 0, 0
+    for b, m in enumerate(blocks):
+        table[b, :m] = order[at:at + m]
+        at += m
+        if any(g == b for g, _ in groups):
+            first = b
+        elif same[b]:
+            table[b, :same[b]] = table[first, :same[b]]
+    return n_pages, table, (n_pages, case["Hkv"], page, case["d"])
+
+
+def _scales(amax):
+    """Bytes of the power-of-two scales 2^(byte - 127) of rows with these largest
+    magnitudes: the smallest with amax <= 448 * scale."""
+    m, e = torch.frexp(amax)                      # amax = m 2^e, m in [0.5, 1)
+    e = torch.where(m > 0.875, e, e - 1) - 8
+    return torch.where(amax == 0, 1, (e + 127).clamp(1, 246))
+
+
+def _power(byte):
+    return (byte.int() << 23).view(torch.float32)
+
+
+def _quantise(x):
+    """fp32 rows [..., d] -> (e4m3 codes, scale bytes [...])."""
+    byte = _scales(x.abs().amax(-1))
+    return (x * _power(254 - byte)[..., None]).to(torch.float8_e4m3fn), byte.to(torch.uint8)
+
+
+def prepare(case, seed):
+    dtype = torch.bfloat16 if case["dtype"] == "bf16" else torch.float32
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    ns, cs, groups = _lengths(case)
+    B, d, Hkv = case["B"], case["d"], case["Hkv"]
+    i32 = dict(dtype=torch.int32, device="cuda")
+
+    def normal(*shape, scale=1.0):
+        return torch.randn(*shape, generator=gen, device="cuda", dtype=dtype) * scale
+
+    lens = [n + c for n, c in zip(ns, cs)]
+    n_pages, table, shape = _pool(case, lens, groups, gen)
+    T = sum(ns)
+    start = [0]
+    for n in ns:
+        start.append(start[-1] + n)
+    s = dict(case=case, dtype=dtype, ns=ns, cs=cs, lens=lens, table=table, n_pages=n_pages, scale=d ** -0.5, T=T,
+             max_n=max(ns), max_len=max(lens), bits=case.get("bits", 8))
+    s["ctx"], s["start"] = torch.tensor(cs, **i32), torch.tensor(start, **i32)
+    s["seq"] = torch.repeat_interleave(torch.arange(B, device="cuda"), torch.tensor(ns, device="cuda"))
+    s["at"] = torch.arange(T, device="cuda") - s["start"][s["seq"]].long()      # a row's place in its chunk
+    if case["op"] == "write":
+        Hq = case["Hq"]
+        s["qkv"] = normal(T, (Hq + 2 * Hkv) * d)
+        s["qg"], s["kg"] = normal(d, scale=0.1) + 1, normal(d, scale=0.1) + 1
+        s["pos"] = (s["at"] + case["pos0"] + 17 * s["seq"]).int()
+        s["q"] = torch.zeros(T, Hq, d, dtype=dtype, device="cuda")
+        for x in "kv":
+            s[x] = torch.zeros(shape, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+            s[x + "s"] = torch.ones(shape[:3], dtype=torch.uint8, device="cuda").view(torch.float8_e8m0fnu)
+    else:
+        # keys with channels of their own size, values with tokens of their own size
+        gain = torch.randn(d, generator=gen, device="cuda").mul_(0.5).exp_()
+        for x in "kv":
+            rows = normal(*shape) * (gain if x == "k" else torch.rand(shape[:3] + (1,), generator=gen, device="cuda") + 0.5)
+            if s["bits"] == 8:
+                s[x], byte = _quantise(rows.float())
+                s[x + "s"] = byte.view(torch.float8_e8m0fnu)
+            else:
+                s[x] = rows.to(dtype)
+        if case["op"] == "read":
+            s["ko"], s["vo"] = (torch.zeros(T, Hkv, d, dtype=dtype, device="cuda") for _ in "kv")
+        else:
+            s["q"] = normal(T, case["Hq"], d, scale=1.2)
+            s["out"] = torch.zeros(T, case["Hq"], d, dtype=dtype, device="cuda")
+            if case["op"] == "shared":
+                s["first"] = torch.tensor([b for b, _ in groups] + [B], **i32)
+                s["prefix"] = torch.tensor([p for _, p in groups], **i32)
+    if own:
+        from lossless_draft_verify_gb300 import vc
+        if s["bits"] == 8:
+            s["cache"] = vc.Paged8Cache(s["k"], s["v"], s["ks"], s["vs"], table, dtype)
+        else:
+            s["cache"] = vc.PagedCache(s["k"], s["v"], table)
+        if case["op"] == "write":
+            s["rope"] = vc.vc_rope_init(case["rotary"], THETA)
+        elif case["op"] == "attn":
+            s["ws"] = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(s["cache"], T, case["Hq"]))
+        elif case["op"] == "shared":
+            size = vc.vc_paged8_attn_shared_workspace_bytes if s["bits"] == 8 else vc.vc_paged_attn_shared_workspace_bytes
+            s["ws"] = vc.Workspace(size(s["cache"], len(groups), T, case["Hq"]))
+    return s
+
+
+# --------------------------------------------------------------------- run --
+def run(s):
+    return _RUN[s["case"]["op"]](s)
+
+
+def _slots(s):
+    """(page, row of the page) of every row's slot."""
+    page = s["case"]["page"]
+    slot = s["ctx"].long()[s["seq"]] + s["at"]
+    return s["table"].long()[s["seq"], slot // page], slot % page
+
+
+def _write(s):
+    c = s["case"]
+    Hq, Hkv, d, r = c["Hq"], c["Hkv"], c["d"], c["rotary"]
+    if own:
+        from lossless_draft_verify_gb300 import vc
+        vc.vc_paged8_append(s["qkv"], s["cache"], s["start"], s["ctx"], s["q"], s["rope"], positions=s["pos"],
+                            q_gain=s["qg"] if c["norm"] else None, k_gain=s["kg"] if c["norm"] else None, eps=EPS)
+        return s["q"], s["k"], s["v"], s["ks"], s["vs"]
+    x = s["qkv"].view(s["T"], Hq + 2 * Hkv, d).float()
+    qk = x[:, :Hq + Hkv]
+    if c["norm"]:
+        gain = torch.cat([s["qg"].float().expand(Hq, d), s["kg"].float().expand(Hkv, d)])
+        qk = qk * torch.rsqrt(qk.square().mean(-1, keepdim=True) + EPS) * gain
+    w = THETA ** (-2.0 * torch.arange(r // 2, device="cuda", dtype=torch.float64) / r)
+    angle = s["pos"].double()[:, None, None] * w
+    cos, sin = angle.cos().float(), angle.sin().float()
+    a, b = qk[..., :r // 2], qk[..., r // 2:r]
+    qk = torch.cat([a * cos - b * sin, b * cos + a * sin, qk[..., r:]], -1)
+    s["q"].copy_(qk[:, :Hq])
+    where, row = _slots(s)
+    for name, rows in (("k", qk[:, Hq:]), ("v", x[:, Hq + Hkv:])):
+        codes, byte = _quantise(rows)
+        s[name].view(torch.uint8)[where, :, row] = codes.view(torch.uint8)
+        s[name + "s"].view(torch.uint8)[where, :, row] = byte
+    return s["q"], s["k"], s["v"], s["ks"], s["vs"]
+
+
+def _read(s):
+    if own:
+        from lossless_draft_verify_gb300 import vc
+        vc.vc_paged8_read(s["cache"], s["start"], s["ctx"], s["ko"], s["vo"])
+        return s["ko"], s["vo"]
+    where, row = _slots(s)
+    for x in "kv":
+        codes = s[x].view(torch.uint8)[where, :, row].view(torch.float8_e4m3fn)
+        s[x + "o"].copy_(codes.float() * _power(s[x + "s"].view(torch.uint8)[where, :, row])[..., None])
+    return s["ko"], s["vo"]
+
+
+def _rows(s, x):
+    """[B][Hkv][tokens][d] in fp32 of the batch's cached tokens (whole pages)."""
+    pages, table = s[x], s["table"]
+    at = table[:, :-(-s["max_len"] // pages.shape[2])].long().clamp(min=0)
+    if s["bits"] == 8:
+        rows = pages.view(torch.uint8)[at].view(torch.float8_e4m3fn).float()
+        rows = rows.mul_(_power(s[x + "s"].view(torch.uint8)[at])[..., None])
+    else:
+        rows = pages[at].float()
+    return rows.transpose(1, 2).reshape(table.shape[0], pages.shape[1], -1, pages.shape[3])
+
+
+def _attn(s):
+    c = s["case"]
+    if own:
+        from lossless_draft_verify_gb300 import vc
+        if c["op"] == "attn":
+            vc.vc_paged8_attn(s["q"], s["cache"], s["start"], s["ctx"], s["scale"], s["out"], s["ws"])
+        else:
+            call = vc.vc_paged8_attn_shared if s["bits"] == 8 else vc.vc_paged_attn_shared
+            call(s["q"], s["cache"], s["first"], s["prefix"], s["start"], s["ctx"], s["scale"], s["out"], s["ws"])
+        return s["out"]
+    B, Hkv, G, d, N = c["B"], c["Hkv"], c["Hq"] // c["Hkv"], c["d"], s["max_n"]
+    k, v = _rows(s, "k"), _rows(s, "v")
+    S = k.shape[2]
+    q = torch.zeros(B, N, Hkv, G, d, device="cuda")
+    q[s["seq"], s["at"]] = s["q"].view(-1, Hkv, G, d).float()
+    q = q.permute(0, 2, 1, 3, 4).reshape(B, Hkv, N * G, d)
+    p = torch.matmul(q, k.transpose(-1, -2)).mul_(s["scale"]).view(B, Hkv, N, G, S)
+    last = s["ctx"].long()[:, None] + torch.arange(N, device="cuda")
+    hidden = torch.arange(S, device="cuda") > last[:, :, None]
+    p.masked_fill_(hidden[:, None, :, None, :], -math.inf)
+    p.sub_(p.amax(-1, keepdim=True)).exp_()
+    p.div_(p.sum(-1, keepdim=True))
+    o = torch.matmul(p.view(B, Hkv, N * G, S), v).view(B, Hkv, N, G, d).permute(0, 2, 1, 3, 4)
+    s["out"].copy_(o[s["seq"], s["at"]].reshape(-1, c["Hq"], d))
+    return s["out"]
+
+
+_RUN = {"write": _write, "read": _read, "attn": _attn, "shared": _attn}
+
+
+# ------------------------------------------------------------------- exact --
+def _two(e):
+    """2^e in 64 bits, exactly."""
+    return ((e.long() + 1023) << 52).view(torch.float64)
+
+
+def _round_e4m3(x):
+    """The nearest of the numbers +-m 2^e, m < 16, e >= -9 (ties to an even m)."""
+    e = (torch.frexp(x).exponent - 4).clamp(min=-9)
+    return (x * _two(-e)).round() * _two(e)
+
+
+def exact(case, seed):
+    s = prepare(case, seed)
+    ns, cs, page, Hkv, d = s["ns"], s["cs"], case["page"], case["Hkv"], case["d"]
+    table = s["table"].tolist()
+
+    def tokens(x, b, h, lo, hi):
+        """Rows lo .. hi - 1 of (sequence b, head h) in 64 bits."""
+        if lo == hi:
+            return torch.zeros(0, d, dtype=torch.float64, device="cuda")
+        used = torch.tensor(table[b][lo // page:-(-hi // page)], device="cuda")
+        if s["bits"] == 8:
+            rows = s[x].view(torch.uint8)[used, h].view(torch.float8_e4m3fn).double()
+            rows = rows * _two(s[x + "s"].view(torch.uint8)[used, h].long() - 127)[..., None]
+        else:
+            rows = s[x][used, h].double()
+        return rows.reshape(-1, d)[lo % page:lo % page + hi - lo]
+
+    if case["op"] == "write":
+        Hq, r = case["Hq"], case["rotary"]
+        x = s["qkv"].double().reshape(s["T"], -1, d)
+        y = x.clone()
+        pos = s["pos"].double()
+        for h in range(Hq + Hkv):
+            u = x[:, h]
+            if case["norm"]:
+                u = u / ((u * u).sum(1) / d + EPS).sqrt()[:, None] * (s["qg"] if h < Hq else s["kg"]).double()
+            y[:, h] = u
+            for j in range(r // 2):
+                t = pos * math.pow(THETA, -2.0 * j / r)
+                y[:, h, j] = u[:, j] * torch.cos(t) - u[:, j + r // 2] * torch.sin(t)
+                y[:, h, j + r // 2] = u[:, j] * torch.sin(t) + u[:, j + r // 2] * torch.cos(t)
+        kv = y[:, Hq:].reshape(s["T"], 2, Hkv, d)
+        big = kv.abs().amax(-1)
+        e = torch.ceil(torch.log2(big / 448)).long()
+        e += (big > 448 * _two(e)).long()
+        e -= (big <= 448 * _two(e - 1)).long()
+        codes = _round_e4m3(kv * _two(-e)[..., None])
+        k, v = s["k"].double(), s["v"].double()
+        ks = torch.full(k.shape[:3], 2.0 ** -126, dtype=torch.float64, device="cuda")
+        vs = ks.clone()
+        row = 0
+        for b, (n, c) in enumerate(zip(ns, cs)):
+            i = 0
+            while i < n:                                # runs of tokens that share a page
+                o = (c + i) % page
+                m = min(n - i, page - o)
+                p = table[b][(c + i) // page]
+                for j, (pool, scales) in enumerate(((k, ks), (v, vs))):
+                    pool[p, :, o:o + m] = codes[row + i:row + i + m, j].transpose(0, 1)
+                    scales[p, :, o:o + m] = _two(e[row + i:row + i + m, j]).T
+                i += m
+            row += n
+        return y[:, :Hq], k, v, ks, vs
+    if case["op"] == "read":
+        ko, vo, row = s["ko"].double(), s["vo"].double(), 0
+        for b, (n, c) in enumerate(zip(ns, cs)):
+            for h in range(Hkv):
+                ko[row:row + n, h] = tokens("k", b, h, c, c + n)
+                vo[row:row + n, h] = tokens("v", b, h, c, c + n)
+            row += n
+        return ko, vo
+    Hq = case["Hq"]
+    out = torch.empty(s["T"], Hq, d, dtype=torch.float64, device="cuda")
+    row = 0
+    for b, (n, c) in enumerate(zip(ns, cs)):
+        sees = torch.arange(n + c, device="cuda")[None] <= c + torch.arange(n, device="cuda")[:, None]
+        for h in range(Hkv):
+            k, v = tokens("k", b, h, 0, n + c), tokens("v", b, h, 0, n + c)
+            for g in range(h * Hq // Hkv, (h + 1) * Hq // Hkv):
+                x = (s["q"][row:row + n, g].double() @ k.T) / math.sqrt(d)
+                e = torch.where(sees, (x - torch.where(sees, x, -math.inf).max(1, keepdim=True).values).exp(), 0.0)
+                out[row:row + n, g] = (e / e.sum(1, keepdim=True)) @ v
+        row += n
+    return out
