@@ -892,6 +892,95 @@ vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_
                          vc_drop_cfg cfg, const vc_paged_cache *dst, int32_t *dst_len, int32_t *kept_idx,
                          int kept_stride, float *scores_out, int scores_out_stride, cudaStream_t stream);
 
+/*
+ * vc_paged_attn_shared -- vc_paged_attn for a batch whose sequences share long
+ * prefixes (one instruction, one document): group g is the sequences
+ * seq_start[g] .. seq_start[g+1] - 1, which begin with the same len[g] tokens.
+ * The whole pages of a prefix (len[g] / page of them) are taken from the table of
+ * the group's first sequence and read once for all rows of the group; the others'
+ * entries for those blocks are not read, and may be the same pages (a shared
+ * prefix) or not there.  A prefix's remaining tokens and all others are read
+ * through each sequence's own table.  Sequences of no group attend on their own.
+ * The results are vc_paged_attn's up to the order of sums, each row's two
+ * halves being joined in fp32 before the one rounding to dt.
+ * seq_start (device int32 [n + 1], ascending), len (device int32 [n]); with n = 0
+ * both may be NULL.  VC_PAGED_BAD_LENGTH also reports a range outside [0, B] or
+ * descending or a length outside [0, max_blocks * page] (its sequences attend on
+ * their own), and a sequence whose ctx_len does not hold its group's whole pages
+ * (it is treated as having no tokens).  Where a sequence's rows do not fit, its
+ * group's results are unspecified.  T * Hq <= 2^29.
+ */
+typedef struct vc_shared_prefix {
+    const int32_t *seq_start;     /* device [n + 1] */
+    const int32_t *len;           /* device [n] */
+    int32_t n;
+} vc_shared_prefix;
+
+size_t vc_paged_attn_shared_workspace_bytes(const vc_paged_cache *cache, int n_groups, int T, int Hq);
+vc_status vc_paged_attn_shared(const void *q, const vc_paged_cache *cache, const vc_shared_prefix *groups,
+                               const int32_t *q_start, const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out,
+                               void *ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* (9) paged cache in 8 bits                                                 */
+/* ------------------------------------------------------------------------ */
+/*
+ * A paged cache at half the memory and half the reads of a bf16 one: the lossy
+ * cache that a server drafts on, where the dense path has the KIVI records (paper
+ * page, "What the paper found": the target model drafts on a compressed cache; the
+ * format is the library's own).  Pages, tables, batches, status bits and limits
+ * are those of (8).
+ *
+ * Format.  A row (token, kv head) is d e4m3 codes (no infinities, largest number
+ * 448) and one byte, its scale's biased exponent: value = code * 2^(byte - 127).
+ * The byte is the smallest in 10 .. 246 with max |row| <= 448 * 2^(byte - 127), the
+ * codes are rounded to nearest, ties to even; rows past 448 * 2^119 saturate.
+ * Every value is a normal bf16 number or zero; one is off by at most 2^-4 of itself,
+ * or by 2^-10 of the scale where that is more.  Any bytes 10 .. 254 may stand in the
+ * scales and any codes but NaN (0x7f, 0xff) in the pages, e.g. those of another
+ * quantizer, as long as the values are finite.
+ * k_pages, v_pages: device [n_pages][Hkv][page][d] codes; k_scale, v_scale: device
+ * [n_pages][Hkv][page] bytes; all 16-byte aligned.  dt is the type of q, k and v
+ * outside the pages (qkv, q_out, q, out, rows read back).
+ */
+typedef struct vc_paged8_cache {
+    void *k_pages, *v_pages;      /* device, e4m3 codes */
+    void *k_scale, *v_scale;      /* device, biased exponents */
+    const int32_t *block_table;   /* device [B][max_blocks] */
+    int32_t *status;              /* device, 1 word: VC_PAGED_* bits are ORed in */
+    int32_t B, Hkv, d, page, n_pages, max_blocks;
+    vc_dtype dt;
+} vc_paged8_cache;
+
+/* vc_paged_append into 8-bit pages: the same arithmetic, k and v rounded once,
+ * from fp32 to codes. */
+vc_status vc_paged8_append(const void *qkv, const void *q_gain, const void *k_gain, float eps, const vc_rope *rope,
+                           const int32_t *positions, const int32_t *q_start, const int32_t *ctx_len, int T, int Hq,
+                           const vc_paged8_cache *cache, void *q_out, cudaStream_t stream);
+
+/*
+ * vc_paged8_read -- cached tokens back as values: packed row i of sequence b is
+ * its slot ctx_len[b] + i, k_out and v_out [T][Hkv][d] in dt, 16-byte aligned
+ * (q_start and ctx_len as for an append: the slots of a chunk, or with ctx_len 0
+ * and q_start by length the whole sequences).  Exact in both types.  T * Hkv <=
+ * 2^30.  Rows of a page outside the pool are left as they are.
+ */
+vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len, int T,
+                         void *k_out, void *v_out, cudaStream_t stream);
+
+/*
+ * vc_paged8_attn, vc_paged8_attn_shared -- vc_paged_attn and vc_paged_attn_shared
+ * over 8-bit pages, as on pages that hold the values: a scale is a power of two, so
+ * the codes are expanded exactly, to bf16 for the tensor cores (dt bf16) or to fp32.
+ */
+size_t vc_paged8_attn_workspace_bytes(const vc_paged8_cache *cache, int T, int Hq);
+vc_status vc_paged8_attn(const void *q, const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len,
+                         int T, int Hq, float sm_scale, void *out, void *ws, size_t ws_bytes, cudaStream_t stream);
+size_t vc_paged8_attn_shared_workspace_bytes(const vc_paged8_cache *cache, int n_groups, int T, int Hq);
+vc_status vc_paged8_attn_shared(const void *q, const vc_paged8_cache *cache, const vc_shared_prefix *groups,
+                                const int32_t *q_start, const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out,
+                                void *ws, size_t ws_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

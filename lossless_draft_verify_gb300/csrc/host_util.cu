@@ -75,4 +75,17 @@ bool tma_map_bf16_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+bool tma_map_u8_2d(CUtensorMap *m, const void *base, uint64_t d, uint64_t rows, uint32_t box_rows)
+{
+    auto fn = tma_encoder();
+    if (!fn) return false;
+    const cuuint64_t dims[3] = {d, rows, 1};
+    const cuuint64_t strides[2] = {d, d * rows};
+    const cuuint32_t box[3] = {(cuuint32_t)d, box_rows, 1};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace vc

@@ -37,6 +37,7 @@ struct Pool {
     const int32_t *table;      // [B][max_blocks]
     int32_t *status;
     int32_t B, Hkv, page_log2, n_pages, max_blocks;
+    uint8_t *k_scale, *v_scale;    // 8-bit pages: [n_pages][Hkv][page], else null
 
     __host__ __device__ __forceinline__ int page() const { return 1 << page_log2; }
     __host__ __device__ __forceinline__ long capacity() const { return (long)max_blocks << page_log2; }
@@ -63,6 +64,21 @@ struct Pool {
 // sequence empty and set the status bit.
 struct Seq {
     int tok0, n, ctx;
+
+    // row i sees keys 0 .. last(i); the sequence has len() of them
+    __host__ __device__ __forceinline__ int last(int i) const { return ctx + i; }
+    __host__ __device__ __forceinline__ int len() const { return ctx + n; }
+};
+
+// An entry of a planned batch (paged_shared.cu): rows and keys of its own.
+// The keys are the slots from `base` (a page's first) of sequence b's table; row
+// i sees keys 0 .. ctx + step i, step 1 for a sequence's own slots, 0 for a prefix,
+// which all rows see whole.  Results go to row out0 + i.
+struct alignas(8) VSeq {
+    int tok0, n, ctx, step, base, b, out0, pad;
+
+    __host__ __device__ __forceinline__ int last(int i) const { return ctx + step * i; }
+    __host__ __device__ __forceinline__ int len() const { return step ? ctx + n : ctx + 1; }
 };
 
 struct RawSeq {
@@ -92,6 +108,22 @@ __host__ __device__ __forceinline__ Seq load_seq(const Pool &P, const int32_t *_
     return check_seq(P, raw_seq(q_start, ctx_len, b), T);
 }
 
+// The sequence that packed row `tok` belongs to: the last one that starts at or
+// before it, by one warp (32 probes a step); -1: none does.
+__device__ __forceinline__ int find_seq(const int32_t *__restrict__ q_start, int B, int tok)
+{
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = B;
+    for (;;) {
+        const int step = (hi - lo + 31) / 32, b = lo + lane * step;
+        const unsigned le = __ballot_sync(0xffffffffu, b < hi && q_start[b] <= tok);
+        if (le == 0) return -1;
+        lo += (31 - __clz(le)) * step;
+        hi = min(hi, lo + step);
+        if (step == 1) return lo;
+    }
+}
+
 // ----- division of the attention work ----------------------------------------
 // A unit is (sequence b, kv head h, row tile mt): BM consecutive rows of the
 // n * G (query, head of the group) rows that share a kv head, row = i * G + g.
@@ -105,7 +137,34 @@ __host__ __device__ __forceinline__ Seq load_seq(const Pool &P, const int32_t *_
 struct WorkDim {
     const int32_t *q_start, *ctx_len;
     int T, G;
+    const VSeq *plan;      // a planned batch's entries, else null
+    int n_plan;
 };
+
+// Entries of a batch: its sequences, or those of its plan.
+template <typename S>
+struct Source;
+template <>
+struct Source<Seq> {
+    using Raw = RawSeq;
+    static __host__ __device__ __forceinline__ int count(const Pool &P, const WorkDim &) { return P.B; }
+    static __host__ __device__ __forceinline__ Raw raw(const WorkDim &W, int b) { return raw_seq(W.q_start, W.ctx_len, b); }
+    static __host__ __device__ __forceinline__ Raw none() { return RawSeq{0, 0, 0}; }
+    static __host__ __device__ __forceinline__ Seq check(const Pool &P, const WorkDim &W, const Raw &r) { return check_seq(P, r, W.T); }
+};
+template <>
+struct Source<VSeq> {
+    using Raw = VSeq;
+    static __host__ __device__ __forceinline__ int count(const Pool &, const WorkDim &W) { return W.n_plan; }
+    static __host__ __device__ __forceinline__ Raw raw(const WorkDim &W, int i) { return W.plan[i]; }
+    static __host__ __device__ __forceinline__ Raw none() { return VSeq{0, 0, 0, 1, 0, 0, 0, 0}; }
+    static __host__ __device__ __forceinline__ VSeq check(const Pool &, const WorkDim &, const Raw &r) { return r; }
+};
+template <typename S>
+__host__ __device__ __forceinline__ S load_entry(const Pool &P, const WorkDim &W, int i)
+{
+    return Source<S>::check(P, W, Source<S>::raw(W, i));
+}
 
 // A unit of at most kWhole is never cut: merging its parts would take longer
 // than it does.  It belongs to the CTA in whose piece its middle lies.  A piece
@@ -142,22 +201,27 @@ template <int BM, int BN>
 struct Units : Cost<BM> {
     using Cost<BM>::kUnitCost;
     // 32-bit arithmetic: a sequence has at most 2^30 rows
-    static __host__ __device__ __forceinline__ int tiles(const Seq &s, int G, int mt)
+    template <typename S>
+    static __host__ __device__ __forceinline__ int tiles(const S &s, int G, int mt)
     {
         const unsigned rows = (unsigned)s.n * G, end = ((unsigned)mt + 1) * BM;
         const unsigned last = (rows < end ? rows : end) - 1;              // last row of the tile
-        return (int)((s.ctx + last / (unsigned)G + 1 + BN - 1) / BN);
+        return (int)(((unsigned)s.last((int)(last / (unsigned)G)) + 1 + BN - 1) / BN);
     }
-    static __host__ __device__ __forceinline__ int weight(const Seq &s, int G, int mt)
+    template <typename S>
+    static __host__ __device__ __forceinline__ int weight(const S &s, int G, int mt)
     {
         return BM == 256 && s.n * G - mt * BM > BM / 2 ? 2 : 1;
     }
-    static __host__ __device__ __forceinline__ int cost(const Seq &s, int G, int mt)
+    template <typename S>
+    static __host__ __device__ __forceinline__ int cost(const S &s, int G, int mt)
     {
         return tiles(s, G, mt) * weight(s, G, mt) + kUnitCost;
     }
-    static __host__ __device__ __forceinline__ int mtiles(const Seq &s, int G) { return (s.n * G + BM - 1) / BM; }
-    static __host__ __device__ __forceinline__ long head_cost(const Seq &s, int G)
+    template <typename S>
+    static __host__ __device__ __forceinline__ int mtiles(const S &s, int G) { return (s.n * G + BM - 1) / BM; }
+    template <typename S>
+    static __host__ __device__ __forceinline__ long head_cost(const S &s, int G)
     {
         long c = 0;
         const int m = mtiles(s, G);
@@ -165,7 +229,8 @@ struct Units : Cost<BM> {
         return c;
     }
     // head, row tile and offset of cost unit x of a sequence (hc: head_cost)
-    static __host__ __device__ __forceinline__ void place(const Seq &s, int G, long hc, long x, Piece &out)
+    template <typename S>
+    static __host__ __device__ __forceinline__ void place(const S &s, int G, long hc, long x, Piece &out)
     {
         out.h = (int)(x / hc);
         x -= out.h * hc;
@@ -187,22 +252,23 @@ struct Units : Cost<BM> {
 // which finds the sequence that holds the piece's beginning, can go straight to
 // its chunk.  One loop serves both: code that runs once is paid for in
 // instruction fetches.
-template <int BM, int BN>
+template <int BM, int BN, typename S = Seq>
 __device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int cta, int n_cta, Piece *out)
 {
     using U = Units<BM, BN>;
-    const int lane = threadIdx.x & 31, chunks = (P.B + 31) / 32;
+    using Src = Source<S>;
+    const int lane = threadIdx.x & 31, count = Src::count(P, W), chunks = (count + 31) / 32;
     auto fetch = [&](int c) {
         const int b = 32 * c + lane;
-        return b < P.B ? raw_seq(W.q_start, W.ctx_len, b) : RawSeq{0, 0, 0};
+        return b < count ? Src::raw(W, b) : Src::none();
     };
     if (lane == 0) out->len = 0;
     long lo = -1, hi = 0, per = 0, before = 0, chunk = 0;
     int c = 0;
-    RawSeq next = fetch(0);
+    typename Src::Raw next = fetch(0);
 #pragma unroll 1
     for (;;) {
-        const Seq s = check_seq(P, next, W.T);
+        const S s = Src::check(P, W, next);
         if (c + 1 < chunks) next = fetch(c + 1);
         const long hc = U::head_cost(s, W.G), x = hc * P.Hkv;
         long incl = x;                               // inclusive over the lanes
@@ -239,7 +305,10 @@ __device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int 
 }
 
 // One unit, or the part of it that falls to this CTA.
-struct Item {
+template <typename S>
+struct ItemOf;
+template <>
+struct ItemOf<Seq> {
     int b, h, mt;
     int tok0, n, ctx;      // the sequence
     int rows;              // valid rows of the tile
@@ -247,15 +316,35 @@ struct Item {
     bool whole;            // the part is the whole unit: written to the output
     bool head;             // a partial unit's first part
     int parts;             // head: how many CTAs share the unit
+
+    __host__ __device__ __forceinline__ int last(int i) const { return ctx + i; }
+    __host__ __device__ __forceinline__ int len() const { return ctx + n; }
+    __host__ __device__ __forceinline__ int first_slot() const { return 0; }
+    __host__ __device__ __forceinline__ int out_tok0() const { return tok0; }
+    __host__ __device__ __forceinline__ void set(int entry, const Seq &s) { b = entry, tok0 = s.tok0, n = s.n, ctx = s.ctx; }
 };
+template <>
+struct ItemOf<VSeq> : ItemOf<Seq> {
+    int step, base, out0;
+
+    __host__ __device__ __forceinline__ int last(int i) const { return ctx + step * i; }
+    __host__ __device__ __forceinline__ int len() const { return step ? ctx + n : ctx + 1; }
+    __host__ __device__ __forceinline__ int first_slot() const { return base; }
+    __host__ __device__ __forceinline__ int out_tok0() const { return out0; }
+    __host__ __device__ __forceinline__ void set(int, const VSeq &s)
+    {
+        b = s.b, tok0 = s.tok0, n = s.n, ctx = s.ctx, step = s.step, base = s.base, out0 = s.out0;
+    }
+};
+using Item = ItemOf<Seq>;
 
 // Walks a piece; every role of a CTA walks it alike.
-template <int BM, int BN>
+template <int BM, int BN, typename S = Seq>
 struct Walk {
     using U = Units<BM, BN>;
-    int b, h, mt;
+    int b, h, mt;          // b: the entry
     long off, left, per;
-    Seq s;
+    S s;
     int m;
 
     __host__ __device__ __forceinline__ void start(const Pool &P, const WorkDim &W, const Piece &p)
@@ -267,24 +356,21 @@ struct Walk {
         left = p.len;
         per = p.per;
         if (left > 0) {
-            s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
+            s = load_entry<S>(P, W, b);
             m = U::mtiles(s, W.G);
         }
     }
     // The next part with at least one key tile; false at the piece's end.
-    __host__ __device__ __forceinline__ bool next(const Pool &P, const WorkDim &W, Item &it)
+    __host__ __device__ __forceinline__ bool next(const Pool &P, const WorkDim &W, ItemOf<S> &it)
     {
         while (left > 0) {
             const int cost = U::cost(s, W.G, mt), weight = U::weight(s, W.G, mt);
             const long take = lmin(left, (long)cost - off);
             const bool uncut = cost <= U::kWhole, mine = !uncut || (off <= cost / 2 && cost / 2 < off + take);
             const long a = uncut ? 0 : off, e = uncut ? cost : off + take;
-            it.b = b;
+            it.set(b, s);
             it.h = h;
             it.mt = mt;
-            it.tok0 = s.tok0;
-            it.n = s.n;
-            it.ctx = s.ctx;
             it.rows = (int)lmin((long)BM, (long)s.n * W.G - (long)mt * BM);
             // the unit's first kUnitCost cost units carry no tile
             it.t_lo = (int)(lmax(a - U::kUnitCost, 0) / weight);
@@ -301,8 +387,8 @@ struct Walk {
                 if (++h == P.Hkv) {
                     h = 0;
                     m = 0;
-                    while (left > 0 && m == 0 && ++b < P.B) {
-                        s = load_seq(P, W.q_start, W.ctx_len, W.T, b);
+                    while (left > 0 && m == 0 && ++b < Source<S>::count(P, W)) {
+                        s = load_entry<S>(P, W, b);
                         m = U::mtiles(s, W.G);
                     }
                     if (m == 0) left = 0;
@@ -378,7 +464,7 @@ __device__ __forceinline__ bool wait_warp(uint64_t *bar, uint32_t parity, int32_
 // ----- launchers ----------------------------------------------------------------------
 // paged_attn_simt.cu: fp32 on the CUDA cores
 constexpr int kSimtKeys = 32;      // the smallest key tile of its variants
-int simt_rows(int T, int G, int B);
+int simt_rows(int T, int G, int B, bool planned);
 int simt_ctas();
 cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                       const Parts &parts, cudaStream_t st);
@@ -392,16 +478,43 @@ int tc_ctas();
 // of 128, at least the table's slots)
 cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                     float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st);
+// A planned batch's attention (W.plan): out is fp32 and lse given
+cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, float *out,
+                            float *lse, const Parts &parts, int32_t *status, cudaStream_t st);
+// paged_attn8_tc.cu: both over 8-bit pages
+cudaError_t attn8_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
+                     const Parts &parts, int32_t *status, cudaStream_t st);
 
 // paged_mass_tc.cu: scores += the attention weight of every slot, lse (log2
 // domain) of every row given
 cudaError_t mass_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float *lse,
                     float *scores, int scores_stride, int32_t *status, cudaStream_t st);
 
-// paged_attn.cu: attention, with scores != null also the attention mass
+// paged_shared.cu: groups of sequences [first[g], first[g + 1]) that share the
+// first prefix[g] tokens.  The plan: an entry per group, then one per sequence.
+struct Groups {
+    const int32_t *first, *prefix;
+    int n;
+};
+cudaError_t plan_shared(const Pool &P, const int32_t *q_start, const int32_t *ctx_len, int T, const Groups &G,
+                        VSeq *plan, cudaStream_t st);
+// out from the halves of every row: o [2][T][Hq][d] and lse [2][T][Hq], the prefix's
+// first; seqs: the plan's entries of the sequences
+cudaError_t join_shared(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, int T, int Hq, const VSeq *seqs,
+                        const float *o, const float *lse, void *out, cudaStream_t st);
+
+// paged_attn.cu: attention, with scores != null also the attention mass; shared:
+// that of groups (scores null, n_groups those of its workspace)
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass);
+size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups);
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
                  int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st);
+cudaError_t attn_shared(const Pool &P, vc_dtype dt, int d, const void *q, const Groups &G, const int32_t *q_start,
+                        const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out, void *ws, cudaStream_t st);
+
+// paged8_read.cu
+cudaError_t read8(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k_out,
+                  void *v_out, cudaStream_t st);
 
 // paged_append.cu
 cudaError_t append(const Pool &P, vc_dtype dt, int d, const void *qkv, const void *q_gain, const void *k_gain,

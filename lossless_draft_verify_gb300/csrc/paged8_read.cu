@@ -1,0 +1,121 @@
+// paged8_read.cu -- cached tokens back from 8-bit pages: row i of a sequence's
+// chunk is its slot ctx + i, as packed rows of bf16 or fp32 values.
+//
+//   x = code * 2^(byte - 127)
+//
+// Bound by HBM: every code is read once, every value written once.  A lane takes
+// as many codes as make one 16-byte store, so that a warp's loads and stores are
+// both whole lines; the tokens of a CTA lie side by side in their page, so a head's
+// rows are one run of it.
+#include <type_traits>
+
+#include "paged.cuh"
+#include "paged8.cuh"
+
+namespace vc {
+namespace paged {
+namespace {
+
+constexpr int kThreads = 256, kTokens = 16;
+
+template <typename E, int D>
+__global__ void __launch_bounds__(kThreads)
+read8_kernel(Pool P, const int32_t *__restrict__ q_start, const int32_t *__restrict__ ctx_len, int T,
+             E *__restrict__ k_out, E *__restrict__ v_out)
+{
+    constexpr int W = 16 / sizeof(E), CH = D / W;           // codes per lane, lanes per row
+    __shared__ long s_row[kTokens];                          // row of head 0 in the pool, or -1
+    pdl_wait();
+    pdl_trigger();
+    const int t0 = blockIdx.x * kTokens, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int t = warp; t < kTokens; t += kThreads / 32) {
+        const int tok = t0 + t;
+        const int b = tok < T ? find_seq(q_start, P.B, tok) : -1;
+        if (lane) continue;
+        long row = -1;
+        if (b >= 0) {
+            const Seq s = load_seq(P, q_start, ctx_len, T, b);
+            const int i = tok - s.tok0, slot = s.ctx + i;
+            if (i >= 0 && i < s.n) {
+                const int page = P.page_of(b, slot >> P.page_log2);
+                if (page >= 0) row = (long)P.row(page, 0, slot & (P.page() - 1));
+            }
+        }
+        s_row[t] = row;
+    }
+    if (blockIdx.x == 0)                                     // lengths that do not fit are reported for all sequences
+        for (int b = threadIdx.x; b < P.B; b += kThreads) load_seq(P, q_start, ctx_len, T, b);
+    __syncthreads();
+    const int items = 2 * P.Hkv * kTokens * CH;              // (k or v, head, token, lane of the row)
+    constexpr int U = 4;
+    for (int i0 = threadIdx.x; i0 < items; i0 += U * kThreads) {
+        uint32_t w[U][W / 4];
+        uint32_t byte[U];
+        long to[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int i = i0 + u * kThreads;
+            to[u] = -1;
+            if (i >= items) continue;
+            const int c = i % CH, t = i / CH % kTokens, kh = i / (CH * kTokens);
+            const int h = kh < P.Hkv ? kh : kh - P.Hkv;
+            if (s_row[t] < 0) continue;
+            const size_t row = (size_t)s_row[t] + ((size_t)h << P.page_log2);
+            const uint8_t *src = (const uint8_t *)(kh < P.Hkv ? P.k : P.v) + row * D + c * W;
+            byte[u] = (kh < P.Hkv ? P.k_scale : P.v_scale)[row];
+            if constexpr (W == 8) {
+                const uint2 x = *reinterpret_cast<const uint2 *>(src);
+                w[u][0] = x.x, w[u][W / 4 - 1] = x.y;
+            } else {
+                w[u][0] = *reinterpret_cast<const uint32_t *>(src);
+            }
+            to[u] = ((long)(t0 + t) * P.Hkv + h) * D + c * W;
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            if (to[u] < 0) continue;
+            const int kh = (i0 + u * kThreads) / (CH * kTokens);
+            E *dst = (kh < P.Hkv ? k_out : v_out) + to[u];
+            const float scale = scale_of(byte[u]);
+            float x[W];
+#pragma unroll
+            for (int j = 0; j < W / 2; ++j) {
+                const float2 f = decode2(w[u][j / 2] >> (j % 2 * 16));
+                x[2 * j] = f.x * scale;
+                x[2 * j + 1] = f.y * scale;
+            }
+            uint32_t o[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (W == 8) {
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(x[2 * j], x[2 * j + 1]);
+                    o[j] = *reinterpret_cast<const uint32_t *>(&p);
+                } else {
+                    o[j] = __float_as_uint(x[j]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+template <typename E>
+cudaError_t launch(const Pool &P, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k, void *v,
+                   cudaStream_t st)
+{
+    const dim3 grid(cdiv(T, kTokens));
+    return d == 128 ? launch_pdl(read8_kernel<E, 128>, grid, dim3(kThreads), 0, st, P, q_start, ctx_len, T, (E *)k, (E *)v)
+                    : launch_pdl(read8_kernel<E, 64>, grid, dim3(kThreads), 0, st, P, q_start, ctx_len, T, (E *)k, (E *)v);
+}
+
+}  // namespace
+
+cudaError_t read8(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k_out,
+                  void *v_out, cudaStream_t st)
+{
+    return dt == VC_BF16 ? launch<__nv_bfloat16>(P, d, q_start, ctx_len, T, k_out, v_out, st)
+                         : launch<float>(P, d, q_start, ctx_len, T, k_out, v_out, st);
+}
+
+}  // namespace paged
+}  // namespace vc

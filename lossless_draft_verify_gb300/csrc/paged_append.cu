@@ -12,7 +12,10 @@
 // 64-bit fraction of a turn, so pos * w_j modulo one turn is an integer
 // product that is exact at any position; sine and cosine are computed once per
 // (token, pair) and shared by the token's heads.
+#include <type_traits>
+
 #include "paged.cuh"
+#include "paged8.cuh"
 
 namespace vc {
 namespace paged {
@@ -86,7 +89,11 @@ struct AppendParams {
 // sequences, pages and angles are looked up, each other one under the arithmetic
 // of the one before (in a graph 19.5 us at 4670 tokens, 22.9 when it is read after
 // it, 20.2 and 21.5 with two and three in flight).
-template <typename E, int D, int TPB>
+//
+// KV8: the pages hold 8-bit rows.  A key or value head's lanes find its largest
+// magnitude together (log2(D/16) exchanges more) and store 8 codes per chunk; the
+// first one stores the scale.
+template <typename E, int D, int TPB, bool KV8>
 __global__ void __launch_bounds__(kThreads, 4)
 append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
 {
@@ -128,19 +135,8 @@ append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
         if (lane == 0) s_page[t] = -2;
         __syncwarp();
         if (tok >= A.T) continue;
-        int lo = 0, hi = A.P.B;
-        for (;;) {
-            const int step = (hi - lo + 31) / 32, b = lo + lane * step;
-            const unsigned le = __ballot_sync(0xffffffffu, b < hi && A.q_start[b] <= tok);
-            if (le == 0) {
-                hi = lo;
-                break;
-            }
-            lo += (31 - __clz(le)) * step;
-            hi = min(hi, lo + step);
-            if (step == 1) break;
-        }
-        if (lane == 0 && lo < hi) {
+        const int lo = find_seq(A.q_start, A.P.B, tok);
+        if (lane == 0 && lo >= 0) {
             const Seq s = load_seq(A.P, A.q_start, A.ctx_len, A.T, lo);
             const int i = tok - s.tok0;
             if (i >= 0 && i < s.n) {
@@ -206,7 +202,28 @@ append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
                 x1[e] = fma2(a, s[e], mul2(b, c[e]));
             }
         }
-        if (on && (hh < A.Hq || s_page[t] >= 0)) {     // a page outside the pool: nothing is written
+        if constexpr (KV8) {
+            float top = 0.f;                           // (unread rows: garbage, which nobody uses)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(x0[e].x), fabsf(x0[e].y)), fmaxf(fabsf(x1[e].x), fabsf(x1[e].y))));
+#pragma unroll
+            for (int o = LANES / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (on && hh >= A.Hq && s_page[t] >= 0) {
+                const uint32_t byte = scale_byte(top);
+                const float inv = inverse_scale(byte);
+                const float2 inv2 = make_float2(inv, inv);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x0[e] = mul2(x0[e], inv2), x1[e] = mul2(x1[e], inv2);
+                const int h = is_v ? hh - A.Hq - A.P.Hkv : hh - A.Hq;
+                const size_t row = A.P.row(s_page[t], h, s_slot[t]);
+                uint8_t *dst = (uint8_t *)(is_v ? A.P.v : A.P.k) + row * D;
+                *reinterpret_cast<uint2 *>(dst + c0) = encode8(x0);
+                *reinterpret_cast<uint2 *>(dst + c1) = encode8(x1);
+                if (l == 0) (is_v ? A.P.v_scale : A.P.k_scale)[row] = (uint8_t)byte;
+            }
+        }
+        if (on && (hh < A.Hq || (!KV8 && s_page[t] >= 0))) {     // a page outside the pool: nothing is written
             E *dst;
             if (hh < A.Hq) {
                 dst = (E *)A.q_out + ((size_t)(t0 + t) * A.Hq + hh) * D;
@@ -221,7 +238,7 @@ append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
     }
 }
 
-template <typename E, int D>
+template <typename E, int D, bool KV8>
 cudaError_t launch(const AppendParams &A, const vc_rope &rope, cudaStream_t st)
 {
     const int heads = A.Hq + 2 * A.P.Hkv, groups = kThreads / (D / 16);
@@ -234,8 +251,8 @@ cudaError_t launch(const AppendParams &A, const vc_rope &rope, cudaStream_t st)
     // rate: sequence, page and angles of four tokens are looked up before a CTA's
     // first store, in two waves of CTAs.
     if (A.T <= 4 * device_sm_count())
-        return launch_pdl(append_kernel<E, D, 1>, dim3(A.T, cdiv(heads, groups)), dim3(kThreads), 0, st, A, rope);
-    return launch_pdl(append_kernel<E, D, 4>, dim3(cdiv(A.T, 4)), dim3(kThreads), 0, st, A, rope);
+        return launch_pdl(append_kernel<E, D, 1, KV8>, dim3(A.T, cdiv(heads, groups)), dim3(kThreads), 0, st, A, rope);
+    return launch_pdl(append_kernel<E, D, 4, KV8>, dim3(cdiv(A.T, 4)), dim3(kThreads), 0, st, A, rope);
 }
 
 }  // namespace
@@ -256,8 +273,13 @@ cudaError_t append(const Pool &P, vc_dtype dt, int d, const void *qkv, const voi
     A.T = T;
     A.Hq = Hq;
     A.eps = eps;
-    if (dt == VC_BF16) return d == 128 ? launch<__nv_bfloat16, 128>(A, rope, st) : launch<__nv_bfloat16, 64>(A, rope, st);
-    return d == 128 ? launch<float, 128>(A, rope, st) : launch<float, 64>(A, rope, st);
+    auto form = [&](auto kv8) {
+        constexpr bool KV8 = decltype(kv8)::value;
+        if (dt == VC_BF16)
+            return d == 128 ? launch<__nv_bfloat16, 128, KV8>(A, rope, st) : launch<__nv_bfloat16, 64, KV8>(A, rope, st);
+        return d == 128 ? launch<float, 128, KV8>(A, rope, st) : launch<float, 64, KV8>(A, rope, st);
+    };
+    return P.k_scale ? form(std::true_type{}) : form(std::false_type{});
 }
 
 }  // namespace paged

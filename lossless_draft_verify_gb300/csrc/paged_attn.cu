@@ -119,11 +119,11 @@ struct WsLayout {
 // the bound 5.39 ms, just past it 7.34 ms.
 constexpr size_t kStoredMost = size_t(1) << 30;
 
-WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool with_rows)
+WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool with_rows, bool planned = false)
 {
     WsLayout w;
     w.n_cta = dt == VC_BF16 ? tc_ctas() : simt_ctas();
-    const long unit = dt == VC_BF16 ? kTcRows : simt_rows(T, G, B);
+    const long unit = dt == VC_BF16 ? kTcRows : simt_rows(T, G, B, planned);
     w.rows_cap = (int)std::min<long>(unit, (long)T * G);
     const size_t n = (size_t)w.n_cta * 2 * w.rows_cap;
     w.desc = kStatusBytes;
@@ -147,6 +147,16 @@ cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq,
                     : launch_pdl(merge_kernel<T, 64>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, lse);
 }
 
+// whether a unit can be cut: not where the block table cannot hold a sequence
+// long enough
+template <typename T>
+bool may_cut(long cap)
+{
+    constexpr int tile = std::is_same_v<T, float> ? kSimtKeys : kTcKeys, weight = std::is_same_v<T, float> ? 1 : 2;
+    using C = Cost<std::is_same_v<T, float> ? 64 : kTcRows>;
+    return (cap + tile - 1) / tile * weight + C::kUnitCost > C::kWhole;
+}
+
 template <typename T>
 cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void *q, int Hq, float sl2, void *out,
                 float *scores, int scores_stride, uint8_t *ws, cudaStream_t st)
@@ -158,11 +168,9 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     float *stored = w.s_stride ? (float *)(ws + w.stored) : nullptr;
     cudaError_t e;
     if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
+    else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, lse, parts, (int32_t *)ws, st);
     else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, stored, w.s_stride, parts, (int32_t *)ws, st);
-    // no unit is cut where the block table cannot hold a sequence long enough
-    constexpr int tile = std::is_same_v<T, float> ? kSimtKeys : kTcKeys, weight = std::is_same_v<T, float> ? 1 : 2;
-    using C = Cost<std::is_same_v<T, float> ? 64 : kTcRows>;
-    if (e == cudaSuccess && (cap + tile - 1) / tile * weight + C::kUnitCost > C::kWhole)
+    if (e == cudaSuccess && may_cut<T>(cap))
         e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
     if (e != cudaSuccess || !scores) return e;
     if constexpr (std::is_same_v<T, float>) {
@@ -175,6 +183,46 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     }
 }
 
+// [the attention's | plan | lse of both halves | o of both halves]
+struct SharedLayout {
+    WsLayout attn;
+    size_t plan, lse, o, bytes;
+};
+
+SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, int n_groups)
+{
+    SharedLayout w;
+    w.attn = layout(dt, d, T, G, Hq, B, cap, false, true);
+    w.plan = w.attn.bytes;
+    w.lse = w.plan + align256(((size_t)B + n_groups) * sizeof(VSeq));
+    w.o = w.lse + align256((size_t)2 * T * Hq * sizeof(float));
+    w.bytes = w.o + (size_t)2 * T * Hq * d * sizeof(float);
+    return w;
+}
+
+template <typename T>
+cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void *q, int Hq, float sl2, const Groups &G,
+                       void *out, uint8_t *ws, cudaStream_t st)
+{
+    const long cap = P.capacity();
+    const SharedLayout w = shared_layout(dt, d, W.T, W.G, Hq, P.B, cap, G.n);
+    const Parts parts = {(PartDesc *)(ws + w.attn.desc), (float2 *)(ws + w.attn.ml), (float *)(ws + w.attn.o),
+                         w.attn.rows_cap};
+    VSeq *plan = (VSeq *)(ws + w.plan);
+    float *lse = (float *)(ws + w.lse), *o = (float *)(ws + w.o);
+    W.plan = plan;
+    W.n_plan = P.B + G.n;
+    cudaError_t e = plan_shared(P, W.q_start, W.ctx_len, W.T, G, plan, st);
+    if (e != cudaSuccess) return e;
+    if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, o, lse, parts, st);
+    else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, o, lse, parts, (int32_t *)ws, st);
+    else e = attn_tc_planned(P, W, d, q, Hq, sl2, o, lse, parts, (int32_t *)ws, st);
+    if (e == cudaSuccess && may_cut<T>(cap))
+        e = merge<float>(parts, w.attn.n_cta, w.attn.rows_cap, d, W.G, Hq, o, lse, st);
+    if (e != cudaSuccess) return e;
+    return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, o, lse, out, st);
+}
+
 }  // namespace
 
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass)
@@ -182,17 +230,27 @@ size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap
     return layout(dt, d, T, Hq / Hkv, Hq, B, cap, mass).bytes;
 }
 
+size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups)
+{
+    return shared_layout(dt, d, T, Hq / Hkv, Hq, B, cap, n_groups).bytes;
+}
+
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
                  int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st)
 {
-    WorkDim W;
-    W.q_start = q_start;
-    W.ctx_len = ctx_len;
-    W.T = T;
-    W.G = Hq / P.Hkv;
+    const WorkDim W = {q_start, ctx_len, T, Hq / P.Hkv, nullptr, 0};
     const float sl2 = sm_scale * kLog2e;
     return dt == VC_BF16 ? run<__nv_bfloat16>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st)
                          : run<float>(P, W, dt, d, q, Hq, sl2, out, scores, scores_stride, (uint8_t *)ws, st);
+}
+
+cudaError_t attn_shared(const Pool &P, vc_dtype dt, int d, const void *q, const Groups &G, const int32_t *q_start,
+                        const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out, void *ws, cudaStream_t st)
+{
+    const WorkDim W = {q_start, ctx_len, T, Hq / P.Hkv, nullptr, 0};
+    const float sl2 = sm_scale * kLog2e;
+    return dt == VC_BF16 ? run_shared<__nv_bfloat16>(P, W, dt, d, q, Hq, sl2, G, out, (uint8_t *)ws, st)
+                         : run_shared<float>(P, W, dt, d, q, Hq, sl2, G, out, (uint8_t *)ws, st);
 }
 
 }  // namespace paged

@@ -1,13 +1,17 @@
 // paged_attn_simt.cu -- causal attention of ragged chunks over a paged cache
 // and its attention mass on the CUDA cores, fp32 throughout: the path of fp32
-// caches, whose products may not be rounded to the tensor cores' input types.
+// rows, whose products may not be rounded to the tensor cores' input types, over
+// fp32 pages or (attention only) 8-bit ones.
 //
 //   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j),
 //   j <= ctx + i, in one pass over the keys with a running maximum and sum;
 //   mass_j = sum_i p_ij / sum_j' p_ij' in a second one, with the final ones.
 #include <cooperative_groups.h>
 
+#include <type_traits>
+
 #include "paged.cuh"
+#include "paged8.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -58,7 +62,11 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // the instructions around them: four chunks of 300 over 2000 tokens, 16/4 heads
 // of 128, 572 us, 37 TFLOP/s (larger tiles leave room for fewer warps); a token of
 // 8 sequences over 4000, 32/8 heads, 157 us, 1.7 TB/s.
-template <int D, int BM, int BN>
+//
+// KV8: a thread holds 16 codes of a K and a V row of the next tile in registers
+// while it computes with the present one, then stores them as fp32 with their
+// scales; the tiles in shared memory are the same.
+template <int D, int BM, int BN, typename SEQ, bool KV8>
 __global__ void __launch_bounds__(kThreads)
 attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float scale_log2, float *__restrict__ out,
                  float *__restrict__ lse_out, Parts parts)
@@ -70,22 +78,23 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
     __shared__ Piece piece;
     pdl_wait();
     pdl_trigger();
-    if (threadIdx.x < 32) find_piece<BM, BN>(P, W, blockIdx.x, gridDim.x, &piece);
+    if (threadIdx.x < 32) find_piece<BM, BN, SEQ>(P, W, blockIdx.x, gridDim.x, &piece);
     __syncthreads();
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const float *pk = (const float *)P.k, *pv = (const float *)P.v;
-    Walk<BM, BN> walk;
+    Walk<BM, BN, SEQ> walk;
     walk.start(P, W, piece);
     if (threadIdx.x == 0) parts.desc[blockIdx.x].parts = 0;
-    Item it;
+    ItemOf<SEQ> it;
     while (walk.next(P, W, it)) {
-        const int row0 = it.mt * BM, len = it.ctx + it.n;
-        auto token_row = [&](int r) {                  // row of q / out of tile row r
+        const int row0 = it.mt * BM, len = it.len();
+        auto row_of = [&](int tok0, int r) {
             const int R = row0 + r;
-            return ((size_t)(it.tok0 + R / W.G) * Hq + it.h * W.G + R % W.G) * D;
+            return ((size_t)(tok0 + R / W.G) * Hq + it.h * W.G + R % W.G) * D;
         };
+        auto token_row = [&](int r) { return row_of(it.out_tok0(), r); };     // of out and lse_out
         __syncthreads();
-        load_rows<D>(sQ, G::PQ, BM, [&](int r) { return r < it.rows ? q + token_row(r) : nullptr; });
+        load_rows<D>(sQ, G::PQ, BM, [&](int r) { return r < it.rows ? q + row_of(it.tok0, r) : nullptr; });
         float m[RT], l[RT];
         float2 acc[RT][CT][2];
         int kmax[RT];
@@ -94,23 +103,38 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
             m[i] = kLowest;
             l[i] = 0.f;
             const int r = ty * RT + i;
-            kmax[i] = r < it.rows ? it.ctx + (row0 + r) / W.G : -1;
+            kmax[i] = r < it.rows ? it.last((row0 + r) / W.G) : -1;
 #pragma unroll
             for (int j = 0; j < CT; ++j) acc[i][j][0] = acc[i][j][1] = make_float2(0.f, 0.f);
         }
         // Key tiles pass through two stages: a tile is on its way while the one
         // before it is computed with, its page numbers are read a tile earlier.
-        constexpr int CH = D / 4, RP = kThreads / CH, NR = BN / RP;
-        const int c4 = (int)threadIdx.x % CH * 4, r0 = threadIdx.x / CH;
+        constexpr int CW = KV8 ? 16 : 4, CH = D / CW, RP = kThreads / CH, NR = KV8 ? 1 : BN / RP;
+        static_assert(!KV8 || RP >= BN, "a thread's codes of a tile");
+        const int c4 = (int)threadIdx.x % CH * CW, r0 = threadIdx.x / CH;
         int pages[NR];
         auto look_up = [&](int t) {
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
                 const int slot = t * BN + r0 + x * RP;
-                pages[x] = t < it.t_hi && slot < len ? P.page_of(it.b, slot >> P.page_log2) : -1;
+                const bool in = t < it.t_hi && slot < len && r0 < BN;
+                pages[x] = in ? P.page_of(it.b, (it.first_slot() + slot) >> P.page_log2) : -1;
             }
         };
+        uint4 k8 = {}, v8 = {};
+        float ks = 0.f, vs = 0.f;
         auto fetch = [&](int t) {
+            if constexpr (KV8) {                       // zeros where there is no row
+                k8 = v8 = make_uint4(0, 0, 0, 0);
+                ks = vs = 0.f;
+                if (pages[0] < 0) return;
+                const size_t row = P.row(pages[0], it.h, (t * BN + r0) & (P.page() - 1));
+                k8 = *reinterpret_cast<const uint4 *>((const uint8_t *)P.k + row * D + c4);
+                v8 = *reinterpret_cast<const uint4 *>((const uint8_t *)P.v + row * D + c4);
+                ks = scale_of(P.k_scale[row]);
+                vs = scale_of(P.v_scale[row]);
+                return;
+            }
             float *k = sKV + (t & 1) * G::STAGE, *v = k + BN * G::PQ;
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
@@ -122,8 +146,20 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
             }
             copy_commit();
         };
+        auto land = [&](int t) {                       // KV8: the fetched tile into its stage
+            if (!KV8 || r0 >= BN) return;
+            float *k = sKV + (t & 1) * G::STAGE + r0 * G::PQ + c4, *v = sKV + (t & 1) * G::STAGE + BN * G::PQ + r0 * D + c4;
+            float x[16];
+            decode16(k8, ks, x);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(k + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            decode16(v8, vs, x);
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(v + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        };
         look_up(it.t_lo);
         fetch(it.t_lo);
+        land(it.t_lo);
         look_up(it.t_lo + 1);
         for (int t = it.t_lo; t < it.t_hi; ++t) {
             const int key0 = t * BN;
@@ -200,6 +236,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
                         }
                     }
             }
+            if (t + 1 < it.t_hi) land(t + 1);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -227,7 +264,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
         if (!it.whole && it.head && threadIdx.x == 0) {
             PartDesc &d = parts.desc[blockIdx.x];
             d.parts = it.parts;
-            d.tok0 = it.tok0;
+            d.tok0 = it.out_tok0();
             d.h = it.h;
             d.row0 = row0;
             d.rows = it.rows;
@@ -370,15 +407,26 @@ mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
     }
 }
 
-template <int D, int BM, int BN>
-cudaError_t launch_attn(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
+template <int D, int BM, int BN, typename SEQ, bool KV8>
+cudaError_t launch_form(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
                         const Parts &parts, int n_cta, cudaStream_t st)
 {
-    auto kern = attn_simt_kernel<D, BM, BN>;
+    auto kern = attn_simt_kernel<D, BM, BN, SEQ, KV8>;
     constexpr int smem = Geom<D, BM, BN>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(n_cta), dim3(kThreads), smem, st, P, W, (const float *)q, Hq, sl2, (float *)out, lse, parts);
+}
+
+template <int D, int BM, int BN>
+cudaError_t launch_attn(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
+                        const Parts &parts, int n_cta, cudaStream_t st)
+{
+    if (P.k_scale)
+        return W.plan ? launch_form<D, BM, BN, VSeq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st)
+                      : launch_form<D, BM, BN, Seq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st);
+    return W.plan ? launch_form<D, BM, BN, VSeq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st)
+                  : launch_form<D, BM, BN, Seq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st);
 }
 
 template <int D, int Z>
@@ -409,15 +457,15 @@ cudaError_t mass_rows(const Pool &P, const WorkDim &W, const void *q, int Hq, fl
 }  // namespace
 
 // rows a CTA holds: 16 where the batch has no more per sequence on average
-// (decoding), else 64
-int simt_rows(int T, int G, int B) { return (long)T * G <= 16l * B ? 16 : 64; }
+// (decoding), else 64; 64 in a planned batch, where a group's rows meet
+int simt_rows(int T, int G, int B, bool planned) { return !planned && (long)T * G <= 16l * B ? 16 : 64; }
 int simt_ctas() { return 2 * device_sm_count(); }
 
 cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                       const Parts &parts, cudaStream_t st)
 {
     const int n = simt_ctas();
-    if (simt_rows(W.T, W.G, P.B) == 16)
+    if (simt_rows(W.T, W.G, P.B, W.plan) == 16)
         return d == 128 ? launch_attn<128, 16, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)
                         : launch_attn<64, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st);
     return d == 128 ? launch_attn<128, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)

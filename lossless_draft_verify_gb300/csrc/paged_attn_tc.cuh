@@ -1,5 +1,5 @@
-// paged_attn_tc.cu -- causal attention of ragged chunks over a paged bf16
-// cache on the tensor cores (TMA, tcgen05, tensor memory).
+// paged_attn_tc.cuh -- causal attention of ragged chunks over a paged cache of
+// bf16 or 8-bit rows on the tensor cores (TMA, tcgen05, tensor memory).
 //
 //   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j), j <= ctx + i
 //
@@ -33,9 +33,17 @@
 // mass of a batch of few rows: G scores of 4 bytes per key and kv head
 // beside 4 d bytes of K and V, instead of a second read of K.
 //
+// With KV8 the pages hold e4m3 codes and a power-of-two scale per row.  The
+// producer brings tiles of codes and their scales into a ring of their own;
+// four more warps (12-15) write them as bf16 tiles, scale included, into the
+// ring that the products read.  code * 2^e is a bf16 number, so this rounds
+// nothing: the output is that of bf16 pages which hold the same numbers.
+//
 // V rows past the sequence's end may hold any bits and 0 * NaN is not 0: those
 // that share the last page with tokens are cleared in shared memory, further
 // pages are not read (their boxes lie outside the map and fill with zeros).
+#pragma once
+
 #include <type_traits>
 
 #include "paged.cuh"
@@ -47,41 +55,50 @@ namespace {
 
 constexpr int BN = 128;
 constexpr int kRowsTile = 128;
-constexpr int kThreads = 352;
-constexpr int kProducer = 8, kIssuer = 9, kProducer2 = 10;     // warps
-constexpr int kSoftmax = 256;
-constexpr int kSharedBytes = 3 << 10;                          // barriers, the roles' walks
+constexpr int kThreads = 352, kThreads8 = 512;
+constexpr int kProducer = 8, kIssuer = 9, kProducer2 = 10, kConverter = 12;     // warps
+constexpr int kSoftmax = 256, kConverters = 128;
+constexpr int kMany = 184, kSome = 80, kFew = 64;              // registers of a thread, by warpgroup (KV8)
 constexpr float kLazy = 8.f;                                   // log2 domain
 
-template <int D>
+template <int D, bool KV8>
 struct Geom {
     static constexpr int HALVES = D / 64;
     static constexpr int TILE = BN * D * 2;                  // bytes of a K or V tile (and of a Q row tile)
-    static constexpr int STAGES = 5 * (128 / D);
+    static constexpr int STAGES = (KV8 ? 3 : 5) * (128 / D);
+    static constexpr int TILE8 = BN * D, ITEM8 = TILE8 + BN; // KV8: a tile's codes; and its scales
+    static constexpr int STAGES8 = KV8 ? 4 * (128 / D) : 0;
     static constexpr int SM_Q = 0;
     static constexpr int SM_KV = 2 * TILE;
-    static constexpr int SM_BAR = SM_KV + STAGES * TILE;
-    static constexpr int SMEM = SM_BAR + kSharedBytes;
+    static constexpr int SM_8 = SM_KV + STAGES * TILE;
+    static constexpr int SM_BAR = SM_8 + STAGES8 * ITEM8;
+    static constexpr int SHARED = KV8 ? 2560 : 3 << 10;      // barriers, the roles' walks
+    static constexpr int SMEM = SM_BAR + SHARED;
     static constexpr uint32_t COL_O = 256;                   // S0 | S1 | O0 | O1
+    static_assert(SMEM <= 227 << 10, "shared memory");
 };
 
+template <typename S, bool KV8>
 struct Shared {
-    uint64_t full[10], empty[10];
+    uint64_t full[KV8 ? 6 : 10], empty[KV8 ? 6 : 10];
+    uint64_t full8[KV8 ? 8 : 1], empty8[KV8 ? 8 : 1];
     uint64_t q_ready, s_full[2], p_ready[2], o_full[2], meet;
     uint32_t tmem;
     Piece piece;
     struct {
-        Walk<256, BN> walk;
-        Item it;
+        Walk<256, BN, S> walk;
+        ItemOf<S> it;
         bool more;
-    } role[11];        // each warp's walk through the piece: in registers it would make the softmax threads spill
+    } role[KV8 ? 14 : 11];   // each warp's walk through the piece: in registers it would make the softmax threads spill
+
+    static __device__ __forceinline__ int index(int warp) { return KV8 && warp >= kConverter ? warp - 2 : warp; }
 };
 
 struct Params {
     Pool P;
     WorkDim W;
     const __nv_bfloat16 *q;
-    __nv_bfloat16 *out;
+    void *out;                     // bf16; fp32 where the batch is planned
     float *lse_out;
     Parts parts;
     int32_t *status;
@@ -94,24 +111,64 @@ struct Params {
 // The warp's next part; false at the end of the piece.  (Of a part, the ring
 // holds K_0 (K_1), then V_i, K_{i + ahead}: the order in which the products
 // need them.)
-__device__ __forceinline__ bool step(Shared *S, int warp, const Params &A)
+template <typename S, bool KV8>
+__device__ __forceinline__ bool step(Shared<S, KV8> *sh, int warp, const Params &A)
 {
-    auto &x = S->role[warp];
+    auto &x = sh->role[sh->index(warp)];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) x.more = x.walk.next(A.P, A.W, x.it);
     __syncwarp();
     return x.more;
 }
 
-template <int D, bool STORE>
-__global__ void __launch_bounds__(kThreads, 1)
+// 16 e4m3 codes times 2^(e - 127) as bf16, exactly.  A code's seven value bits,
+// shifted to where bf16 has its exponent's low bits and its mantissa, are the
+// number times 2^-120, subnormal codes included.
+__device__ __forceinline__ void expand16(const uint4 &w, uint32_t e, uint4 (&o)[2])
+{
+    // the factor 2^(e - 7) leaves bf16's range for rows past 448 * 2^7: in two steps
+    const uint32_t e1 = min(e + 120u, 254u), e2 = e + 247u - e1;
+    const uint32_t m1 = e1 << 7 | e1 << 23, m2 = e2 << 7 | e2 << 23;
+    const bool two = __any_sync(0xffffffffu, e2 != 127u);
+    const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+    uint32_t y[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t t = ((x[i] >> 4) & 0x07070707u) | (x[i] & 0x80808080u), l = (x[i] << 4) & 0xf0f0f0f0u;
+        y[2 * i] = __byte_perm(l, t, 0x5140);
+        y[2 * i + 1] = __byte_perm(l, t, 0x7362);
+    }
+    auto times = [&](uint32_t m) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const __nv_bfloat162 p = __hmul2(*reinterpret_cast<const __nv_bfloat162 *>(&y[i]),
+                                             *reinterpret_cast<const __nv_bfloat162 *>(&m));
+            y[i] = *reinterpret_cast<const uint32_t *>(&p);
+        }
+    };
+    times(m1);
+    if (two) times(m2);
+    o[0] = make_uint4(y[0], y[1], y[2], y[3]);
+    o[1] = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+template <int N>
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(N)); }
+template <int N>
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(N)); }
+
+template <int D, bool STORE, typename SEQ, bool KV8>
+__global__ void __launch_bounds__(KV8 ? kThreads8 : kThreads, 1)
 attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Params A)
 {
-    using G = Geom<D>;
-    constexpr int NST = G::STAGES;
+    using G = Geom<D, KV8>;
+    using Sh = Shared<SEQ, KV8>;
+    using It = ItemOf<SEQ>;
+    constexpr int NST = G::STAGES, NST8 = KV8 ? G::STAGES8 : 1;
+    constexpr bool PLANNED = std::is_same_v<SEQ, VSeq>;
     extern __shared__ __align__(1024) uint8_t sm[];
-    Shared *S = reinterpret_cast<Shared *>(sm + G::SM_BAR);
-    static_assert(sizeof(Shared) <= kSharedBytes, "shared block");
+    Sh *S = reinterpret_cast<Sh *>(sm + G::SM_BAR);
+    static_assert(sizeof(Sh) <= G::SHARED, "shared block");
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_wait();
     if (smem_u32(sm) & 1023u) {                              // never expected: the swizzled tiles need it
@@ -123,8 +180,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&S->full[i], 1);
+            mbar_init(&S->full[i], KV8 ? kConverters : 1);
             mbar_init(&S->empty[i], 1);
+        }
+        for (int i = 0; i < G::STAGES8; ++i) {
+            mbar_init(&S->full8[i], 1);
+            mbar_init(&S->empty8[i], kConverters);
         }
         mbar_init(&S->q_ready, kSoftmax);
         mbar_init(&S->meet, kSoftmax);
@@ -139,185 +200,295 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         tc::tmem_alloc(&S->tmem, 512);
         tc::tmem_relinquish();
     }
-    if (warp == kProducer) find_piece<256, BN>(A.P, A.W, blockIdx.x, gridDim.x, &S->piece);
+    if (warp == kProducer) find_piece<256, BN, SEQ>(A.P, A.W, blockIdx.x, gridDim.x, &S->piece);
     tc::fence_before();
     __syncthreads();
     tc::fence_after();
     pdl_trigger();
     const uint32_t tmem = S->tmem;
-    if (lane == 0) S->role[warp].walk.start(A.P, A.W, S->piece);
-
-    if (warp == kProducer || warp == kProducer2) {
-        // ------------------------------------------------------- producer --
-        const Item &it = S->role[warp].it;
-        if (lane == 0) {
-            tc::prefetch_tmap(&tmK);
-            tc::prefetch_tmap(&tmV);
-        }
-        // the two warps share a tile's boxes (at most 16), one to a lane
-        const int boxes = BN / A.box_rows * G::HALVES, mine = (boxes + 1) / 2;
-        const int box = (warp == kProducer2 ? mine : 0) + lane, bp = box / G::HALVES, half = box % G::HALVES;
-        const bool on = lane < mine && box < boxes;
-        Ring<NST> ring;
-        bool ok = true, filled = false;                      // filled: the ring has been round once
-        auto load = [&](const CUtensorMap *map, int row) {
-            const int s = ring.slot;
-            if (filled) {
-                if (lane == 0) ok = wait_bar(&S->empty[s], ring.phase ^ 1, A.status, 91);
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-                if (!ok) return;
+    const bool idle = KV8 && warp > kIssuer && warp < kConverter;
+    if (lane == 0 && !idle) S->role[S->index(warp)].walk.start(A.P, A.W, S->piece);
+    // KV8: 128 registers a thread at launch; the warpgroups share them as
+    // 2 x 184 + 64 + 80 = 4 x 128.
+    if (warp >= kProducer && warp < kConverter) {
+        if constexpr (KV8) fewer_registers<kFew>();          // the whole warpgroup
+        if (KV8 && warp == kProducer) {
+            // ------------------------------------------------ producer of codes --
+            // A lane per box of the tile: its rows' codes (zeros past the sequence's
+            // end and through a bad page number), and their scales where there are any.
+            const It &it = S->role[warp].it;
+            if (lane == 0) {
+                tc::prefetch_tmap(&tmK);
+                tc::prefetch_tmap(&tmV);
             }
-            uint8_t *dst = sm + G::SM_KV + s * G::TILE;
-            // (the other warp's boxes may land first: the phase ends with this arrival and all bytes)
-            if (lane == 0 && warp == kProducer) mbar_arrive_expect_tx(&S->full[s], G::TILE);
-            __syncwarp();
-            if (on)
-                tc::tma_load_3d(dst + half * (BN * 128) + bp * A.box_rows * 128, map, half * 64, row, 0, &S->full[s]);
+            const bool on = lane < BN / A.box_rows;
+            Ring<NST8> ring;
+            bool ok = true, filled = false;
+            auto load = [&](const CUtensorMap *map, const uint8_t *scale, int row) {
+                const int s = ring.slot;
+                if (filled) {
+                    ok = wait_warp(&S->empty8[s], ring.phase ^ 1, A.status, 104);
+                    if (!ok) return;
+                }
+                uint8_t *dst = sm + G::SM_8 + s * G::ITEM8;
+                const bool has = on && row < A.n_rows;
+                const unsigned all = __ballot_sync(0xffffffffu, has);
+                if (lane == 0) mbar_arrive_expect_tx(&S->full8[s], G::TILE8 + __popc(all) * A.box_rows);
+                __syncwarp();
+                if (on) tc::tma_load_3d(dst + lane * A.box_rows * D, map, 0, row, 0, &S->full8[s]);
+                if (has) bulk_g2s(dst + G::TILE8 + lane * A.box_rows, scale + row, A.box_rows, &S->full8[s]);
+                ring.next();
+                filled = filled || ring.slot == 0;
+            };
+            while (ok && step(S, warp, A)) {
+                const int n = it.t_hi - it.t_lo, len = it.len();
+                const int ahead = it.rows > kRowsTile ? 1 : 2;
+                auto entry = [&](int i) {
+                    const int slot = (it.t_lo + i) * BN + lane * A.box_rows;
+                    return on && i < n && slot < len
+                               ? A.P.table[(size_t)it.b * A.P.max_blocks + ((it.first_slot() + slot) >> A.P.page_log2)] : 0;
+                };
+                auto row = [&](int i, int page) {
+                    const int slot = (it.t_lo + i) * BN + lane * A.box_rows;
+                    if (!on || slot >= len) return A.n_rows;
+                    if ((unsigned)page < (unsigned)A.P.n_pages)
+                        return (int)A.P.row(page, it.h, slot & (A.P.page() - 1));
+                    set_flag(A.P.status, VC_PAGED_BAD_PAGE);
+                    return A.n_rows;
+                };
+                int e0 = entry(0), e1 = entry(1), e2 = entry(2);
+                load(&tmK, A.P.k_scale, row(0, e0));
+                if (ok && ahead == 2 && n > 1) load(&tmK, A.P.k_scale, row(1, e1));
+                for (int i = 0; i < n && ok; ++i) {
+                    const int e3 = entry(i + 3);
+                    load(&tmV, A.P.v_scale, row(i, e0));
+                    if (ok && i + ahead < n) load(&tmK, A.P.k_scale, row(i + ahead, ahead == 1 ? e1 : e2));
+                    e0 = e1, e1 = e2, e2 = e3;
+                }
+            }
+            if (!ok && lane == 0)                                // copies in flight end before the CTA does
+                for (int i = 0; i < NST8; ++i) {
+                    if (filled || i < ring.slot) mbar_wait(&S->full8[i], i < ring.slot ? ring.phase : ring.phase ^ 1);
+                }
+        } else if (!KV8 && (warp == kProducer || warp == kProducer2)) {
+            // ------------------------------------------------------- producer --
+            const It &it = S->role[warp].it;
+            if (lane == 0) {
+                tc::prefetch_tmap(&tmK);
+                tc::prefetch_tmap(&tmV);
+            }
+            // the two warps share a tile's boxes (at most 16), one to a lane
+            const int boxes = BN / A.box_rows * G::HALVES, mine = (boxes + 1) / 2;
+            const int box = (warp == kProducer2 ? mine : 0) + lane, bp = box / G::HALVES, half = box % G::HALVES;
+            const bool on = lane < mine && box < boxes;
+            Ring<NST> ring;
+            bool ok = true, filled = false;                      // filled: the ring has been round once
+            auto load = [&](const CUtensorMap *map, int row) {
+                const int s = ring.slot;
+                if (filled) {
+                    if (lane == 0) ok = wait_bar(&S->empty[s], ring.phase ^ 1, A.status, 91);
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (!ok) return;
+                }
+                uint8_t *dst = sm + G::SM_KV + s * G::TILE;
+                // (the other warp's boxes may land first: the phase ends with this arrival and all bytes)
+                if (lane == 0 && warp == kProducer) mbar_arrive_expect_tx(&S->full[s], G::TILE);
+                __syncwarp();
+                if (on)
+                    tc::tma_load_3d(dst + half * (BN * 128) + bp * A.box_rows * 128, map, half * 64, row, 0, &S->full[s]);
+                ring.next();
+                filled = filled || ring.slot == 0;
+            };
+            while (ok && step(S, warp, A)) {
+                const int n = it.t_hi - it.t_lo, len = it.len();
+                const int ahead = it.rows > kRowsTile ? 1 : 2;
+                // the lane's box of key tile i: its table entry is read some tiles
+                // before it is looked at
+                auto entry = [&](int i) {
+                    const int slot = (it.t_lo + i) * BN + bp * A.box_rows;
+                    return on && i < n && slot < len
+                               ? A.P.table[(size_t)it.b * A.P.max_blocks + ((it.first_slot() + slot) >> A.P.page_log2)] : 0;
+                };
+                // past the sequence's end or through a bad page number: a row
+                // outside the map, which fills with zeros
+                auto row = [&](int i, int page) {
+                    const int slot = (it.t_lo + i) * BN + bp * A.box_rows;
+                    if (!on || slot >= len) return A.n_rows;
+                    if ((unsigned)page < (unsigned)A.P.n_pages)
+                        return (int)A.P.row(page, it.h, slot & (A.P.page() - 1));
+                    set_flag(A.P.status, VC_PAGED_BAD_PAGE);
+                    return A.n_rows;
+                };
+                int e0 = entry(0), e1 = entry(1), e2 = entry(2);
+                load(&tmK, row(0, e0));
+                if (ok && ahead == 2 && n > 1) load(&tmK, row(1, e1));
+                for (int i = 0; i < n && ok; ++i) {
+                    const int e3 = entry(i + 3);
+                    load(&tmV, row(i, e0));
+                    if (ok && i + ahead < n) load(&tmK, row(i + ahead, ahead == 1 ? e1 : e2));
+                    e0 = e1, e1 = e2, e2 = e3;
+                }
+            }
+            if (!ok && lane == 0)                                // copies in flight end before the CTA does
+                for (int i = 0; i < NST; ++i) {
+                    if (filled || i < ring.slot) mbar_wait(&S->full[i], i < ring.slot ? ring.phase : ring.phase ^ 1);
+                }
+        } else if (warp == kIssuer) {
+            // -------------------------------------------------------- issuer --
+            // The warp runs as one and an elected thread issues: operands that are
+            // the same for the whole warp then stay in uniform registers.  All
+            // tensor memory is this CTA's, so its addresses are constants.
+            const It &it = S->role[warp].it;
+            constexpr uint32_t idS = tc::idesc_bf16(kRowsTile, BN, false, false);
+            constexpr uint32_t idO = tc::idesc_bf16(kRowsTile, D, false, true);
+            constexpr uint32_t hi = tc::desc_hi(1024, tc::kSwizzle128B), HALF = BN * 128 >> 4;
+            const uint32_t kv_lo = tc::desc_lo(smem_u32(sm + G::SM_KV), BN * 128), q_lo = tc::desc_lo(smem_u32(sm), 16);
+            Ring<NST> ring;
+            uint32_t units = 0, ready[2] = {0, 0};               // q_ready, p_ready phases
+            bool ok = tmem == 0;
+            if (!ok) report_timeout(A.status, 89);               // never expected
+            auto arrived = [&](const Ring<NST> &x) { return wait_warp(&S->full[x.slot], x.phase, A.status, 92); };
+            auto release = [&]() {                               // once the products issued so far are done
+                if (tc::elect()) tc::commit(&S->empty[ring.slot]);
+                ring.next();
+            };
+            // S of stream T: row tile QT against a K tile
+            auto issue_S = [&](auto T, auto QT, int slot) {
+                const uint32_t a = q_lo + QT * (G::TILE >> 4), k = kv_lo + slot * (G::TILE >> 4);
+                if (tc::elect()) {
+                    tc::mma_ss2<false>(T * BN, a, hi, k, hi, idS);
+#pragma unroll
+                    for (int kk = 1; kk < D / 16; ++kk)
+                        tc::mma_ss2<true>(T * BN, a + (kk >> 2) * HALF + (kk & 3) * 2, hi, k + (kk >> 2) * HALF + (kk & 3) * 2,
+                                          hi, idS);
+                    tc::commit(&S->s_full[T]);
+                }
+            };
+            auto issue_PV = [&](auto T, int slot, bool first, bool last) {
+                constexpr uint32_t d = G::COL_O + T * D, p = T * BN;
+                const uint32_t v = kv_lo + slot * (G::TILE >> 4);
+                if (tc::elect()) {
+                    tc::mma_ts2(d, p, v, hi, idO, first ? 0u : 1u);
+#pragma unroll
+                    for (int kk = 1; kk < BN / 16; ++kk) tc::mma_ts2(d, p + kk * 8, v + kk * (2048 >> 4), hi, idO, 1u);
+                    if (last) tc::commit(&S->o_full[T]);
+                }
+            };
+            using C0 = std::integral_constant<int, 0>;
+            using C1 = std::integral_constant<int, 1>;
+            auto p_wait = [&](auto T) {
+                const bool r = wait_warp(&S->p_ready[T], ready[T] & 1, A.status, 93);
+                ++ready[T];
+                tc::fence_after();
+                return r;
+            };
+            while (ok && step(S, warp, A)) {
+                const int n = it.t_hi - it.t_lo;
+                ok = wait_warp(&S->q_ready, units & 1, A.status, 94);
+                ++units;
+                tc::fence_after();
+                ok = ok && arrived(ring);
+                if (!ok) break;
+                if (it.rows > kRowsTile) {
+                    // the streams are two row tiles on the same keys
+                    issue_S(C0{}, C0{}, ring.slot);
+                    issue_S(C1{}, C1{}, ring.slot);
+                    release();
+                    for (int j = 0; j < n; ++j) {
+                        const bool more = j + 1 < n;
+                        const Ring<NST> k = ring.after();        // K_{j+1}, after V_j
+                        ok = arrived(ring) && (!more || arrived(k)) && p_wait(C0{});
+                        if (!ok) break;
+                        issue_PV(C0{}, ring.slot, j == 0, !more);
+                        if (more) issue_S(C0{}, C0{}, k.slot);
+                        ok = p_wait(C1{});
+                        if (!ok) break;
+                        issue_PV(C1{}, ring.slot, j == 0, !more);
+                        release();
+                        if (more) {
+                            issue_S(C1{}, C1{}, ring.slot);
+                            release();
+                        }
+                    }
+                } else {
+                    // the streams take the key tiles of one row tile in turn
+                    issue_S(C0{}, C0{}, ring.slot);
+                    release();
+                    if (n > 1) {
+                        ok = arrived(ring);
+                        if (!ok) break;
+                        issue_S(C1{}, C0{}, ring.slot);
+                        release();
+                    }
+                    auto one = [&](auto T, int j) {
+                        ok = arrived(ring) && p_wait(T);
+                        if (!ok) return;
+                        issue_PV(T, ring.slot, j < 2, j + 2 >= n);
+                        release();
+                        if (j + 2 < n) {
+                            ok = arrived(ring);
+                            if (!ok) return;
+                            issue_S(T, C0{}, ring.slot);
+                            release();
+                        }
+                    };
+                    for (int j = 0; j < n && ok; j += 2) {
+                        one(C0{}, j);
+                        if (ok && j + 1 < n) one(C1{}, j + 1);
+                    }
+                }
+            }
+        }
+    } else if (KV8 && warp >= kConverter) {
+        // ------------------------------------------------------ converter --
+        fewer_registers<kSome>();
+        const It &it = S->role[S->index(warp)].it;
+        constexpr int CH = D / 16;                           // 16-byte chunks of a row of codes
+        const int x0 = threadIdx.x - kConverter * 32, c = x0 % CH;
+        Ring<NST> ring;
+        Ring<NST8> ring8;
+        bool ok = true, filled = false;
+        // the next tile; rows from `live` on become zeros
+        auto convert = [&](int live) {
+            ok = wait_warp(&S->full8[ring8.slot], ring8.phase, A.status, 102) &&
+                 (!filled || wait_warp(&S->empty[ring.slot], ring.phase ^ 1, A.status, 103));
+            if (!ok) return;
+            const uint8_t *src = sm + G::SM_8 + ring8.slot * G::ITEM8;
+            uint8_t *dst = sm + G::SM_KV + ring.slot * G::TILE + (c >> 2) * (BN * 128);
+#pragma unroll 4
+            for (int i = 0; i < BN * CH / kConverters; ++i) {
+                const int x = x0 + i * kConverters, row = x / CH;
+                uint4 w = *reinterpret_cast<const uint4 *>(src + x * 16);
+                uint32_t e = src[G::TILE8 + row];
+                if (row >= live) w = make_uint4(0, 0, 0, 0), e = 127;
+                uint4 o[2];
+                expand16(w, e, o);
+                // the halves' chunks fall on the same banks: odd ones first in the second
+                const int j = 2 * (c & 3), odd = c >> 2;
+                *reinterpret_cast<uint4 *>(dst + row * 128 + (((j + odd) ^ (row & 7)) << 4)) = odd ? o[1] : o[0];
+                *reinterpret_cast<uint4 *>(dst + row * 128 + (((j + 1 - odd) ^ (row & 7)) << 4)) = odd ? o[0] : o[1];
+            }
+            fence_async_smem();
+            mbar_arrive(&S->full[ring.slot]);
+            mbar_arrive(&S->empty8[ring8.slot]);
             ring.next();
+            ring8.next();
             filled = filled || ring.slot == 0;
         };
         while (ok && step(S, warp, A)) {
-            const int n = it.t_hi - it.t_lo, len = it.ctx + it.n;
-            const int ahead = it.rows > kRowsTile ? 1 : 2;
-            // the lane's box of key tile i: its table entry is read some tiles
-            // before it is looked at
-            auto entry = [&](int i) {
-                const int slot = (it.t_lo + i) * BN + bp * A.box_rows;
-                return on && i < n && slot < len
-                           ? A.P.table[(size_t)it.b * A.P.max_blocks + (slot >> A.P.page_log2)] : 0;
-            };
-            // past the sequence's end or through a bad page number: a row
-            // outside the map, which fills with zeros
-            auto row = [&](int i, int page) {
-                const int slot = (it.t_lo + i) * BN + bp * A.box_rows;
-                if (!on || slot >= len) return A.n_rows;
-                if ((unsigned)page < (unsigned)A.P.n_pages)
-                    return (int)A.P.row(page, it.h, slot & (A.P.page() - 1));
-                set_flag(A.P.status, VC_PAGED_BAD_PAGE);
-                return A.n_rows;
-            };
-            int e0 = entry(0), e1 = entry(1), e2 = entry(2);
-            load(&tmK, row(0, e0));
-            if (ok && ahead == 2 && n > 1) load(&tmK, row(1, e1));
+            const int n = it.t_hi - it.t_lo, ahead = it.rows > kRowsTile ? 1 : 2;
+            auto live = [&](int i) { return it.len() - (it.t_lo + i) * BN; };
+            convert(live(0));
+            if (ok && ahead == 2 && n > 1) convert(live(1));
             for (int i = 0; i < n && ok; ++i) {
-                const int e3 = entry(i + 3);
-                load(&tmV, row(i, e0));
-                if (ok && i + ahead < n) load(&tmK, row(i + ahead, ahead == 1 ? e1 : e2));
-                e0 = e1, e1 = e2, e2 = e3;
-            }
-        }
-        if (!ok && lane == 0)                                // copies in flight end before the CTA does
-            for (int i = 0; i < NST; ++i) {
-                if (filled || i < ring.slot) mbar_wait(&S->full[i], i < ring.slot ? ring.phase : ring.phase ^ 1);
-            }
-    } else if (warp == kIssuer) {
-        // -------------------------------------------------------- issuer --
-        // The warp runs as one and an elected thread issues: operands that are
-        // the same for the whole warp then stay in uniform registers.  All
-        // tensor memory is this CTA's, so its addresses are constants.
-        const Item &it = S->role[warp].it;
-        constexpr uint32_t idS = tc::idesc_bf16(kRowsTile, BN, false, false);
-        constexpr uint32_t idO = tc::idesc_bf16(kRowsTile, D, false, true);
-        constexpr uint32_t hi = tc::desc_hi(1024, tc::kSwizzle128B), HALF = BN * 128 >> 4;
-        const uint32_t kv_lo = tc::desc_lo(smem_u32(sm + G::SM_KV), BN * 128), q_lo = tc::desc_lo(smem_u32(sm), 16);
-        Ring<NST> ring;
-        uint32_t units = 0, ready[2] = {0, 0};               // q_ready, p_ready phases
-        bool ok = tmem == 0;
-        if (!ok) report_timeout(A.status, 89);               // never expected
-        auto arrived = [&](const Ring<NST> &x) { return wait_warp(&S->full[x.slot], x.phase, A.status, 92); };
-        auto release = [&]() {                               // once the products issued so far are done
-            if (tc::elect()) tc::commit(&S->empty[ring.slot]);
-            ring.next();
-        };
-        // S of stream T: row tile QT against a K tile
-        auto issue_S = [&](auto T, auto QT, int slot) {
-            const uint32_t a = q_lo + QT * (G::TILE >> 4), k = kv_lo + slot * (G::TILE >> 4);
-            if (tc::elect()) {
-                tc::mma_ss2<false>(T * BN, a, hi, k, hi, idS);
-#pragma unroll
-                for (int kk = 1; kk < D / 16; ++kk)
-                    tc::mma_ss2<true>(T * BN, a + (kk >> 2) * HALF + (kk & 3) * 2, hi, k + (kk >> 2) * HALF + (kk & 3) * 2,
-                                      hi, idS);
-                tc::commit(&S->s_full[T]);
-            }
-        };
-        auto issue_PV = [&](auto T, int slot, bool first, bool last) {
-            constexpr uint32_t d = G::COL_O + T * D, p = T * BN;
-            const uint32_t v = kv_lo + slot * (G::TILE >> 4);
-            if (tc::elect()) {
-                tc::mma_ts2(d, p, v, hi, idO, first ? 0u : 1u);
-#pragma unroll
-                for (int kk = 1; kk < BN / 16; ++kk) tc::mma_ts2(d, p + kk * 8, v + kk * (2048 >> 4), hi, idO, 1u);
-                if (last) tc::commit(&S->o_full[T]);
-            }
-        };
-        using C0 = std::integral_constant<int, 0>;
-        using C1 = std::integral_constant<int, 1>;
-        auto p_wait = [&](auto T) {
-            const bool r = wait_warp(&S->p_ready[T], ready[T] & 1, A.status, 93);
-            ++ready[T];
-            tc::fence_after();
-            return r;
-        };
-        while (ok && step(S, warp, A)) {
-            const int n = it.t_hi - it.t_lo;
-            ok = wait_warp(&S->q_ready, units & 1, A.status, 94);
-            ++units;
-            tc::fence_after();
-            ok = ok && arrived(ring);
-            if (!ok) break;
-            if (it.rows > kRowsTile) {
-                // the streams are two row tiles on the same keys
-                issue_S(C0{}, C0{}, ring.slot);
-                issue_S(C1{}, C1{}, ring.slot);
-                release();
-                for (int j = 0; j < n; ++j) {
-                    const bool more = j + 1 < n;
-                    const Ring<NST> k = ring.after();        // K_{j+1}, after V_j
-                    ok = arrived(ring) && (!more || arrived(k)) && p_wait(C0{});
-                    if (!ok) break;
-                    issue_PV(C0{}, ring.slot, j == 0, !more);
-                    if (more) issue_S(C0{}, C0{}, k.slot);
-                    ok = p_wait(C1{});
-                    if (!ok) break;
-                    issue_PV(C1{}, ring.slot, j == 0, !more);
-                    release();
-                    if (more) {
-                        issue_S(C1{}, C1{}, ring.slot);
-                        release();
-                    }
-                }
-            } else {
-                // the streams take the key tiles of one row tile in turn
-                issue_S(C0{}, C0{}, ring.slot);
-                release();
-                if (n > 1) {
-                    ok = arrived(ring);
-                    if (!ok) break;
-                    issue_S(C1{}, C0{}, ring.slot);
-                    release();
-                }
-                auto one = [&](auto T, int j) {
-                    ok = arrived(ring) && p_wait(T);
-                    if (!ok) return;
-                    issue_PV(T, ring.slot, j < 2, j + 2 >= n);
-                    release();
-                    if (j + 2 < n) {
-                        ok = arrived(ring);
-                        if (!ok) return;
-                        issue_S(T, C0{}, ring.slot);
-                        release();
-                    }
-                };
-                for (int j = 0; j < n && ok; j += 2) {
-                    one(C0{}, j);
-                    if (ok && j + 1 < n) one(C1{}, j + 1);
-                }
+                convert(live(i));
+                if (ok && i + ahead < n) convert(live(i + ahead));
             }
         }
     } else {
         // ------------------------------------------------------- softmax --
-        const Item &it = S->role[warp].it;
+        if constexpr (KV8) more_registers<kMany>();
+        const It &it = S->role[warp].it;
         const int t = warp >> 2;                             // stream
         const int r = threadIdx.x & 127;                     // row of the stream's tile
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -335,13 +506,15 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
         float2 *ml_x = reinterpret_cast<float2 *>(sm + G::SM_Q + G::TILE);
         if (threadIdx.x == 0) A.parts.desc[blockIdx.x].parts = 0;
         while (ok && step(S, warp, A)) {
-            const int n = it.t_hi - it.t_lo, len = it.ctx + it.n;
+            const int n = it.t_hi - it.t_lo, len = it.len();
             const bool big = it.rows > kRowsTile;
             const int row0 = it.mt * 256;
-            auto out_row = [&](int rr) {                     // row of q, out and lse_out
+            auto head_row = [&](int tok0, int rr) {
                 const int R = row0 + rr;
-                return (size_t)(it.tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G;
+                return (size_t)(tok0 + R / A.W.G) * A.Hq + it.h * A.W.G + R % A.W.G;
             };
+            auto q_row = [&](int rr) { return head_row(it.tok0, rr); };
+            auto out_row = [&](int rr) { return head_row(it.out_tok0(), rr); };   // of out and lse_out
             {
                 // Q: big, the stream's tile; else each group half of the one tile
                 constexpr int CH = D / 8, RP = 128 / CH;     // 16-byte chunks per row, rows per pass
@@ -356,7 +529,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         const int rr = lo + i0 + e * RP;
                         x[e] = make_uint4(0, 0, 0, 0);
                         if (i0 + e * RP < cnt && base + rr < it.rows)
-                            x[e] = *reinterpret_cast<const uint4 *>(A.q + out_row(base + rr) * D + c * 8);
+                            x[e] = *reinterpret_cast<const uint4 *>(A.q + q_row(base + rr) * D + c * 8);
                     }
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -373,15 +546,16 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             }
             const int R = (big ? t * 128 : 0) + r;           // row within the unit
             const bool valid = R < it.rows;
-            const int kmax = valid ? it.ctx + (row0 + R) / A.W.G : -1;
+            const int kmax = valid ? it.last((row0 + R) / A.W.G) : -1;
             // keys every row of the tile sees
-            const int kall = it.ctx + (row0 + (big ? t * 128 : 0)) / A.W.G;
-            float *s_row = STORE && valid ? A.s_out + (long)out_row(R) * A.s_stride : nullptr;
+            const int kall = it.last((row0 + (big ? t * 128 : 0)) / A.W.G);
+            float *s_row = STORE && valid ? A.s_out + (long)q_row(R) * A.s_stride : nullptr;
             float m = kLowestProduct, l = 0.f;               // m: of the products
             const int mine = big ? n : (n + 1 - t) / 2;      // this stream's steps
             // V rows of the last page past the sequence's end, before the product
             // with key tile i (big: stream 0's comes first)
             auto zero_tail = [&](int i) {
+                if constexpr (KV8) return;                   // the converters have done it
                 const int key0 = (it.t_lo + i) * BN;
                 if (i != n - 1 || key0 + BN <= len || (big && t == 1)) return;
                 const uint32_t vi = item + 2u * n - 1;       // the part's last ring item
@@ -519,7 +693,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         x[e] = __uint_as_float(o[e]) * w0;
                         if (!big && n > 1) x[e] = fmaf(__uint_as_float(o1[e]), w1, x[e]);
                     }
-                    if (valid && it.whole) {
+                    if (PLANNED && valid && it.whole) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4)
+                            *reinterpret_cast<float4 *>((float *)A.out + row * D + c + e) =
+                                make_float4(x[e] * inv, x[e + 1] * inv, x[e + 2] * inv, x[e + 3] * inv);
+                    } else if (valid && it.whole) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 8) {
                             uint32_t w[4];
@@ -528,7 +707,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                                 const __nv_bfloat162 b = __floats2bfloat162_rn(x[e + 2 * k] * inv, x[e + 2 * k + 1] * inv);
                                 w[k] = *reinterpret_cast<const uint32_t *>(&b);
                             }
-                            *reinterpret_cast<uint4 *>(A.out + row * D + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4 *>((__nv_bfloat16 *)A.out + row * D + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
                         }
                     } else if (valid) {
 #pragma unroll
@@ -568,7 +747,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             if (!it.whole && it.head && threadIdx.x == 0) {
                 PartDesc &d = A.parts.desc[blockIdx.x];
                 d.parts = it.parts;
-                d.tok0 = it.tok0;
+                d.tok0 = it.out_tok0();
                 d.h = it.h;
                 d.row0 = row0;
                 d.rows = it.rows;
@@ -585,7 +764,7 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
 }
 
-template <int D, bool STORE>
+template <int D, bool STORE, typename SEQ, bool KV8>
 cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
                    float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st)
 {
@@ -593,7 +772,7 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     A.P = P;
     A.W = W;
     A.q = (const __nv_bfloat16 *)q;
-    A.out = (__nv_bfloat16 *)out;
+    A.out = out;
     A.lse_out = lse;
     A.parts = parts;
     A.status = status;
@@ -604,29 +783,22 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     A.n_rows = (P.n_pages * P.Hkv) << P.page_log2;
     A.sl2 = std::max(sl2, 1e-38f);     // a masked product is -inf; times zero it would be NaN
     CUtensorMap mk, mv;
-    const uint64_t bytes = (uint64_t)D * 2;
-    if (!tma_map_bf16_3d(&mk, P.k, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1) ||
-        !tma_map_bf16_3d(&mv, P.v, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1))
-        return cudaErrorInvalidValue;
-    auto kern = attn_tc_kernel<D, STORE>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, Geom<D>::SMEM);
+    if constexpr (KV8) {
+        if (!tma_map_u8_2d(&mk, P.k, D, A.n_rows, A.box_rows) || !tma_map_u8_2d(&mv, P.v, D, A.n_rows, A.box_rows))
+            return cudaErrorInvalidValue;
+    } else {
+        const uint64_t bytes = (uint64_t)D * 2;
+        if (!tma_map_bf16_3d(&mk, P.k, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1) ||
+            !tma_map_bf16_3d(&mv, P.v, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, A.box_rows, 1))
+            return cudaErrorInvalidValue;
+    }
+    auto kern = attn_tc_kernel<D, STORE, SEQ, KV8>;
+    constexpr int smem = Geom<D, KV8>::SMEM;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(tc_ctas()), dim3(kThreads), Geom<D>::SMEM, st, mk, mv, A);
+    return launch_pdl(kern, dim3(tc_ctas()), dim3(KV8 ? kThreads8 : kThreads), smem, st, mk, mv, A);
 }
 
 }  // namespace
-
-int tc_ctas() { return device_sm_count(); }
-
-cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
-                    float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st)
-{
-    if (s_out)
-        return d == 128 ? launch<128, true>(P, W, q, Hq, sl2, out, lse, s_out, s_stride, parts, status, st)
-                        : launch<64, true>(P, W, q, Hq, sl2, out, lse, s_out, s_stride, parts, status, st);
-    return d == 128 ? launch<128, false>(P, W, q, Hq, sl2, out, lse, nullptr, 0, parts, status, st)
-                    : launch<64, false>(P, W, q, Hq, sl2, out, lse, nullptr, 0, parts, status, st);
-}
-
 }  // namespace paged
 }  // namespace vc

@@ -447,6 +447,30 @@ paged::Pool paged_pool(const vc_paged_cache *c)
     while ((1 << P.page_log2) < c->page) ++P.page_log2;
     P.n_pages = c->n_pages;
     P.max_blocks = c->max_blocks;
+    P.k_scale = P.v_scale = nullptr;
+    return P;
+}
+
+// What an 8-bit cache has in common with others: all that the checks look at.
+vc_paged_cache paged8_base(const vc_paged8_cache *c)
+{
+    return vc_paged_cache{c->k_pages, c->v_pages, c->block_table, c->status, c->B, c->Hkv, c->d, c->page,
+                          c->n_pages, c->max_blocks, c->dt};
+}
+
+bool paged8_ok(const vc_paged8_cache *c)
+{
+    if (!c || !c->k_scale || !c->v_scale || !aligned(c->k_scale, 16) || !aligned(c->v_scale, 16)) return false;
+    const vc_paged_cache b = paged8_base(c);
+    return paged_ok(&b);
+}
+
+paged::Pool paged8_pool(const vc_paged8_cache *c)
+{
+    const vc_paged_cache b = paged8_base(c);
+    paged::Pool P = paged_pool(&b);
+    P.k_scale = (uint8_t *)c->k_scale;
+    P.v_scale = (uint8_t *)c->v_scale;
     return P;
 }
 
@@ -456,23 +480,69 @@ size_t paged_attn_ws(const vc_paged_cache *c, int T, int Hq, bool mass)
     return paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page, mass);
 }
 
-vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const int32_t *q_start, const int32_t *ctx_len,
-                          int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws,
-                          size_t ws_bytes, cudaStream_t stream)
+bool shared_ok(const vc_shared_prefix *s)
 {
-    if (!paged_ok(c) || !q_start || !ctx_len || !ws || !paged_heads_ok(c, T, Hq)) return VC_ERR_INVALID;
+    return s->n >= 0 && (s->n == 0 || (s->seq_start && s->len));
+}
+
+// the rows of both halves are numbered with 31 bits, as are the plan's entries
+// times the heads
+bool shared_supported(const vc_paged_cache *c, int n_groups, int T, int Hq)
+{
+    return (int64_t)T * Hq <= (1 << 29) && (int64_t)c->B + n_groups <= INT32_MAX / 64 / c->Hkv;
+}
+
+// c: what the checks look at; P: the pool that the kernels see
+vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const paged::Pool &P, const int32_t *q_start,
+                          const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out, float *scores,
+                          int scores_stride, const vc_shared_prefix *shared, void *ws, size_t ws_bytes,
+                          cudaStream_t stream)
+{
+    if (!q_start || !ctx_len || !ws || !paged_heads_ok(c, T, Hq)) return VC_ERR_INVALID;
     if (T > 0 && (!q || !out || q == out)) return VC_ERR_INVALID;      // an empty batch's may be null
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(ws, 256)) return VC_ERR_INVALID;
     if (!(sm_scale >= 0.f) || sm_scale > FLT_MAX) return VC_ERR_INVALID;
+    if (shared && !shared_ok(shared)) return VC_ERR_INVALID;
     if (!paged_supported(c) || !paged_rows_ok(c, T, Hq)) return VC_ERR_UNSUPPORTED;
+    if (shared && !shared_supported(c, shared->n, T, Hq)) return VC_ERR_UNSUPPORTED;
     // scores of products up to 1e30, and their differences, stay finite in the log2 domain
     if (sm_scale > 1e8f) return VC_ERR_UNSUPPORTED;
     if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
-    if (ws_bytes < paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page,
-                                     scores != nullptr)) return VC_ERR_INVALID;
+    const long cap = (long)c->max_blocks * c->page;
+    if (ws_bytes < (shared ? paged::attn_shared_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, shared->n)
+                           : paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, scores != nullptr)))
+        return VC_ERR_INVALID;
     if (T == 0) return VC_OK;
-    return cuda_status(paged::attn(paged_pool(c), c->dt, c->d, q, q_start, ctx_len, T, Hq, sm_scale, out, scores,
-                                   scores_stride, ws, stream));
+    if (shared)
+        return cuda_status(paged::attn_shared(P, c->dt, c->d, q, paged::Groups{shared->seq_start, shared->len, shared->n},
+                                              q_start, ctx_len, T, Hq, sm_scale, out, ws, stream));
+    return cuda_status(paged::attn(P, c->dt, c->d, q, q_start, ctx_len, T, Hq, sm_scale, out, scores, scores_stride, ws,
+                                   stream));
+}
+
+size_t paged_shared_ws(const vc_paged_cache *c, int n_groups, int T, int Hq)
+{
+    if (n_groups < 0 || !paged_supported(c) || !paged_heads_ok(c, T, Hq) || !paged_rows_ok(c, T, Hq) ||
+        !shared_supported(c, n_groups, T, Hq))
+        return 0;
+    return paged::attn_shared_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page, n_groups);
+}
+
+vc_status paged_append_call(const void *qkv, const void *q_gain, const void *k_gain, float eps, const vc_rope *rope,
+                            const int32_t *positions, const int32_t *q_start, const int32_t *ctx_len, int T, int Hq,
+                            const vc_paged_cache *c, const paged::Pool &P, void *q_out, cudaStream_t stream)
+{
+    if (!rope || !q_start || !ctx_len) return VC_ERR_INVALID;
+    if (T > 0 && (!qkv || !q_out || qkv == q_out)) return VC_ERR_INVALID;
+    if (!paged_heads_ok(c, T, Hq) || (q_gain == nullptr) != (k_gain == nullptr)) return VC_ERR_INVALID;
+    if (!(eps >= 0.f) || eps > FLT_MAX || !aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16) ||
+        !aligned(k_gain, 16))
+        return VC_ERR_INVALID;
+    if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > c->d) return VC_ERR_INVALID;
+    if (!paged_supported(c) || !paged_rows_ok(c, T, Hq)) return VC_ERR_UNSUPPORTED;
+    if (T == 0) return VC_OK;
+    return cuda_status(paged::append(P, c->dt, c->d, qkv, q_gain, k_gain, eps, *rope, positions, q_start, ctx_len, T, Hq,
+                                     q_out, stream));
 }
 
 }  // namespace
@@ -506,17 +576,31 @@ vc_status vc_paged_append(const void *qkv, const void *q_gain, const void *k_gai
                           const int32_t *positions, const int32_t *q_start, const int32_t *ctx_len, int T, int Hq,
                           const vc_paged_cache *cache, void *q_out, cudaStream_t stream)
 {
-    if (!paged_ok(cache) || !rope || !q_start || !ctx_len) return VC_ERR_INVALID;
-    if (T > 0 && (!qkv || !q_out || qkv == q_out)) return VC_ERR_INVALID;
-    if (!paged_heads_ok(cache, T, Hq) || (q_gain == nullptr) != (k_gain == nullptr)) return VC_ERR_INVALID;
-    if (!(eps >= 0.f) || eps > FLT_MAX || !aligned(qkv, 16) || !aligned(q_out, 16) || !aligned(q_gain, 16) ||
-        !aligned(k_gain, 16))
-        return VC_ERR_INVALID;
-    if (rope->rotary_dim < 16 || rope->rotary_dim % 16 || rope->rotary_dim > cache->d) return VC_ERR_INVALID;
-    if (!paged_supported(cache) || !paged_rows_ok(cache, T, Hq)) return VC_ERR_UNSUPPORTED;
+    if (!paged_ok(cache)) return VC_ERR_INVALID;
+    return paged_append_call(qkv, q_gain, k_gain, eps, rope, positions, q_start, ctx_len, T, Hq, cache,
+                             paged_pool(cache), q_out, stream);
+}
+
+vc_status vc_paged8_append(const void *qkv, const void *q_gain, const void *k_gain, float eps, const vc_rope *rope,
+                           const int32_t *positions, const int32_t *q_start, const int32_t *ctx_len, int T, int Hq,
+                           const vc_paged8_cache *cache, void *q_out, cudaStream_t stream)
+{
+    if (!paged8_ok(cache)) return VC_ERR_INVALID;
+    const vc_paged_cache c = paged8_base(cache);
+    return paged_append_call(qkv, q_gain, k_gain, eps, rope, positions, q_start, ctx_len, T, Hq, &c, paged8_pool(cache),
+                             q_out, stream);
+}
+
+vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len, int T,
+                         void *k_out, void *v_out, cudaStream_t stream)
+{
+    if (!paged8_ok(cache) || !q_start || !ctx_len || T < 0) return VC_ERR_INVALID;
+    if (T > 0 && (!k_out || !v_out || k_out == v_out)) return VC_ERR_INVALID;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16)) return VC_ERR_INVALID;
+    const vc_paged_cache c = paged8_base(cache);
+    if (!paged_supported(&c) || (int64_t)T * c.Hkv > (1 << 30)) return VC_ERR_UNSUPPORTED;
     if (T == 0) return VC_OK;
-    return cuda_status(paged::append(paged_pool(cache), cache->dt, cache->d, qkv, q_gain, k_gain, eps, *rope, positions,
-                                     q_start, ctx_len, T, Hq, q_out, stream));
+    return cuda_status(paged::read8(paged8_pool(cache), c.dt, c.d, q_start, ctx_len, T, k_out, v_out, stream));
 }
 
 size_t vc_paged_attn_workspace_bytes(const vc_paged_cache *cache, int T, int Hq)
@@ -527,7 +611,56 @@ size_t vc_paged_attn_workspace_bytes(const vc_paged_cache *cache, int T, int Hq)
 vc_status vc_paged_attn(const void *q, const vc_paged_cache *cache, const int32_t *q_start, const int32_t *ctx_len,
                         int T, int Hq, float sm_scale, void *out, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
-    return paged_attn_call(q, cache, q_start, ctx_len, T, Hq, sm_scale, out, nullptr, 0, ws, ws_bytes, stream);
+    if (!paged_ok(cache)) return VC_ERR_INVALID;
+    return paged_attn_call(q, cache, paged_pool(cache), q_start, ctx_len, T, Hq, sm_scale, out, nullptr, 0, nullptr, ws,
+                           ws_bytes, stream);
+}
+
+size_t vc_paged8_attn_workspace_bytes(const vc_paged8_cache *cache, int T, int Hq)
+{
+    if (!paged8_ok(cache)) return 0;
+    const vc_paged_cache c = paged8_base(cache);
+    return paged_attn_ws(&c, T, Hq, false);
+}
+
+vc_status vc_paged8_attn(const void *q, const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len,
+                         int T, int Hq, float sm_scale, void *out, void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!paged8_ok(cache)) return VC_ERR_INVALID;
+    const vc_paged_cache c = paged8_base(cache);
+    return paged_attn_call(q, &c, paged8_pool(cache), q_start, ctx_len, T, Hq, sm_scale, out, nullptr, 0, nullptr, ws,
+                           ws_bytes, stream);
+}
+
+size_t vc_paged_attn_shared_workspace_bytes(const vc_paged_cache *cache, int n_groups, int T, int Hq)
+{
+    return paged_ok(cache) ? paged_shared_ws(cache, n_groups, T, Hq) : 0;
+}
+
+vc_status vc_paged_attn_shared(const void *q, const vc_paged_cache *cache, const vc_shared_prefix *groups,
+                               const int32_t *q_start, const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out,
+                               void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!paged_ok(cache) || !groups) return VC_ERR_INVALID;
+    return paged_attn_call(q, cache, paged_pool(cache), q_start, ctx_len, T, Hq, sm_scale, out, nullptr, 0, groups, ws,
+                           ws_bytes, stream);
+}
+
+size_t vc_paged8_attn_shared_workspace_bytes(const vc_paged8_cache *cache, int n_groups, int T, int Hq)
+{
+    if (!paged8_ok(cache)) return 0;
+    const vc_paged_cache c = paged8_base(cache);
+    return paged_shared_ws(&c, n_groups, T, Hq);
+}
+
+vc_status vc_paged8_attn_shared(const void *q, const vc_paged8_cache *cache, const vc_shared_prefix *groups,
+                                const int32_t *q_start, const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out,
+                                void *ws, size_t ws_bytes, cudaStream_t stream)
+{
+    if (!paged8_ok(cache) || !groups) return VC_ERR_INVALID;
+    const vc_paged_cache c = paged8_base(cache);
+    return paged_attn_call(q, &c, paged8_pool(cache), q_start, ctx_len, T, Hq, sm_scale, out, nullptr, 0, groups, ws,
+                           ws_bytes, stream);
 }
 
 size_t vc_paged_attn_h2o_workspace_bytes(const vc_paged_cache *cache, int T, int Hq)
@@ -539,9 +672,9 @@ vc_status vc_paged_attn_h2o(const void *q, const vc_paged_cache *cache, const in
                             const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out, float *scores,
                             int scores_stride, void *ws, size_t ws_bytes, cudaStream_t stream)
 {
-    if (!scores) return VC_ERR_INVALID;
-    return paged_attn_call(q, cache, q_start, ctx_len, T, Hq, sm_scale, out, scores, scores_stride, ws, ws_bytes,
-                           stream);
+    if (!scores || !paged_ok(cache)) return VC_ERR_INVALID;
+    return paged_attn_call(q, cache, paged_pool(cache), q_start, ctx_len, T, Hq, sm_scale, out, scores, scores_stride,
+                           nullptr, ws, ws_bytes, stream);
 }
 
 vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_cache *src, const int32_t *src_len,

@@ -59,6 +59,16 @@ class PagedCacheC(ctypes.Structure):
                 ("max_blocks", c_int32), ("dt", c_int)]
 
 
+class Paged8CacheC(ctypes.Structure):
+    _fields_ = [("k_pages", c_void_p), ("v_pages", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("block_table", c_void_p), ("status", c_void_p), ("B", c_int32), ("Hkv", c_int32), ("d", c_int32),
+                ("page", c_int32), ("n_pages", c_int32), ("max_blocks", c_int32), ("dt", c_int)]
+
+
+class SharedPrefixC(ctypes.Structure):
+    _fields_ = [("seq_start", c_void_p), ("len", c_void_p), ("n", c_int32)]
+
+
 class Rope(ctypes.Structure):
     _fields_ = [("turn", ctypes.c_uint64 * 64), ("rotary_dim", c_int32), ("reserved", c_int32)]
 
@@ -206,6 +216,19 @@ def load() -> ctypes.CDLL:
     L.vc_paged_attn_h2o.argtypes = [P, PC, P, P, c_int, c_int, c_float, P, P, c_int, P, c_size_t, P]
     L.vc_paged_evict.restype = c_int
     L.vc_paged_evict.argtypes = [P, c_int, PC, P, DropCfg, PC, P, P, c_int, P, c_int, P]
+    SP, P8 = ctypes.POINTER(SharedPrefixC), ctypes.POINTER(Paged8CacheC)
+    L.vc_paged8_append.restype = c_int
+    L.vc_paged8_append.argtypes = [P, P, P, c_float, ctypes.POINTER(Rope), P, P, P, c_int, c_int, P8, P, P]
+    L.vc_paged8_read.restype = c_int
+    L.vc_paged8_read.argtypes = [P8, P, P, c_int, P, P, P]
+    L.vc_paged8_attn_workspace_bytes.restype = c_size_t
+    L.vc_paged8_attn_workspace_bytes.argtypes = [P8, c_int, c_int]
+    L.vc_paged8_attn.restype = c_int
+    L.vc_paged8_attn.argtypes = [P, P8, P, P, c_int, c_int, c_float, P, P, c_size_t, P]
+    for name, cache in (("vc_paged_attn_shared", PC), ("vc_paged8_attn_shared", P8)):
+        size, call = getattr(L, name + "_workspace_bytes"), getattr(L, name)
+        size.restype, size.argtypes = c_size_t, [cache, c_int, c_int, c_int]
+        call.restype, call.argtypes = c_int, [P, cache, SP, P, P, c_int, c_int, c_float, P, P, c_size_t, P]
     _lib = L
     return L
 
@@ -224,7 +247,10 @@ EXPORTED = ["vc_status_str", "vc_version", "vc_check", "vc_workspace_init", "vc_
             "vc_verify_attn_h2o_workspace_bytes", "vc_verify_attn_h2o", "vc_decoder_set_layer_events",
             "vc_gemm_swiglu", "vc_swap_in_rows", "vc_gemm_rms", "vc_rope_init", "vc_rope_init_freqs",
             "vc_paged_append", "vc_paged_attn_workspace_bytes", "vc_paged_attn",
-            "vc_paged_attn_h2o_workspace_bytes", "vc_paged_attn_h2o", "vc_paged_evict"]
+            "vc_paged_attn_h2o_workspace_bytes", "vc_paged_attn_h2o", "vc_paged_evict",
+            "vc_paged_attn_shared_workspace_bytes", "vc_paged_attn_shared", "vc_paged8_append", "vc_paged8_read",
+            "vc_paged8_attn_workspace_bytes", "vc_paged8_attn", "vc_paged8_attn_shared_workspace_bytes",
+            "vc_paged8_attn_shared"]
 
 TRACE_KINDS = ["gemm_qkv", "gemm_o", "gemm_gate_up", "gemm_down", "gemm_head", "draft_attn", "verify_attn"]
 
@@ -786,6 +812,9 @@ class PagedCache:
         self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
         self.c = PagedCacheC(k.data_ptr(), v.data_ptr(), block_table.data_ptr(), self.status.data_ptr(), self.B,
                              self.Hkv, self.d, self.page, self.n_pages, self.max_blocks, _dt(k))
+        self._prepare()
+
+    def _prepare(self):
         # what every call needs, made once (a call's checks are most of its host time)
         self.ref = ctypes.byref(self.c)
         self._index = self.device.index if self.device.type == "cuda" else None
@@ -820,6 +849,37 @@ class PagedCache:
             raise ValueError(f"q_start [{self.B + 1}] and ctx_len [{self.B}] expected")
 
 
+class Paged8Cache(PagedCache):
+    """A page pool in 8 bits and the block table of one batch (include/vc.h,
+    vc_paged8_cache): k, v [n_pages][Hkv][page][d] float8_e4m3fn or uint8 codes,
+    k_scale, v_scale [n_pages][Hkv][page] float8_e8m0fnu or uint8 exponents; dtype:
+    bfloat16 or float32, of the rows outside the pages.  Like PagedCache, it keeps
+    no copy."""
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 block_table: torch.Tensor, dtype: torch.dtype = torch.bfloat16):
+        codes, exponents = (torch.uint8, torch.float8_e4m3fn), (torch.uint8, torch.float8_e8m0fnu)
+        assert k.dim() == 4 and k.shape == v.shape and k.dtype in codes and v.dtype in codes
+        assert k_scale.shape == k.shape[:3] == v_scale.shape
+        assert k_scale.dtype in exponents and v_scale.dtype in exponents
+        assert all(t.is_contiguous() and t.device == k.device for t in (k, v, k_scale, v_scale, block_table))
+        assert block_table.dim() == 2 and block_table.dtype == torch.int32
+        self.k, self.v, self.k_scale, self.v_scale, self.block_table = k, v, k_scale, v_scale, block_table
+        self.n_pages, self.Hkv, self.page, self.d = k.shape
+        self.B, self.max_blocks = block_table.shape
+        self.dtype, self.device = dtype, k.device
+        self.status = torch.zeros(1, dtype=torch.int32, device=k.device)
+        self.c = Paged8CacheC(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(),
+                              block_table.data_ptr(), self.status.data_ptr(), self.B, self.Hkv, self.d, self.page,
+                              self.n_pages, self.max_blocks, _dt(torch.empty(0, dtype=dtype)))
+        self._prepare()
+
+
+def _is8(cache, want: bool):
+    if isinstance(cache, Paged8Cache) != want:
+        raise TypeError("a Paged8Cache is expected" if want else "a PagedCache of bf16 or fp32 rows is expected")
+
+
 def vc_rope_init(rotary_dim: int, theta: float) -> Rope:
     r = Rope()
     _check(load().vc_rope_init(ctypes.byref(r), int(rotary_dim), float(theta)), "vc_rope_init")
@@ -835,11 +895,7 @@ def vc_rope_init_freqs(inv_freq) -> Rope:
     return r
 
 
-def vc_paged_append(qkv, cache: PagedCache, q_start, ctx_len, q_out, rope: Rope, positions=None, q_gain=None,
-                    k_gain=None, eps: float = 1e-6, stream=None):
-    """qkv [T][(Hq + 2 Hkv) d] -> q_out [T][Hq][d] and the cache's pages, with
-    per-head RMS norm (q_gain, k_gain [d]; both or neither) and rotation at
-    positions int32 [T] (None: the tokens' slots)."""
+def _paged_append(name, qkv, cache, q_start, ctx_len, q_out, rope, positions, q_gain, k_gain, eps, stream):
     T, Hq, d = q_out.shape
     dtype = cache.dtype
     cache._check(qkv, q_start, ctx_len, q_out, positions, q_gain, k_gain)
@@ -853,9 +909,40 @@ def vc_paged_append(qkv, cache: PagedCache, q_start, ctx_len, q_out, rope: Rope,
     if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
         raise TypeError("positions is int32 [T]")
     cache._on_gpu()
-    _check(load().vc_paged_append(qkv.data_ptr(), _ptr(q_gain), _ptr(k_gain), float(eps), ctypes.byref(rope),
-                                  _ptr(positions), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq, cache.ref,
-                                  q_out.data_ptr(), cache._stream(stream)), "vc_paged_append")
+    _check(getattr(load(), name)(qkv.data_ptr(), _ptr(q_gain), _ptr(k_gain), float(eps), ctypes.byref(rope),
+                                 _ptr(positions), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq, cache.ref,
+                                 q_out.data_ptr(), cache._stream(stream)), name)
+
+
+def vc_paged_append(qkv, cache: PagedCache, q_start, ctx_len, q_out, rope: Rope, positions=None, q_gain=None,
+                    k_gain=None, eps: float = 1e-6, stream=None):
+    """qkv [T][(Hq + 2 Hkv) d] -> q_out [T][Hq][d] and the cache's pages, with
+    per-head RMS norm (q_gain, k_gain [d]; both or neither) and rotation at
+    positions int32 [T] (None: the tokens' slots)."""
+    _is8(cache, False)
+    _paged_append("vc_paged_append", qkv, cache, q_start, ctx_len, q_out, rope, positions, q_gain, k_gain, eps, stream)
+
+
+def vc_paged8_append(qkv, cache: Paged8Cache, q_start, ctx_len, q_out, rope: Rope, positions=None, q_gain=None,
+                     k_gain=None, eps: float = 1e-6, stream=None):
+    """vc_paged_append into 8-bit pages (qkv, q_out and the gains in cache.dtype)."""
+    _is8(cache, True)
+    _paged_append("vc_paged8_append", qkv, cache, q_start, ctx_len, q_out, rope, positions, q_gain, k_gain, eps, stream)
+
+
+def vc_paged8_read(cache: Paged8Cache, q_start, ctx_len, k_out, v_out, stream=None):
+    """Cached tokens back as values: row i of sequence b is its slot ctx_len[b]
+    + i; k_out, v_out [T][Hkv][d] in cache.dtype."""
+    _is8(cache, True)
+    cache._check(q_start, ctx_len, k_out, v_out)
+    cache._check_batch(q_start, ctx_len)
+    if k_out.dim() != 3 or k_out.shape != v_out.shape or k_out.shape[1:] != (cache.Hkv, cache.d):
+        raise ValueError(f"k_out and v_out [T][{cache.Hkv}][{cache.d}] expected")
+    if k_out.dtype != cache.dtype or v_out.dtype != cache.dtype:
+        raise TypeError("k_out and v_out have the cache's dtype")
+    cache._on_gpu()
+    _check(load().vc_paged8_read(cache.ref, q_start.data_ptr(), ctx_len.data_ptr(), k_out.shape[0], k_out.data_ptr(),
+                                 v_out.data_ptr(), cache._stream(stream)), "vc_paged8_read")
 
 
 def vc_paged_attn_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
@@ -864,6 +951,21 @@ def vc_paged_attn_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
 
 def vc_paged_attn_h2o_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
     return int(load().vc_paged_attn_h2o_workspace_bytes(cache.ref, T, Hq))
+
+
+def vc_paged8_attn_workspace_bytes(cache: Paged8Cache, T: int, Hq: int) -> int:
+    _is8(cache, True)
+    return int(load().vc_paged8_attn_workspace_bytes(cache.ref, T, Hq))
+
+
+def vc_paged_attn_shared_workspace_bytes(cache: PagedCache, n_groups: int, T: int, Hq: int) -> int:
+    _is8(cache, False)
+    return int(load().vc_paged_attn_shared_workspace_bytes(cache.ref, n_groups, T, Hq))
+
+
+def vc_paged8_attn_shared_workspace_bytes(cache: Paged8Cache, n_groups: int, T: int, Hq: int) -> int:
+    _is8(cache, True)
+    return int(load().vc_paged8_attn_shared_workspace_bytes(cache.ref, n_groups, T, Hq))
 
 
 def _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores=None):
@@ -880,6 +982,7 @@ def _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores=None):
 def vc_paged_attn(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, ws: Workspace, stream=None):
     """Causal attention of the batch's chunks over the pages: q, out [T][Hq][d],
     q_start int32 [B + 1], ctx_len int32 [B]."""
+    _is8(cache, False)
     T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws)
     cache._on_gpu()
     _check(load().vc_paged_attn(q.data_ptr(), cache.ref, q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
@@ -887,10 +990,53 @@ def vc_paged_attn(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, 
            "vc_paged_attn")
 
 
+def vc_paged8_attn(q, cache: Paged8Cache, q_start, ctx_len, sm_scale: float, out, ws: Workspace, stream=None):
+    """vc_paged_attn over 8-bit pages: q, out [T][Hq][d] in cache.dtype."""
+    _is8(cache, True)
+    T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws)
+    cache._on_gpu()
+    _check(load().vc_paged8_attn(q.data_ptr(), cache.ref, q_start.data_ptr(), ctx_len.data_ptr(), T, Hq,
+                                 float(sm_scale), out.data_ptr(), ws.ptr, ws.nbytes, cache._stream(stream)),
+           "vc_paged8_attn")
+
+
+def _paged_attn_shared(name, q, cache, seq_start, prefix_len, q_start, ctx_len, sm_scale, out, ws, stream):
+    T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws)
+    cache._check(seq_start, prefix_len)
+    if seq_start.dtype != torch.int32 or prefix_len.dtype != torch.int32:
+        raise TypeError("seq_start and prefix_len are int32")
+    if prefix_len.dim() != 1 or seq_start.shape != (prefix_len.shape[0] + 1,):
+        raise ValueError("seq_start [n + 1] and prefix_len [n] expected")
+    cache._on_gpu()
+    groups = SharedPrefixC(seq_start.data_ptr(), prefix_len.data_ptr(), prefix_len.shape[0])
+    _check(getattr(load(), name)(q.data_ptr(), cache.ref, ctypes.byref(groups), q_start.data_ptr(), ctx_len.data_ptr(),
+                                 T, Hq, float(sm_scale), out.data_ptr(), ws.ptr, ws.nbytes, cache._stream(stream)),
+           name)
+
+
+def vc_paged_attn_shared(q, cache: PagedCache, seq_start, prefix_len, q_start, ctx_len, sm_scale: float, out,
+                         ws: Workspace, stream=None):
+    """vc_paged_attn where the sequences seq_start[g] .. seq_start[g + 1] - 1
+    (int32 [n + 1]) share their first prefix_len[g] (int32 [n]) tokens: one pass
+    over a prefix's whole pages for all of its group."""
+    _is8(cache, False)
+    _paged_attn_shared("vc_paged_attn_shared", q, cache, seq_start, prefix_len, q_start, ctx_len, sm_scale, out, ws,
+                       stream)
+
+
+def vc_paged8_attn_shared(q, cache: Paged8Cache, seq_start, prefix_len, q_start, ctx_len, sm_scale: float, out,
+                          ws: Workspace, stream=None):
+    """vc_paged_attn_shared over 8-bit pages."""
+    _is8(cache, True)
+    _paged_attn_shared("vc_paged8_attn_shared", q, cache, seq_start, prefix_len, q_start, ctx_len, sm_scale, out, ws,
+                       stream)
+
+
 def vc_paged_attn_h2o(q, cache: PagedCache, q_start, ctx_len, sm_scale: float, out, scores, ws: Workspace,
                       stream=None):
     """vc_paged_attn that adds every cached token's attention weight to scores
     fp32 [B][Hkv][S], S >= the cache's slots."""
+    _is8(cache, False)
     T, Hq = _paged_attn_args(q, cache, q_start, ctx_len, out, ws, scores)
     if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != cache._units:
         raise ValueError(f"scores is fp32 [{cache.B}][{cache.Hkv}][slots]")
@@ -905,6 +1051,7 @@ def vc_paged_evict(scores, src: PagedCache, src_len, keep_top: int, keep_recent:
     """The keep_recent newest and keep_top best-scored other tokens of every
     (sequence, kv head) of src, into dst's pages: scores fp32 [B][Hkv][S],
     kept_idx int32 [B][Hkv][n], scores_out fp32 [B][Hkv][n] or None."""
+    _is8(src, False), _is8(dst, False)
     src._check(scores, src_len, dst.k, dst_len, kept_idx, scores_out)
     units = src._units
     for t, dt in ((scores, torch.float32), (kept_idx, torch.int32), (scores_out, torch.float32)):
