@@ -35,7 +35,7 @@
 //
 // With KV8 the pages hold e4m3 codes and a power-of-two scale per row.  The
 // producer brings tiles of codes and their scales into a ring of their own;
-// four more warps (12-15) write them as bf16 tiles, scale included, into the
+// eight more warps (12-19) write them as bf16 tiles, scale included, into the
 // ring that the products read.  code * 2^e is a bf16 number, so this rounds
 // nothing: the output is that of bf16 pages which hold the same numbers.
 //
@@ -55,10 +55,11 @@ namespace {
 
 constexpr int BN = 128;
 constexpr int kRowsTile = 128;
-constexpr int kThreads = 352, kThreads8 = 512;
+constexpr int kThreads = 352, kThreads8 = 640;
 constexpr int kProducer = 8, kIssuer = 9, kProducer2 = 10, kConverter = 12;     // warps
-constexpr int kSoftmax = 256, kConverters = 128;
-constexpr int kMany = 184, kSome = 80, kFew = 64;              // registers of a thread, by warpgroup (KV8)
+constexpr int kSoftmax = 256, kConverters = 256;
+constexpr int kEnd = -1;
+constexpr int kMany = 168, kSome = 48, kFew = 48;              // registers of a thread, by warpgroup (KV8)
 constexpr float kLazy = 8.f;                                   // log2 domain
 
 template <int D, bool KV8>
@@ -82,6 +83,7 @@ template <typename S, bool KV8>
 struct Shared {
     uint64_t full[KV8 ? 6 : 10], empty[KV8 ? 6 : 10];
     uint64_t full8[KV8 ? 8 : 1], empty8[KV8 ? 8 : 1];
+    int live8[KV8 ? 8 : 1];      // rows of the tile of codes that hold tokens; none is to come: kEnd
     uint64_t q_ready, s_full[2], p_ready[2], o_full[2], meet;
     uint32_t tmem;
     Piece piece;
@@ -89,9 +91,7 @@ struct Shared {
         Walk<256, BN, S> walk;
         ItemOf<S> it;
         bool more;
-    } role[KV8 ? 14 : 11];   // each warp's walk through the piece: in registers it would make the softmax threads spill
-
-    static __device__ __forceinline__ int index(int warp) { return KV8 && warp >= kConverter ? warp - 2 : warp; }
+    } role[KV8 ? 10 : 11];   // each warp's walk through the piece: in registers it would make the softmax threads spill
 };
 
 struct Params {
@@ -114,7 +114,7 @@ struct Params {
 template <typename S, bool KV8>
 __device__ __forceinline__ bool step(Shared<S, KV8> *sh, int warp, const Params &A)
 {
-    auto &x = sh->role[sh->index(warp)];
+    auto &x = sh->role[warp];
     __syncwarp();
     if ((threadIdx.x & 31) == 0) x.more = x.walk.next(A.P, A.W, x.it);
     __syncwarp();
@@ -123,13 +123,14 @@ __device__ __forceinline__ bool step(Shared<S, KV8> *sh, int warp, const Params 
 
 // 16 e4m3 codes times 2^(e - 127) as bf16, exactly.  A code's seven value bits,
 // shifted to where bf16 has its exponent's low bits and its mantissa, are the
-// number times 2^-120, subnormal codes included.
+// number times 2^-120, subnormal codes included; the factor 2^(e - 7) sets that
+// right.  It leaves bf16's range where e > 134 (rows past 448 * 2^7), which TWO
+// takes in two steps.
+template <bool TWO>
 __device__ __forceinline__ void expand16(const uint4 &w, uint32_t e, uint4 (&o)[2])
 {
-    // the factor 2^(e - 7) leaves bf16's range for rows past 448 * 2^7: in two steps
-    const uint32_t e1 = min(e + 120u, 254u), e2 = e + 247u - e1;
+    const uint32_t e1 = TWO ? min(e + 120u, 254u) : e + 120u, e2 = e + 247u - e1;
     const uint32_t m1 = e1 << 7 | e1 << 23, m2 = e2 << 7 | e2 << 23;
-    const bool two = __any_sync(0xffffffffu, e2 != 127u);
     const uint32_t x[4] = {w.x, w.y, w.z, w.w};
     uint32_t y[8];
 #pragma unroll
@@ -147,7 +148,7 @@ __device__ __forceinline__ void expand16(const uint4 &w, uint32_t e, uint4 (&o)[
         }
     };
     times(m1);
-    if (two) times(m2);
+    if (TWO) times(m2);
     o[0] = make_uint4(y[0], y[1], y[2], y[3]);
     o[1] = make_uint4(y[4], y[5], y[6], y[7]);
 }
@@ -180,12 +181,12 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < NST; ++i) {
-            mbar_init(&S->full[i], KV8 ? kConverters : 1);
+            mbar_init(&S->full[i], KV8 ? kConverters / 32 : 1);
             mbar_init(&S->empty[i], 1);
         }
         for (int i = 0; i < G::STAGES8; ++i) {
             mbar_init(&S->full8[i], 1);
-            mbar_init(&S->empty8[i], kConverters);
+            mbar_init(&S->empty8[i], kConverters / 32);
         }
         mbar_init(&S->q_ready, kSoftmax);
         mbar_init(&S->meet, kSoftmax);
@@ -206,10 +207,9 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     tc::fence_after();
     pdl_trigger();
     const uint32_t tmem = S->tmem;
-    const bool idle = KV8 && warp > kIssuer && warp < kConverter;
-    if (lane == 0 && !idle) S->role[S->index(warp)].walk.start(A.P, A.W, S->piece);
-    // KV8: 128 registers a thread at launch; the warpgroups share them as
-    // 2 x 184 + 64 + 80 = 4 x 128.
+    if (lane == 0 && (!KV8 || warp <= kIssuer)) S->role[warp].walk.start(A.P, A.W, S->piece);
+    // KV8: 96 registers a thread at launch; the warpgroups share them as
+    // 2 x 168 + 3 x 48 = 5 x 96.
     if (warp >= kProducer && warp < kConverter) {
         if constexpr (KV8) fewer_registers<kFew>();          // the whole warpgroup
         if (KV8 && warp == kProducer) {
@@ -224,16 +224,23 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
             const bool on = lane < BN / A.box_rows;
             Ring<NST8> ring;
             bool ok = true, filled = false;
-            auto load = [&](const CUtensorMap *map, const uint8_t *scale, int row) {
+            auto load = [&](const CUtensorMap *map, const uint8_t *scale, int row, int live) {
                 const int s = ring.slot;
                 if (filled) {
                     ok = wait_warp(&S->empty8[s], ring.phase ^ 1, A.status, 104);
                     if (!ok) return;
                 }
+                if (live == kEnd) {
+                    if (lane == 0) S->live8[s] = kEnd, mbar_arrive(&S->full8[s]);
+                    return;
+                }
                 uint8_t *dst = sm + G::SM_8 + s * G::ITEM8;
                 const bool has = on && row < A.n_rows;
                 const unsigned all = __ballot_sync(0xffffffffu, has);
-                if (lane == 0) mbar_arrive_expect_tx(&S->full8[s], G::TILE8 + __popc(all) * A.box_rows);
+                if (lane == 0) {
+                    S->live8[s] = live;
+                    mbar_arrive_expect_tx(&S->full8[s], G::TILE8 + __popc(all) * A.box_rows);
+                }
                 __syncwarp();
                 if (on) tc::tma_load_3d(dst + lane * A.box_rows * D, map, 0, row, 0, &S->full8[s]);
                 if (has) bulk_g2s(dst + G::TILE8 + lane * A.box_rows, scale + row, A.box_rows, &S->full8[s]);
@@ -256,16 +263,18 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     set_flag(A.P.status, VC_PAGED_BAD_PAGE);
                     return A.n_rows;
                 };
+                auto live = [&](int i) { return min(len - (it.t_lo + i) * BN, BN); };
                 int e0 = entry(0), e1 = entry(1), e2 = entry(2);
-                load(&tmK, A.P.k_scale, row(0, e0));
-                if (ok && ahead == 2 && n > 1) load(&tmK, A.P.k_scale, row(1, e1));
+                load(&tmK, A.P.k_scale, row(0, e0), live(0));
+                if (ok && ahead == 2 && n > 1) load(&tmK, A.P.k_scale, row(1, e1), live(1));
                 for (int i = 0; i < n && ok; ++i) {
                     const int e3 = entry(i + 3);
-                    load(&tmV, A.P.v_scale, row(i, e0));
-                    if (ok && i + ahead < n) load(&tmK, A.P.k_scale, row(i + ahead, ahead == 1 ? e1 : e2));
+                    load(&tmV, A.P.v_scale, row(i, e0), live(i));
+                    if (ok && i + ahead < n) load(&tmK, A.P.k_scale, row(i + ahead, ahead == 1 ? e1 : e2), live(i + ahead));
                     e0 = e1, e1 = e2, e2 = e3;
                 }
             }
+            if (ok) load(nullptr, nullptr, 0, kEnd);
             if (!ok && lane == 0)                                // copies in flight end before the CTA does
                 for (int i = 0; i < NST8; ++i) {
                     if (filled || i < ring.slot) mbar_wait(&S->full8[i], i < ring.slot ? ring.phase : ring.phase ^ 1);
@@ -442,48 +451,53 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
     } else if (KV8 && warp >= kConverter) {
         // ------------------------------------------------------ converter --
         fewer_registers<kSome>();
-        const It &it = S->role[S->index(warp)].it;
-        constexpr int CH = D / 16;                           // 16-byte chunks of a row of codes
-        const int x0 = threadIdx.x - kConverter * 32, c = x0 % CH;
+        // A thread expands chunk c (16 codes) of every STEPth row.  Eight lanes
+        // take four chunks of one half of a row and, heads of 128, four of the other
+        // half of the row beside it: their reads and both their (swizzled) writes then
+        // fall on all banks.
+        constexpr int CH = D / 16, STEP = kConverters / CH, N = BN / STEP;
+        const int x0 = threadIdx.x - kConverter * 32, c = x0 % CH, half = c >> 2;
+        const int r0 = CH == 8 ? x0 / 16 * 2 + (half ^ (x0 >> 3 & 1)) : x0 / CH;
+        // (rows a multiple of 8 apart are swizzled alike)
+        const int at0 = (2 * (c & 3) ^ (r0 & 7)) << 4, at1 = ((2 * (c & 3) + 1) ^ (r0 & 7)) << 4;
         Ring<NST> ring;
         Ring<NST8> ring8;
         bool ok = true, filled = false;
-        // the next tile; rows from `live` on become zeros
-        auto convert = [&](int live) {
-            ok = wait_warp(&S->full8[ring8.slot], ring8.phase, A.status, 102) &&
-                 (!filled || wait_warp(&S->empty[ring.slot], ring.phase ^ 1, A.status, 103));
-            if (!ok) return;
-            const uint8_t *src = sm + G::SM_8 + ring8.slot * G::ITEM8;
-            uint8_t *dst = sm + G::SM_KV + ring.slot * G::TILE + (c >> 2) * (BN * 128);
-#pragma unroll 4
-            for (int i = 0; i < BN * CH / kConverters; ++i) {
-                const int x = x0 + i * kConverters, row = x / CH;
-                uint4 w = *reinterpret_cast<const uint4 *>(src + x * 16);
-                uint32_t e = src[G::TILE8 + row];
-                if (row >= live) w = make_uint4(0, 0, 0, 0), e = 127;
-                uint4 o[2];
-                expand16(w, e, o);
-                // the halves' chunks fall on the same banks: odd ones first in the second
-                const int j = 2 * (c & 3), odd = c >> 2;
-                *reinterpret_cast<uint4 *>(dst + row * 128 + (((j + odd) ^ (row & 7)) << 4)) = odd ? o[1] : o[0];
-                *reinterpret_cast<uint4 *>(dst + row * 128 + (((j + 1 - odd) ^ (row & 7)) << 4)) = odd ? o[0] : o[1];
-            }
+        for (;;) {
+            ok = wait_warp(&S->full8[ring8.slot], ring8.phase, A.status, 102);
+            const int live = S->live8[ring8.slot];           // rows from there on become zeros
+            if (!ok || live == kEnd) break;
+            ok = !filled || wait_warp(&S->empty[ring.slot], ring.phase ^ 1, A.status, 103);
+            if (!ok) break;
+            const uint8_t *item = sm + G::SM_8 + ring8.slot * G::ITEM8, *src = item + r0 * D + c * 16;
+            const uint8_t *scale = item + G::TILE8 + r0;
+            uint8_t *dst = sm + G::SM_KV + ring.slot * G::TILE + half * (BN * 128) + r0 * 128;
+            const int rows = (live - r0 + STEP - 1) / STEP;       // of this thread that are there
+            // the largest scale of the tile's 128, four to a lane
+            const uint32_t e4 = *reinterpret_cast<const uint32_t *>(item + G::TILE8 + 4 * lane);
+            const bool two = __any_sync(0xffffffffu, __vcmpgtu4(e4, 0x86868686u) != 0);      // 134
+            auto expand = [&](auto t) {
+#pragma unroll 2
+                for (int i = 0; i < N; ++i) {
+                    uint4 w = *reinterpret_cast<const uint4 *>(src + i * STEP * D), o[2];
+                    const uint32_t e = scale[i * STEP];
+                    if (i >= rows) w = make_uint4(0, 0, 0, 0);
+                    expand16<decltype(t)::value>(w, i < rows ? e : 127u, o);
+                    *reinterpret_cast<uint4 *>(dst + i * STEP * 128 + at0) = o[0];
+                    *reinterpret_cast<uint4 *>(dst + i * STEP * 128 + at1) = o[1];
+                }
+            };
+            if (two) expand(std::true_type{});
+            else expand(std::false_type{});
             fence_async_smem();
-            mbar_arrive(&S->full[ring.slot]);
-            mbar_arrive(&S->empty8[ring8.slot]);
+            __syncwarp();
+            if (lane == 0) {                                 // (256 arrivals a tile would take as long as the rest)
+                mbar_arrive(&S->full[ring.slot]);
+                mbar_arrive(&S->empty8[ring8.slot]);
+            }
             ring.next();
             ring8.next();
             filled = filled || ring.slot == 0;
-        };
-        while (ok && step(S, warp, A)) {
-            const int n = it.t_hi - it.t_lo, ahead = it.rows > kRowsTile ? 1 : 2;
-            auto live = [&](int i) { return it.len() - (it.t_lo + i) * BN; };
-            convert(live(0));
-            if (ok && ahead == 2 && n > 1) convert(live(1));
-            for (int i = 0; i < n && ok; ++i) {
-                convert(live(i));
-                if (ok && i + ahead < n) convert(live(i + ahead));
-            }
         }
     } else {
         // ------------------------------------------------------- softmax --
