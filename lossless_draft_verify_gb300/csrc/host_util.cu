@@ -75,7 +75,8 @@ bool tma_map_bf16_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-bool tma_map_u8_2d(CUtensorMap *m, const void *base, uint64_t d, uint64_t rows, uint32_t box_rows)
+bool tma_map_u8_2d(CUtensorMap *m, const void *base, uint64_t d, uint64_t rows, uint32_t box_rows,
+                   bool swizzle)
 {
     auto fn = tma_encoder();
     if (!fn) return false;
@@ -83,8 +84,10 @@ bool tma_map_u8_2d(CUtensorMap *m, const void *base, uint64_t d, uint64_t rows, 
     const cuuint64_t strides[2] = {d, d * rows};
     const cuuint32_t box[3] = {(cuuint32_t)d, box_rows, 1};
     const cuuint32_t estr[3] = {1, 1, 1};
+    const CUtensorMapSwizzle how = !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                   : d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base), dims, strides, box, estr,
-              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, how, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 

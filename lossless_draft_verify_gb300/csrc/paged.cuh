@@ -177,11 +177,18 @@ __host__ __device__ __forceinline__ S load_entry(const Pool &P, const WorkDim &W
 // longer and their units less: at 1, 2, 4 and 8 a token of 8 sequences over 4000
 // takes 163, 162, 169 and 175 us, four chunks of 300 over 2000 578, 582, 585 and
 // 590, four chunks up to 17 over 2000 at most 27, 27, 27 and 25.
-template <int BM>
+template <int BM, int BN = 0>
 struct Cost {
     static constexpr int kUnitCost = BM == 256 ? 16 : 1;
     static constexpr int kMinPiece = BM == 256 ? 10 : 2;
     static constexpr int kWhole = BM == 256 ? 20 : 3;
+};
+// A warp's piece of 16-key tiles (paged_attn8_few.cu).
+template <int BM>
+struct Cost<BM, 16> {
+    static constexpr int kUnitCost = 4;
+    static constexpr int kMinPiece = 12;
+    static constexpr int kWhole = 16;
 };
 
 // What one CTA has to do: from unit (b, h, mt), cost offset `off` within it,
@@ -198,8 +205,8 @@ __host__ __device__ inline long piece_len(long total, int n_cta, int min_len)
 }
 
 template <int BM, int BN>
-struct Units : Cost<BM> {
-    using Cost<BM>::kUnitCost;
+struct Units : Cost<BM, BN> {
+    using Cost<BM, BN>::kUnitCost;
     // 32-bit arithmetic: a sequence has at most 2^30 rows
     template <typename S>
     static __host__ __device__ __forceinline__ int tiles(const S &s, int G, int mt)
@@ -481,6 +488,14 @@ cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int H
 // A planned batch's attention (W.plan): out is fp32 and lse given
 cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, float *out,
                             float *lse, const Parts &parts, int32_t *status, cudaStream_t st);
+// paged_attn8_few.cu: over 8-bit pages, for batches of few rows: pieces per warp,
+// row tiles of few_rows() (0: none, the batch has too many)
+constexpr int kFewKeys = 16, kFewWarps = 12;
+int few_pieces();
+inline int few_rows(int T, int G, int B) { return (long)T * G <= 8l * B ? 8 : (long)T * G <= 16l * B ? 16 : 0; }
+cudaError_t attn8_few(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2, void *out,
+                      const Parts &parts, int32_t *status, cudaStream_t st);
+
 // paged_attn8_tc.cu: both over 8-bit pages
 cudaError_t attn8_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                      const Parts &parts, int32_t *status, cudaStream_t st);
@@ -505,7 +520,7 @@ cudaError_t join_shared(const Pool &P, vc_dtype dt, int d, const int32_t *q_star
 
 // paged_attn.cu: attention, with scores != null also the attention mass; shared:
 // that of groups (scores null, n_groups those of its workspace)
-size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass);
+size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass, bool kv8);
 size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups);
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
                  int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st);

@@ -119,11 +119,16 @@ struct WsLayout {
 // the bound 5.39 ms, just past it 7.34 ms.
 constexpr size_t kStoredMost = size_t(1) << 30;
 
-WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool with_rows, bool planned = false)
+// A batch over 8-bit pages whose rows are few takes a kernel of its own.  Row
+// tiles of 8, 16 (few_rows), else 256.
+bool is_few(vc_dtype dt, int T, int G, int B, bool kv8) { return kv8 && dt == VC_BF16 && few_rows(T, G, B); }
+
+WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool with_rows, bool kv8, bool planned = false)
 {
     WsLayout w;
-    w.n_cta = dt == VC_BF16 ? tc_ctas() : simt_ctas();
-    const long unit = dt == VC_BF16 ? kTcRows : simt_rows(T, G, B, planned);
+    const bool few = !planned && is_few(dt, T, G, B, kv8);
+    w.n_cta = few ? few_pieces() : dt == VC_BF16 ? tc_ctas() : simt_ctas();
+    const long unit = few ? few_rows(T, G, B) : dt == VC_BF16 ? kTcRows : simt_rows(T, G, B, planned);
     w.rows_cap = (int)std::min<long>(unit, (long)T * G);
     const size_t n = (size_t)w.n_cta * 2 * w.rows_cap;
     w.desc = kStatusBytes;
@@ -150,8 +155,10 @@ cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq,
 // whether a unit can be cut: not where the block table cannot hold a sequence
 // long enough
 template <typename T>
-bool may_cut(long cap)
+bool may_cut(long cap, bool few = false)
 {
+    using F = Cost<8, kFewKeys>;
+    if (few) return (cap + kFewKeys - 1) / kFewKeys + F::kUnitCost > F::kWhole;
     constexpr int tile = std::is_same_v<T, float> ? kSimtKeys : kTcKeys, weight = std::is_same_v<T, float> ? 1 : 2;
     using C = Cost<std::is_same_v<T, float> ? 64 : kTcRows>;
     return (cap + tile - 1) / tile * weight + C::kUnitCost > C::kWhole;
@@ -162,15 +169,17 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
                 float *scores, int scores_stride, uint8_t *ws, cudaStream_t st)
 {
     const long cap = P.capacity();
-    const WsLayout w = layout(dt, d, W.T, W.G, Hq, P.B, cap, scores != nullptr);
+    const WsLayout w = layout(dt, d, W.T, W.G, Hq, P.B, cap, scores != nullptr, P.k_scale);
     Parts parts = {(PartDesc *)(ws + w.desc), (float2 *)(ws + w.ml), (float *)(ws + w.o), w.rows_cap};
     float *lse = scores ? (float *)(ws + w.rows) : nullptr;
     float *stored = w.s_stride ? (float *)(ws + w.stored) : nullptr;
     cudaError_t e;
+    const bool few = is_few(dt, W.T, W.G, P.B, P.k_scale);
     if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
+    else if (few) e = attn8_few(P, W, d, few_rows(W.T, W.G, P.B), q, Hq, sl2, out, parts, (int32_t *)ws, st);
     else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, lse, parts, (int32_t *)ws, st);
     else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, stored, w.s_stride, parts, (int32_t *)ws, st);
-    if (e == cudaSuccess && may_cut<T>(cap))
+    if (e == cudaSuccess && may_cut<T>(cap, few))
         e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
     if (e != cudaSuccess || !scores) return e;
     if constexpr (std::is_same_v<T, float>) {
@@ -192,7 +201,7 @@ struct SharedLayout {
 SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, int n_groups)
 {
     SharedLayout w;
-    w.attn = layout(dt, d, T, G, Hq, B, cap, false, true);
+    w.attn = layout(dt, d, T, G, Hq, B, cap, false, false, true);
     w.plan = w.attn.bytes;
     w.lse = w.plan + align256(((size_t)B + n_groups) * sizeof(VSeq));
     w.o = w.lse + align256((size_t)2 * T * Hq * sizeof(float));
@@ -225,9 +234,9 @@ cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void 
 
 }  // namespace
 
-size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass)
+size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass, bool kv8)
 {
-    return layout(dt, d, T, Hq / Hkv, Hq, B, cap, mass).bytes;
+    return layout(dt, d, T, Hq / Hkv, Hq, B, cap, mass, kv8).bytes;
 }
 
 size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups)

@@ -474,10 +474,10 @@ paged::Pool paged8_pool(const vc_paged8_cache *c)
     return P;
 }
 
-size_t paged_attn_ws(const vc_paged_cache *c, int T, int Hq, bool mass)
+size_t paged_attn_ws(const vc_paged_cache *c, int T, int Hq, bool mass, bool kv8 = false)
 {
     if (!paged_ok(c) || !paged_supported(c) || !paged_heads_ok(c, T, Hq) || !paged_rows_ok(c, T, Hq)) return 0;
-    return paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page, mass);
+    return paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page, mass, kv8);
 }
 
 bool shared_ok(const vc_shared_prefix *s)
@@ -510,7 +510,7 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const paged::P
     if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
     const long cap = (long)c->max_blocks * c->page;
     if (ws_bytes < (shared ? paged::attn_shared_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, shared->n)
-                           : paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, scores != nullptr)))
+                           : paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, scores != nullptr, P.k_scale)))
         return VC_ERR_INVALID;
     if (T == 0) return VC_OK;
     if (shared)
@@ -620,7 +620,7 @@ size_t vc_paged8_attn_workspace_bytes(const vc_paged8_cache *cache, int T, int H
 {
     if (!paged8_ok(cache)) return 0;
     const vc_paged_cache c = paged8_base(cache);
-    return paged_attn_ws(&c, T, Hq, false);
+    return paged_attn_ws(&c, T, Hq, false, true);
 }
 
 vc_status vc_paged8_attn(const void *q, const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len,

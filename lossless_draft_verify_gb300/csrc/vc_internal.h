@@ -104,7 +104,8 @@ int device_sm_count();
 bool tma_map_bf16_3d(CUtensorMap *m, const void *base, uint64_t d0, uint64_t d1, uint64_t d2,
                      uint64_t stride1_bytes, uint64_t stride2_bytes, uint32_t b0, uint32_t b1, uint32_t b2);
 // Tensor map of `rows` dense rows of d bytes (a third dimension of one), boxes
-// of box_rows whole rows, not swizzled, zero fill out of bounds.
-bool tma_map_u8_2d(CUtensorMap *m, const void *base, uint64_t d, uint64_t rows, uint32_t box_rows);
+// of box_rows whole rows, swizzled by the row's d bytes (128 or 64) or not, zero
+// fill out of bounds.
+bool tma_map_u8_2d(CUtensorMap *m, const void *base, uint64_t d, uint64_t rows, uint32_t box_rows, bool swizzle = false);
 
 }  // namespace vc
