@@ -177,18 +177,21 @@ __host__ __device__ __forceinline__ S load_entry(const Pool &P, const WorkDim &W
 // longer and their units less: at 1, 2, 4 and 8 a token of 8 sequences over 4000
 // takes 163, 162, 169 and 175 us, four chunks of 300 over 2000 578, 582, 585 and
 // 590, four chunks up to 17 over 2000 at most 27, 27, 27 and 25.
-template <int BM, int BN = 0>
+template <int BM>
 struct Cost {
     static constexpr int kUnitCost = BM == 256 ? 16 : 1;
     static constexpr int kMinPiece = BM == 256 ? 10 : 2;
     static constexpr int kWhole = BM == 256 ? 20 : 3;
 };
-// A warp's piece of 16-key tiles (paged_attn8_few.cu).
-template <int BM>
-struct Cost<BM, 16> {
-    static constexpr int kUnitCost = 4;
-    static constexpr int kMinPiece = 12;
-    static constexpr int kWhole = 16;
+// Pieces of one warp each, in tiles of few_keys() (paged_attn8_few.cu).  A lone warp
+// takes about 1 us for a tile, so small batches are cut finely: unit cost, least piece
+// and whole units of 3, 8, 12 and of 2, 2, 4, one token of one sequence over 1000 (32/8
+// heads of 128) 23.9 and 12.4 us, of 16 over 500 21.5 and 14.7, of 16 over 32768 179 and
+// 177.5; only 128 sequences of 150 tokens take longer, 17.1 and 25.4.
+struct CostFew {
+    static constexpr int kUnitCost = 2;
+    static constexpr int kMinPiece = 2;
+    static constexpr int kWhole = 4;
 };
 
 // What one CTA has to do: from unit (b, h, mt), cost offset `off` within it,
@@ -204,9 +207,9 @@ __host__ __device__ inline long piece_len(long total, int n_cta, int min_len)
     return lmax((total + n_cta - 1) / n_cta, min_len);
 }
 
-template <int BM, int BN>
-struct Units : Cost<BM, BN> {
-    using Cost<BM, BN>::kUnitCost;
+template <int BM, int BN, typename C = Cost<BM>>
+struct Units : C {
+    using C::kUnitCost;
     // 32-bit arithmetic: a sequence has at most 2^30 rows
     template <typename S>
     static __host__ __device__ __forceinline__ int tiles(const S &s, int G, int mt)
@@ -259,10 +262,10 @@ struct Units : Cost<BM, BN> {
 // which finds the sequence that holds the piece's beginning, can go straight to
 // its chunk.  One loop serves both: code that runs once is paid for in
 // instruction fetches.
-template <int BM, int BN, typename S = Seq>
+template <int BM, int BN, typename S = Seq, typename C = Cost<BM>>
 __device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int cta, int n_cta, Piece *out)
 {
-    using U = Units<BM, BN>;
+    using U = Units<BM, BN, C>;
     using Src = Source<S>;
     const int lane = threadIdx.x & 31, count = Src::count(P, W), chunks = (count + 31) / 32;
     auto fetch = [&](int c) {
@@ -346,9 +349,9 @@ struct ItemOf<VSeq> : ItemOf<Seq> {
 using Item = ItemOf<Seq>;
 
 // Walks a piece; every role of a CTA walks it alike.
-template <int BM, int BN, typename S = Seq>
+template <int BM, int BN, typename S = Seq, typename C = Cost<BM>>
 struct Walk {
-    using U = Units<BM, BN>;
+    using U = Units<BM, BN, C>;
     int b, h, mt;          // b: the entry
     long off, left, per;
     S s;
@@ -489,9 +492,9 @@ cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int H
 cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, float *out,
                             float *lse, const Parts &parts, int32_t *status, cudaStream_t st);
 // paged_attn8_few.cu: over 8-bit pages, for batches of few rows: pieces per warp,
-// row tiles of few_rows() (0: none, the batch has too many)
-constexpr int kFewKeys = 16, kFewWarps = 12;
-int few_pieces();
+// row tiles of few_rows() (0: the batch has too many)
+constexpr int few_keys(int d) { return d == 128 ? 32 : 64; }      // of a tile: 4 KB of codes
+int few_pieces(int rows);
 inline int few_rows(int T, int G, int B) { return (long)T * G <= 8l * B ? 8 : (long)T * G <= 16l * B ? 16 : 0; }
 cudaError_t attn8_few(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2, void *out,
                       const Parts &parts, int32_t *status, cudaStream_t st);

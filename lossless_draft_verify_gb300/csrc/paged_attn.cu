@@ -57,6 +57,125 @@ merge_kernel(Parts parts, int G, int Hq, T *__restrict__ out, float *__restrict_
     }
 }
 
+// The same where pieces are many and small (a warp's each).  A CTA looks at the
+// descriptions of sixteen pieces.  Units of few parts: a warp per row.  Others: the
+// warps share the rows and, where those are fewer, their parts.  What it takes are
+// round trips to L2, so a warp asks for eight parts at once and rescales its running
+// sum by their maximum.  Of a decode step (16 sequences of 32768 tokens, 32/8 heads)
+// with a warp per row 180 us in all, with shared parts 173.
+constexpr int kManyWarps = 16, kFewParts = 4, kAtOnce = 8;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(32 * kManyWarps)
+merge_many_kernel(Parts parts, int n_piece, int G, int Hq, T *__restrict__ out)
+{
+    constexpr int V = D / 32;
+    __shared__ PartDesc s_desc[kManyWarps];
+    __shared__ float s_acc[kManyWarps][D];
+    __shared__ float2 s_ml[kManyWarps];
+    pdl_wait();
+    pdl_trigger();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c0 = blockIdx.x * kManyWarps;
+    if (lane == 0) {
+        if (c0 + warp < n_piece) s_desc[warp] = parts.desc[c0 + warp];
+        else s_desc[warp].parts = 0;
+    }
+    __syncthreads();
+    float acc[V], M, L;
+    auto join = [&](float m, float l, const float (&x)[V]) {
+        const float top = fmaxf(M, m), a = ex2(M - top), b = ex2(m - top);
+        M = top;
+        L = fmaf(b, l, L * a);
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = fmaf(b, x[e], acc[e] * a);
+    };
+    // parts p0, p0 + step .. of row r of the unit that begins in piece c0 + i
+    auto add = [&](int i, int n, int r, int p0, int step) {
+        M = kLowest, L = 0.f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        for (int p = p0; p < n; p += kAtOnce * step) {
+            float2 ml[kAtOnce];
+            float x[kAtOnce][V];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const int pk = p + k * step;
+                ml[k] = make_float2(kLowest, 0.f);
+#pragma unroll
+                for (int e = 0; e < V; ++e) x[k][e] = 0.f;
+                if (pk >= n) continue;
+                const size_t at = parts.row(c0 + i + pk, pk == 0 ? 1 : 0, r);
+                ml[k] = parts.ml[at];
+                const float *o = parts.o + at * D + V * lane;
+                if constexpr (V == 4) {
+                    const float4 y = *reinterpret_cast<const float4 *>(o);
+                    x[k][0] = y.x, x[k][1] = y.y, x[k][2] = y.z, x[k][3] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2 *>(o);
+                    x[k][0] = y.x, x[k][1] = y.y;
+                }
+            }
+            float top = M;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+            const float a = ex2(M - top);
+            M = top;
+            L *= a;
+#pragma unroll
+            for (int e = 0; e < V; ++e) acc[e] *= a;
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float w = ex2(ml[k].x - top);
+                L = fmaf(w, ml[k].y, L);
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] = fmaf(w, x[k][e], acc[e]);
+            }
+        }
+    };
+    auto store = [&](const PartDesc &d, int r) {
+        const int R = d.row0 + r;
+        const float inv = 1.f / L;
+        T *o = out + ((size_t)(d.tok0 + R / G) * Hq + d.h * G + R % G) * D + V * lane;
+#pragma unroll
+        for (int e = 0; e < V; ++e) o[e] = Elem<T>::from_f(acc[e] * inv);
+    };
+    int turn = 0;
+    for (int i = 0; i < kManyWarps; ++i) {
+        const PartDesc d = s_desc[i];
+        if (d.parts == 0 || d.parts > kFewParts) continue;
+        for (int r = 0; r < d.rows; ++r) {
+            if (turn++ % kManyWarps != warp) continue;
+            add(i, d.parts, r, 0, 1);
+            store(d, r);
+        }
+    }
+    for (int i = 0; i < kManyWarps; ++i) {
+        const PartDesc d = s_desc[i];
+        if (d.parts <= kFewParts) continue;
+        int share = kManyWarps;                              // warps per row
+        while (share > 1 && d.rows * share > kManyWarps) share /= 2;
+        const int sub = warp % share;
+        for (int r0 = 0; r0 < d.rows; r0 += kManyWarps / share) {
+            const int r = r0 + warp / share;
+            add(i, r < d.rows ? d.parts : 0, r, sub, share);
+#pragma unroll
+            for (int e = 0; e < V; ++e) s_acc[warp][V * lane + e] = acc[e];
+            if (lane == 0) s_ml[warp] = make_float2(M, L);
+            __syncthreads();
+            if (sub == 0 && r < d.rows) {
+                for (int k = 1; k < share; ++k) {
+                    float x[V];
+#pragma unroll
+                    for (int e = 0; e < V; ++e) x[e] = s_acc[warp + k][V * lane + e];
+                    join(s_ml[warp + k].x, s_ml[warp + k].y, x);
+                }
+                store(d, r);
+            }
+            __syncthreads();
+        }
+    }
+}
+
 // scores[b][h][j] += sum over the sequence's rows that see slot j of 2^(s - lse),
 // from stored products: four slots per thread, the rows one after another.  A
 // score is rounded before lse is subtracted, as for the row's maximum, so that no
@@ -127,7 +246,7 @@ WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool 
 {
     WsLayout w;
     const bool few = !planned && is_few(dt, T, G, B, kv8);
-    w.n_cta = few ? few_pieces() : dt == VC_BF16 ? tc_ctas() : simt_ctas();
+    w.n_cta = few ? few_pieces(few_rows(T, G, B)) : dt == VC_BF16 ? tc_ctas() : simt_ctas();
     const long unit = few ? few_rows(T, G, B) : dt == VC_BF16 ? kTcRows : simt_rows(T, G, B, planned);
     w.rows_cap = (int)std::min<long>(unit, (long)T * G);
     const size_t n = (size_t)w.n_cta * 2 * w.rows_cap;
@@ -152,13 +271,20 @@ cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq,
                     : launch_pdl(merge_kernel<T, 64>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, lse);
 }
 
+cudaError_t merge_many(const Parts &parts, int n_piece, int d, int G, int Hq, void *out, cudaStream_t st)
+{
+    using E = __nv_bfloat16;
+    const dim3 grid(cdiv(n_piece, kManyWarps)), block(32 * kManyWarps);
+    return d == 128 ? launch_pdl(merge_many_kernel<E, 128>, grid, block, 0, st, parts, n_piece, G, Hq, (E *)out)
+                    : launch_pdl(merge_many_kernel<E, 64>, grid, block, 0, st, parts, n_piece, G, Hq, (E *)out);
+}
+
 // whether a unit can be cut: not where the block table cannot hold a sequence
 // long enough
 template <typename T>
-bool may_cut(long cap, bool few = false)
+bool may_cut(long cap, int d, bool few = false)
 {
-    using F = Cost<8, kFewKeys>;
-    if (few) return (cap + kFewKeys - 1) / kFewKeys + F::kUnitCost > F::kWhole;
+    if (few) return (cap + few_keys(d) - 1) / few_keys(d) + CostFew::kUnitCost > CostFew::kWhole;
     constexpr int tile = std::is_same_v<T, float> ? kSimtKeys : kTcKeys, weight = std::is_same_v<T, float> ? 1 : 2;
     using C = Cost<std::is_same_v<T, float> ? 64 : kTcRows>;
     return (cap + tile - 1) / tile * weight + C::kUnitCost > C::kWhole;
@@ -179,8 +305,9 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     else if (few) e = attn8_few(P, W, d, few_rows(W.T, W.G, P.B), q, Hq, sl2, out, parts, (int32_t *)ws, st);
     else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, lse, parts, (int32_t *)ws, st);
     else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, stored, w.s_stride, parts, (int32_t *)ws, st);
-    if (e == cudaSuccess && may_cut<T>(cap, few))
-        e = merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
+    if (e == cudaSuccess && may_cut<T>(cap, d, few))
+        e = few ? merge_many(parts, w.n_cta, d, W.G, Hq, out, st)
+                : merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
     if (e != cudaSuccess || !scores) return e;
     if constexpr (std::is_same_v<T, float>) {
         return mass_simt(P, W, d, q, Hq, sl2, lse, scores, scores_stride, st);
@@ -226,7 +353,7 @@ cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void 
     if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, o, lse, parts, st);
     else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, o, lse, parts, (int32_t *)ws, st);
     else e = attn_tc_planned(P, W, d, q, Hq, sl2, o, lse, parts, (int32_t *)ws, st);
-    if (e == cudaSuccess && may_cut<T>(cap))
+    if (e == cudaSuccess && may_cut<T>(cap, d))
         e = merge<float>(parts, w.attn.n_cta, w.attn.rows_cap, d, W.G, Hq, o, lse, st);
     if (e != cudaSuccess) return e;
     return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, o, lse, out, st);
