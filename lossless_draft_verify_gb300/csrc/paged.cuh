@@ -183,7 +183,7 @@ struct Cost {
     static constexpr int kMinPiece = BM == 256 ? 10 : 2;
     static constexpr int kWhole = BM == 256 ? 20 : 3;
 };
-// Pieces of one warp each, in tiles of few_keys() (paged_attn8_few.cu).  A lone warp
+// Pieces of one warp each, in tiles of few_keys() (paged_attn_few.cuh).  A lone warp
 // takes about 1 us for a tile, so small batches are cut finely: unit cost, least piece
 // and whole units of 3, 8, 12 and of 2, 2, 4, one token of one sequence over 1000 (32/8
 // heads of 128) 23.9 and 12.4 us, of 16 over 500 21.5 and 14.7, of 16 over 32768 179 and
@@ -432,6 +432,27 @@ struct Parts {
     }
 };
 
+// Where a row of a planned batch's halves is: in the output (parts 0), or in parts as
+// PartDesc has them, row r of each.  Written with the row's first part.
+struct Place {
+    uint32_t cta_parts, r;     // cta | parts << 16
+
+    static __host__ __device__ __forceinline__ Place in_output() { return Place{0, 0}; }
+    static __host__ __device__ __forceinline__ Place in_parts(int cta, int parts, int r)
+    {
+        return Place{(uint32_t)cta | (uint32_t)parts << 16, (uint32_t)r};
+    }
+    __host__ __device__ __forceinline__ int cta() const { return (int)(cta_parts & 0xffffu); }
+    __host__ __device__ __forceinline__ int parts() const { return (int)(cta_parts >> 16); }
+};
+// What a planned batch's attention leaves: o (normalised) and lse of the rows that
+// are not in parts, and every row's place.
+struct Halves {
+    float *o;                  // [2][T][Hq][d], the prefix's half first
+    float *lse;                // [2][T][Hq]
+    Place *place;              // [2][T][Hq]
+};
+
 // ----- pieces of the tensor-core kernels ----------------------------------------------
 __device__ __forceinline__ float ex2(float x)
 {
@@ -477,7 +498,7 @@ constexpr int kSimtKeys = 32;      // the smallest key tile of its variants
 int simt_rows(int T, int G, int B, bool planned);
 int simt_ctas();
 cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
-                      const Parts &parts, cudaStream_t st);
+                      const Parts &parts, cudaStream_t st, Place *place = nullptr);
 cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float *lse,
                       float *scores, int scores_stride, cudaStream_t st);
 
@@ -488,20 +509,27 @@ int tc_ctas();
 // of 128, at least the table's slots)
 cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
                     float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st);
-// A planned batch's attention (W.plan): out is fp32 and lse given
-cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, float *out,
-                            float *lse, const Parts &parts, int32_t *status, cudaStream_t st);
-// paged_attn8_few.cu: over 8-bit pages, for batches of few rows: pieces per warp,
-// row tiles of few_rows() (0: the batch has too many)
-constexpr int few_keys(int d) { return d == 128 ? 32 : 64; }      // of a tile: 4 KB of codes
+// A planned batch's attention (W.plan)
+cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const Halves &H,
+                            const Parts &parts, int32_t *status, cudaStream_t st);
+// paged_attn_few.cuh: for batches of few rows: pieces per warp, row tiles of few_rows()
+// (0: the batch has too many).  Over 8-bit pages, and planned batches over bf16 ones:
+// begun beside the kernel launched before, which is not waited for
+constexpr int few_keys(int d, bool kv8) { return 4096 / (kv8 ? d : 2 * d); }      // of a tile: 4 KB
 int few_pieces(int rows);
 inline int few_rows(int T, int G, int B) { return (long)T * G <= 8l * B ? 8 : (long)T * G <= 16l * B ? 16 : 0; }
 cudaError_t attn8_few(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2, void *out,
                       const Parts &parts, int32_t *status, cudaStream_t st);
+cudaError_t attn8_few_planned(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2,
+                              const Halves &H, const Parts &parts, int32_t *status, cudaStream_t st);
+cudaError_t attn_few_planned(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2,
+                             const Halves &H, const Parts &parts, int32_t *status, cudaStream_t st);
 
 // paged_attn8_tc.cu: both over 8-bit pages
-cudaError_t attn8_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
+cudaError_t attn8_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out,
                      const Parts &parts, int32_t *status, cudaStream_t st);
+cudaError_t attn8_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const Halves &H,
+                             const Parts &parts, int32_t *status, cudaStream_t st);
 
 // paged_mass_tc.cu: scores += the attention weight of every slot, lse (log2
 // domain) of every row given
@@ -516,10 +544,10 @@ struct Groups {
 };
 cudaError_t plan_shared(const Pool &P, const int32_t *q_start, const int32_t *ctx_len, int T, const Groups &G,
                         VSeq *plan, cudaStream_t st);
-// out from the halves of every row: o [2][T][Hq][d] and lse [2][T][Hq], the prefix's
-// first; seqs: the plan's entries of the sequences
+// out from the halves of every row; seqs: the plan's entries of the sequences; pre,
+// own: the parts of the prefixes' half and of the other
 cudaError_t join_shared(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, int T, int Hq, const VSeq *seqs,
-                        const float *o, const float *lse, void *out, cudaStream_t st);
+                        const Halves &H, const Parts &pre, const Parts &own, void *out, cudaStream_t st);
 
 // paged_attn.cu: attention, with scores != null also the attention mass; shared:
 // that of groups (scores null, n_groups those of its workspace)

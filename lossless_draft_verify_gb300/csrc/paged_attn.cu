@@ -135,7 +135,8 @@ merge_many_kernel(Parts parts, int n_piece, int G, int Hq, T *__restrict__ out)
     auto store = [&](const PartDesc &d, int r) {
         const int R = d.row0 + r;
         const float inv = 1.f / L;
-        T *o = out + ((size_t)(d.tok0 + R / G) * Hq + d.h * G + R % G) * D + V * lane;
+        const size_t row = (size_t)(d.tok0 + R / G) * Hq + d.h * G + R % G;
+        T *o = out + row * D + V * lane;
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = Elem<T>::from_f(acc[e] * inv);
     };
@@ -281,10 +282,14 @@ cudaError_t merge_many(const Parts &parts, int n_piece, int d, int G, int Hq, vo
 
 // whether a unit can be cut: not where the block table cannot hold a sequence
 // long enough
-template <typename T>
-bool may_cut(long cap, int d, bool few = false)
+bool may_cut_few(long cap, int d, bool kv8)
 {
-    if (few) return (cap + few_keys(d) - 1) / few_keys(d) + CostFew::kUnitCost > CostFew::kWhole;
+    return (cap + few_keys(d, kv8) - 1) / few_keys(d, kv8) + CostFew::kUnitCost > CostFew::kWhole;
+}
+
+template <typename T>
+bool may_cut(long cap)
+{
     constexpr int tile = std::is_same_v<T, float> ? kSimtKeys : kTcKeys, weight = std::is_same_v<T, float> ? 1 : 2;
     using C = Cost<std::is_same_v<T, float> ? 64 : kTcRows>;
     return (cap + tile - 1) / tile * weight + C::kUnitCost > C::kWhole;
@@ -303,9 +308,9 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     const bool few = is_few(dt, W.T, W.G, P.B, P.k_scale);
     if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
     else if (few) e = attn8_few(P, W, d, few_rows(W.T, W.G, P.B), q, Hq, sl2, out, parts, (int32_t *)ws, st);
-    else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, lse, parts, (int32_t *)ws, st);
+    else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, parts, (int32_t *)ws, st);
     else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, stored, w.s_stride, parts, (int32_t *)ws, st);
-    if (e == cudaSuccess && may_cut<T>(cap, d, few))
+    if (e == cudaSuccess && (few ? may_cut_few(cap, d, true) : may_cut<T>(cap)))
         e = few ? merge_many(parts, w.n_cta, d, W.G, Hq, out, st)
                 : merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
     if (e != cudaSuccess || !scores) return e;
@@ -319,20 +324,28 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     }
 }
 
-// [the attention's | plan | lse of both halves | o of both halves]
+// [the attention's | that of the sequences' own slots, where the rows are few | plan |
+// places, lse and o of both halves]
 struct SharedLayout {
-    WsLayout attn;
-    size_t plan, lse, o, bytes;
+    WsLayout attn, own;
+    int few;                   // rows of a unit of the sequences' own slots; 0: all goes one way
+    size_t own_at, plan, place, lse, o, bytes;
 };
 
 SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, int n_groups)
 {
     SharedLayout w;
+    const size_t rows = (size_t)2 * T * Hq;
     w.attn = layout(dt, d, T, G, Hq, B, cap, false, false, true);
-    w.plan = w.attn.bytes;
-    w.lse = w.plan + align256(((size_t)B + n_groups) * sizeof(VSeq));
-    w.o = w.lse + align256((size_t)2 * T * Hq * sizeof(float));
-    w.bytes = w.o + (size_t)2 * T * Hq * d * sizeof(float);
+    w.few = dt == VC_BF16 ? few_rows(T, G, B) : 0;
+    w.own_at = w.attn.bytes;
+    w.own.bytes = 0;
+    if (w.few) w.own = layout(dt, d, T, G, Hq, B, cap, false, true);
+    w.plan = w.own_at + w.own.bytes;
+    w.place = w.plan + align256(((size_t)B + n_groups) * sizeof(VSeq));
+    w.lse = w.place + align256(rows * sizeof(Place));
+    w.o = w.lse + align256(rows * sizeof(float));
+    w.bytes = w.o + rows * d * sizeof(float);
     return w;
 }
 
@@ -340,23 +353,30 @@ template <typename T>
 cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void *q, int Hq, float sl2, const Groups &G,
                        void *out, uint8_t *ws, cudaStream_t st)
 {
-    const long cap = P.capacity();
-    const SharedLayout w = shared_layout(dt, d, W.T, W.G, Hq, P.B, cap, G.n);
-    const Parts parts = {(PartDesc *)(ws + w.attn.desc), (float2 *)(ws + w.attn.ml), (float *)(ws + w.attn.o),
-                         w.attn.rows_cap};
+    const SharedLayout w = shared_layout(dt, d, W.T, W.G, Hq, P.B, P.capacity(), G.n);
+    auto parts_at = [&](const WsLayout &x, uint8_t *at) {
+        return Parts{(PartDesc *)(at + x.desc), (float2 *)(at + x.ml), (float *)(at + x.o), x.rows_cap};
+    };
+    const Parts parts = parts_at(w.attn, ws), own = w.few ? parts_at(w.own, ws + w.own_at) : parts;
+    const Halves H = {(float *)(ws + w.o), (float *)(ws + w.lse), (Place *)(ws + w.place)};
     VSeq *plan = (VSeq *)(ws + w.plan);
-    float *lse = (float *)(ws + w.lse), *o = (float *)(ws + w.o);
-    W.plan = plan;
-    W.n_plan = P.B + G.n;
+    int32_t *status = (int32_t *)ws;
     cudaError_t e = plan_shared(P, W.q_start, W.ctx_len, W.T, G, plan, st);
     if (e != cudaSuccess) return e;
-    if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, o, lse, parts, st);
-    else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, o, lse, parts, (int32_t *)ws, st);
-    else e = attn_tc_planned(P, W, d, q, Hq, sl2, o, lse, parts, (int32_t *)ws, st);
-    if (e == cudaSuccess && may_cut<T>(cap, d))
-        e = merge<float>(parts, w.attn.n_cta, w.attn.rows_cap, d, W.G, Hq, o, lse, st);
+    W.plan = plan;
+    W.n_plan = w.few ? G.n : P.B + G.n;
+    if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, H.o, H.lse, parts, st, H.place);
+    else if (P.k_scale) e = attn8_tc_planned(P, W, d, q, Hq, sl2, H, parts, status, st);
+    else e = attn_tc_planned(P, W, d, q, Hq, sl2, H, parts, status, st);
+    if (e == cudaSuccess && w.few) {
+        // The kernel before took the prefixes; the sequences' own slots follow beside its end.
+        W.plan = plan + G.n;
+        W.n_plan = P.B;
+        e = P.k_scale ? attn8_few_planned(P, W, d, w.few, q, Hq, sl2, H, own, status, st)
+                      : attn_few_planned(P, W, d, w.few, q, Hq, sl2, H, own, status, st);
+    }
     if (e != cudaSuccess) return e;
-    return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, o, lse, out, st);
+    return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, H, parts, own, out, st);
 }
 
 }  // namespace

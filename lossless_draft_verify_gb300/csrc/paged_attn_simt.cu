@@ -69,7 +69,7 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 template <int D, int BM, int BN, typename SEQ, bool KV8>
 __global__ void __launch_bounds__(kThreads)
 attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float scale_log2, float *__restrict__ out,
-                 float *__restrict__ lse_out, Parts parts)
+                 float *__restrict__ lse_out, Parts parts, Place *__restrict__ place)
 {
     constexpr int RT = BM / 16, KT = BN / 16, CT = D / 64;
     using G = Geom<D, BM, BN>;
@@ -244,6 +244,9 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
             for (int o = 1; o < 16; o <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
             const int r = ty * RT + i;
             if (r >= it.rows) continue;
+            if constexpr (std::is_same_v<SEQ, VSeq>)
+                if (tx == 0 && it.head)
+                    place[token_row(r) / D] = it.whole ? Place::in_output() : Place::in_parts(blockIdx.x, it.parts, r);
             if (it.whole) {
                 float *o = out + token_row(r);
                 const float inv = 1.f / l[i];
@@ -409,24 +412,24 @@ mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
 
 template <int D, int BM, int BN, typename SEQ, bool KV8>
 cudaError_t launch_form(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
-                        const Parts &parts, int n_cta, cudaStream_t st)
+                        const Parts &parts, int n_cta, cudaStream_t st, Place *place)
 {
     auto kern = attn_simt_kernel<D, BM, BN, SEQ, KV8>;
     constexpr int smem = Geom<D, BM, BN>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3(n_cta), dim3(kThreads), smem, st, P, W, (const float *)q, Hq, sl2, (float *)out, lse, parts);
+    return launch_pdl(kern, dim3(n_cta), dim3(kThreads), smem, st, P, W, (const float *)q, Hq, sl2, (float *)out, lse, parts, place);
 }
 
 template <int D, int BM, int BN>
 cudaError_t launch_attn(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
-                        const Parts &parts, int n_cta, cudaStream_t st)
+                        const Parts &parts, int n_cta, cudaStream_t st, Place *place)
 {
     if (P.k_scale)
-        return W.plan ? launch_form<D, BM, BN, VSeq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st)
-                      : launch_form<D, BM, BN, Seq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st);
-    return W.plan ? launch_form<D, BM, BN, VSeq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st)
-                  : launch_form<D, BM, BN, Seq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st);
+        return W.plan ? launch_form<D, BM, BN, VSeq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place)
+                      : launch_form<D, BM, BN, Seq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place);
+    return W.plan ? launch_form<D, BM, BN, VSeq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place)
+                  : launch_form<D, BM, BN, Seq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place);
 }
 
 template <int D, int Z>
@@ -462,14 +465,14 @@ int simt_rows(int T, int G, int B, bool planned) { return !planned && (long)T * 
 int simt_ctas() { return 2 * device_sm_count(); }
 
 cudaError_t attn_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out, float *lse,
-                      const Parts &parts, cudaStream_t st)
+                      const Parts &parts, cudaStream_t st, Place *place)
 {
     const int n = simt_ctas();
     if (simt_rows(W.T, W.G, P.B, W.plan) == 16)
-        return d == 128 ? launch_attn<128, 16, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)
-                        : launch_attn<64, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st);
-    return d == 128 ? launch_attn<128, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st)
-                    : launch_attn<64, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st);
+        return d == 128 ? launch_attn<128, 16, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st, place)
+                        : launch_attn<64, 16, 64>(P, W, q, Hq, sl2, out, lse, parts, n, st, place);
+    return d == 128 ? launch_attn<128, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st, place)
+                    : launch_attn<64, 64, 32>(P, W, q, Hq, sl2, out, lse, parts, n, st, place);
 }
 
 cudaError_t mass_simt(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const float *lse,

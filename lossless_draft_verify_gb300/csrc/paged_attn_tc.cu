@@ -18,11 +18,11 @@ cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int H
                     : launch<64, false, Seq, false>(P, W, q, Hq, sl2, out, lse, nullptr, 0, parts, status, st);
 }
 
-cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, float *out,
-                            float *lse, const Parts &parts, int32_t *status, cudaStream_t st)
+cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const Halves &H,
+                            const Parts &parts, int32_t *status, cudaStream_t st)
 {
-    return d == 128 ? launch<128, false, VSeq, false>(P, W, q, Hq, sl2, out, lse, nullptr, 0, parts, status, st)
-                    : launch<64, false, VSeq, false>(P, W, q, Hq, sl2, out, lse, nullptr, 0, parts, status, st);
+    return d == 128 ? launch<128, false, VSeq, false>(P, W, q, Hq, sl2, H.o, H.lse, nullptr, 0, parts, status, st, H.place)
+                    : launch<64, false, VSeq, false>(P, W, q, Hq, sl2, H.o, H.lse, nullptr, 0, parts, status, st, H.place);
 }
 
 }  // namespace paged

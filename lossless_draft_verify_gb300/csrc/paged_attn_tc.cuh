@@ -100,6 +100,7 @@ struct Params {
     const __nv_bfloat16 *q;
     void *out;                     // bf16; fp32 where the batch is planned
     float *lse_out;
+    Place *place;                  // planned
     Parts parts;
     int32_t *status;
     float *s_out;                  // STORE: products of row r of q at s_out + r * s_stride
@@ -731,6 +732,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                     }
                 }
                 if (valid && c0 == 0) {
+                    if (PLANNED && it.head)
+                        A.place[out_row(R)] = it.whole ? Place::in_output() : Place::in_parts(blockIdx.x, it.parts, R);
                     if (!it.whole) A.parts.ml[pr] = make_float2(M, L);
                     else if (A.lse_out) A.lse_out[row] = M + log2f(L);
                 }
@@ -780,7 +783,8 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
 
 template <int D, bool STORE, typename SEQ, bool KV8>
 cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
-                   float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st)
+                   float *s_out, long s_stride, const Parts &parts, int32_t *status, cudaStream_t st,
+                   Place *place = nullptr)
 {
     Params A;
     A.P = P;
@@ -788,6 +792,7 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     A.q = (const __nv_bfloat16 *)q;
     A.out = out;
     A.lse_out = lse;
+    A.place = place;
     A.parts = parts;
     A.status = status;
     A.s_out = s_out;

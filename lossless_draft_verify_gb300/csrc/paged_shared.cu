@@ -4,10 +4,11 @@
 // A row's keys are its group's prefix and its sequence's own slots.  The plan has
 // an entry per group, in which all rows of the group's sequences meet the prefix's
 // keys (one pass over them, no mask), and one per sequence for its own slots.  The
-// attention kernels take an entry as they take a sequence; each half of a row
-// leaves o_i (normalised) and lse_i = log2 sum 2^s in fp32, and
+// attention kernels take an entry as they take a sequence, and leave what they found
+// of a row in fp32, in one piece or in several, with its place: o_i, sums l_i and
+// maxima m_i, of which
 //
-//   o = sum_i 2^(lse_i - M) o_i / sum_i 2^(lse_i - M),  M = max lse_i.
+//   o = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,  M = max m_i.
 #include "paged.cuh"
 
 namespace vc {
@@ -65,13 +66,15 @@ plan_kernel(Pool P, const int32_t *__restrict__ q_start, const int32_t *__restri
     plan[v] = s;
 }
 
-// A warp per (row, four heads), lane l at channels 4 l (2 l) of each.
-constexpr int kJoinWarps = 4, kJoinHeads = 4;
+// A warp per (row, some heads), lane l at channels 4 l (2 l) of each.  What it takes
+// are round trips to L2: eight parts are asked for at once, and the running sum is
+// rescaled by their maximum.
+constexpr int kJoinWarps = 4, kAtOnce = 8;
 
 template <typename E, int D>
 __global__ void __launch_bounds__(32 * kJoinWarps)
-join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, const VSeq *__restrict__ seqs,
-            const float *__restrict__ o, const float *__restrict__ lse, E *__restrict__ out)
+join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, int heads, const VSeq *__restrict__ seqs, Halves H,
+            Parts pre, Parts own, E *__restrict__ out)
 {
     pdl_wait();
     pdl_trigger();
@@ -83,36 +86,74 @@ join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, const VSe
     const VSeq s = seqs[b];
     if (tok < s.tok0 || tok >= s.tok0 + s.n) return;
     const size_t half = (size_t)T * Hq;
-#pragma unroll
-    for (int i = 0; i < kJoinHeads; ++i) {
-        const int h = blockIdx.y * kJoinHeads + i;
-        if (h >= Hq) return;
+    for (int h = blockIdx.y * heads; h < min(Hq, (int)(blockIdx.y + 1) * heads); ++h) {
         const size_t row = (size_t)tok * Hq + h;
-        float x[V];
-        const float *own = o + (half + row) * D + V * lane, *pre = o + row * D + V * lane;
+        Place at[2] = {Place::in_output(), H.place[half + row]};
+        if (s.base > 0) at[0] = H.place[row];
+        float M = kLowest, L = 0.f, acc[V];
 #pragma unroll
-        for (int e = 0; e < V; ++e) x[e] = own[e];
-        if (s.base > 0) {
-            const float a = lse[row], c = lse[half + row], M = fmaxf(a, c);
-            float wa = exp2f(a - M), wc = exp2f(c - M);
-            const float inv = 1.f / (wa + wc);
-            wa *= inv, wc *= inv;
+        for (int e = 0; e < V; ++e) acc[e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < V; ++e) x[e] = fmaf(wa, pre[e], wc * x[e]);
+        for (int x = 0; x < 2; ++x) {
+            if (x == 0 && s.base == 0) continue;
+            const Parts &parts = x == 0 ? pre : own;
+            const size_t here = x * half + row;
+            const int n = at[x].parts();
+            // a row in the output is one part with a sum of one
+            for (int p0 = 0; p0 < max(n, 1); p0 += kAtOnce) {
+                float2 ml[kAtOnce];
+                float y[kAtOnce][V];
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const int p = p0 + k;
+                    ml[k] = make_float2(kLowest, 0.f);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) y[k][e] = 0.f;
+                    if (p >= max(n, 1)) continue;
+                    const size_t pr = n ? parts.row(at[x].cta() + p, p == 0 ? 1 : 0, at[x].r) : here;
+                    ml[k] = n ? parts.ml[pr] : make_float2(H.lse[here], 1.f);
+                    const float *o = (n ? parts.o : H.o) + pr * D + V * lane;
+                    if constexpr (V == 4) {
+                        const float4 z = *reinterpret_cast<const float4 *>(o);
+                        y[k][0] = z.x, y[k][1] = z.y, y[k][2] = z.z, y[k][3] = z.w;
+                    } else {
+                        const float2 z = *reinterpret_cast<const float2 *>(o);
+                        y[k][0] = z.x, y[k][1] = z.y;
+                    }
+                }
+                float top = M;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) top = fmaxf(top, ml[k].x);
+                const float a = exp2f(M - top);
+                M = top;
+                L *= a;
+#pragma unroll
+                for (int e = 0; e < V; ++e) acc[e] *= a;
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const float w = exp2f(ml[k].x - top);
+                    L = fmaf(w, ml[k].y, L);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) acc[e] = fmaf(w, y[k][e], acc[e]);
+                }
+            }
         }
+        const float inv = 1.f / L;
         E *dst = out + row * D + V * lane;
 #pragma unroll
-        for (int e = 0; e < V; ++e) dst[e] = Elem<E>::from_f(x[e]);
+        for (int e = 0; e < V; ++e) dst[e] = Elem<E>::from_f(acc[e] * inv);
     }
 }
 
 template <typename E>
-cudaError_t launch_join(int B, const int32_t *q_start, int T, int Hq, int d, const VSeq *seqs, const float *o,
-                        const float *lse, void *out, cudaStream_t st)
+cudaError_t launch_join(int B, const int32_t *q_start, int T, int Hq, int d, const VSeq *seqs, const Halves &H,
+                        const Parts &pre, const Parts &own, void *out, cudaStream_t st)
 {
-    const dim3 grid(cdiv(T, kJoinWarps), cdiv(Hq, kJoinHeads)), block(32 * kJoinWarps);
-    return d == 128 ? launch_pdl(join_kernel<E, 128>, grid, block, 0, st, B, q_start, T, Hq, seqs, o, lse, (E *)out)
-                    : launch_pdl(join_kernel<E, 64>, grid, block, 0, st, B, q_start, T, Hq, seqs, o, lse, (E *)out);
+    // a warp per head while there are warps to spare, else it looks up its token once
+    const int heads = (long)T * Hq <= 64l * device_sm_count() ? 1 : 4;
+    const dim3 grid(cdiv(T, kJoinWarps), cdiv(Hq, heads)), block(32 * kJoinWarps);
+    return d == 128 ? launch_pdl(join_kernel<E, 128>, grid, block, 0, st, B, q_start, T, Hq, heads, seqs, H, pre, own, (E *)out)
+                    : launch_pdl(join_kernel<E, 64>, grid, block, 0, st, B, q_start, T, Hq, heads, seqs, H, pre, own, (E *)out);
 }
 
 }  // namespace
@@ -125,10 +166,10 @@ cudaError_t plan_shared(const Pool &P, const int32_t *q_start, const int32_t *ct
 }
 
 cudaError_t join_shared(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, int T, int Hq, const VSeq *seqs,
-                        const float *o, const float *lse, void *out, cudaStream_t st)
+                        const Halves &H, const Parts &pre, const Parts &own, void *out, cudaStream_t st)
 {
-    return dt == VC_BF16 ? launch_join<__nv_bfloat16>(P.B, q_start, T, Hq, d, seqs, o, lse, out, st)
-                         : launch_join<float>(P.B, q_start, T, Hq, d, seqs, o, lse, out, st);
+    return dt == VC_BF16 ? launch_join<__nv_bfloat16>(P.B, q_start, T, Hq, d, seqs, H, pre, own, out, st)
+                         : launch_join<float>(P.B, q_start, T, Hq, d, seqs, H, pre, own, out, st);
 }
 
 }  // namespace paged
