@@ -106,6 +106,7 @@ struct Params {
     float *s_out;                  // STORE: products of row r of q at s_out + r * s_stride
     long s_stride;
     int Hq, box_rows, n_rows;      // n_rows: rows of the pool's tensor map
+    bool wide;                     // out lies on a boundary of 32 bytes
     float sl2;
 };
 
@@ -152,6 +153,13 @@ __device__ __forceinline__ void expand16(const uint4 &w, uint32_t e, uint4 (&o)[
     if (TWO) times(m2);
     o[0] = make_uint4(y[0], y[1], y[2], y[3]);
     o[1] = make_uint4(y[4], y[5], y[6], y[7]);
+}
+
+// 32 bytes, on a boundary of 32
+__device__ __forceinline__ void store32(void *p, const uint32_t *x)
+{
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "l"(p), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]), "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7]) : "memory");
 }
 
 template <int N>
@@ -536,23 +544,26 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                 const int c = r % CH, q0 = r / CH;
                 uint8_t *sQ = sm + G::SM_Q + (big ? t * G::TILE : 0);
                 const int lo = big ? 0 : t * 64, cnt = big ? 128 : 64, base = big ? t * 128 : 0;
-#pragma unroll 1
-                for (int i0 = q0; i0 < cnt; i0 += 8 * RP) {
-                    uint4 x[8];                              // eight loads in flight
+                constexpr int PASSES = 128 / RP;             // (D / 8 loads of 16 bytes, all in flight)
+                const int step_tok = RP / A.W.G, step_g = RP % A.W.G;
+                int tok = (row0 + base + lo + q0) / A.W.G, gq = (row0 + base + lo + q0) % A.W.G;
+                uint4 x[PASSES];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int rr = lo + i0 + e * RP;
-                        x[e] = make_uint4(0, 0, 0, 0);
-                        if (i0 + e * RP < cnt && base + rr < it.rows)
-                            x[e] = *reinterpret_cast<const uint4 *>(A.q + q_row(base + rr) * D + c * 8);
-                    }
+                for (int e = 0; e < PASSES; ++e) {
+                    const int rr = lo + q0 + e * RP;
+                    x[e] = make_uint4(0, 0, 0, 0);
+                    if (q0 + e * RP < cnt && base + rr < it.rows)
+                        x[e] = *reinterpret_cast<const uint4 *>(
+                            A.q + ((size_t)(it.tok0 + tok) * A.Hq + it.h * A.W.G + gq) * D + c * 8);
+                    tok += step_tok, gq += step_g;
+                    if (gq >= A.W.G) gq -= A.W.G, ++tok;
+                }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int rr = lo + i0 + e * RP;
-                        if (i0 + e * RP < cnt)
-                            *reinterpret_cast<uint4 *>(sQ + (c >> 3) * (BN * 128) + rr * 128 +
-                                                       (((c & 7) ^ (rr & 7)) << 4)) = x[e];
-                    }
+                for (int e = 0; e < PASSES; ++e) {
+                    const int rr = lo + q0 + e * RP;
+                    if (q0 + e * RP < cnt)
+                        *reinterpret_cast<uint4 *>(sQ + (c >> 3) * (BN * 128) + rr * 128 +
+                                                   (((c & 7) ^ (rr & 7)) << 4)) = x[e];
                 }
                 fence_async_smem();
                 tc::fence_before();
@@ -708,27 +719,31 @@ attn_tc_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ 
                         x[e] = __uint_as_float(o[e]) * w0;
                         if (!big && n > 1) x[e] = fmaf(__uint_as_float(o1[e]), w1, x[e]);
                     }
-                    if (PLANNED && valid && it.whole) {
+                    // A thread writes its own row, so a warp's store is 32 separate
+                    // pieces: whole sectors of 32 bytes each, half as many as with 16
+                    // (a part's 256 x 128 fp32 are 4096 pieces of an SM).
+                    if (valid && it.whole && !PLANNED) {
+                        uint32_t w[16];
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>((float *)A.out + row * D + c + e) =
-                                make_float4(x[e] * inv, x[e + 1] * inv, x[e + 2] * inv, x[e + 3] * inv);
-                    } else if (valid && it.whole) {
+                        for (int e = 0; e < 16; ++e) {
+                            const __nv_bfloat162 b = __floats2bfloat162_rn(x[2 * e] * inv, x[2 * e + 1] * inv);
+                            w[e] = *reinterpret_cast<const uint32_t *>(&b);
+                        }
+                        __nv_bfloat16 *dst = (__nv_bfloat16 *)A.out + row * D + c;
+                        if (A.wide) {
+                            store32(dst, w);
+                            store32(dst + 16, w + 8);
+                        } else {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            uint32_t w[4];
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const __nv_bfloat162 b = __floats2bfloat162_rn(x[e + 2 * k] * inv, x[e + 2 * k + 1] * inv);
-                                w[k] = *reinterpret_cast<const uint32_t *>(&b);
-                            }
-                            *reinterpret_cast<uint4 *>((__nv_bfloat16 *)A.out + row * D + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            for (int e = 0; e < 16; e += 4)
+                                *reinterpret_cast<uint4 *>(dst + 2 * e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
                         }
                     } else if (valid) {
+                        float *dst = (it.whole ? (float *)A.out + row * D : A.parts.o + pr * D) + c;
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4)
-                            *reinterpret_cast<float4 *>(A.parts.o + pr * D + c + e) =
-                                make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(x[e] * inv);
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) store32(dst + e, o + e);
                     }
                 }
                 if (valid && c0 == 0) {
@@ -793,6 +808,7 @@ cudaError_t launch(const Pool &P, const WorkDim &W, const void *q, int Hq, float
     A.out = out;
     A.lse_out = lse;
     A.place = place;
+    A.wide = ((uintptr_t)out & 31) == 0;
     A.parts = parts;
     A.status = status;
     A.s_out = s_out;
