@@ -513,15 +513,17 @@ cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int H
 cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const Halves &H,
                             const Parts &parts, int32_t *status, cudaStream_t st);
 // paged_attn_few.cuh: for batches of few rows: pieces per warp, row tiles of few_rows()
-// (0: the batch has too many).  Over 8-bit pages, and planned batches over bf16 ones:
-// begun beside the kernel launched before, which is not waited for
+// (0: the batch has too many), of fp32 rows 8 or 16 in all batches.  Over 8-bit pages,
+// and planned batches over bf16 ones: begun beside the kernel launched before, which
+// is waited for at the end only, unless it is the plan's (first)
 constexpr int few_keys(int d, bool kv8) { return 4096 / (kv8 ? d : 2 * d); }      // of a tile: 4 KB
 int few_pieces(int rows);
 inline int few_rows(int T, int G, int B) { return (long)T * G <= 8l * B ? 8 : (long)T * G <= 16l * B ? 16 : 0; }
-cudaError_t attn8_few(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2, void *out,
-                      const Parts &parts, int32_t *status, cudaStream_t st);
-cudaError_t attn8_few_planned(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2,
-                              const Halves &H, const Parts &parts, int32_t *status, cudaStream_t st);
+cudaError_t attn8_few(const Pool &P, const WorkDim &W, vc_dtype dt, int d, int rows, const void *q, int Hq, float sl2,
+                      void *out, const Parts &parts, int32_t *status, cudaStream_t st);
+cudaError_t attn8_few_planned(const Pool &P, const WorkDim &W, vc_dtype dt, int d, int rows, const void *q, int Hq,
+                              float sl2, const Halves &H, bool first, const Parts &parts, int32_t *status,
+                              cudaStream_t st);
 cudaError_t attn_few_planned(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2,
                              const Halves &H, const Parts &parts, int32_t *status, cudaStream_t st);
 
@@ -552,7 +554,7 @@ cudaError_t join_shared(const Pool &P, vc_dtype dt, int d, const int32_t *q_star
 // paged_attn.cu: attention, with scores != null also the attention mass; shared:
 // that of groups (scores null, n_groups those of its workspace)
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass, bool kv8);
-size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups);
+size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups, bool kv8);
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,
                  int T, int Hq, float sm_scale, void *out, float *scores, int scores_stride, void *ws, cudaStream_t st);
 cudaError_t attn_shared(const Pool &P, vc_dtype dt, int d, const void *q, const Groups &G, const int32_t *q_start,

@@ -47,17 +47,5 @@ __device__ __forceinline__ float2 decode2(uint32_t codes)
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));
 }
 
-// 16 codes times `scale`
-__device__ __forceinline__ void decode16(const uint4 &w, float scale, float (&x)[16])
-{
-    const uint32_t c[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float2 f = decode2(c[i / 2] >> (i % 2 * 16));
-        x[2 * i] = f.x * scale;
-        x[2 * i + 1] = f.y * scale;
-    }
-}
-
 }  // namespace paged
 }  // namespace vc

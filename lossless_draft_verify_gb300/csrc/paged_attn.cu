@@ -239,16 +239,21 @@ struct WsLayout {
 // the bound 5.39 ms, just past it 7.34 ms.
 constexpr size_t kStoredMost = size_t(1) << 30;
 
-// A batch over 8-bit pages whose rows are few takes a kernel of its own.  Row
-// tiles of 8, 16 (few_rows), else 256.
-bool is_few(vc_dtype dt, int T, int G, int B, bool kv8) { return kv8 && dt == VC_BF16 && few_rows(T, G, B); }
+// A batch over 8-bit pages whose rows are few, or fp32, takes a kernel of its own.
+// The rows of its units, 8 or 16; 0: the batch does not.
+int few_unit(vc_dtype dt, int T, int G, int B, bool kv8)
+{
+    const int rows = kv8 ? few_rows(T, G, B) : 0;
+    return rows || !kv8 || dt == VC_BF16 ? rows : 16;
+}
 
-WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool with_rows, bool kv8, bool planned = false)
+WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool with_rows, bool kv8, bool planned = false,
+                int few = 0)
 {
     WsLayout w;
-    const bool few = !planned && is_few(dt, T, G, B, kv8);
-    w.n_cta = few ? few_pieces(few_rows(T, G, B)) : dt == VC_BF16 ? tc_ctas() : simt_ctas();
-    const long unit = few ? few_rows(T, G, B) : dt == VC_BF16 ? kTcRows : simt_rows(T, G, B, planned);
+    if (!planned && !few) few = few_unit(dt, T, G, B, kv8);
+    w.n_cta = few ? few_pieces(few) : dt == VC_BF16 ? tc_ctas() : simt_ctas();
+    const long unit = few ? few : dt == VC_BF16 ? kTcRows : simt_rows(T, G, B, planned);
     w.rows_cap = (int)std::min<long>(unit, (long)T * G);
     const size_t n = (size_t)w.n_cta * 2 * w.rows_cap;
     w.desc = kStatusBytes;
@@ -272,9 +277,9 @@ cudaError_t merge(const Parts &parts, int n_cta, int rows, int d, int G, int Hq,
                     : launch_pdl(merge_kernel<T, 64>, grid, dim3(32 * kMergeWarps), 0, st, parts, G, Hq, (T *)out, lse);
 }
 
+template <typename E>
 cudaError_t merge_many(const Parts &parts, int n_piece, int d, int G, int Hq, void *out, cudaStream_t st)
 {
-    using E = __nv_bfloat16;
     const dim3 grid(cdiv(n_piece, kManyWarps)), block(32 * kManyWarps);
     return d == 128 ? launch_pdl(merge_many_kernel<E, 128>, grid, block, 0, st, parts, n_piece, G, Hq, (E *)out)
                     : launch_pdl(merge_many_kernel<E, 64>, grid, block, 0, st, parts, n_piece, G, Hq, (E *)out);
@@ -305,13 +310,13 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     float *lse = scores ? (float *)(ws + w.rows) : nullptr;
     float *stored = w.s_stride ? (float *)(ws + w.stored) : nullptr;
     cudaError_t e;
-    const bool few = is_few(dt, W.T, W.G, P.B, P.k_scale);
-    if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
-    else if (few) e = attn8_few(P, W, d, few_rows(W.T, W.G, P.B), q, Hq, sl2, out, parts, (int32_t *)ws, st);
+    const int few = few_unit(dt, W.T, W.G, P.B, P.k_scale);
+    if (few) e = attn8_few(P, W, dt, d, few, q, Hq, sl2, out, parts, (int32_t *)ws, st);
+    else if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
     else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, parts, (int32_t *)ws, st);
     else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, stored, w.s_stride, parts, (int32_t *)ws, st);
     if (e == cudaSuccess && (few ? may_cut_few(cap, d, true) : may_cut<T>(cap)))
-        e = few ? merge_many(parts, w.n_cta, d, W.G, Hq, out, st)
+        e = few ? merge_many<T>(parts, w.n_cta, d, W.G, Hq, out, st)
                 : merge<T>(parts, w.n_cta, w.rows_cap, d, W.G, Hq, out, lse, st);
     if (e != cudaSuccess || !scores) return e;
     if constexpr (std::is_same_v<T, float>) {
@@ -328,19 +333,19 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
 // places, lse and o of both halves]
 struct SharedLayout {
     WsLayout attn, own;
-    int few;                   // rows of a unit of the sequences' own slots; 0: all goes one way
+    int few;                   // rows of a unit of the sequences' own slots (fp32 over 8-bit pages: of all); 0: all goes one way
     size_t own_at, plan, place, lse, o, bytes;
 };
 
-SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, int n_groups)
+SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, int n_groups, bool kv8)
 {
     SharedLayout w;
     const size_t rows = (size_t)2 * T * Hq;
     w.attn = layout(dt, d, T, G, Hq, B, cap, false, false, true);
-    w.few = dt == VC_BF16 ? few_rows(T, G, B) : 0;
+    w.few = dt == VC_BF16 ? few_rows(T, G, B) : kv8 ? 16 : 0;
     w.own_at = w.attn.bytes;
     w.own.bytes = 0;
-    if (w.few) w.own = layout(dt, d, T, G, Hq, B, cap, false, true);
+    if (w.few) w.own = layout(dt, d, T, G, Hq, B, cap, false, true, false, w.few);
     w.plan = w.own_at + w.own.bytes;
     w.place = w.plan + align256(((size_t)B + n_groups) * sizeof(VSeq));
     w.lse = w.place + align256(rows * sizeof(Place));
@@ -353,7 +358,7 @@ template <typename T>
 cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void *q, int Hq, float sl2, const Groups &G,
                        void *out, uint8_t *ws, cudaStream_t st)
 {
-    const SharedLayout w = shared_layout(dt, d, W.T, W.G, Hq, P.B, P.capacity(), G.n);
+    const SharedLayout w = shared_layout(dt, d, W.T, W.G, Hq, P.B, P.capacity(), G.n, P.k_scale);
     auto parts_at = [&](const WsLayout &x, uint8_t *at) {
         return Parts{(PartDesc *)(at + x.desc), (float2 *)(at + x.ml), (float *)(at + x.o), x.rows_cap};
     };
@@ -364,19 +369,21 @@ cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void 
     cudaError_t e = plan_shared(P, W.q_start, W.ctx_len, W.T, G, plan, st);
     if (e != cudaSuccess) return e;
     W.plan = plan;
-    W.n_plan = w.few ? G.n : P.B + G.n;
-    if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, H.o, H.lse, parts, st, H.place);
+    W.n_plan = w.few && dt == VC_BF16 ? G.n : P.B + G.n;
+    if (dt == VC_F32 && P.k_scale)
+        e = attn8_few_planned(P, W, dt, d, w.few, q, Hq, sl2, H, true, own, status, st);
+    else if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, H.o, H.lse, parts, st, H.place);
     else if (P.k_scale) e = attn8_tc_planned(P, W, d, q, Hq, sl2, H, parts, status, st);
     else e = attn_tc_planned(P, W, d, q, Hq, sl2, H, parts, status, st);
-    if (e == cudaSuccess && w.few) {
+    if (e == cudaSuccess && w.few && dt == VC_BF16) {
         // The kernel before took the prefixes; the sequences' own slots follow beside its end.
         W.plan = plan + G.n;
         W.n_plan = P.B;
-        e = P.k_scale ? attn8_few_planned(P, W, d, w.few, q, Hq, sl2, H, own, status, st)
+        e = P.k_scale ? attn8_few_planned(P, W, dt, d, w.few, q, Hq, sl2, H, false, own, status, st)
                       : attn_few_planned(P, W, d, w.few, q, Hq, sl2, H, own, status, st);
     }
     if (e != cudaSuccess) return e;
-    return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, H, parts, own, out, st);
+    return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, H, dt == VC_F32 ? own : parts, own, out, st);
 }
 
 }  // namespace
@@ -386,9 +393,9 @@ size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap
     return layout(dt, d, T, Hq / Hkv, Hq, B, cap, mass, kv8).bytes;
 }
 
-size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups)
+size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups, bool kv8)
 {
-    return shared_layout(dt, d, T, Hq / Hkv, Hq, B, cap, n_groups).bytes;
+    return shared_layout(dt, d, T, Hq / Hkv, Hq, B, cap, n_groups, kv8).bytes;
 }
 
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,

@@ -1,6 +1,6 @@
 // paged_attn_few.cuh -- causal attention over 8-bit pages, and over bf16 pages in
 // planned batches, for batches of few rows (decoding, drafting): up to 16 (query,
-// head) rows per kv head.
+// head) rows per kv head; and of fp32 rows over 8-bit pages in all batches.
 //
 //   out_i = sum_j p_ij 2^f_j v_j / sum_j p_ij,  p_ij = exp(scale 2^e_j q_i . k_j)
 //
@@ -28,8 +28,13 @@
 // sequences that share a prefix, a few hundred tokens each, for which the tensor-core
 // kernel's 8 us per unit are too many.
 //
-// Ranges.  q is scaled to f16 by its row's largest exponent (an element is off by
-// 2^-25 of the row's largest, at most).  The running maximum is raised when it has
+// fp32 rows over 8-bit pages take the same products: the codes are exact operands, and
+// q and the weights are two f16 terms each, 22 bits, for twice the products (the CUDA
+// cores take 583 us for four chunks of 300 over 2000, 16/4 heads of 128, and 169 for a
+// token of 8 sequences over 4000, 32/8 heads).
+//
+// Ranges.  q is scaled by its row's largest exponent to 2^14 (beside the roundings to
+// 11 or 22 bits, an element is off by at most 2^-39 of the row's largest).  The running maximum is raised when it has
 // grown by more than 2^8, as in the tensor-core kernel.  The weights p 2^f, which
 // become f16, are scaled by a power of two per row such that the largest so far lies
 // at 2^6: what is lost below f16's smallest number is 2^-31 of it per key.
@@ -51,11 +56,12 @@ namespace {
 constexpr int kBlock = 16;                                     // rows of a request: they lie in one page
 constexpr float kLazy = 8.f, kGrown = 4096.f;                  // log2 domain; a lane's sum with a weight above 2^kLazy
 constexpr float kLeast = -3e38f;                               // a row that has seen no key
+constexpr float kQTop = 16384.f;                               // q rows lie in [kQTop, 2 kQTop) at their largest
 constexpr float kTop = 64.f, kMost = 32768.f;                  // where weights are put, and how far they may grow
 
 // Warps of a CTA (their accumulators are what limits them) and tiles, of K and V, of
 // a warp's ring: 192 KB in all.
-template <int D, int NB, bool KV8>
+template <int D, int NB, bool KV8, typename E>
 struct Geom {
     static constexpr int ROW = KV8 ? D : 2 * D;                // bytes
     static constexpr int BN = few_keys(D, KV8), BLOCKS = BN / kBlock, TILE = BN * ROW, STAGE = 2 * TILE;
@@ -78,12 +84,13 @@ struct Warp {
 struct Params {
     Pool P;
     WorkDim W;
-    const __nv_bfloat16 *q;
-    __nv_bfloat16 *out;
+    const void *q;
+    void *out;
     Halves H;                          // instead, where the batch is planned
     Parts parts;
     int32_t *status;
     int Hq, n_rows;
+    bool first;                        // planned: the kernel launched before is the plan's
     float sl2;
 };
 
@@ -92,9 +99,13 @@ __device__ __forceinline__ uint32_t half2_of(uint32_t codes)   // the low 16 bit
     const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)codes, __NV_E4M3);
     return *reinterpret_cast<const uint32_t *>(&h);
 }
-__device__ __forceinline__ uint32_t pack_half2(float a, float b)
+// the pair's nearest f16 numbers; leaves what they lack
+__device__ __forceinline__ uint32_t take_half2(float &a, float &b)
 {
     const __half2 h = __floats2half2_rn(a, b);
+    const float2 f = __half22float2(h);
+    a -= f.x;
+    b -= f.y;
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b)
@@ -142,12 +153,15 @@ __device__ __forceinline__ uint4 chunk(const uint8_t *tile, int r, int c)
 // NB: blocks of 8 rows.  Lane 4 g + q holds, of S^T, keys g and g + 8 of rows 2 q
 // and 2 q + 1 (of each block), of O^T channels D/8 g .. + D/8 - 1 (KV8) or g + 8 i of
 // the same rows.
-template <int D, int NB, typename SEQ, bool KV8>
-__global__ void __launch_bounds__(32 * Geom<D, NB, KV8>::WARPS, 1)
+template <int D, int NB, typename SEQ, bool KV8, typename E>
+__global__ void __launch_bounds__(32 * Geom<D, NB, KV8, E>::WARPS, 1)
 attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, Params A)
 {
     constexpr int BM = 8 * NB, KS = D / 16, MT = D / 16, KC = D / 64;    // k steps, m tiles, chunks of a K row per lane
-    using G = Geom<D, NB, KV8>;
+    constexpr bool F32 = std::is_same_v<E, float>;
+    constexpr int TERMS = F32 ? 2 : 1;                       // f16 terms of q and of the weights
+    static_assert(KV8 || !F32, "fp32 rows: 8-bit pages");
+    using G = Geom<D, NB, KV8, E>;
     using It = ItemOf<SEQ>;
     constexpr bool PLANNED = std::is_same_v<SEQ, VSeq>;
     constexpr int BN = G::BN, kBlocks = G::BLOCKS, TILE = G::TILE, kStages = G::STAGES, kWarps = G::WARPS;
@@ -160,7 +174,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int n_piece = gridDim.x * kWarps, me = warp * gridDim.x + blockIdx.x;
     // A planned batch's entries come from the kernel before the one before this, which
     // has waited for it; that one runs beside this kernel (see the end).
-    if (!PLANNED) pdl_wait();
+    if (!PLANNED || A.first) pdl_wait();
     if (lane == 0) {
         A.parts.desc[me].parts = 0;
         for (int i = 0; i < kStages; ++i) mbar_init(&S.full[i], 1);
@@ -186,7 +200,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     int pending = 0, asked = -1, used = 0;                   // tiles on their way; parts asked for, and in use
     int left = 0, at = 0, page = 0, page_next = 0;           // tiles to ask for; a lane's page numbers of 32 blocks
     const int what = lane & 3, block = lane >> 2 & (kBlocks - 1);      // K, V, K's scales, V's (or second boxes); of lanes that request
-    uint32_t b[NB][KS][2];
+    uint32_t b[NB][KS][TERMS][2];
     float qs[NB][2];                                         // log2 e times the scale, the row's own with it
     float o[NB][MT][4], m[NB][2], l[NB][2], put[NB][2], level[NB][2];
     int kmax[NB][2], kall = 0, key0 = -1;
@@ -257,36 +271,45 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 const bool on = 8 * x + g < it.rows;
                 float back = 1.f;
                 if constexpr (KV8) {
-                    uint4 w[2 * KC] = {};
-                    const __nv_bfloat16 *src = A.q + (on ? row_of(it.tok0, 8 * x + g) * D : 0);
+                    float w[KC][16];                         // this lane's channels of the row
+                    const E *src = (const E *)A.q + (on ? row_of(it.tok0, 8 * x + g) * D : 0) + q4 * 16;
+                    float top = 0.f;
 #pragma unroll
-                    for (int i = 0; i < 2 * KC; ++i)
-                        if (on) w[i] = *reinterpret_cast<const uint4 *>(src + (i / 2) * 64 + q4 * 16 + (i % 2) * 8);
-                    uint32_t top = 0;                                // the largest magnitude's bits
+                    for (int c = 0; c < KC; ++c) {
+                        constexpr int PER = 16 / sizeof(E);
 #pragma unroll
-                    for (int i = 0; i < 2 * KC; ++i) {
-                        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                        for (int i = 0; i < 16; i += PER) {
+                            uint4 z = make_uint4(0, 0, 0, 0);
+                            if (on) z = *reinterpret_cast<const uint4 *>(src + c * 64 + i);
+                            const uint32_t u[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) top = max(top, max(u[e] & 0x7fffu, u[e] >> 16 & 0x7fffu));
+                            for (int k = 0; k < 4; ++k) {
+                                if constexpr (F32) w[c][i + k] = __uint_as_float(u[k]);
+                                else w[c][i + 2 * k] = bf16_lo(u[k]), w[c][i + 2 * k + 1] = bf16_hi(u[k]);
+                            }
+                        }
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) top = fmaxf(top, fabsf(w[c][i]));
                     }
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const uint32_t ex = min(max(top >> 7, 27u), 253u);
-                    const float inv = scale_of(254u - ex);
-                    back = scale_of(ex);
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                    const uint32_t ex = min(max(__float_as_uint(top) >> 23, 27u), 253u);
+                    const float inv = scale_of(254u - ex) * kQTop;
+                    back = scale_of(ex) / kQTop;
 #pragma unroll
-                    for (int i = 0; i < 2 * KC; ++i) {
-                        const uint32_t u[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                    for (int c = 0; c < KC; ++c)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)                  // chunk i holds k steps 2 i, 2 i + 1
-                            b[x][2 * i + e / 2][e % 2] = pack_half2(bf16_lo(u[e]) * inv, bf16_hi(u[e]) * inv);
-                    }
+                        for (int i = 0; i < 16; i += 2) {    // four channels are a k step's
+                            float lo = w[c][i] * inv, hi = w[c][i + 1] * inv;
+#pragma unroll
+                            for (int k = 0; k < TERMS; ++k) b[x][4 * c + i / 4][k][i / 2 % 2] = take_half2(lo, hi);
+                        }
                 } else {
-                    const uint32_t *src = reinterpret_cast<const uint32_t *>(A.q + (on ? row_of(it.tok0, 8 * x + g) * D : 0));
+                    const uint32_t *src = reinterpret_cast<const uint32_t *>((const E *)A.q + (on ? row_of(it.tok0, 8 * x + g) * D : 0));
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
-                        b[x][i][0] = on ? src[8 * i + q4] : 0;
-                        b[x][i][1] = on ? src[8 * i + 4 + q4] : 0;
+                        b[x][i][0][0] = on ? src[8 * i + q4] : 0;
+                        b[x][i][0][1] = on ? src[8 * i + 4 + q4] : 0;
                     }
                 }
 #pragma unroll
@@ -337,7 +360,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                             for (int x = 0; x < NB; ++x) {
                                 if (e == 0) acc[x][y][c][0] = acc[x][y][c][1] = acc[x][y][c][2] = acc[x][y][c][3] = 0.f;
-                                mma_bf16(acc[x][y][c], a, b[x][4 * c + e][0], b[x][4 * c + e][1]);
+                                mma_bf16(acc[x][y][c], a, b[x][4 * c + e][0][0], b[x][4 * c + e][0][1]);
                             }
                         }
             } else {
@@ -360,7 +383,9 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                             for (int x = 0; x < NB; ++x) {
                                 if (e == 0) acc[x][y][c][0] = acc[x][y][c][1] = acc[x][y][c][2] = acc[x][y][c][3] = 0.f;
-                                mma(acc[x][y][c], a, b[x][4 * c + e][0], b[x][4 * c + e][1]);
+#pragma unroll
+                                for (int k = 0; k < TERMS; ++k)
+                                    mma(acc[x][y][c], a, b[x][4 * c + e][k][0], b[x][4 * c + e][k][1]);
                             }
                         }
                 }
@@ -386,7 +411,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                             if (key0 + g + 8 * j > kmax[x][r]) s[x][j][r] = __uint_as_float(0xff800000u);
             }
             // ---- weights ----
-            uint32_t w[NB][2 * kBlocks];
+            uint32_t w[NB][2 * kBlocks][TERMS];
             float sum[NB][2];
             for (int moves = 0;; ++moves) {
                 bool far = false;
@@ -403,8 +428,13 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                             sum[x][r] += p;
                             u[r] = KV8 ? p * (vs[j] * put[x][r]) : p;
                         }
-                        w[x][j] = KV8 ? pack_half2(u[0], u[1]) : pack_bf16(u[0], u[1]);
-                        if (KV8) most = __hmax2(most, *reinterpret_cast<const __half2 *>(&w[x][j]));
+                        if constexpr (KV8) {
+#pragma unroll
+                            for (int k = 0; k < TERMS; ++k) w[x][j][k] = take_half2(u[0], u[1]);
+                            most = __hmax2(most, *reinterpret_cast<const __half2 *>(&w[x][j][0]));
+                        } else {
+                            w[x][j][0] = pack_bf16(u[0], u[1]);
+                        }
                     }
                     far = far || fmaxf(sum[x][0], sum[x][1]) > kGrown ||
                           (KV8 && fmaxf(__low2float(most), __high2float(most)) > kMost);
@@ -451,7 +481,9 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 l[x][0] += sum[x][0];
                 l[x][1] += sum[x][1];
 #pragma unroll
-                for (int j = 0; j < 2 * kBlocks; ++j) w[x][j] = transpose8(w[x][j]);
+                for (int j = 0; j < 2 * kBlocks; ++j)
+#pragma unroll
+                    for (int k = 0; k < TERMS; ++k) w[x][j][k] = transpose8(w[x][j][k]);
             }
             // ---- O^T += V^T P^T: of each block, rows 2 q, 2 q + 1, 2 q + 8, 2 q + 9 at this lane's channels ----
             if constexpr (!KV8) {
@@ -470,7 +502,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                             }
                         }
 #pragma unroll
-                        for (int x = 0; x < NB; ++x) mma_bf16(o[x][t], a, w[x][2 * y], w[x][2 * y + 1]);
+                        for (int x = 0; x < NB; ++x) mma_bf16(o[x][t], a, w[x][2 * y][0], w[x][2 * y + 1][0]);
                     }
             } else {
 #pragma unroll
@@ -501,7 +533,9 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         const uint32_t c = __byte_perm(v[0][t / 2], v[1][t / 2], sel), z = __byte_perm(v[2][t / 2], v[3][t / 2], sel);
                         const uint32_t a[4] = {half2_of(c), half2_of(c >> 16), half2_of(z), half2_of(z >> 16)};
 #pragma unroll
-                        for (int x = 0; x < NB; ++x) mma(o[x][t], a, w[x][2 * y], w[x][2 * y + 1]);
+                        for (int x = 0; x < NB; ++x)
+#pragma unroll
+                            for (int k = 0; k < TERMS; ++k) mma(o[x][t], a, w[x][2 * y][k], w[x][2 * y + 1][k]);
                     }
                 }
             }
@@ -530,15 +564,15 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                 for (int t = 0; t < MT; ++t) y[2 * t] = o[x][t][r] * f, y[2 * t + 1] = o[x][t][2 + r] * f;
                 const size_t row = it.whole ? head_row(R) : A.parts.row(me, it.head ? 1 : 0, R);
-                if (it.whole && !PLANNED) {
-                    __nv_bfloat16 *dst = A.out + row * D + 2 * MT * g;
+                if (it.whole && !PLANNED && !F32) {
+                    __nv_bfloat16 *dst = (__nv_bfloat16 *)A.out + row * D + 2 * MT * g;
                     static_assert(KV8 || PLANNED, "a lane's channels are side by side");
 #pragma unroll
                     for (int e = 0; e < 2 * MT; e += 8)
                         *reinterpret_cast<uint4 *>(dst + e) = make_uint4(pack_bf16(y[e], y[e + 1]), pack_bf16(y[e + 2], y[e + 3]),
                                                                          pack_bf16(y[e + 4], y[e + 5]), pack_bf16(y[e + 6], y[e + 7]));
                 } else {
-                    float *dst = (it.whole ? A.H.o : A.parts.o) + row * D;
+                    float *dst = (!it.whole ? A.parts.o : PLANNED ? A.H.o : (float *)A.out) + row * D;
                     if constexpr (KV8) {
 #pragma unroll
                         for (int e = 0; e < 2 * MT; e += 4)
@@ -550,8 +584,8 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     if (g == 0) {
                         if (PLANNED && it.head)
                             A.H.place[head_row(R)] = it.whole ? Place::in_output() : Place::in_parts(me, it.parts, R);
-                        if (it.whole) A.H.lse[row] = top + log2f(sum);
-                        else A.parts.ml[row] = make_float2(top, sum);
+                        if (!it.whole) A.parts.ml[row] = make_float2(top, sum);
+                        else if (PLANNED) A.H.lse[row] = top + log2f(sum);
                     }
                 }
             }
@@ -577,16 +611,17 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     }
 }
 
-template <int D, int NB, typename SEQ, bool KV8>
+template <int D, int NB, typename SEQ, bool KV8, typename E>
 cudaError_t launch_few(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, const Halves &H,
-                       const Parts &parts, int32_t *status, cudaStream_t st)
+                       bool first, const Parts &parts, int32_t *status, cudaStream_t st)
 {
-    using G = Geom<D, NB, KV8>;
+    using G = Geom<D, NB, KV8, E>;
     Params A;
     A.P = P;
     A.W = W;
-    A.q = (const __nv_bfloat16 *)q;
-    A.out = (__nv_bfloat16 *)out;
+    A.q = q;
+    A.out = out;
+    A.first = first;
     A.H = H;
     A.parts = parts;
     A.status = status;
@@ -603,21 +638,21 @@ cudaError_t launch_few(const Pool &P, const WorkDim &W, const void *q, int Hq, f
             !tma_map_bf16_3d(&mv, P.v, D, A.n_rows, 1, bytes, bytes * A.n_rows, 64, kBlock, 1))
             return cudaErrorInvalidValue;
     }
-    auto kern = attn_few_kernel<D, NB, SEQ, KV8>;
+    auto kern = attn_few_kernel<D, NB, SEQ, KV8, E>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, G::SMEM);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3(device_sm_count()), dim3(32 * G::WARPS), G::SMEM, st, mk, mv, A);
 }
 
-template <typename SEQ, bool KV8>
+template <typename SEQ, bool KV8, typename E>
 cudaError_t few_form(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2, void *out,
-                     const Halves &H, const Parts &parts, int32_t *status, cudaStream_t st)
+                     const Halves &H, bool first, const Parts &parts, int32_t *status, cudaStream_t st)
 {
     if (rows == 8)
-        return d == 128 ? launch_few<128, 1, SEQ, KV8>(P, W, q, Hq, sl2, out, H, parts, status, st)
-                        : launch_few<64, 1, SEQ, KV8>(P, W, q, Hq, sl2, out, H, parts, status, st);
-    return d == 128 ? launch_few<128, 2, SEQ, KV8>(P, W, q, Hq, sl2, out, H, parts, status, st)
-                    : launch_few<64, 2, SEQ, KV8>(P, W, q, Hq, sl2, out, H, parts, status, st);
+        return d == 128 ? launch_few<128, 1, SEQ, KV8, E>(P, W, q, Hq, sl2, out, H, first, parts, status, st)
+                        : launch_few<64, 1, SEQ, KV8, E>(P, W, q, Hq, sl2, out, H, first, parts, status, st);
+    return d == 128 ? launch_few<128, 2, SEQ, KV8, E>(P, W, q, Hq, sl2, out, H, first, parts, status, st)
+                    : launch_few<64, 2, SEQ, KV8, E>(P, W, q, Hq, sl2, out, H, first, parts, status, st);
 }
 
 }  // namespace

@@ -1,7 +1,6 @@
 // paged_attn_simt.cu -- causal attention of ragged chunks over a paged cache
 // and its attention mass on the CUDA cores, fp32 throughout: the path of fp32
-// rows, whose products may not be rounded to the tensor cores' input types, over
-// fp32 pages or (attention only) 8-bit ones.
+// rows, whose products may not be rounded to the tensor cores' input types.
 //
 //   out_i = sum_j p_ij v_j / sum_j p_ij,  p_ij = exp(scale q_i . k_j),
 //   j <= ctx + i, in one pass over the keys with a running maximum and sum;
@@ -11,7 +10,6 @@
 #include <type_traits>
 
 #include "paged.cuh"
-#include "paged8.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -62,11 +60,7 @@ __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group 
 // the instructions around them: four chunks of 300 over 2000 tokens, 16/4 heads
 // of 128, 572 us, 37 TFLOP/s (larger tiles leave room for fewer warps); a token of
 // 8 sequences over 4000, 32/8 heads, 157 us, 1.7 TB/s.
-//
-// KV8: a thread holds 16 codes of a K and a V row of the next tile in registers
-// while it computes with the present one, then stores them as fp32 with their
-// scales; the tiles in shared memory are the same.
-template <int D, int BM, int BN, typename SEQ, bool KV8>
+template <int D, int BM, int BN, typename SEQ>
 __global__ void __launch_bounds__(kThreads)
 attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float scale_log2, float *__restrict__ out,
                  float *__restrict__ lse_out, Parts parts, Place *__restrict__ place)
@@ -109,32 +103,18 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
         }
         // Key tiles pass through two stages: a tile is on its way while the one
         // before it is computed with, its page numbers are read a tile earlier.
-        constexpr int CW = KV8 ? 16 : 4, CH = D / CW, RP = kThreads / CH, NR = KV8 ? 1 : BN / RP;
-        static_assert(!KV8 || RP >= BN, "a thread's codes of a tile");
-        const int c4 = (int)threadIdx.x % CH * CW, r0 = threadIdx.x / CH;
+        constexpr int CH = D / 4, RP = kThreads / CH, NR = BN / RP;
+        const int c4 = (int)threadIdx.x % CH * 4, r0 = threadIdx.x / CH;
         int pages[NR];
         auto look_up = [&](int t) {
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
                 const int slot = t * BN + r0 + x * RP;
-                const bool in = t < it.t_hi && slot < len && r0 < BN;
+                const bool in = t < it.t_hi && slot < len;
                 pages[x] = in ? P.page_of(it.b, (it.first_slot() + slot) >> P.page_log2) : -1;
             }
         };
-        uint4 k8 = {}, v8 = {};
-        float ks = 0.f, vs = 0.f;
         auto fetch = [&](int t) {
-            if constexpr (KV8) {                       // zeros where there is no row
-                k8 = v8 = make_uint4(0, 0, 0, 0);
-                ks = vs = 0.f;
-                if (pages[0] < 0) return;
-                const size_t row = P.row(pages[0], it.h, (t * BN + r0) & (P.page() - 1));
-                k8 = *reinterpret_cast<const uint4 *>((const uint8_t *)P.k + row * D + c4);
-                v8 = *reinterpret_cast<const uint4 *>((const uint8_t *)P.v + row * D + c4);
-                ks = scale_of(P.k_scale[row]);
-                vs = scale_of(P.v_scale[row]);
-                return;
-            }
             float *k = sKV + (t & 1) * G::STAGE, *v = k + BN * G::PQ;
 #pragma unroll
             for (int x = 0; x < NR; ++x) {
@@ -146,20 +126,8 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
             }
             copy_commit();
         };
-        auto land = [&](int t) {                       // KV8: the fetched tile into its stage
-            if (!KV8 || r0 >= BN) return;
-            float *k = sKV + (t & 1) * G::STAGE + r0 * G::PQ + c4, *v = sKV + (t & 1) * G::STAGE + BN * G::PQ + r0 * D + c4;
-            float x[16];
-            decode16(k8, ks, x);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(k + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-            decode16(v8, vs, x);
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) *reinterpret_cast<float4 *>(v + i) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
-        };
         look_up(it.t_lo);
         fetch(it.t_lo);
-        land(it.t_lo);
         look_up(it.t_lo + 1);
         for (int t = it.t_lo; t < it.t_hi; ++t) {
             const int key0 = t * BN;
@@ -236,7 +204,6 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
                         }
                     }
             }
-            if (t + 1 < it.t_hi) land(t + 1);
         }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
@@ -410,11 +377,11 @@ mass_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
     }
 }
 
-template <int D, int BM, int BN, typename SEQ, bool KV8>
+template <int D, int BM, int BN, typename SEQ>
 cudaError_t launch_form(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
                         const Parts &parts, int n_cta, cudaStream_t st, Place *place)
 {
-    auto kern = attn_simt_kernel<D, BM, BN, SEQ, KV8>;
+    auto kern = attn_simt_kernel<D, BM, BN, SEQ>;
     constexpr int smem = Geom<D, BM, BN>::SMEM;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
@@ -425,11 +392,9 @@ template <int D, int BM, int BN>
 cudaError_t launch_attn(const Pool &P, const WorkDim &W, const void *q, int Hq, float sl2, void *out, float *lse,
                         const Parts &parts, int n_cta, cudaStream_t st, Place *place)
 {
-    if (P.k_scale)
-        return W.plan ? launch_form<D, BM, BN, VSeq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place)
-                      : launch_form<D, BM, BN, Seq, true>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place);
-    return W.plan ? launch_form<D, BM, BN, VSeq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place)
-                  : launch_form<D, BM, BN, Seq, false>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place);
+    if constexpr (BM == 64)                            // (simt_rows: a planned batch's)
+        if (W.plan) return launch_form<D, BM, BN, VSeq>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place);
+    return launch_form<D, BM, BN, Seq>(P, W, q, Hq, sl2, out, lse, parts, n_cta, st, place);
 }
 
 template <int D, int Z>

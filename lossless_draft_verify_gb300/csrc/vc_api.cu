@@ -509,7 +509,7 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const paged::P
     if (sm_scale > 1e8f) return VC_ERR_UNSUPPORTED;
     if (scores && scores_stride < c->max_blocks * c->page) return VC_ERR_INVALID;
     const long cap = (long)c->max_blocks * c->page;
-    if (ws_bytes < (shared ? paged::attn_shared_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, shared->n)
+    if (ws_bytes < (shared ? paged::attn_shared_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, shared->n, P.k_scale)
                            : paged::attn_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, cap, scores != nullptr, P.k_scale)))
         return VC_ERR_INVALID;
     if (T == 0) return VC_OK;
@@ -520,12 +520,12 @@ vc_status paged_attn_call(const void *q, const vc_paged_cache *c, const paged::P
                                    stream));
 }
 
-size_t paged_shared_ws(const vc_paged_cache *c, int n_groups, int T, int Hq)
+size_t paged_shared_ws(const vc_paged_cache *c, int n_groups, int T, int Hq, bool kv8 = false)
 {
     if (n_groups < 0 || !paged_supported(c) || !paged_heads_ok(c, T, Hq) || !paged_rows_ok(c, T, Hq) ||
         !shared_supported(c, n_groups, T, Hq))
         return 0;
-    return paged::attn_shared_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page, n_groups);
+    return paged::attn_shared_ws_bytes(c->dt, c->d, T, Hq, c->Hkv, c->B, (long)c->max_blocks * c->page, n_groups, kv8);
 }
 
 vc_status paged_append_call(const void *qkv, const void *q_gain, const void *k_gain, float eps, const vc_rope *rope,
@@ -650,7 +650,7 @@ size_t vc_paged8_attn_shared_workspace_bytes(const vc_paged8_cache *cache, int n
 {
     if (!paged8_ok(cache)) return 0;
     const vc_paged_cache c = paged8_base(cache);
-    return paged_shared_ws(&c, n_groups, T, Hq);
+    return paged_shared_ws(&c, n_groups, T, Hq, true);
 }
 
 vc_status vc_paged8_attn_shared(const void *q, const vc_paged8_cache *cache, const vc_shared_prefix *groups,
