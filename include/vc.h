@@ -963,7 +963,7 @@ vc_status vc_paged8_append(const void *qkv, const void *q_gain, const void *k_ga
  * its slot ctx_len[b] + i, k_out and v_out [T][Hkv][d] in dt, 16-byte aligned
  * (q_start and ctx_len as for an append: the slots of a chunk, or with ctx_len 0
  * and q_start by length the whole sequences).  Exact in both types.  T * Hkv <=
- * 2^30.  Rows of a page outside the pool are left as they are.
+ * 2^30, Hkv <= 2^19.  Rows of a page outside the pool are left as they are.
  */
 vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len, int T,
                          void *k_out, void *v_out, cudaStream_t stream);

@@ -179,6 +179,7 @@ __host__ __device__ __forceinline__ S load_entry(const Pool &P, const WorkDim &W
 // 590, four chunks up to 17 over 2000 at most 27, 27, 27 and 25.
 template <int BM>
 struct Cost {
+    static constexpr bool kByTiles = false;
     static constexpr int kUnitCost = BM == 256 ? 16 : 1;
     static constexpr int kMinPiece = BM == 256 ? 10 : 2;
     static constexpr int kWhole = BM == 256 ? 20 : 3;
@@ -189,6 +190,7 @@ struct Cost {
 // heads of 128) 23.9 and 12.4 us, of 16 over 500 21.5 and 14.7, of 16 over 32768 179 and
 // 177.5; only 128 sequences of 150 tokens take longer, 17.1 and 25.4.
 struct CostFew {
+    static constexpr bool kByTiles = true;
     static constexpr int kUnitCost = 2;
     static constexpr int kMinPiece = 2;
     static constexpr int kWhole = 4;
@@ -230,9 +232,30 @@ struct Units : C {
     }
     template <typename S>
     static __host__ __device__ __forceinline__ int mtiles(const S &s, int G) { return (s.n * G + BM - 1) / BM; }
+    // Row tiles of few rows are many, and many have the same tiles: how many take
+    // `t` tiles at most.
+    template <typename S>
+    static __host__ __device__ __forceinline__ int upto(const S &s, int G, int t, int m, int last)
+    {
+        if (t >= last) return m;
+        const long tok = (long)t * BN - s.ctx;               // tokens whose last key lies in the first t tiles
+        return tok <= 0 ? 0 : (int)lmin((tok * G) / BM, m);
+    }
     template <typename S>
     static __host__ __device__ __forceinline__ long head_cost(const S &s, int G)
     {
+        if constexpr (C::kByTiles) {
+            const int m = mtiles(s, G);
+            if (m == 0) return 0;
+            long c = (long)m * kUnitCost;
+            const int first = tiles(s, G, 0), last = tiles(s, G, m - 1);
+            for (int t = first, before = 0; t <= last; ++t) {
+                const int n = upto(s, G, t, m, last);
+                c += (long)(n - before) * t;
+                before = n;
+            }
+            return c;
+        }
         long c = 0;
         const int m = mtiles(s, G);
         for (int i = 0; i < m; ++i) c += cost(s, G, i);
@@ -245,6 +268,23 @@ struct Units : C {
         out.h = (int)(x / hc);
         x -= out.h * hc;
         int mt = 0;
+        if constexpr (C::kByTiles) {                         // past the row tiles of fewer tiles
+            const int m = mtiles(s, G), last = tiles(s, G, m - 1);
+            for (int t = tiles(s, G, 0); t <= last; ++t) {
+                const int n = upto(s, G, t, m, last);
+                const long c = (long)(n - mt) * (t + kUnitCost);
+                if (x < c) {
+                    mt += (int)(x / (t + kUnitCost));
+                    x %= t + kUnitCost;
+                    break;
+                }
+                x -= c;
+                mt = n;
+            }
+            out.mt = mt;
+            out.off = x;
+            return;
+        }
         for (;;) {
             const int t = cost(s, G, mt);
             if (x < t) break;

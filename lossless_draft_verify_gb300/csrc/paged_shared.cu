@@ -17,16 +17,20 @@ namespace {
 
 constexpr int kPlanThreads = 128;
 
-// Slots of group g that its sequences share: whole pages; none where it has one
-// sequence only, or a length or range that does not fit.
-__device__ __forceinline__ int shared_slots(const Pool &P, const Groups &G, int g)
+// A group: its rows, and the slots that its sequences share: whole pages; none where
+// it has one sequence only, or a length or range that does not fit.
+struct Group {
+    int row0, row1, slots;
+};
+__device__ __forceinline__ Group load_group(const Pool &P, const Groups &G, const int32_t *__restrict__ q_start, int T, int g)
 {
     const int s0 = G.first[g], s1 = G.first[g + 1], n = G.prefix[g];
-    if (s0 < 0 || s1 < s0 || s1 > P.B || n < 0 || n > P.capacity()) {
-        set_flag(P.status, VC_PAGED_BAD_LENGTH);
-        return 0;
+    if (s0 >= 0 && s1 >= s0 && s1 <= P.B && n >= 0 && n <= P.capacity()) {
+        const int a = q_start[s0], e = q_start[s1];
+        if (a >= 0 && e >= a && e <= T) return Group{a, e, s1 - s0 < 2 ? 0 : n & -P.page()};
     }
-    return s1 - s0 < 2 ? 0 : n & -P.page();
+    set_flag(P.status, VC_PAGED_BAD_LENGTH);
+    return Group{0, 0, 0};
 }
 
 __global__ void __launch_bounds__(kPlanThreads)
@@ -39,11 +43,8 @@ plan_kernel(Pool P, const int32_t *__restrict__ q_start, const int32_t *__restri
     if (v >= G.n + P.B) return;
     VSeq s = {0, 0, 0, 1, 0, 0, 0, 0};
     if (v < G.n) {
-        const int n = shared_slots(P, G, v);
-        if (n > 0) {
-            const int a = q_start[G.first[v]], e = q_start[G.first[v + 1]];
-            if (a >= 0 && e >= a && e <= T) s = VSeq{a, e - a, n - 1, 0, 0, G.first[v], a, 0};
-        }
+        const Group g = load_group(P, G, q_start, T, v);
+        if (g.slots > 0) s = VSeq{g.row0, g.row1 - g.row0, g.slots - 1, 0, 0, G.first[v], g.row0, 0};
     } else {
         const int b = v - G.n;
         const Seq q = load_seq(P, q_start, ctx_len, T, b);
@@ -55,7 +56,11 @@ plan_kernel(Pool P, const int32_t *__restrict__ q_start, const int32_t *__restri
             else hi = mid;
         }
         int base = 0;
-        if (lo > 0 && b < G.first[lo]) base = shared_slots(P, G, lo - 1);
+        if (lo > 0 && b < G.first[lo]) {
+            const Group g = load_group(P, G, q_start, T, lo - 1);
+            // (rows out of order: the group's do not hold these)
+            if (g.row0 <= q.tok0 && q.tok0 + q.n <= g.row1) base = g.slots;
+        }
         s = VSeq{q.tok0, q.n, q.ctx - base, 1, base, b, T + q.tok0, 0};
         if (q.n > 0 && q.ctx < base) {                       // a context that does not hold the prefix
             set_flag(P.status, VC_PAGED_BAD_LENGTH);
@@ -150,7 +155,7 @@ cudaError_t launch_join(int B, const int32_t *q_start, int T, int Hq, int d, con
                         const Parts &pre, const Parts &own, void *out, cudaStream_t st)
 {
     // a warp per head while there are warps to spare, else it looks up its token once
-    const int heads = (long)T * Hq <= 64l * device_sm_count() ? 1 : 4;
+    const int heads = (long)T * Hq <= 64l * device_sm_count() ? 1 : std::max(4, cdiv(Hq, 65535));
     const dim3 grid(cdiv(T, kJoinWarps), cdiv(Hq, heads)), block(32 * kJoinWarps);
     return d == 128 ? launch_pdl(join_kernel<E, 128>, grid, block, 0, st, B, q_start, T, Hq, heads, seqs, H, pre, own, (E *)out)
                     : launch_pdl(join_kernel<E, 64>, grid, block, 0, st, B, q_start, T, Hq, heads, seqs, H, pre, own, (E *)out);

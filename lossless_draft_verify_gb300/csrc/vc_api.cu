@@ -482,7 +482,7 @@ size_t paged_attn_ws(const vc_paged_cache *c, int T, int Hq, bool mass, bool kv8
 
 bool shared_ok(const vc_shared_prefix *s)
 {
-    return s->n >= 0 && (s->n == 0 || (s->seq_start && s->len));
+    return s->n >= 0 && (s->n == 0 || (s->seq_start && s->len && aligned(s->seq_start, 4) && aligned(s->len, 4)));
 }
 
 // the rows of both halves are numbered with 31 bits, as are the plan's entries
@@ -598,7 +598,8 @@ vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, c
     if (T > 0 && (!k_out || !v_out || k_out == v_out)) return VC_ERR_INVALID;
     if (!aligned(k_out, 16) || !aligned(v_out, 16)) return VC_ERR_INVALID;
     const vc_paged_cache c = paged8_base(cache);
-    if (!paged_supported(&c) || (int64_t)T * c.Hkv > (1 << 30)) return VC_ERR_UNSUPPORTED;
+    if (!paged_supported(&c) || (int64_t)T * c.Hkv > (1 << 30) || c.Hkv > (1 << 19))
+        return VC_ERR_UNSUPPORTED;
     if (T == 0) return VC_OK;
     return cuda_status(paged::read8(paged8_pool(cache), c.dt, c.d, q_start, ctx_len, T, k_out, v_out, stream));
 }
