@@ -223,3 +223,263 @@ def test_attention_of_rows_of_very_different_sizes(d, dtype):
     q = bt.randn(bt.T, 8, d)
     out = _attn(vc, bt, q, d ** -0.5)
     _compare(bt, q, out, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ns,cs", [([1, 1], [1500, 700]), ([3, 40], [1500, 700]), ([200], [900])])
+@pytest.mark.parametrize("scale,peak", [(0.0, 1.0), (0.3, 6.0), (1.0, 4.0)])
+def test_attention_scales(ns, cs, scale, peak, dtype):
+    """A scale of zero (the mean of what is visible) and peaked weights: the
+    running maximum moves by far more than a few powers of two."""
+    vc = lib()
+    bt = Batch8(ns, cs, 2, 128, 64, dtype, seed=9, spread=scale == 0.3)
+    q = bt.randn(bt.T, 8, 128, scale=peak)
+    out = _attn(vc, bt, q, scale)
+    _compare(bt, q, out, scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("d", [64, 128])
+def test_values_far_apart_in_size(d, dtype):
+    """The first keys carry values of 2^40 under weights of about 2^-60, the last
+    ones ordinary values under ordinary weights, and the other way round: what is
+    small beside the largest product is lost, nothing else."""
+    vc = lib()
+    for flip in (False, True):
+        bt = Batch8([1, 2], [300, 1000], 1, d, 16, dtype, seed=3)
+        q = bt.randn(bt.T, 4, d)
+        q[..., 0] = 8.0
+        for b in range(2):
+            L = bt.lens[b]
+            for i in range(L):
+                p, r = bt.table[b][i // 16], i % 16
+                old = (i < L // 2) != flip
+                bt.ks[p, :, r] = torch.tensor(120, dtype=torch.uint8).view(torch.float8_e8m0fnu)
+                bt.k8.view(torch.uint8)[p, :, r, 0] = 0xf0 if old else 0x00          # -128 and 0
+                bt.vs.view(torch.uint8)[p, :, r] = 127 + 40 if old else 122
+        # the values the bytes stand for
+        bt.k = paged8_ref.values(bt.k8, bt.ks.view(torch.uint8)).to(dtype).cuda()
+        bt.v = paged8_ref.values(bt.v8, bt.vs.view(torch.uint8)).to(dtype).cuda()
+        out = _attn(vc, bt, q, 5.0)
+        _compare(bt, q, out, 5.0)
+
+
+def test_attention_gives_the_bits_of_bf16_pages():
+    """Where both take the tensor-core kernel (more than 16 rows per kv head) the
+    expansion is exact: the same bits as pages that hold the values."""
+    vc = lib()
+    bt = Batch8([90, 33], [1300, 200], 2, 128, 32, BF, seed=3, spread=True)
+    q = bt.randn(bt.T, 8, 128)
+    a = _attn(vc, bt, q, 0.1)
+    cache = vc.PagedCache(bt.k, bt.v, bt.block_table)
+    ws = vc.Workspace(vc.vc_paged_attn_workspace_bytes(cache, bt.T, 8))
+    b = torch.full_like(q, 7.0)
+    vc.vc_paged_attn(q, cache, bt.q_start, bt.ctx, 0.1, b, ws)
+    assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ns,cs,Hq", [([1] * 3, [1300, 40, 200], 8), ([5, 1, 90], [1300, 40, 200], 8)])
+def test_attention_repeats_and_rides_in_a_graph(ns, cs, Hq, dtype):
+    """Two calls give the same bits; so does a captured call, on a side stream
+    with the eager call's workspace, also over new lengths and queries."""
+    vc = lib()
+    bt = Batch8(ns, cs, 2, 128, 32, dtype, seed=3)
+    cache = bt.cache8(vc)
+    q = bt.randn(bt.T, Hq, 128)
+    ws = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(cache, bt.T, Hq))
+    a = _attn(vc, bt, q, 0.1, cache, ws)
+    assert torch.equal(a, _attn(vc, bt, q, 0.1, cache, ws))
+    out, k, v = torch.zeros_like(q), *(torch.zeros(bt.T, 2, 128, dtype=dtype, device="cuda") for _ in "kv")
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=torch.cuda.Stream(), capture_error_mode="thread_local"):
+        vc.vc_paged8_attn(q, cache, bt.q_start, bt.ctx, 0.1, out, ws)
+        vc.vc_paged8_read(cache, bt.q_start, bt.ctx, k, v)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, a)
+    q.copy_(bt.randn(*q.shape))
+    n2 = [max(n - 2, 0) for n in ns]
+    bt.start = [0, n2[0], n2[0] + n2[1], sum(n2)]
+    bt.q_start.copy_(torch.tensor(bt.start, dtype=torch.int32))
+    bt.ctx.copy_(torch.tensor([1000, 41, 199], dtype=torch.int32))
+    out.fill_(7.0), k.fill_(7.0)
+    g.replay()
+    torch.cuda.synchronize()
+    bt.ns, bt.cs = n2, [1000, 41, 199]
+    bt.lens = [c + n for c, n in zip(bt.cs, n2)]
+    _compare(bt, q, out, 0.1, "replayed")
+    for b in range(3):
+        for h in range(2):
+            assert torch.equal(k[bt.start[b]:bt.start[b + 1], h].cpu().double(), bt.rows(bt.k, b, h)[bt.cs[b]:])
+    assert (k[sum(n2):] == 7).all() and vc.vc_poll_status(ws) == 0
+
+
+def test_two_graphs_share_a_workspace():
+    """Nothing of a call stays in the workspace: captured batches of other shapes
+    and kernels replay in turn on one."""
+    vc = lib()
+    jobs, need = [], 0
+    for ns, cs, Hq, dt in (([1, 1, 1], [3000, 77, 900], 8, BF), ([60, 200], [500, 40], 4, BF), ([7, 1], [600, 50], 4, F32)):
+        bt = Batch8(ns, cs, 2, 128, 32, dt, seed=len(jobs))
+        cache = bt.cache8(vc)
+        q = bt.randn(bt.T, Hq, 128)
+        need = max(need, vc.vc_paged8_attn_workspace_bytes(cache, bt.T, Hq))
+        jobs.append((bt, cache, q, torch.full_like(q, 7.0)))
+    ws = vc.Workspace(need)
+    graphs = []
+    for bt, cache, q, out in jobs:
+        _attn(vc, bt, q, 0.1, cache, ws)
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], capture_error_mode="thread_local"):
+            vc.vc_paged8_attn(q, cache, bt.q_start, bt.ctx, 0.1, out, ws)
+    for _ in range(2):
+        for (bt, cache, q, out), g in zip(jobs, graphs):
+            out.fill_(7.0)
+            g.replay()
+    torch.cuda.synchronize()
+    for bt, cache, q, out in jobs:
+        _compare(bt, q, out, 0.1)
+    assert vc.vc_poll_status(ws) == 0
+
+
+def test_two_calls_at_once_on_two_streams():
+    vc = lib()
+    jobs = []
+    for i in range(4):
+        bt = Batch8([1, 1] if i < 2 else [30, 1], [900 + i, 2000], 2, 128, 64, BF, seed=20 + i)
+        cache = bt.cache8(vc)
+        q = bt.randn(bt.T, 8, 128)
+        ws = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(cache, bt.T, 8))
+        jobs.append((bt, cache, q, torch.full_like(q, 7.0), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for bt, cache, q, out, ws, st in jobs:
+            vc.vc_paged8_attn(q, cache, bt.q_start, bt.ctx, 0.1, out, ws, stream=st)
+    torch.cuda.synchronize()
+    for bt, cache, q, out, ws, st in jobs:
+        _compare(bt, q, out, 0.1)
+
+
+@pytest.mark.parametrize("ns", [[9, 2], [2, 1]])
+def test_sixteen_byte_alignment_is_enough(ns):
+    vc = lib()
+    bt = Batch8(ns, [300, 77], 2, 64, 16, BF, seed=6)
+
+    def shifted(t):
+        n = 16 // t.element_size()
+        x = torch.zeros(t.numel() + n, dtype=torch.uint8 if t.element_size() == 1 else t.dtype, device="cuda")[n:]
+        return x.view(t.dtype).view(t.shape).copy_(t)
+    q = shifted(bt.randn(bt.T, 16, 64))
+    bt.k8, bt.v8, bt.ks, bt.vs = (shifted(t.view(torch.uint8)) for t in (bt.k8, bt.v8, bt.ks, bt.vs))
+    out = _attn(vc, bt, q, 0.2, out=shifted(torch.full_like(q, 7.0)))
+    _compare(bt, q, out, 0.2)
+    k, v = (shifted(torch.zeros(bt.T, 2, 64, dtype=BF, device="cuda")) for _ in "kv")
+    vc.vc_paged8_read(bt.cache8(vc), bt.q_start, bt.ctx, k, v)
+    assert torch.equal(v[:ns[0], 1].cpu().double(), bt.rows(bt.v, 0, 1)[300:])
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_pools_past_two_to_the_31_elements(dtype):
+    """Pages whose codes lie past 2^31 bytes: every operator gives what it gives
+    on a small pool, bit for bit."""
+    vc = lib()
+    Hkv, page, d = 4, 256, 128
+    for ns in ([1, 1], [40, 3]):
+        small = Batch8(ns, [600, 255], Hkv, d, page, dtype, seed=7, width=4)
+        n_big = 2 ** 31 // (Hkv * page * d) + 20
+        shift = n_big - small.n_pages
+        table = torch.where(small.block_table >= 0, small.block_table + shift, small.block_table)
+        big = [torch.zeros((n_big,) + t.shape[1:], dtype=torch.uint8, device="cuda") for t in (small.k8, small.v8, small.ks, small.vs)]
+        for x, t in zip(big, (small.k8, small.v8, small.ks, small.vs)):
+            x[shift:] = t.view(torch.uint8)
+        q = small.randn(small.T, 16, d)
+        qkv = small.randn(small.T, (16 + 2 * Hkv) * d)
+        got = []
+        for cache in (small.cache8(vc), vc.Paged8Cache(*big, table, dtype)):
+            ws = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(cache, small.T, 16))
+            out, qo = torch.empty_like(q), torch.empty_like(q)
+            k, v = (torch.empty(small.T, Hkv, d, dtype=dtype, device="cuda") for _ in "kv")
+            vc.vc_paged8_append(qkv, cache, small.q_start, small.ctx, qo, vc.vc_rope_init(d, 1e4))
+            vc.vc_paged8_attn(q, cache, small.q_start, small.ctx, 0.1, out, ws)
+            vc.vc_paged8_read(cache, small.q_start, small.ctx, k, v)
+            torch.cuda.synchronize()
+            assert int(cache.status) == 0 and vc.vc_poll_status(ws) == 0
+            got.append((out, qo, k, v))
+        for a, b in zip(*got):
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ns", [[4, 6, 2, 3], [1, 1, 1, 1], [40, 60, 20, 30]])
+def test_what_does_not_fit_is_reported_and_left_alone(ns, dtype):
+    """Bad page numbers and lengths: the status word says so, nothing outside the
+    pool is touched and the other sequences' results stand."""
+    vc = lib()
+    bt = Batch8(ns, [100, 333, 40, 64], 2, 128, 32, dtype, seed=5)
+    q = bt.randn(bt.T, 4, 128)
+    cache = bt.cache8(vc)
+    ws = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(cache, bt.T, 4))
+    bt.block_table[1, 3], bt.block_table[1, 5] = bt.n_pages, -7
+    bt.ctx[2] = cache.slots                                  # more than the table holds
+    out = torch.full_like(q, 7.0)
+    k, v = (torch.full((bt.T, 2, 128), 7.0, dtype=dtype, device="cuda") for _ in "kv")
+
+    def call():
+        cache.status.zero_()
+        out.fill_(7.0)
+        vc.vc_paged8_attn(q, cache, bt.q_start, bt.ctx, 0.1, out, ws)
+        torch.cuda.synchronize()
+        assert vc.vc_poll_status(ws) == 0
+        return int(cache.status)
+    assert call() == vc.VC_PAGED_BAD_PAGE | vc.VC_PAGED_BAD_LENGTH
+    want, tol, _, _ = paged_ref.attn(bt, q, 0.1)
+    for b in (0, 3):
+        r = slice(bt.start[b], bt.start[b + 1])
+        close(out[r], want[r], tol[r], f"sequence {b}")
+    assert (out[bt.start[2]:bt.start[3]] == 7.0).all()
+    cache.status.zero_()
+    bt.block_table[0, 3] = bt.n_pages + 5                    # slots 96 on: the chunk's first page
+    vc.vc_paged8_read(cache, bt.q_start, bt.ctx, k, v)
+    torch.cuda.synchronize()
+    assert int(cache.status) == vc.VC_PAGED_BAD_PAGE | vc.VC_PAGED_BAD_LENGTH
+    assert (k[0] == 7).all() and (v[0] == 7).all() and (k[bt.start[2]:bt.start[3]] == 7).all()
+    assert torch.equal(k[bt.start[3]:, 1].cpu().double(), bt.rows(bt.k, 3, 1)[64:])
+    kept = bt.k8.view(torch.uint8).clone()
+    cache.status.zero_()
+    vc.vc_paged8_append(bt.randn(bt.T, 8 * 128), cache, bt.q_start, bt.ctx, torch.empty_like(q), vc.vc_rope_init(128, 1e4))
+    torch.cuda.synchronize()
+    assert int(cache.status) == vc.VC_PAGED_BAD_PAGE | vc.VC_PAGED_BAD_LENGTH
+    mine = {bt.table[b][s // 32] for b in (0, 1, 3) for s in range(bt.cs[b], bt.lens[b])} - {bt.table[0][3]}
+    for p in set(range(bt.n_pages)) - mine:
+        assert torch.equal(bt.k8.view(torch.uint8)[p], kept[p])
+    bt.q_start[4] = bt.T + 1                                 # the last sequence leaves the packed rows
+    assert call() & vc.VC_PAGED_BAD_LENGTH and (out[bt.start[3]:] == 7.0).all()
+
+
+def test_empty_batches():
+    vc = lib()
+    bt = Batch8([0, 0], [30, 0], 2, 64, 16, BF)
+    cache = bt.cache8(vc)
+    q, k = torch.zeros(0, 4, 64, dtype=BF, device="cuda"), torch.zeros(0, 2, 64, dtype=BF, device="cuda")
+    ws = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(cache, 0, 4))
+    vc.vc_paged8_attn(q, cache, bt.q_start, bt.ctx, 0.1, q.clone(), ws)
+    vc.vc_paged8_read(cache, bt.q_start, bt.ctx, k, k.clone())
+    vc.vc_paged8_append(torch.zeros(0, 8 * 64, dtype=BF, device="cuda"), cache, bt.q_start, bt.ctx, q, vc.vc_rope_init(64, 1e4))
+    bt = Batch8([0, 0], [30, 0], 2, 64, 16, BF, tail_rows=3)  # rows of no sequence only
+    q = bt.randn(3, 4, 64)
+    out = _attn(vc, bt, q, 0.1)
+    assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_table_much_wider_than_its_sequences_and_many_sequences(dtype):
+    """Few rows, 700 sequences, a table of 5000 pages: the results of a narrow one."""
+    vc = lib()
+    bt = Batch8([1] * 700, [(13 * i) % 90 for i in range(700)], 1, 64, 16, dtype, seed=1)
+    q = bt.randn(bt.T, 4, 64)
+    out = _attn(vc, bt, q, 0.125)
+    _compare(bt, q, out, 0.125)
+    wide = torch.full((700, 5000), -1, dtype=torch.int32, device="cuda")
+    wide[:, :bt.width] = bt.block_table
+    assert torch.equal(out, _attn(vc, bt, q, 0.125, bt.cache8(vc, wide)))
