@@ -156,7 +156,17 @@ append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)
         // the angle in turns, as a signed 64-bit fraction
         const int64_t f = (int64_t)((uint64_t)(int64_t)s_pos[t] * rope.turn[j]);
         float sn, cs;
-        sincospif((float)f * 0x1p-63f, &sn, &cs);
+        const float near = (float)f;
+        sincospif(near * 0x1p-63f, &sn, &cs);
+        if constexpr (KV8) {
+            // what the angle's rounding left out, a first-order step: a value whose last
+            // bit is off is another code where it lies between two (f rounds to at most
+            // 2^63, and the difference's bits are those of the exact one)
+            const int64_t left = (int64_t)((uint64_t)f - (uint64_t)(near >= 0x1p63f ? INT64_MIN : (int64_t)near));
+            const float step = (float)left * (float)(3.14159265358979323846 * 0x1p-63), s0 = sn;
+            sn = fmaf(step, cs, sn);
+            cs = fmaf(-step, s0, cs);
+        }
         s_cos[t][j / 8 * 12 + j % 8] = cs;
         s_sin[t][j / 8 * 12 + j % 8] = sn;
     }

@@ -29,8 +29,9 @@
 // kernel's 8 us per unit are too many.
 //
 // fp32 rows over 8-bit pages take the same products: the codes are exact operands, and
-// q and the weights are two f16 terms each, 22 bits, for twice the products (the CUDA
-// cores take 583 us for four chunks of 300 over 2000, 16/4 heads of 128, and 169 for a
+// q and the weights are two f16 terms each, 22 bits, for twice the products.  The unit
+// does not round its running sums to nearest, so each product of 16 is added to them
+// outside it.  (The CUDA cores take 583 us for four chunks of 300 over 2000, 16/4 heads of 128, and 169 for a
 // token of 8 sequences over 4000, 32/8 heads).
 //
 // Ranges.  q is scaled by its row's largest exponent to 2^14 (beside the roundings to
@@ -383,9 +384,16 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
                             for (int x = 0; x < NB; ++x) {
                                 if (e == 0) acc[x][y][c][0] = acc[x][y][c][1] = acc[x][y][c][2] = acc[x][y][c][3] = 0.f;
+                                if constexpr (F32) {
+                                    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                                for (int k = 0; k < TERMS; ++k)
-                                    mma(acc[x][y][c], a, b[x][4 * c + e][k][0], b[x][4 * c + e][k][1]);
+                                    for (int k = TERMS - 1; k >= 0; --k)
+                                        mma(part, a, b[x][4 * c + e][k][0], b[x][4 * c + e][k][1]);
+#pragma unroll
+                                    for (int i = 0; i < 4; ++i) acc[x][y][c][i] += part[i];
+                                } else {
+                                    mma(acc[x][y][c], a, b[x][4 * c + e][0][0], b[x][4 * c + e][0][1]);
+                                }
                             }
                         }
                 }
@@ -534,8 +542,15 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         const uint32_t a[4] = {half2_of(c), half2_of(c >> 16), half2_of(z), half2_of(z >> 16)};
 #pragma unroll
                         for (int x = 0; x < NB; ++x)
+                            if constexpr (F32) {
+                                float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                            for (int k = 0; k < TERMS; ++k) mma(o[x][t], a, w[x][2 * y][k], w[x][2 * y + 1][k]);
+                                for (int k = TERMS - 1; k >= 0; --k) mma(part, a, w[x][2 * y][k], w[x][2 * y + 1][k]);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) o[x][t][i] += part[i];
+                            } else {
+                                mma(o[x][t], a, w[x][2 * y][0], w[x][2 * y + 1][0]);
+                            }
                     }
                 }
             }
