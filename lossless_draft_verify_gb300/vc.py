@@ -827,11 +827,13 @@ class PagedCache:
 
     def _check(self, *tensors):
         """Contiguous tensors on the pool's device, which is the current one."""
-        if self._index is not None and self._index != torch._C._cuda_getDevice():
+        here = self._index
+        if here is None:
+            here = -1                                # the CPU's number
+        elif here != torch._C._cuda_getDevice():
             raise ValueError(f"the pool is on {self.device}, the current device is {torch.cuda.current_device()}")
-        device = self.device
         for t in tensors:
-            if t is not None and (t.device != device or not t.is_contiguous()):
+            if t is not None and (t.get_device() != here or not t.is_contiguous()):
                 raise ValueError("tensors must be contiguous and on the pool's device")
 
     def _on_gpu(self):
@@ -902,16 +904,20 @@ def _paged_append(name, qkv, cache, q_start, ctx_len, q_out, rope, positions, q_
     cache._check_batch(q_start, ctx_len)
     if d != cache.d or qkv.numel() != T * (Hq + 2 * cache.Hkv) * d:
         raise ValueError(f"qkv {tuple(qkv.shape)} and q_out {tuple(q_out.shape)} do not fit {cache.Hkv} kv heads")
-    if (qkv.dtype != dtype or q_out.dtype != dtype
-            or (q_gain is not None and (q_gain.dtype != dtype or q_gain.numel() != d))
-            or (k_gain is not None and (k_gain.dtype != dtype or k_gain.numel() != d))):
-        raise TypeError("qkv, q_out and the gains have the cache's dtype, the gains d entries")
+    if qkv.dtype != dtype or q_out.dtype != dtype:
+        raise TypeError("qkv and q_out have the cache's dtype")
+    for t in (q_gain, k_gain):
+        if t is not None and (t.dtype != dtype or t.numel() != d):
+            raise TypeError("the gains have the cache's dtype and d entries")
     if positions is not None and (positions.dtype != torch.int32 or positions.shape != (T,)):
         raise TypeError("positions is int32 [T]")
     cache._on_gpu()
-    _check(getattr(load(), name)(qkv.data_ptr(), _ptr(q_gain), _ptr(k_gain), float(eps), ctypes.byref(rope),
-                                 _ptr(positions), q_start.data_ptr(), ctx_len.data_ptr(), T, Hq, cache.ref,
-                                 q_out.data_ptr(), cache._stream(stream)), name)
+    rc = getattr(_lib or load(), name)(qkv.data_ptr(), None if q_gain is None else q_gain.data_ptr(),
+                                       None if k_gain is None else k_gain.data_ptr(), float(eps), rope,
+                                       None if positions is None else positions.data_ptr(), q_start.data_ptr(),
+                                       ctx_len.data_ptr(), T, Hq, cache.ref, q_out.data_ptr(), cache._stream(stream))
+    if rc:
+        raise VcError(rc, name)
 
 
 def vc_paged_append(qkv, cache: PagedCache, q_start, ctx_len, q_out, rope: Rope, positions=None, q_gain=None,
@@ -936,13 +942,16 @@ def vc_paged8_read(cache: Paged8Cache, q_start, ctx_len, k_out, v_out, stream=No
     _is8(cache, True)
     cache._check(q_start, ctx_len, k_out, v_out)
     cache._check_batch(q_start, ctx_len)
-    if k_out.dim() != 3 or k_out.shape != v_out.shape or k_out.shape[1:] != (cache.Hkv, cache.d):
+    shape = k_out.shape
+    if len(shape) != 3 or shape != v_out.shape or shape[1] != cache.Hkv or shape[2] != cache.d:
         raise ValueError(f"k_out and v_out [T][{cache.Hkv}][{cache.d}] expected")
     if k_out.dtype != cache.dtype or v_out.dtype != cache.dtype:
         raise TypeError("k_out and v_out have the cache's dtype")
     cache._on_gpu()
-    _check(load().vc_paged8_read(cache.ref, q_start.data_ptr(), ctx_len.data_ptr(), k_out.shape[0], k_out.data_ptr(),
-                                 v_out.data_ptr(), cache._stream(stream)), "vc_paged8_read")
+    rc = (_lib or load()).vc_paged8_read(cache.ref, q_start.data_ptr(), ctx_len.data_ptr(), shape[0], k_out.data_ptr(),
+                                         v_out.data_ptr(), cache._stream(stream))
+    if rc:
+        raise VcError(rc, "vc_paged8_read")
 
 
 def vc_paged_attn_workspace_bytes(cache: PagedCache, T: int, Hq: int) -> int:
