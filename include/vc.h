@@ -902,7 +902,9 @@ vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_
  * prefix) or not there.  A prefix's remaining tokens and all others are read
  * through each sequence's own table.  Sequences of no group attend on their own.
  * The results are vc_paged_attn's up to the order of sums, each row's two
- * halves being joined in fp32 before the one rounding to dt.
+ * halves being joined in fp32 before the one rounding to dt.  The workspace holds
+ * both halves of every row: 8 (d + 3) bytes per row and query head, beside
+ * vc_paged_attn's.
  * seq_start (device int32 [n + 1], ascending), len (device int32 [n]); with n = 0
  * both may be NULL.  VC_PAGED_BAD_LENGTH also reports a range outside [0, B] or
  * descending or a length outside [0, max_blocks * page] (its sequences attend on
@@ -970,8 +972,15 @@ vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, c
 
 /*
  * vc_paged8_attn, vc_paged8_attn_shared -- vc_paged_attn and vc_paged_attn_shared
- * over 8-bit pages, as on pages that hold the values: a scale is a power of two, so
- * the codes are expanded exactly, to bf16 for the tensor cores (dt bf16) or to fp32.
+ * over 8-bit pages, as on pages that hold the values: codes and scales enter the
+ * products exactly, whatever the scales.  bf16 rows: the softmax weights are rounded
+ * to bf16, in batches of at most 16 rows T * Hq / Hkv / B to f16 instead, placed by
+ * their row's largest weighted value (a weight below 2^-31 of that is lost); there q
+ * is exact down to 2^-39 of its row's largest element.  fp32 rows: q and the weights
+ * as two f16 terms, 22 bits, sums in fp32.
+ * Batches of at least 4096 rows T * Hq / Hkv / B (bf16) hold their pages as bf16
+ * in the workspace, 4 d bytes per table slot and kv head, where that is 1 GiB at most.
+ * The order of a row's sums depends on the lengths of the whole batch.
  */
 size_t vc_paged8_attn_workspace_bytes(const vc_paged8_cache *cache, int T, int Hq);
 vc_status vc_paged8_attn(const void *q, const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len,

@@ -600,7 +600,9 @@ cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t
 cudaError_t attn_shared(const Pool &P, vc_dtype dt, int d, const void *q, const Groups &G, const int32_t *q_start,
                         const int32_t *ctx_len, int T, int Hq, float sm_scale, void *out, void *ws, cudaStream_t st);
 
-// paged8_read.cu
+// paged8_read.cu: rows back; the batch's pages as bf16 pages [B][max_blocks] with their table
+cudaError_t expand8(const Pool &P, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k_out,
+                    void *v_out, int32_t *table_out, cudaStream_t st);
 cudaError_t read8(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k_out,
                   void *v_out, cudaStream_t st);
 

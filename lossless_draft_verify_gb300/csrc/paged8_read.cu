@@ -99,6 +99,45 @@ read8_kernel(Pool P, const int32_t *__restrict__ q_start, const int32_t *__restr
     }
 }
 
+// The pages of a batch as bf16 pages of their own, in the order of its table, and
+// the table that names them (a bad page number stays one).  A head's rows of a page are
+// one run of codes, and of values; blockIdx.y: the head.  Every thread looks its
+// pages up itself: no barrier, so that one page's look-ups pass under another's copy.
+__global__ void __launch_bounds__(kThreads)
+expand8_kernel(Pool P, const int32_t *__restrict__ q_start, const int32_t *__restrict__ ctx_len, int T, int d_log2,
+               uint4 *__restrict__ k_out, uint4 *__restrict__ v_out, int32_t *__restrict__ table_out)
+{
+    pdl_wait();
+    pdl_trigger();
+    const int blocks = P.B * P.max_blocks, chunks = (P.page() << d_log2) / 8, h = blockIdx.y;      // of 8 codes
+    for (int i = blockIdx.x; i < blocks; i += gridDim.x) {
+        const int b = i / P.max_blocks, blk = i % P.max_blocks;
+        const int len = load_seq(P, q_start, ctx_len, T, b).len();
+        const int page = ((long)blk << P.page_log2) < len ? P.page_of(b, blk) : -1;
+        if (h == 0 && threadIdx.x == 0) table_out[i] = page >= 0 ? i : -1;
+        if (page < 0) continue;
+        const size_t row0 = P.row(page, h, 0), to = ((size_t)i * P.Hkv + h) * chunks;
+#pragma unroll 4
+        for (int c = threadIdx.x; c < chunks; c += kThreads) {
+            const size_t row = row0 + (c * 8 >> d_log2), at = (row0 << d_log2) + (size_t)c * 8;
+            auto expand = [&](const void *codes, const uint8_t *scales) {
+                const uint2 w = *reinterpret_cast<const uint2 *>((const uint8_t *)codes + at);
+                const float s = scale_of(scales[row]);
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = decode2((j < 2 ? w.x : w.y) >> (j % 2 * 16));
+                    const __nv_bfloat162 p = __floats2bfloat162_rn(f.x * s, f.y * s);
+                    o[j] = *reinterpret_cast<const uint32_t *>(&p);
+                }
+                return make_uint4(o[0], o[1], o[2], o[3]);
+            };
+            k_out[to + c] = expand(P.k, P.k_scale);
+            v_out[to + c] = expand(P.v, P.v_scale);
+        }
+    }
+}
+
 template <typename E>
 cudaError_t launch(const Pool &P, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k, void *v,
                    cudaStream_t st)
@@ -109,6 +148,15 @@ cudaError_t launch(const Pool &P, int d, const int32_t *q_start, const int32_t *
 }
 
 }  // namespace
+
+cudaError_t expand8(const Pool &P, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k_out,
+                    void *v_out, int32_t *table_out, cudaStream_t st)
+{
+    // eight CTAs per SM over the heads (at most 2^30 / 64 / 512 heads of a workspace's pages)
+    const int each = std::max(1, std::min(P.B * P.max_blocks, 8 * device_sm_count() / P.Hkv));
+    return launch_pdl(expand8_kernel, dim3(each, P.Hkv), dim3(kThreads), 0, st, P, q_start, ctx_len, T,
+                      d == 128 ? 7 : 6, (uint4 *)k_out, (uint4 *)v_out, table_out);
+}
 
 cudaError_t read8(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, const int32_t *ctx_len, int T, void *k_out,
                   void *v_out, cudaStream_t st)

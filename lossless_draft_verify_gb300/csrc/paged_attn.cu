@@ -223,12 +223,14 @@ sum_kernel(Pool P, WorkDim W, const float *__restrict__ s_in, long s_stride, flo
 }
 
 struct WsLayout {
-    size_t desc, ml, o, rows, stored, bytes;
+    size_t desc, ml, o, rows, stored, k, v, table, bytes;
+    bool expand;               // 8-bit pages: taken as bf16 pages at k, v
     int rows_cap, n_cta;
     long s_stride;             // stored products of a row; 0: not stored
 };
 
-// [status | desc | partial (m, l) | partial o | lse of every row | stored scores]
+// [status | desc | partial (m, l) | partial o | lse of every row | stored scores |
+//  expanded K | V | table]
 // The scores of a bf16 batch are stored, for the mass, where it has 16 rows per
 // sequence and kv head at most on average.  Stored and with a second pass over
 // K, 32/8 heads: one token of 16 sequences over 32768 372 and 507 us, four over
@@ -238,6 +240,13 @@ struct WsLayout {
 // table slots) the memory is saved at the price of the second pass: full tables at
 // the bound 5.39 ms, just past it 7.34 ms.
 constexpr size_t kStoredMost = size_t(1) << 30;
+// 8-bit pages that many row tiles read (rows per sequence and kv head, on average)
+// are expanded to bf16 pages once instead of by each tile, where those, again by the
+// table, take no more memory than that.  Chunks over 30000 tokens, 32/8 heads, by each
+// tile and once: heads of 128, 512 tokens (2048 rows) 243 and 242 us, 1024 467 and 418,
+// 2048 915 and 766; heads of 64, 188 and 199, 362 and 357, 704 and 674.
+constexpr long kExpandRows = 4096;
+constexpr size_t kExpandMost = size_t(1) << 30;
 
 // A batch over 8-bit pages whose rows are few, or fp32, takes a kernel of its own.
 // The rows of its units, 8 or 16; 0: the batch does not.
@@ -264,7 +273,12 @@ WsLayout layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, bool 
     w.s_stride = (cap + kTcKeys - 1) / kTcKeys * kTcKeys;
     if (!with_rows || dt != VC_BF16 || (long)T * G > 16l * B || (size_t)T * Hq * w.s_stride * sizeof(float) > kStoredMost)
         w.s_stride = 0;
-    w.bytes = w.stored + align256((size_t)T * Hq * w.s_stride * sizeof(float));
+    w.k = w.stored + align256((size_t)T * Hq * w.s_stride * sizeof(float));
+    const size_t pages = (size_t)B * cap * (Hq / G) * d * 2;             // bytes of K or V
+    w.expand = kv8 && !planned && !few && (long)T * G >= kExpandRows * B && 2 * pages <= kExpandMost && Hq / G <= 65535;
+    w.v = w.k + (w.expand ? align256(pages) : 0);
+    w.table = w.v + (w.expand ? align256(pages) : 0);
+    w.bytes = w.table + (w.expand ? align256((size_t)B * (cap / 16) * sizeof(int32_t)) : 0);      // pages of 16 at least
     return w;
 }
 
@@ -313,7 +327,16 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     const int few = few_unit(dt, W.T, W.G, P.B, P.k_scale);
     if (few) e = attn8_few(P, W, dt, d, few, q, Hq, sl2, out, parts, (int32_t *)ws, st);
     else if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, out, lse, parts, st);
-    else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, parts, (int32_t *)ws, st);
+    else if (w.expand) {
+        Pool X = P;
+        X.k = ws + w.k;
+        X.v = ws + w.v;
+        X.k_scale = X.v_scale = nullptr;
+        X.table = (const int32_t *)(ws + w.table);
+        X.n_pages = P.B * P.max_blocks;
+        e = expand8(P, d, W.q_start, W.ctx_len, W.T, X.k, X.v, (int32_t *)(ws + w.table), st);
+        if (e == cudaSuccess) e = attn_tc(X, W, d, q, Hq, sl2, out, nullptr, nullptr, 0, parts, (int32_t *)ws, st);
+    } else if (P.k_scale) e = attn8_tc(P, W, d, q, Hq, sl2, out, parts, (int32_t *)ws, st);
     else e = attn_tc(P, W, d, q, Hq, sl2, out, lse, stored, w.s_stride, parts, (int32_t *)ws, st);
     if (e == cudaSuccess && (few ? may_cut_few(cap, d, true) : may_cut<T>(cap)))
         e = few ? merge_many<T>(parts, w.n_cta, d, W.G, Hq, out, st)

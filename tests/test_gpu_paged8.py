@@ -483,3 +483,29 @@ def test_a_table_much_wider_than_its_sequences_and_many_sequences(dtype):
     wide = torch.full((700, 5000), -1, dtype=torch.int32, device="cuda")
     wide[:, :bt.width] = bt.block_table
     assert torch.equal(out, _attn(vc, bt, q, 0.125, bt.cache8(vc, wide)))
+
+
+@pytest.mark.parametrize("ns,cs,Hq,Hkv,d,page", [([1100], [300], 8, 2, 128, 16), ([1030], [0], 8, 2, 64, 256),
+                                                 ([1500, 600], [77, 1], 8, 2, 64, 32)])
+def test_attention_of_many_rows(ns, cs, Hq, Hkv, d, page):
+    """From 4096 rows per sequence and kv head on the pages are expanded first:
+    the bits of bf16 pages, bad pages and padded rows as everywhere."""
+    vc = lib()
+    bt = Batch8(ns, cs, Hkv, d, page, BF, seed=5, spread=True, head_rows=1, tail_rows=2, width=2)
+    q = bt.randn(bt.T, Hq, d)
+    cache = bt.cache8(vc)
+    ws = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(cache, bt.T, Hq))
+    assert ws.nbytes >= 4 * bt.B * cache.slots * Hkv * d
+    out = _attn(vc, bt, q, 0.1, cache, ws)
+    _compare(bt, q, out, 0.1)
+    full = vc.PagedCache(bt.k, bt.v, bt.block_table)
+    other = torch.full_like(q, 7.0)
+    vc.vc_paged_attn(q, full, bt.q_start, bt.ctx, 0.1, other,
+                     vc.Workspace(vc.vc_paged_attn_workspace_bytes(full, bt.T, Hq)))
+    assert torch.equal(out, other)
+    bt.block_table[0, 2] = bt.n_pages
+    vc.vc_paged8_attn(q, cache, bt.q_start, bt.ctx, 0.1, out, ws)
+    torch.cuda.synchronize()
+    assert int(cache.status) == vc.VC_PAGED_BAD_PAGE and vc.vc_poll_status(ws) == 0
+    if len(ns) > 1:
+        assert torch.equal(out[bt.start[1]:], other[bt.start[1]:])

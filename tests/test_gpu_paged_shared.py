@@ -325,3 +325,36 @@ def test_a_server_run():
     step([5, 9, 1], True)
     step([1, 1, 1], True)
     step([30, 1, 17], True)
+
+
+def test_programmatic_launch_changes_no_result():
+    """VC_PDL=0 (a process of its own) gives the same bits: no kernel of the chain
+    starts on something that an earlier one has not finished."""
+    import hashlib
+    import os
+    import subprocess
+    import sys
+    code = """
+import sys, hashlib, torch
+sys.path[:0] = [%r, %r]
+import test_gpu_paged_shared as t
+from helpers import lib
+vc, h = lib(), hashlib.sha256()
+for i, (dt, bits, ns) in enumerate(t.FORMS):
+    bt, sh, q = t._case(ns, [5, 0, 70, 200, 9, 31], [0, 3], [900, 260], 8, 2, 64, 16, dt, bits, seed=i)
+    cache = sh.cache(vc)
+    ws = None
+    for _ in range(20):
+        out, cache, ws = t._call(vc, sh, q, 0.1, cache, ws)
+    h.update(out.cpu().view(torch.uint8).numpy().tobytes())
+print(h.hexdigest())
+"""
+    here = os.path.dirname(os.path.abspath(__file__))
+    code = code % (os.path.dirname(here), here)
+    got = []
+    for pdl in ("1", "0"):
+        r = subprocess.run([sys.executable, "-c", code], env=dict(os.environ, VC_PDL=pdl), capture_output=True, text=True,
+                           timeout=300)
+        assert r.returncode == 0, r.stderr[-2000:]
+        got.append(r.stdout.strip().splitlines()[-1])
+    assert got[0] == got[1] and len(got[0]) == hashlib.sha256().digest_size * 2
