@@ -35,8 +35,8 @@
 // token of 8 sequences over 4000, 32/8 heads).
 //
 // Ranges.  q is scaled by its row's largest exponent to 2^14 (beside the roundings to
-// 11 or 22 bits, an element is off by at most 2^-39 of the row's largest).  The running maximum is raised when it has
-// grown by more than 2^8, as in the tensor-core kernel.  The weights p 2^f, which
+// 11 or 22 bits, an element is off by at most 2^-39 of the row's largest; rows below
+// 2^-112 are taken as of that size).  The running maximum is raised when it has grown by more than 2^8, as in the tensor-core kernel.  The weights p 2^f, which
 // become f16, are scaled by a power of two per row such that the largest so far lies
 // at 2^6: what is lost below f16's smallest number is 2^-31 of it per key.
 #pragma once
@@ -202,7 +202,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     int left = 0, at = 0, page = 0, page_next = 0;           // tiles to ask for; a lane's page numbers of 32 blocks
     const int what = lane & 3, block = lane >> 2 & (kBlocks - 1);      // K, V, K's scales, V's (or second boxes); of lanes that request
     uint32_t b[NB][KS][TERMS][2];
-    float qs[NB][2];                                         // log2 e times the scale, the row's own with it
+    float qs[NB][2], back[NB][2];                            // log2 e times the scale; back: what products are scaled with first
     float o[NB][MT][4], m[NB][2], l[NB][2], put[NB][2], level[NB][2];
     int kmax[NB][2], kall = 0, key0 = -1;
     for (;;) {
@@ -270,7 +270,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
 #pragma unroll
             for (int x = 0; x < NB; ++x) {
                 const bool on = 8 * x + g < it.rows;
-                float back = 1.f;
+                uint32_t ex = 127 + 14;                      // of the row's scale, 2^(ex - 141)
                 if constexpr (KV8) {
                     float w[KC][16];                         // this lane's channels of the row
                     const E *src = (const E *)A.q + (on ? row_of(it.tok0, 8 * x + g) * D : 0) + q4 * 16;
@@ -294,9 +294,8 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     }
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                     top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                    const uint32_t ex = min(max(__float_as_uint(top) >> 23, 27u), 253u);
+                    ex = min(max(__float_as_uint(top) >> 23, 15u), 253u);
                     const float inv = scale_of(254u - ex) * kQTop;
-                    back = scale_of(ex) / kQTop;
 #pragma unroll
                     for (int c = 0; c < KC; ++c)
 #pragma unroll
@@ -315,7 +314,11 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    qs[x][r] = fmaxf(KV8 ? A.sl2 * __shfl_sync(0xffffffffu, back, 8 * q4 + 4 * r) : A.sl2, 1e-38f);   // -inf * 0: NaN
+                    // a scale below one meets the products before the keys' scales do, one
+                    // above after them: nothing overflows that the product itself does not
+                    const int of = KV8 ? (int)__shfl_sync(0xffffffffu, ex, 8 * q4 + 4 * r) - 14 : 127;
+                    back[x][r] = scale_of(min(of, 127));
+                    qs[x][r] = fmaxf(A.sl2 * scale_of(max(of, 127)), 1e-38f);      // -inf * 0: NaN
                     const int R = 8 * x + 2 * q4 + r;
                     kmax[x][r] = R < it.rows ? it.last((row0 + R) / A.W.G) : -1;
                 }
@@ -346,7 +349,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 ks[j] = KV8 ? scale_of(sc[8 * j]) : 1.f;
                 vs[j] = !KV8 ? 1.f : g + 8 * j < live ? scale_of(sc[BN + 8 * j]) : 0.f;
             }
-            // ---- S^T = K Q^T; s[x][j][r]: key g + 8 j, row 2 q + r, less the scale of q ----
+            // ---- S^T = K Q^T; s[x][j][r]: key g + 8 j, row 2 q + r, less a scale of q above one ----
             // (a chain of products per block and chunk: one chain would wait for itself)
             float s[NB][2 * kBlocks][2], acc[NB][kBlocks][KC][4];
             if constexpr (!KV8) {
@@ -407,7 +410,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         float v = acc[x][y][0][e];
 #pragma unroll
                         for (int c = 1; c < KC; ++c) v += acc[x][y][c][e];
-                        s[x][2 * y + (e >> 1)][e & 1] = KV8 ? v * ks[2 * y + (e >> 1)] : v;
+                        s[x][2 * y + (e >> 1)][e & 1] = KV8 ? v * back[x][e & 1] * ks[2 * y + (e >> 1)] : v;
                     }
             if (key0 + BN - 1 > kall) {                      // some row does not see all keys
 #pragma unroll

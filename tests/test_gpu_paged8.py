@@ -264,6 +264,24 @@ def test_values_far_apart_in_size(d, dtype):
         _compare(bt, q, out, 5.0)
 
 
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ns,Hq", [([1, 2], 4), ([2, 1], 10), ([30, 9], 4)])
+@pytest.mark.parametrize("size", [112, 60, -60, -108])
+def test_large_keys_under_small_queries(size, ns, Hq, dtype):
+    """Keys of 2^size under queries of 2^-size, products of ordinary size; one query
+    row in three is 2^-40 of the others."""
+    vc = lib()
+    bt = Batch8(ns, [300, 77], 1, 128, 16, dtype, seed=4)
+    byte = bt.ks.view(torch.uint8)
+    byte[byte < 255] += torch.tensor(size, dtype=torch.int8, device="cuda").view(torch.uint8)
+    assert int(byte.min()) >= 10
+    bt.k = paged8_ref.values(bt.k8, byte).to(dtype).cuda()
+    q = bt.randn(bt.T, Hq, 128) * 2.0 ** -size
+    q[:, ::3] *= 2.0 ** -40 if size < 100 else 1.0
+    out = _attn(vc, bt, q, 0.1)
+    _compare(bt, q, out, 0.1)
+
+
 def test_attention_gives_the_bits_of_bf16_pages():
     """Where both take the tensor-core kernel (more than 16 rows per kv head) the
     expansion is exact: the same bits as pages that hold the values."""
