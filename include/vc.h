@@ -981,6 +981,7 @@ vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, c
  * Batches of at least 4096 rows T * Hq / Hkv / B (bf16) hold their pages as bf16
  * in the workspace, 4 d bytes per table slot and kv head, where that is 1 GiB at most.
  * The order of a row's sums depends on the lengths of the whole batch.
+ * A workspace for T rows (vc_paged_attn_shared's, too) is enough for fewer.
  */
 size_t vc_paged8_attn_workspace_bytes(const vc_paged8_cache *cache, int T, int Hq);
 vc_status vc_paged8_attn(const void *q, const vc_paged8_cache *cache, const int32_t *q_start, const int32_t *ctx_len,

@@ -411,14 +411,26 @@ cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void 
 
 }  // namespace
 
+// The kernels of few rows need more than those of a few more: what a batch of T rows
+// is asked for is enough for one of fewer rows, too.  (Of as many as take one kernel
+// the largest batch needs most.)
+template <typename F>
+size_t most_up_to(int T, int G, int B, F bytes)
+{
+    auto at = [&](long rows) { return bytes((int)std::min<long>(T, rows * B / G)); };
+    return std::max({bytes(T), at(8), at(16)});
+}
+
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass, bool kv8)
 {
-    return layout(dt, d, T, Hq / Hkv, Hq, B, cap, mass, kv8).bytes;
+    auto bytes = [&](int t) { return layout(dt, d, t, Hq / Hkv, Hq, B, cap, mass, kv8).bytes; };
+    return kv8 ? most_up_to(T, Hq / Hkv, B, bytes) : bytes(T);
 }
 
 size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups, bool kv8)
 {
-    return shared_layout(dt, d, T, Hq / Hkv, Hq, B, cap, n_groups, kv8).bytes;
+    return most_up_to(T, Hq / Hkv, B,
+                      [&](int t) { return shared_layout(dt, d, t, Hq / Hkv, Hq, B, cap, n_groups, kv8).bytes; });
 }
 
 cudaError_t attn(const Pool &P, vc_dtype dt, int d, const void *q, const int32_t *q_start, const int32_t *ctx_len,

@@ -63,6 +63,19 @@ def test_bad_caches_of_a_shared_prefix_are_refused(vc, kw, want):
     assert L.vc_paged_attn_shared_workspace_bytes(c, 1, 4, 4) == 0
 
 
+@pytest.mark.parametrize("dt", [0, 1])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("B,Hq", [(1, 2), (3, 14), (16, 8), (2, 256)])
+def test_a_workspace_is_enough_for_fewer_rows(vc, B, Hq, d, dt):
+    L = vc.load()
+    c, c8 = _cache(vc, B=B, d=d, dt=dt), _cache8(vc, B=B, d=d, dt=dt)
+    for size in (lambda T: L.vc_paged8_attn_workspace_bytes(c8, T, Hq),
+                 lambda T: L.vc_paged8_attn_shared_workspace_bytes(c8, 3, T, Hq),
+                 lambda T: L.vc_paged_attn_shared_workspace_bytes(c, 3, T, Hq)):
+        need = [size(T) for T in [*range(1, 200), 1000, 4000, 20000]]
+        assert need[0] > 0 and need == sorted(need)
+
+
 def test_bad_arguments_are_refused(vc):
     L = vc.load()
     c, c8, rope = _cache(vc), _cache8(vc), vc.vc_rope_init(128, 1e4)
