@@ -92,7 +92,8 @@ struct AppendParams {
 //
 // KV8: the pages hold 8-bit rows.  A key or value head's lanes find its largest
 // magnitude together (log2(D/16) exchanges more) and store 8 codes per chunk; the
-// first one stores the scale.
+// first one stores the scale.  4670 tokens on inputs not in L2 23.4 us for 105 MB, 66% of
+// the copy rate, bound as below; 16 tokens 3.7 in a graph.
 template <typename E, int D, int TPB, bool KV8>
 __global__ void __launch_bounds__(kThreads, 4)
 append_kernel(AppendParams A, const __grid_constant__ vc_rope rope)

@@ -37,7 +37,10 @@
 // producer brings tiles of codes and their scales into a ring of their own;
 // eight more warps (12-19) write them as bf16 tiles, scale included, into the
 // ring that the products read.  code * 2^e is a bf16 number, so this rounds
-// nothing: the output is that of bf16 pages which hold the same numbers.
+// nothing: the output is that of bf16 pages which hold the same numbers.  It serves
+// 17 to 4095 rows per sequence and kv head: nine tokens of 16 sequences over 16384 (36
+// rows) 216 us, 1024 over 30000 467; the expansion of a tile is what is added to the
+// chain (169 us and, of 2048 over 30000, 728 of 917 without its arithmetic).
 //
 // V rows past the sequence's end may hold any bits and 0 * NaN is not 0: those
 // that share the last page with tokens are cleared in shared memory, further
