@@ -565,7 +565,7 @@ cudaError_t attn8_few_planned(const Pool &P, const WorkDim &W, vc_dtype dt, int 
                               float sl2, const Halves &H, bool first, const Parts &parts, int32_t *status,
                               cudaStream_t st);
 cudaError_t attn_few_planned(const Pool &P, const WorkDim &W, int d, int rows, const void *q, int Hq, float sl2,
-                             const Halves &H, const Parts &parts, int32_t *status, cudaStream_t st);
+                             const Halves &H, bool first, const Parts &parts, int32_t *status, cudaStream_t st);
 
 // paged_attn8_tc.cu: both over 8-bit pages
 cudaError_t attn8_tc(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, void *out,

@@ -352,13 +352,23 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
     }
 }
 
-// [the attention's | that of the sequences' own slots, where the rows are few | plan |
+// [the attention's | that of the kernel of few rows, where it has a part | plan |
 // places, lse and o of both halves]
 struct SharedLayout {
     WsLayout attn, own;
-    int few;                   // rows of a unit of the sequences' own slots (fp32 over 8-bit pages: of all); 0: all goes one way
+    int few;                   // rows of a unit of the kernel of few rows; 0: it has no part
+    bool all;                  // it takes all, else the sequences' own slots
     size_t own_at, plan, place, lse, o, bytes;
 };
+
+// Where groups have at most this many rows per kv head, on average, the kernel of few rows
+// takes the prefixes too: a launch and units of 8 us less, a pass over the prefix more for
+// each 16 rows.  Through the tensor-core kernel and so, contexts of up to 300 after the
+// prefix, 32/8 heads of 128, bf16 and 8-bit pages: 4 sequences (16 rows) over 512 28, 22
+// and 14, 17 us, over 8192 34, 33 and 21, 20, over 32768 48, 50 and 40, 31; 8 over 512
+// 29, 30 and 16, 17, over 8192 34, 40 and 26, 23, over 32768 48, 49 and 57, 45; 16 over
+// 512 29, 31 and 17, 19, over 8192 35, 41 and 38, 34, over 32768 51, 52 and 99, 75.
+constexpr long kGroupRows = 32;
 
 SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, int n_groups, bool kv8)
 {
@@ -366,6 +376,8 @@ SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long
     const size_t rows = (size_t)2 * T * Hq;
     w.attn = layout(dt, d, T, G, Hq, B, cap, false, false, true);
     w.few = dt == VC_BF16 ? few_rows(T, G, B) : kv8 ? 16 : 0;
+    w.all = w.few && (dt == VC_F32 || n_groups == 0 || (long)T * G <= kGroupRows * n_groups);
+    if (w.all && dt == VC_BF16 && n_groups) w.few = (long)T * G <= 8l * n_groups ? 8 : 16;
     w.own_at = w.attn.bytes;
     w.own.bytes = 0;
     if (w.few) w.own = layout(dt, d, T, G, Hq, B, cap, false, true, false, w.few);
@@ -392,21 +404,23 @@ cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void 
     cudaError_t e = plan_shared(P, W.q_start, W.ctx_len, W.T, G, plan, st);
     if (e != cudaSuccess) return e;
     W.plan = plan;
-    W.n_plan = w.few && dt == VC_BF16 ? G.n : P.B + G.n;
-    if (dt == VC_F32 && P.k_scale)
-        e = attn8_few_planned(P, W, dt, d, w.few, q, Hq, sl2, H, true, own, status, st);
+    W.n_plan = w.few && !w.all ? G.n : P.B + G.n;
+    auto few = [&] {
+        return P.k_scale ? attn8_few_planned(P, W, dt, d, w.few, q, Hq, sl2, H, w.all, own, status, st)
+                         : attn_few_planned(P, W, d, w.few, q, Hq, sl2, H, w.all, own, status, st);
+    };
+    if (w.all) e = few();
     else if constexpr (std::is_same_v<T, float>) e = attn_simt(P, W, d, q, Hq, sl2, H.o, H.lse, parts, st, H.place);
     else if (P.k_scale) e = attn8_tc_planned(P, W, d, q, Hq, sl2, H, parts, status, st);
     else e = attn_tc_planned(P, W, d, q, Hq, sl2, H, parts, status, st);
-    if (e == cudaSuccess && w.few && dt == VC_BF16) {
+    if (e == cudaSuccess && w.few && !w.all) {
         // The kernel before took the prefixes; the sequences' own slots follow beside its end.
         W.plan = plan + G.n;
         W.n_plan = P.B;
-        e = P.k_scale ? attn8_few_planned(P, W, dt, d, w.few, q, Hq, sl2, H, false, own, status, st)
-                      : attn_few_planned(P, W, d, w.few, q, Hq, sl2, H, own, status, st);
+        e = few();
     }
     if (e != cudaSuccess) return e;
-    return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, H, dt == VC_F32 ? own : parts, own, out, st);
+    return join_shared(P, dt, d, W.q_start, W.T, Hq, plan + G.n, H, w.all ? own : parts, own, out, st);
 }
 
 }  // namespace
@@ -415,21 +429,21 @@ cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void 
 // is asked for is enough for one of fewer rows, too.  (Of as many as take one kernel
 // the largest batch needs most.)
 template <typename F>
-size_t most_up_to(int T, int G, int B, F bytes)
+size_t most_up_to(int T, int G, int B, int n_groups, F bytes)
 {
-    auto at = [&](long rows) { return bytes((int)std::min<long>(T, rows * B / G)); };
-    return std::max({bytes(T), at(8), at(16)});
+    auto at = [&](long rows) { return bytes((int)std::min<long>(T, rows / G)); };
+    return std::max({bytes(T), at(8l * B), at(16l * B), at(8l * n_groups), at(kGroupRows * n_groups)});
 }
 
 size_t attn_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, bool mass, bool kv8)
 {
     auto bytes = [&](int t) { return layout(dt, d, t, Hq / Hkv, Hq, B, cap, mass, kv8).bytes; };
-    return kv8 ? most_up_to(T, Hq / Hkv, B, bytes) : bytes(T);
+    return kv8 ? most_up_to(T, Hq / Hkv, B, 0, bytes) : bytes(T);
 }
 
 size_t attn_shared_ws_bytes(vc_dtype dt, int d, int T, int Hq, int Hkv, int B, long cap, int n_groups, bool kv8)
 {
-    return most_up_to(T, Hq / Hkv, B,
+    return most_up_to(T, Hq / Hkv, B, n_groups,
                       [&](int t) { return shared_layout(dt, d, t, Hq / Hkv, Hq, B, cap, n_groups, kv8).bytes; });
 }
 

@@ -27,7 +27,7 @@
 // bf16 pages (KV8 false) take the same products of bf16 operands: K through ldmatrix,
 // V through its transposing form, and nothing is scaled.  They serve the own slots of
 // sequences that share a prefix, a few hundred tokens each, for which the tensor-core
-// kernel's 8 us per unit are too many.
+// kernel's 8 us per unit are too many, and the prefixes of small groups.
 //
 // fp32 rows over 8-bit pages take the same products: the codes are exact operands, and
 // q and the weights are two f16 terms each, 22 bits, for twice the products.  The unit

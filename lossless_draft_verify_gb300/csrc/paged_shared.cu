@@ -14,8 +14,8 @@
 // without sharing (vc_paged_attn; most of its reads of a prefix hit L2), 32/8 heads of
 // 128: one token of 32 sequences, a prefix of 32768 and up to 700 tokens of their own
 // 59 and 428 us; 32 in two groups of up to 32000 over 8-bit pages 79 and 189; 24 chunks
-// up to 17 in three groups, 28/4 heads, 81 and 105; where a prefix is short the two
-// launches more cost more than it saves (4 sequences, 600 tokens: 21 and 18).
+// up to 17 in three groups, 28/4 heads, 81 and 105; four over 600 tokens 12.5 and 18,
+// over 8192 and up to 300 of their own 21 and 30.
 #include "paged.cuh"
 
 namespace vc {
@@ -78,20 +78,28 @@ plan_kernel(Pool P, const int32_t *__restrict__ q_start, const int32_t *__restri
     plan[v] = s;
 }
 
-// A warp per (row, some heads), lane l at channels 4 l (2 l) of each.  What it takes
-// are round trips to L2: eight parts are asked for at once, and the running sum is
-// rescaled by their maximum.
-constexpr int kJoinWarps = 4, kAtOnce = 8;
+// A row's parts by one warp, lane l at channels 4 l (2 l), or, where rows are few, by
+// all warps of a CTA.  What it takes are round trips to L2: a warp asks for
+// eight parts at once, and its running sum is rescaled by their maximum.
+// Four sequences over a prefix of 32768 in 8-bit pages, 230 parts of a row (128 rows): 44
+// us by a warp, 30 by eight; a decode step of 32 (1024 rows, 20 parts) 59 and 61.
+constexpr int kAtOnce = 8;
+constexpr long kSharedRows = 2;                              // per SM, at most: a CTA per row
 
-template <typename E, int D>
-__global__ void __launch_bounds__(32 * kJoinWarps)
+template <bool SHARED>
+constexpr int kJoinWarps = SHARED ? 8 : 4;
+
+template <typename E, int D, bool SHARED>
+__global__ void __launch_bounds__(32 * kJoinWarps<SHARED>)
 join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, int heads, const VSeq *__restrict__ seqs, Halves H,
             Parts pre, Parts own, E *__restrict__ out)
 {
+    constexpr int V = D / 32, W = kJoinWarps<SHARED>, STEP = SHARED ? W : 1;
+    __shared__ float s_acc[W][D];
+    __shared__ float2 s_ml[W];
     pdl_wait();
     pdl_trigger();
-    constexpr int V = D / 32;
-    const int lane = threadIdx.x & 31, tok = blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tok = SHARED ? blockIdx.x : blockIdx.x * W + warp;
     if (tok >= T) return;
     const int b = find_seq(q_start, B, tok);
     if (b < 0) return;
@@ -105,6 +113,8 @@ join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, int heads
         float M = kLowest, L = 0.f, acc[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.f;
+        // (a loop per half: with one over both a pass costs more than it saves, the
+        // decode step below 67 us)
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (x == 0 && s.base == 0) continue;
@@ -112,12 +122,12 @@ join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, int heads
             const size_t here = x * half + row;
             const int n = at[x].parts();
             // a row in the output is one part with a sum of one
-            for (int p0 = 0; p0 < max(n, 1); p0 += kAtOnce) {
+            for (int p0 = SHARED ? warp : 0; p0 < max(n, 1); p0 += kAtOnce * STEP) {
                 float2 ml[kAtOnce];
                 float y[kAtOnce][V];
 #pragma unroll
                 for (int k = 0; k < kAtOnce; ++k) {
-                    const int p = p0 + k;
+                    const int p = p0 + k * STEP;
                     ml[k] = make_float2(kLowest, 0.f);
 #pragma unroll
                     for (int e = 0; e < V; ++e) y[k][e] = 0.f;
@@ -150,22 +160,43 @@ join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, int heads
                 }
             }
         }
-        const float inv = 1.f / L;
-        E *dst = out + row * D + V * lane;
+        if constexpr (SHARED) {
 #pragma unroll
-        for (int e = 0; e < V; ++e) dst[e] = Elem<E>::from_f(acc[e] * inv);
+            for (int e = 0; e < V; ++e) s_acc[warp][V * lane + e] = acc[e];
+            if (lane == 0) s_ml[warp] = make_float2(M, L);
+            __syncthreads();
+            if (threadIdx.x < D) {
+                float x = 0.f;
+                M = kLowest, L = 0.f;
+                for (int k = 0; k < W; ++k) M = fmaxf(M, s_ml[k].x);
+                for (int k = 0; k < W; ++k) {
+                    const float w = exp2f(s_ml[k].x - M);
+                    L = fmaf(w, s_ml[k].y, L);
+                    x = fmaf(w, s_acc[k][threadIdx.x], x);
+                }
+                out[row * D + threadIdx.x] = Elem<E>::from_f(x / L);
+            }
+            __syncthreads();
+        } else {
+            const float inv = 1.f / L;
+            E *dst = out + row * D + V * lane;
+#pragma unroll
+            for (int e = 0; e < V; ++e) dst[e] = Elem<E>::from_f(acc[e] * inv);
+        }
     }
 }
 
-template <typename E>
-cudaError_t launch_join(int B, const int32_t *q_start, int T, int Hq, int d, const VSeq *seqs, const Halves &H,
+template <typename E, int D>
+cudaError_t launch_join(int B, const int32_t *q_start, int T, int Hq, const VSeq *seqs, const Halves &H,
                         const Parts &pre, const Parts &own, void *out, cudaStream_t st)
 {
+    const long rows = (long)T * Hq;
+    if (rows <= kSharedRows * device_sm_count())
+        return launch_pdl(join_kernel<E, D, true>, dim3(T, Hq), dim3(32 * kJoinWarps<true>), 0, st, B, q_start, T, Hq, 1, seqs, H, pre, own, (E *)out);
     // a warp per head while there are warps to spare, else it looks up its token once
-    const int heads = (long)T * Hq <= 64l * device_sm_count() ? 1 : std::max(4, cdiv(Hq, 65535));
-    const dim3 grid(cdiv(T, kJoinWarps), cdiv(Hq, heads)), block(32 * kJoinWarps);
-    return d == 128 ? launch_pdl(join_kernel<E, 128>, grid, block, 0, st, B, q_start, T, Hq, heads, seqs, H, pre, own, (E *)out)
-                    : launch_pdl(join_kernel<E, 64>, grid, block, 0, st, B, q_start, T, Hq, heads, seqs, H, pre, own, (E *)out);
+    const int heads = rows <= 64l * device_sm_count() ? 1 : std::max(4, cdiv(Hq, 65535));
+    return launch_pdl(join_kernel<E, D, false>, dim3(cdiv(T, kJoinWarps<false>), cdiv(Hq, heads)),
+                      dim3(32 * kJoinWarps<false>), 0, st, B, q_start, T, Hq, heads, seqs, H, pre, own, (E *)out);
 }
 
 }  // namespace
@@ -180,8 +211,12 @@ cudaError_t plan_shared(const Pool &P, const int32_t *q_start, const int32_t *ct
 cudaError_t join_shared(const Pool &P, vc_dtype dt, int d, const int32_t *q_start, int T, int Hq, const VSeq *seqs,
                         const Halves &H, const Parts &pre, const Parts &own, void *out, cudaStream_t st)
 {
-    return dt == VC_BF16 ? launch_join<__nv_bfloat16>(P.B, q_start, T, Hq, d, seqs, H, pre, own, out, st)
-                         : launch_join<float>(P.B, q_start, T, Hq, d, seqs, H, pre, own, out, st);
+    auto form = [&](auto elem) {
+        using E = decltype(elem);
+        return d == 128 ? launch_join<E, 128>(P.B, q_start, T, Hq, seqs, H, pre, own, out, st)
+                        : launch_join<E, 64>(P.B, q_start, T, Hq, seqs, H, pre, own, out, st);
+    };
+    return dt == VC_BF16 ? form(__nv_bfloat16{}) : form(0.f);
 }
 
 }  // namespace paged

@@ -21,8 +21,6 @@ class Shared:
     def __init__(self, bt, first, prefix, bits, apart=False):
         self.bt, self.bits = bt, bits
         self.first, self.prefix = list(first) + [bt.B], list(prefix)
-        if first and isinstance(first[-1], tuple):
-            raise ValueError
         i32 = dict(dtype=torch.int32, device=bt.device)
         table = [list(r) for r in bt.table]
         for g, n in enumerate(self.prefix):
@@ -103,6 +101,23 @@ def _case(ns, own, first, prefix, Hq, Hkv, d, page, dtype, bits, seed=0, **kw):
             cs[b] += n
     bt = Batch8(ns, cs, Hkv, d, page, dtype, seed=seed, **kw)
     return bt, Shared(bt, first, prefix, bits), bt.randn(bt.T, Hq, d, scale=1.5)
+
+
+@pytest.mark.parametrize("bits", [16, 8])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ns,own,first,prefix,Hq,Hkv,d,page", [
+    ([1] * 3, [5, 0, 90], [0], [9000], 8, 2, 128, 64),       # 12 rows, many parts of each
+    ([1, 2, 2], [0, 300, 7], [0], [5000], 12, 2, 64, 16),    # 30 rows
+    ([1] * 20, [11 * i for i in range(20)], [0, 10, 12, 14, 16], [1100, 40, 700, 16, 300], 8, 2, 128, 32),    # one group of 40
+    ([1] * 20, [3000] + [2] * 19, [0], [2000], 8, 2, 128, 64),     # 80 rows; an own context of many parts
+    ([1] * 5, [700, 1, 2, 3, 4], [], [], 8, 2, 64, 32)])     # no group
+def test_groups_of_few_rows(ns, own, first, prefix, Hq, Hkv, d, page, dtype, bits):
+    vc = lib()
+    bt, sh, q = _case(ns, own, first, prefix, Hq, Hkv, d, page, dtype, bits, seed=7)
+    out, cache, ws = _call(vc, sh, q, d ** -0.5)
+    assert vc.vc_poll_status(ws) == 0 and int(cache.status) == 0
+    _compare(bt, q, out, d ** -0.5)
+    assert torch.equal(out, _call(vc, sh, q, d ** -0.5, cache, ws)[0])
 
 
 FORMS = [(dt, bits, ns) for dt in (BF, F32) for bits in (16, 8) for ns in ([1] * 6, [17, 3, 30, 9, 1, 20])]
