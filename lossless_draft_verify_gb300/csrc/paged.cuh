@@ -204,6 +204,20 @@ struct Piece {
     long per;          // the length of a full piece
 };
 
+// With the entry that it begins in.
+template <typename S>
+struct PieceOf : Piece {
+    S s;
+};
+
+// a / b of numbers that are not negative: 64-bit division takes a hundred instructions.
+// For the kernel of few rows; the tensor-core kernel gains nothing from it, nor from the
+// entry found with the piece (a verify batch of nine chunks 384 us, with that 391).
+__host__ __device__ inline long quotient(long a, long b)
+{
+    return (unsigned long)(a | b) >> 32 == 0 ? (long)((unsigned)a / (unsigned)b) : a / b;
+}
+
 __host__ __device__ inline long piece_len(long total, int n_cta, int min_len)
 {
     return lmax((total + n_cta - 1) / n_cta, min_len);
@@ -265,7 +279,7 @@ struct Units : C {
     template <typename S>
     static __host__ __device__ __forceinline__ void place(const S &s, int G, long hc, long x, Piece &out)
     {
-        out.h = (int)(x / hc);
+        out.h = (int)(C::kByTiles ? quotient(x, hc) : x / hc);
         x -= out.h * hc;
         int mt = 0;
         if constexpr (C::kByTiles) {                         // past the row tiles of fewer tiles
@@ -274,8 +288,9 @@ struct Units : C {
                 const int n = upto(s, G, t, m, last);
                 const long c = (long)(n - mt) * (t + kUnitCost);
                 if (x < c) {
-                    mt += (int)(x / (t + kUnitCost));
-                    x %= t + kUnitCost;
+                    const int i = (int)quotient(x, t + kUnitCost);
+                    mt += i;
+                    x -= (long)i * (t + kUnitCost);
                     break;
                 }
                 x -= c;
@@ -301,9 +316,11 @@ struct Units : C {
 // the first 32 chunks of 32 sequences, one per lane, so that the second one,
 // which finds the sequence that holds the piece's beginning, can go straight to
 // its chunk.  One loop serves both: code that runs once is paid for in
-// instruction fetches.
+// instruction fetches.  A round trip saved here is one less of a small call's few: of
+// one token over 200 (8-bit pages) the kernel took 7 us, 2.1 of them here and 1.6 up to
+// the first request for keys.
 template <int BM, int BN, typename S = Seq, typename C = Cost<BM>>
-__device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int cta, int n_cta, Piece *out)
+__device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int cta, int n_cta, PieceOf<S> *out)
 {
     using U = Units<BM, BN, C>;
     using Src = Source<S>;
@@ -333,6 +350,7 @@ __device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int 
             if (here) {
                 U::place(s, W.G, hc, lo - start, *out);
                 out->b = 32 * c + lane;
+                out->s = s;
                 out->per = per;
                 out->len = hi - lo;
             }
@@ -343,13 +361,13 @@ __device__ __forceinline__ void find_piece(const Pool &P, const WorkDim &W, int 
         before += sum;
         if (++c < chunks) continue;
         if (lo >= 0) break;                          // not reached: lo lies below the total
-        per = piece_len(before, n_cta, U::kMinPiece);
+        per = C::kByTiles ? lmax(quotient(before + n_cta - 1, n_cta), U::kMinPiece) : piece_len(before, n_cta, U::kMinPiece);
         lo = per * cta;
         hi = lmin(before, lo + per);
         if (lo >= hi) break;
         c = __popc(__ballot_sync(0xffffffffu, lane < chunks && chunk <= lo));   // chunks that end at or before lo
         before = c ? __shfl_sync(0xffffffffu, chunk, c - 1) : 0;
-        next = fetch(c);
+        if (chunks > 1) next = fetch(c);
     }
     __syncwarp();
 }
@@ -410,6 +428,19 @@ struct Walk {
             m = U::mtiles(s, W.G);
         }
     }
+    __host__ __device__ __forceinline__ void start(const WorkDim &W, const PieceOf<S> &p)
+    {
+        b = p.b;
+        h = p.h;
+        mt = p.mt;
+        off = p.off;
+        left = p.len;
+        per = p.per;
+        if (left > 0) {
+            s = p.s;
+            m = U::mtiles(s, W.G);
+        }
+    }
     // The next part with at least one key tile; false at the piece's end.
     __host__ __device__ __forceinline__ bool next(const Pool &P, const WorkDim &W, ItemOf<S> &it)
     {
@@ -429,7 +460,10 @@ struct Walk {
             it.head = starts;
             it.whole = starts && ends;
             it.parts = 0;
-            if (starts && !ends) it.parts = 1 + (int)((cost - e + per - 1) / per);
+            if (starts && !ends) {
+                const long rest = cost - e + per - 1;
+                it.parts = 1 + (int)(C::kByTiles ? quotient(rest, per) : rest / per);
+            }
             left -= take;
             off = 0;
             if (++mt == m) {

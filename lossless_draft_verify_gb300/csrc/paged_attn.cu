@@ -140,19 +140,23 @@ merge_many_kernel(Parts parts, int n_piece, int G, int Hq, T *__restrict__ out)
 #pragma unroll
         for (int e = 0; e < V; ++e) o[e] = Elem<T>::from_f(acc[e] * inv);
     };
+    // units of few parts, and of many
+    const int n_parts = s_desc[lane % kManyWarps].parts;
+    unsigned few = __ballot_sync(0xffffffffu, lane < kManyWarps && n_parts > 0 && n_parts <= kFewParts);
+    unsigned many = __ballot_sync(0xffffffffu, lane < kManyWarps && n_parts > kFewParts);
     int turn = 0;
-    for (int i = 0; i < kManyWarps; ++i) {
+    for (; few; few &= few - 1) {
+        const int i = __ffs(few) - 1;
         const PartDesc d = s_desc[i];
-        if (d.parts == 0 || d.parts > kFewParts) continue;
         for (int r = 0; r < d.rows; ++r) {
             if (turn++ % kManyWarps != warp) continue;
             add(i, d.parts, r, 0, 1);
             store(d, r);
         }
     }
-    for (int i = 0; i < kManyWarps; ++i) {
+    for (; many; many &= many - 1) {
+        const int i = __ffs(many) - 1;
         const PartDesc d = s_desc[i];
-        if (d.parts <= kFewParts) continue;
         int share = kManyWarps;                              // warps per row
         while (share > 1 && d.rows * share > kManyWarps) share /= 2;
         const int sub = warp % share;

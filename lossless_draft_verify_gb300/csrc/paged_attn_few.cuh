@@ -76,7 +76,7 @@ template <int BM, int BN, int STAGES, typename SEQ>
 struct Warp {
     uint64_t full[STAGES];
     alignas(16) uint8_t scale[STAGES][2][BN];
-    Piece piece;
+    PieceOf<SEQ> piece;
     Walk<BM, BN, SEQ, CostFew> walk;
     ItemOf<SEQ> part[4];               // the parts asked for last; the arithmetic is STAGES tiles behind
     bool more;
@@ -176,6 +176,10 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     const int n_piece = gridDim.x * kWarps, me = warp * gridDim.x + blockIdx.x;
     // A planned batch's entries come from the kernel before the one before this, which
     // has waited for it; that one runs beside this kernel (see the end).
+    if (threadIdx.x == 0) {
+        tc::prefetch_tmap(&tmK);
+        tc::prefetch_tmap(&tmV);
+    }
     if (!PLANNED || A.first) pdl_wait();
     if (lane == 0) {
         A.parts.desc[me].parts = 0;
@@ -188,9 +192,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     if (!placed && lane == 0) report_timeout(A.status, 110); // never expected
     if (!PLANNED && (!placed || S.piece.len <= 0)) return;
     if (lane == 0) {
-        S.walk.start(A.P, A.W, S.piece);
-        tc::prefetch_tmap(&tmK);
-        tc::prefetch_tmap(&tmV);
+        S.walk.start(A.W, S.piece);
     }
 
     // One loop over the piece's tiles: requests first, then the arithmetic of the tile

@@ -69,7 +69,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
     using G = Geom<D, BM, BN>;
     extern __shared__ __align__(16) float smf[];
     float *sQ = smf, *sKV = sQ + BM * G::PQ, *sP = sKV + 2 * G::STAGE;
-    __shared__ Piece piece;
+    __shared__ PieceOf<SEQ> piece;
     pdl_wait();
     pdl_trigger();
     if (threadIdx.x < 32) find_piece<BM, BN, SEQ>(P, W, blockIdx.x, gridDim.x, &piece);
@@ -77,7 +77,7 @@ attn_simt_kernel(Pool P, WorkDim W, const float *__restrict__ q, int Hq, float s
     const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
     const float *pk = (const float *)P.k, *pv = (const float *)P.v;
     Walk<BM, BN, SEQ> walk;
-    walk.start(P, W, piece);
+    walk.start(W, piece);
     if (threadIdx.x == 0) parts.desc[blockIdx.x].parts = 0;
     ItemOf<SEQ> it;
     while (walk.next(P, W, it)) {

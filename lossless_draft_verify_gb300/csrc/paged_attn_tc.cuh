@@ -89,7 +89,7 @@ struct Shared {
     int live8[KV8 ? 8 : 1];      // rows of the tile of codes that hold tokens; none is to come: kEnd
     uint64_t q_ready, s_full[2], p_ready[2], o_full[2], meet;
     uint32_t tmem;
-    Piece piece;
+    PieceOf<S> piece;
     struct {
         Walk<256, BN, S> walk;
         ItemOf<S> it;

@@ -101,15 +101,17 @@ join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, int heads
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, tok = SHARED ? blockIdx.x : blockIdx.x * W + warp;
     if (tok >= T) return;
+    const size_t half = (size_t)T * Hq;
+    auto place_of = [&](int x, int h) { return H.place[x * half + (size_t)tok * Hq + h]; };
+    // (asked for before it is known whether they were written)
+    Place at[2] = {place_of(0, blockIdx.y * heads), place_of(1, blockIdx.y * heads)};
     const int b = find_seq(q_start, B, tok);
     if (b < 0) return;
     const VSeq s = seqs[b];
     if (tok < s.tok0 || tok >= s.tok0 + s.n) return;
-    const size_t half = (size_t)T * Hq;
     for (int h = blockIdx.y * heads; h < min(Hq, (int)(blockIdx.y + 1) * heads); ++h) {
         const size_t row = (size_t)tok * Hq + h;
-        Place at[2] = {Place::in_output(), H.place[half + row]};
-        if (s.base > 0) at[0] = H.place[row];
+        if (h > (int)blockIdx.y * heads) at[0] = place_of(0, h), at[1] = place_of(1, h);
         float M = kLowest, L = 0.f, acc[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.f;
