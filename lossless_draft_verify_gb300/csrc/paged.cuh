@@ -192,8 +192,8 @@ struct Cost {
 struct CostFew {
     static constexpr bool kByTiles = true;
     static constexpr int kUnitCost = 2;
-    static constexpr int kMinPiece = 2;
-    static constexpr int kWhole = 4;
+    static constexpr int kMinPiece = 1;
+    static constexpr int kWhole = 3;
 };
 
 // What one CTA has to do: from unit (b, h, mt), cost offset `off` within it,
