@@ -183,17 +183,27 @@ struct Cost {
     static constexpr int kUnitCost = BM == 256 ? 16 : 1;
     static constexpr int kMinPiece = BM == 256 ? 10 : 2;
     static constexpr int kWhole = BM == 256 ? 20 : 3;
+    static constexpr int kSlack = 0;
 };
 // Pieces of one warp each, in tiles of few_keys() (paged_attn_few.cuh).  A lone warp
 // takes about 1 us for a tile, so small batches are cut finely: unit cost, least piece
-// and whole units of 3, 8, 12 and of 2, 2, 4, one token of one sequence over 1000 (32/8
-// heads of 128) 23.9 and 12.4 us, of 16 over 500 21.5 and 14.7, of 16 over 32768 179 and
-// 177.5; only 128 sequences of 150 tokens take longer, 17.1 and 25.4.
+// and whole units of 3, 8, 12, of 2, 2, 4 and of 2, 1, 3, one token of one sequence over
+// 1000 (32/8 heads of 128) 23.9, 11.6 and 10.7 us, of 16 over 500 21.5, 12.8 and 12.6, of
+// 16 over 32768 the same.  A unit that is little longer (kSlack) than a piece is not cut
+// either: cutting, and without, 128 sequences of 150 tokens 26.5 and 19.9 us, 96 20.8 and
+// 17.8, 128 of 250 30.3 and 27.0.
 struct CostFew {
     static constexpr bool kByTiles = true;
     static constexpr int kUnitCost = 2;
     static constexpr int kMinPiece = 1;
     static constexpr int kWhole = 3;
+    static constexpr int kSlack = 4;
+};
+// fp32 rows, whose tiles take longer, and planned batches, whose pieces pass from long
+// units to short ones: with a slack four chunks up to 17 over 2000 21.0 us for 16.5, 32
+// sequences in two groups over 8-bit pages 80.9 for 78.3.
+struct CostFewCut : CostFew {
+    static constexpr int kSlack = 0;
 };
 
 // What one CTA has to do: from unit (b, h, mt), cost offset `off` within it,
@@ -447,7 +457,7 @@ struct Walk {
         while (left > 0) {
             const int cost = U::cost(s, W.G, mt), weight = U::weight(s, W.G, mt);
             const long take = lmin(left, (long)cost - off);
-            const bool uncut = cost <= U::kWhole, mine = !uncut || (off <= cost / 2 && cost / 2 < off + take);
+            const bool uncut = cost <= U::kWhole || (C::kByTiles && cost > per && cost <= per + C::kSlack), mine = !uncut || (off <= cost / 2 && cost / 2 < off + take);
             const long a = uncut ? 0 : off, e = uncut ? cost : off + take;
             it.set(b, s);
             it.h = h;

@@ -72,12 +72,12 @@ struct Geom {
     static constexpr int BOXES = KV8 || D == 64 ? 1 : 2;       // of a block: rows of 128 bytes at most
 };
 
-template <int BM, int BN, int STAGES, typename SEQ>
+template <int BM, int BN, int STAGES, typename SEQ, typename C>
 struct Warp {
     uint64_t full[STAGES];
     alignas(16) uint8_t scale[STAGES][2][BN];
     PieceOf<SEQ> piece;
-    Walk<BM, BN, SEQ, CostFew> walk;
+    Walk<BM, BN, SEQ, C> walk;
     ItemOf<SEQ> part[4];               // the parts asked for last; the arithmetic is STAGES tiles behind
     bool more;
     static_assert(STAGES < 4, "parts");
@@ -166,11 +166,12 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
     using G = Geom<D, NB, KV8, E>;
     using It = ItemOf<SEQ>;
     constexpr bool PLANNED = std::is_same_v<SEQ, VSeq>;
+    using C = std::conditional_t<F32 || PLANNED, CostFewCut, CostFew>;
     constexpr int BN = G::BN, kBlocks = G::BLOCKS, TILE = G::TILE, kStages = G::STAGES, kWarps = G::WARPS;
     extern __shared__ __align__(1024) uint8_t sm[];
-    __shared__ Warp<BM, BN, kStages, SEQ> warps[kWarps];
+    __shared__ Warp<BM, BN, kStages, SEQ, C> warps[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, q4 = lane & 3;
-    Warp<BM, BN, kStages, SEQ> &S = warps[warp];
+    Warp<BM, BN, kStages, SEQ, C> &S = warps[warp];
     uint8_t *tiles = sm + warp * kStages * G::STAGE;
     // neighbouring pieces on different SMs
     const int n_piece = gridDim.x * kWarps, me = warp * gridDim.x + blockIdx.x;
@@ -186,7 +187,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         for (int i = 0; i < kStages; ++i) mbar_init(&S.full[i], 1);
         fence_mbar_init();
     }
-    find_piece<BM, BN, SEQ, CostFew>(A.P, A.W, me, n_piece, &S.piece);
+    find_piece<BM, BN, SEQ, C>(A.P, A.W, me, n_piece, &S.piece);
     if (!PLANNED) pdl_trigger();
     const bool placed = (smem_u32(sm) & 1023u) == 0;         // the swizzled tiles need it
     if (!placed && lane == 0) report_timeout(A.status, 110); // never expected

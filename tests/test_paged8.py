@@ -306,6 +306,8 @@ int main()
         division<16, 32, CostFew>(r);
         division<8, 64, CostFew>(r);
         division<16, 16, CostFew>(r);
+        division<8, 32, CostFewCut>(r);
+        division<16, 64, CostFewCut>(r);
         division<256, 128, Cost<256>>(r);
         division<64, 32, Cost<64>>(r);
     }
