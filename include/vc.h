@@ -905,7 +905,7 @@ vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_
  * halves being joined in fp32 before the one rounding to dt.  The workspace holds
  * both halves of every row: 8 (d + 3) bytes per row and query head, beside
  * vc_paged_attn's.  Over prefixes of fewer than some thousand tokens it may take
- * longer than vc_paged_attn, by 15 us at most (GB300).
+ * longer than vc_paged_attn, by some 20 us at most (GB300).
  * seq_start (device int32 [n + 1], ascending), len (device int32 [n]); with n = 0
  * both may be NULL.  VC_PAGED_BAD_LENGTH also reports a range outside [0, B] or
  * descending or a length outside [0, max_blocks * page] (its sequences attend on

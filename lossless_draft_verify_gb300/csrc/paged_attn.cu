@@ -366,7 +366,8 @@ struct SharedLayout {
     size_t own_at, plan, place, lse, o, bytes;
 };
 
-// Where groups have at most this many rows per kv head, on average, the kernel of few rows
+// Where groups have at most this many rows per kv head, on average (their ranges lie on the
+// device), the kernel of few rows
 // takes the prefixes too: a launch and units of 8 us less, a pass over the prefix more for
 // each 16 rows.  Through the tensor-core kernel and so, contexts of up to 300 after the
 // prefix, 32/8 heads of 128, bf16 and 8-bit pages: 4 sequences (16 rows) over 512 28, 22

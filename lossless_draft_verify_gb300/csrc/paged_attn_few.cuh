@@ -17,8 +17,8 @@
 // The scales meet the products and the weights, not the codes.  The tensor-core kernel
 // (paged_attn_tc.cuh) writes bf16 tiles to shared memory instead, which costs more
 // than it saves where rows are few (a decode step of 16 x 32768 tokens, 32/8 heads of
-// 128, 1.08 GB: 180 us here, 88% of the copy rate, 392 there; four tokens of 16 over
-// 8192, 16 rows, 73 and 122; from 24 rows on there is nothing between them).
+// 128, 1.08 GB: 176 us here, 90% of the copy rate, 392 there; four tokens of 16 over
+// 8192, 16 rows, 69 and 122; from 24 rows on there is nothing between them).
 //
 // A warp is alone with its piece of the batch: it requests the K and V rows of 4 KB
 // tiles by TMA ahead of its arithmetic, past a unit's end too, and needs no barrier but
@@ -32,7 +32,7 @@
 // fp32 rows over 8-bit pages take the same products: the codes are exact operands, and
 // q and the weights are two f16 terms each, 22 bits, for twice the products.  The unit
 // does not round its running sums to nearest, so each product of 16 is added to them
-// outside it.  Four chunks of 300 over 2000, 16/4 heads of 128, take 229 us
+// outside it.  Four chunks of 300 over 2000, 16/4 heads of 128, take 233 us
 // (583 on the CUDA cores), a token of 8 sequences over 4000, 32/8 heads, 27 (169).
 //
 // Ranges.  q is scaled by its row's largest exponent to 2^14 (beside the roundings to

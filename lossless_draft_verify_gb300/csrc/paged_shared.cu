@@ -14,7 +14,7 @@
 // without sharing (vc_paged_attn; most of its reads of a prefix hit L2), 32/8 heads of
 // 128: one token of 32 sequences, a prefix of 32768 and up to 700 tokens of their own
 // 59 and 428 us; 32 in two groups of up to 32000 over 8-bit pages 79 and 189; 24 chunks
-// up to 17 in three groups, 28/4 heads, 81 and 105; four over 600 tokens 12.5 and 18,
+// up to 17 in three groups, 28/4 heads, 81 and 105; four over 600 tokens 11.5 and 18,
 // over 8192 and up to 300 of their own 21 and 30.
 #include "paged.cuh"
 
