@@ -441,7 +441,8 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         for (int r = 0; r < 2; ++r) {
                             const float p = ex2((s[x][j][r] - m[x][r]) * qs[x][r]);
                             sum[x][r] += p;
-                            u[r] = KV8 ? p * (vs[j] * put[x][r]) : p;
+                            // (vs * put may be infinite beside a weight of zero)
+                            u[r] = !KV8 ? p : p > 0.f ? p * (vs[j] * put[x][r]) : 0.f;
                         }
                         if constexpr (KV8) {
 #pragma unroll
@@ -475,9 +476,10 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         if constexpr (KV8) {
                             const float big = over_keys([&](int j) { return ex2((s[x][j][r] - mn) * qs[x][r]) * vs[j]; });
                             const float lv = fmaxf(level[x][r] * alpha, big);
-                            // kTop over the level's power of two; the exponent within fp32's range
+                            // kTop over the level's power of two, the exponent within fp32's range; a row
+                            // that has seen no key keeps its place
                             const uint32_t ex = min(max(__float_as_uint(lv) >> 23, 7u), 253u);
-                            to = scale_of(254u - ex) * kTop;
+                            to = lv > 0.f ? scale_of(254u - ex) * kTop : put[x][r];
                             from = 1.f / put[x][r];
                             level[x][r] = lv;
                         }

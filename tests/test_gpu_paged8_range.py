@@ -1,0 +1,131 @@
+"""Attention over 8-bit pages where values are far apart in size, or far from
+one: a weight that is zero stays so beside any value, and one that is not is kept
+wherever its row's values lie.  Against the fp64 form (paged_ref.py, where the
+tolerances are derived; the joins of shared prefixes are covered by the (L + 16) u
+of their sums, as every row but those that must be exact sees 100 keys or more)."""
+import pytest
+import torch
+
+import paged8_ref
+import paged_ref
+from helpers import lib
+from paged8_ref import Batch8
+from paged_ref import close
+from test_gpu_paged_shared import Shared
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+
+
+def _scale_values(bt, slots, byte, zero=False):
+    """The values of sequence b's slots, for b, slots of a dict, under scales of
+    this byte, or all zeros."""
+    for b, ii in slots.items():
+        for i in ii:
+            p, r = bt.table[b][i // bt.page], i % bt.page
+            bt.vs.view(torch.uint8)[p, :, r] = byte
+            if zero:
+                bt.v8.view(torch.uint8)[p, :, r] = 0
+    bt.v = paged8_ref.values(bt.v8, bt.vs).to(bt.dtype).cuda()
+
+
+def _run(vc, bt, q, scale, sh=None):
+    out = torch.full_like(q, 7.0)
+    T, Hq, _ = q.shape
+    if sh is None:
+        cache = bt.cache8(vc)
+        ws = vc.Workspace(vc.vc_paged8_attn_workspace_bytes(cache, T, Hq))
+        vc.vc_paged8_attn(q, cache, bt.q_start, bt.ctx, scale, out, ws)
+    else:
+        cache = sh.cache(vc)
+        size, call = ((vc.vc_paged8_attn_shared_workspace_bytes, vc.vc_paged8_attn_shared) if sh.bits == 8 else
+                      (vc.vc_paged_attn_shared_workspace_bytes, vc.vc_paged_attn_shared))
+        ws = vc.Workspace(size(cache, len(sh.prefix), T, Hq))
+        call(q, cache, sh.seq_start, sh.len, bt.q_start, bt.ctx, scale, out, ws)
+    assert vc.vc_poll_status(ws) == 0 and int(cache.status) == 0
+    return out
+
+
+def _compare(bt, q, out, scale, lost=0.0):
+    want, tol, _, _ = paged_ref.attn(bt, q, scale)
+    close(out, want, tol + lost, "out")
+
+
+# chunks, contexts, Hq, Hkv, d: contexts that end at a key tile (32 keys of 128
+# channels, 64 of 64), so that a chunk's first rows see nothing of its last tile
+LATE = [([2], [1023], 32, 8, 128), ([2] * 4, [2047] * 4, 32, 8, 128), ([4], [511], 32, 8, 128), ([2], [1023], 8, 8, 64),
+        ([3, 1, 2], [1022, 300, 639], 8, 2, 64), ([100], [1000], 2, 2, 128)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("byte", [129, 132, 159, 200])
+@pytest.mark.parametrize("case", range(len(LATE)))
+def test_large_values_that_earlier_rows_do_not_see(case, byte, dtype):
+    """The values of every token but a chunk's first are 1000, 10^4, 2^40 and 2^80:
+    nothing of them reaches the rows before."""
+    vc = lib()
+    ns, cs, Hq, Hkv, d = LATE[case]
+    bt = Batch8(ns, cs, Hkv, d, 64, dtype, seed=case)
+    _scale_values(bt, {b: range(cs[b] + 1, cs[b] + ns[b]) for b in range(bt.B)}, byte)
+    q = bt.randn(bt.T, Hq, d)
+    _compare(bt, q, _run(vc, bt, q, d ** -0.5), d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("byte", [132, 140, 200])
+@pytest.mark.parametrize("ns,cs", [([2], [0]), ([5, 2], [0, 40]), ([3, 1], [64, 0]), ([40], [31])])
+def test_rows_that_have_seen_only_zeros(ns, cs, byte, dtype):
+    """Zeros up to a chunk's first token, large values after it: the first rows are
+    exactly zero."""
+    vc = lib()
+    for d in (64, 128):
+        bt = Batch8(ns, cs, 2, d, 16, dtype, seed=5)
+        _scale_values(bt, {b: range(cs[b] + 1) for b in range(bt.B)}, 10, zero=True)
+        _scale_values(bt, {b: range(cs[b] + 1, cs[b] + ns[b]) for b in range(bt.B)}, byte)
+        q = bt.randn(bt.T, 8, d)
+        out = _run(vc, bt, q, 0.1)
+        _compare(bt, q, out, 0.1)
+        for b in range(bt.B):
+            assert (out[bt.start[b]] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("byte", [140, 200])
+@pytest.mark.parametrize("ns,cs", [([1, 1], [300, 20]), ([2, 3], [0, 31]), ([40], [77])])
+def test_a_value_of_zero_under_the_only_weight(ns, cs, byte, dtype):
+    """Key 0 has all the weight and a value of zero; the others' weights, 2^-230,
+    are no fp32 numbers and may be lost whatever their values: 2^-126 of each."""
+    vc = lib()
+    bt = Batch8(ns, cs, 1, 128, 16, dtype, seed=6)
+    bt.ks.view(torch.uint8)[bt.ks.view(torch.uint8) < 255] = 120
+    bt.k8.view(torch.uint8)[..., 0] = 0xf0                   # -128 * 2^-7
+    for b in range(bt.B):
+        bt.k8.view(torch.uint8)[bt.table[b][0], :, 0, 0] = 0
+    bt.k = paged8_ref.values(bt.k8, bt.ks).to(dtype).cuda()
+    _scale_values(bt, {b: range(1, bt.lens[b]) for b in range(bt.B)}, byte)
+    _scale_values(bt, {b: [0] for b in range(bt.B)}, 10, zero=True)
+    q = torch.zeros(bt.T, 4, 128, dtype=dtype, device="cuda")
+    q[..., 0] = 8.0
+    _compare(bt, q, _run(vc, bt, q, 20.0), 20.0, lost=max(bt.lens) * 2.0 ** -126 * 2.0 ** (byte - 127 + 9))
+
+
+# chunks, contexts after the prefix, groups' first sequences, prefixes, Hq, Hkv, d, page
+SHARED = [([2, 4, 2], [15, 47, 31], [0], [1040], 8, 2, 128, 16),      # a small group
+          ([2] * 6, [31, 63, 0, 1, 95, 31], [0], [512], 16, 2, 128, 64),      # own slots only through the kernel of few rows
+          ([2, 1, 3, 4], [63, 100, 190, 126], [0, 2], [320, 128], 8, 2, 64, 64),
+          ([50, 9], [30, 60], [0], [256], 2, 2, 128, 32)]
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("byte", [129, 140, 200])
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_large_values_after_a_shared_prefix(case, byte, dtype):
+    vc = lib()
+    ns, own, first, prefix, Hq, Hkv, d, page = SHARED[case]
+    cs = [c + prefix[max(g for g, f in enumerate(first) if f <= b)] for b, c in enumerate(own)]
+    bt = Batch8(ns, cs, Hkv, d, page, dtype, seed=case)
+    sh = Shared(bt, first, prefix, 8)
+    _scale_values(bt, {b: range(cs[b] + 1, cs[b] + ns[b]) for b in range(bt.B)}, byte)
+    q = bt.randn(bt.T, Hq, d)
+    _compare(bt, q, _run(vc, bt, q, d ** -0.5, sh), d ** -0.5)
