@@ -58,6 +58,10 @@ namespace {
 constexpr int kBlock = 16;                                     // rows of a request: they lie in one page
 constexpr float kLazy = 8.f, kGrown = 4096.f;                  // log2 domain; a lane's sum with a weight above 2^kLazy
 constexpr float kLeast = -3e38f;                               // a row that has seen no key
+// The least scale of scores (log2 domain).  A product of -inf times zero would be NaN;
+// a row's first key lies 30 above kLeast at least, so that its maximum and the place of
+// its weights move there; products of 1e30 change a weight by 1e-7.
+constexpr float kLeastScore = 1e-37f;
 constexpr float kQTop = 16384.f;                               // q rows lie in [kQTop, 2 kQTop) at their largest
 constexpr float kTop = 64.f, kMost = 32768.f;                  // where weights are put, and how far they may grow
 
@@ -322,7 +326,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                     // above after them: nothing overflows that the product itself does not
                     const int of = KV8 ? (int)__shfl_sync(0xffffffffu, ex, 8 * q4 + 4 * r) - 14 : 127;
                     back[x][r] = scale_of(min(of, 127));
-                    qs[x][r] = fmaxf(A.sl2 * scale_of(max(of, 127)), 1e-38f);      // -inf * 0: NaN
+                    qs[x][r] = fmaxf(A.sl2 * scale_of(max(of, 127)), kLeastScore);
                     const int R = 8 * x + 2 * q4 + r;
                     kmax[x][r] = R < it.rows ? it.last((row0 + R) / A.W.G) : -1;
                 }

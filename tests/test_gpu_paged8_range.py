@@ -129,3 +129,36 @@ def test_large_values_after_a_shared_prefix(case, byte, dtype):
     _scale_values(bt, {b: range(cs[b] + 1, cs[b] + ns[b]) for b in range(bt.B)}, byte)
     q = bt.randn(bt.T, Hq, d)
     _compare(bt, q, _run(vc, bt, q, d ** -0.5, sh), d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("less", [0, 23, 60, 100])
+@pytest.mark.parametrize("scale", [0.0, 1e-30, 2.0 ** -20])
+@pytest.mark.parametrize("ns,cs", [([1, 1], [300, 1000]), ([2, 3], [1023, 95]), ([40], [200])])
+def test_small_values_under_small_scales(ns, cs, scale, less, dtype):
+    """Values of 2^-less under weights that are nearly or exactly the same: their
+    mean, however small."""
+    vc = lib()
+    bt = Batch8(ns, cs, 2, 128, 16, dtype, seed=8)
+    byte = bt.vs.view(torch.uint8)
+    byte[byte < 255] -= less
+    assert int(byte.min()) >= 10
+    bt.v = paged8_ref.values(bt.v8, bt.vs).to(dtype).cuda()
+    q = bt.randn(bt.T, 8, 128)
+    _compare(bt, q, _run(vc, bt, q, scale), scale)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_small_values_of_a_shared_prefix_under_a_scale_of_zero(case, dtype, bits):
+    vc = lib()
+    ns, own, first, prefix, Hq, Hkv, d, page = SHARED[case]
+    cs = [c + prefix[max(g for g, f in enumerate(first) if f <= b)] for b, c in enumerate(own)]
+    bt = Batch8(ns, cs, Hkv, d, page, dtype, seed=case)
+    sh = Shared(bt, first, prefix, bits)
+    byte = bt.vs.view(torch.uint8)
+    byte[byte < 255] -= 40
+    bt.v = paged8_ref.values(bt.v8, bt.vs).to(dtype).cuda()
+    q = bt.randn(bt.T, Hq, d)
+    _compare(bt, q, _run(vc, bt, q, 0.0, sh), 0.0)
