@@ -63,6 +63,7 @@ constexpr float kLeast = -3e38f;                               // a row that has
 // its weights move there; products of 1e30 change a weight by 1e-7.
 constexpr float kLeastScore = 1e-37f;
 constexpr float kQTop = 16384.f;                               // q rows lie in [kQTop, 2 kQTop) at their largest
+constexpr int kBack = 48;                                      // log2: by how much products may be scaled up
 constexpr float kTop = 64.f, kMost = 32768.f;                  // where weights are put, and how far they may grow
 
 // Warps of a CTA (their accumulators are what limits them) and tiles, of K and V, of
@@ -322,11 +323,12 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    // a scale below one meets the products before the keys' scales do, one
-                    // above after them: nothing overflows that the product itself does not
+                    // a row's scale meets the products (below 2^32) before the keys' scales do,
+                    // what is above kBack with the scale of the scores: nothing overflows that
+                    // the product or the score itself does not
                     const int of = KV8 ? (int)__shfl_sync(0xffffffffu, ex, 8 * q4 + 4 * r) - 14 : 127;
-                    back[x][r] = scale_of(min(of, 127));
-                    qs[x][r] = fmaxf(A.sl2 * scale_of(max(of, 127)), kLeastScore);
+                    back[x][r] = scale_of(min(of, 127 + kBack));
+                    qs[x][r] = fmaxf(A.sl2 * scale_of(127 + max(of - 127 - kBack, 0)), kLeastScore);
                     const int R = 8 * x + 2 * q4 + r;
                     kmax[x][r] = R < it.rows ? it.last((row0 + R) / A.W.G) : -1;
                 }
@@ -357,7 +359,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 ks[j] = KV8 ? scale_of(sc[8 * j]) : 1.f;
                 vs[j] = !KV8 ? 1.f : g + 8 * j < live ? scale_of(sc[BN + 8 * j]) : 0.f;
             }
-            // ---- S^T = K Q^T; s[x][j][r]: key g + 8 j, row 2 q + r, less a scale of q above one ----
+            // ---- S^T = K Q^T; s[x][j][r]: key g + 8 j, row 2 q + r, less what q's scale has above 2^kBack ----
             // (a chain of products per block and chunk: one chain would wait for itself)
             float s[NB][2 * kBlocks][2], acc[NB][kBlocks][KC][4];
             if constexpr (!KV8) {

@@ -162,3 +162,30 @@ def test_small_values_of_a_shared_prefix_under_a_scale_of_zero(case, dtype, bits
     bt.v = paged8_ref.values(bt.v8, bt.vs).to(dtype).cuda()
     q = bt.randn(bt.T, Hq, d)
     _compare(bt, q, _run(vc, bt, q, 0.0, sh), 0.0)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("ns,cs,Hq", [([1, 1], [300, 77], 4), ([3, 2], [95, 640], 4), ([30], [200], 4)])
+@pytest.mark.parametrize("size,scale", [(120, 1e6), (126, 1e8), (100, 1e8)])
+def test_large_queries_under_large_scales(size, scale, ns, cs, Hq, dtype):
+    """Queries of 2^size meet keys of 2^-117 times 0 to 15 under a large scale:
+    every score is finite, and the row's output is the value of its largest key."""
+    vc = lib()
+    bt = Batch8(ns, cs, 2, 128, 16, dtype, seed=12)
+    bt.ks.view(torch.uint8)[bt.ks.view(torch.uint8) < 255] = 10
+    code = torch.tensor([0x08 * (i % 16) for i in range(max(bt.lens))], dtype=torch.uint8)      # 0, 2^-6 .. 2^8
+    for b in range(bt.B):
+        turn = torch.randperm(bt.lens[b], generator=bt.g)
+        for i in range(bt.lens[b]):
+            p, r = bt.table[b][i // 16], i % 16
+            bt.k8.view(torch.uint8)[p, :, r] = 0
+            bt.k8.view(torch.uint8)[p, :, r, 0] = code[int(turn[i]) % 15]
+        bt.k8.view(torch.uint8)[bt.table[b][0], :, 3, 0] = 0x7e      # the largest: slot 3
+    q = torch.zeros(bt.T, Hq, 128, dtype=dtype, device="cuda")
+    q[..., 0] = 2.0 ** size
+    q[..., 1] = -2.0 ** size                                 # meets zeros
+    out = _run(vc, bt, q, scale)
+    for b in range(bt.B):
+        for h in range(2):
+            want = bt.rows(bt.v, b, h)[3].expand(ns[b], Hq // 2, 128)
+            assert torch.equal(out[bt.start[b]:bt.start[b + 1], h * Hq // 2:(h + 1) * Hq // 2].cpu().double(), want)
