@@ -481,7 +481,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         float to = 1.f, from = 1.f;
                         if constexpr (KV8) {
                             const float big = over_keys([&](int j) { return ex2((s[x][j][r] - mn) * qs[x][r]) * vs[j]; });
-                            const float lv = fmaxf(level[x][r] * alpha, big);
+                            const float lv = fminf(fmaxf(level[x][r] * alpha, big), 3e38f);      // (infinite, it would stay so)
                             // kTop over the level's power of two, the exponent within fp32's range; a row
                             // that has seen no key keeps its place
                             const uint32_t ex = min(max(__float_as_uint(lv) >> 23, 7u), 253u);

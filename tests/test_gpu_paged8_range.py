@@ -189,3 +189,31 @@ def test_large_queries_under_large_scales(size, scale, ns, cs, Hq, dtype):
         for h in range(2):
             want = bt.rows(bt.v, b, h)[3].expand(ns[b], Hq // 2, 128)
             assert torch.equal(out[bt.start[b]:bt.start[b + 1], h * Hq // 2:(h + 1) * Hq // 2].cpu().double(), want)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+def test_a_scale_of_the_largest_size_is_forgotten(dtype):
+    """Keys whose values are zeros under scales of 2^127, then keys of 2^112 times
+    their weights with ordinary values: those are the result.  (Two query heads, so
+    that one's maximum moves while the other's weights lie above one; as many units as
+    leave a warp with some of them whole.)"""
+    vc = lib()
+    B, L = 240, 160
+    bt = Batch8([1] * B, [L - 1] * B, 8, 128, 32, dtype, seed=3)
+    k8, ks, v8, vs = (t.view(torch.uint8) for t in (bt.k8, bt.ks, bt.v8, bt.vs))
+    k8.zero_(), ks.fill_(127)
+    at = [torch.tensor([bt.table[b][i] for b in range(B)]).long().cuda() for i in range(5)]
+    v8[at[0]] = 0
+    v8[at[1]] = 0
+    vs[at[0]] = 254
+    vs[at[1]] = 254
+    for i, code in ((1, 0x4e), (2, 0x6e), (3, 0x6e), (4, 0x6e)):     # scores 0, 7 and 112
+        k8[at[i], :, :, 0] = code
+        if i > 1:
+            vs[at[i]] = 139
+    bt.k = paged8_ref.values(bt.k8, bt.ks).to(dtype).cuda()
+    bt.v = paged8_ref.values(bt.v8, bt.vs).to(dtype).cuda()
+    q = torch.zeros(B, 16, 128, dtype=dtype, device="cuda")
+    q[:, 0::2, 0], q[:, 1::2, 0] = 1.0, 4.0
+    scale = 0.6931472
+    _compare(bt, q, _run(vc, bt, q, scale), scale)
