@@ -508,7 +508,7 @@ struct Parts {
     PartDesc *desc;    // [n_cta]
     float2 *ml;        // [n_cta][2][rows_cap]: running maximum (log2 domain) and sum
     float *o;          // [n_cta][2][rows_cap][d], not divided by the sum
-    int rows_cap;
+    int rows_cap, n_cta;
 
     __device__ __forceinline__ size_t row(int cta, int slot, int r) const
     {
@@ -528,6 +528,12 @@ struct Place {
     }
     __host__ __device__ __forceinline__ int cta() const { return (int)(cta_parts & 0xffffu); }
     __host__ __device__ __forceinline__ int parts() const { return (int)(cta_parts >> 16); }
+    // Whether it names parts that are there: not where a wait ran out (reported) before
+    // it was written, and the workspace holds whatever it did.
+    __host__ __device__ __forceinline__ bool fits(const Parts &p) const
+    {
+        return parts() > 0 && cta() + parts() <= p.n_cta && r < (uint32_t)p.rows_cap;
+    }
 };
 // What a planned batch's attention leaves: o (normalised) and lse of the rows that
 // are not in parts, and every row's place.

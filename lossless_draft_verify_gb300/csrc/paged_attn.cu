@@ -325,7 +325,7 @@ cudaError_t run(const Pool &P, const WorkDim &W, vc_dtype dt, int d, const void 
 {
     const long cap = P.capacity();
     const WsLayout w = layout(dt, d, W.T, W.G, Hq, P.B, cap, scores != nullptr, P.k_scale);
-    Parts parts = {(PartDesc *)(ws + w.desc), (float2 *)(ws + w.ml), (float *)(ws + w.o), w.rows_cap};
+    Parts parts = {(PartDesc *)(ws + w.desc), (float2 *)(ws + w.ml), (float *)(ws + w.o), w.rows_cap, w.n_cta};
     float *lse = scores ? (float *)(ws + w.rows) : nullptr;
     float *stored = w.s_stride ? (float *)(ws + w.stored) : nullptr;
     cudaError_t e;
@@ -401,7 +401,7 @@ cudaError_t run_shared(const Pool &P, WorkDim W, vc_dtype dt, int d, const void 
 {
     const SharedLayout w = shared_layout(dt, d, W.T, W.G, Hq, P.B, P.capacity(), G.n, P.k_scale);
     auto parts_at = [&](const WsLayout &x, uint8_t *at) {
-        return Parts{(PartDesc *)(at + x.desc), (float2 *)(at + x.ml), (float *)(at + x.o), x.rows_cap};
+        return Parts{(PartDesc *)(at + x.desc), (float2 *)(at + x.ml), (float *)(at + x.o), x.rows_cap, x.n_cta};
     };
     const Parts parts = parts_at(w.attn, ws), own = w.few ? parts_at(w.own, ws + w.own_at) : parts;
     const Halves H = {(float *)(ws + w.o), (float *)(ws + w.lse), (Place *)(ws + w.place)};

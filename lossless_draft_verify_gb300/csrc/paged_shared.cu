@@ -112,6 +112,8 @@ join_kernel(int B, const int32_t *__restrict__ q_start, int T, int Hq, int heads
     for (int h = blockIdx.y * heads; h < min(Hq, (int)(blockIdx.y + 1) * heads); ++h) {
         const size_t row = (size_t)tok * Hq + h;
         if (h > (int)blockIdx.y * heads) at[0] = place_of(0, h), at[1] = place_of(1, h);
+        if (!at[0].fits(pre)) at[0] = Place::in_output();
+        if (!at[1].fits(own)) at[1] = Place::in_output();
         float M = kLowest, L = 0.f, acc[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) acc[e] = 0.f;

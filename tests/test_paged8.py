@@ -325,3 +325,36 @@ def test_division_on_the_host(tmp_path):
                     str(src), "-o", str(exe)], check=True, capture_output=True, text=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
+
+
+PLACES = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "paged.cuh"
+using namespace vc::paged;
+#define NEED(x) do { if (!(x)) { std::printf("line %d: %s\n", __LINE__, #x); std::exit(1); } } while (0)
+int main()
+{
+    const Parts p{nullptr, nullptr, nullptr, 16, 1824};
+    NEED(!Place::in_output().fits(p));
+    NEED(Place::in_parts(0, 2, 0).fits(p) && Place::in_parts(1822, 2, 15).fits(p) && Place::in_parts(0, 1824, 3).fits(p));
+    NEED(!Place::in_parts(1823, 2, 0).fits(p) && !Place::in_parts(0, 1825, 0).fits(p) && !Place::in_parts(5, 2, 16).fits(p));
+    for (uint32_t x : {0x7f800000u, 0x7fc00000u, 0xffffffffu, 0x3f800000u, 0x00010720u, 0x40000001u})
+        for (uint32_t r : {0u, 15u, 16u, 0xffffffffu, 0x80000000u}) {
+            const Place at{x, r};
+            NEED(!at.fits(p) || (at.cta() + at.parts() <= 1824 && at.parts() > 0 && r < 16));
+        }
+    std::printf("ok\n");
+}
+"""
+
+
+def test_a_place_that_was_never_written_names_nothing_outside_the_parts(tmp_path):
+    """After a wait that ran out the join finds whatever the workspace held."""
+    from lossless_draft_verify_gb300 import build
+    src, exe = tmp_path / "places.cu", tmp_path / "places"
+    src.write_text(PLACES)
+    subprocess.run([build.nvcc(), "-std=c++17", "-O1", "--expt-relaxed-constexpr", "-I", build.INCLUDE, "-I", build.CSRC,
+                    str(src), "-o", str(exe)], check=True, capture_output=True, text=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=60)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout
