@@ -171,7 +171,7 @@ def _scales(amax):
     magnitudes: the smallest with amax <= 448 * scale."""
     m, e = torch.frexp(amax)                      # amax = m 2^e, m in [0.5, 1)
     e = torch.where(m > 0.875, e, e - 1) - 8
-    return torch.where(amax == 0, 10, (e + 127).clamp(10, 246))
+    return torch.where(amax == 0, 1, (e + 127).clamp(1, 246))
 
 
 def _power(byte):
