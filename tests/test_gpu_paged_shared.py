@@ -373,3 +373,40 @@ print(h.hexdigest())
         assert r.returncode == 0, r.stderr[-2000:]
         got.append(r.stdout.strip().splitlines()[-1])
     assert got[0] == got[1] and len(got[0]) == hashlib.sha256().digest_size * 2
+
+
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_in_a_row_on_one_workspace_do_not_meet(graph):
+    """Batches of other lengths, groups, types and kernels follow one another without a
+    pause on one workspace: a kernel that began too early would read the plan, the
+    parts or the places of the call before.  The bits of each call alone."""
+    vc = lib()
+    jobs = []
+    for i, (dt, bits, ns) in enumerate(FORMS * 2):
+        far = i >= len(FORMS)
+        own, prefix = ([900, 3, 40, 0, 2000, 5], [260, 1300]) if far else ([5, 0, 70, 200, 9, 31], [900, 260])
+        bt, sh, q = _case(ns[::-1] if far else ns, own, [0, 2] if far else [0, 3], prefix, 8, 2, 64, 16, dt, bits, seed=i)
+        want, cache, ws = _call(vc, sh, q, 0.1)
+        torch.cuda.synchronize()
+        _compare(bt, q, want, 0.1)
+        jobs.append((sh, q, cache, want, ws.nbytes))
+    one = vc.Workspace(max(j[4] for j in jobs))
+    order = [(7 * i) % len(jobs) for i in range(6 * len(jobs))]      # every batch after another kind of one
+    outs = [torch.full_like(jobs[i][1], 7.0) for i in order]
+
+    def run():
+        for i, out in zip(order, outs):
+            sh, q, cache, _, _ = jobs[i]
+            _call(vc, sh, q, 0.1, cache, one, out)
+    if graph:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, capture_error_mode="thread_local"):
+            run()
+        g.replay()
+        g.replay()
+    else:
+        run()
+    torch.cuda.synchronize()
+    assert vc.vc_poll_status(one) == 0
+    for i, out in zip(order, outs):
+        assert torch.equal(out, jobs[i][3]), i
