@@ -447,8 +447,10 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         for (int r = 0; r < 2; ++r) {
                             const float p = ex2((s[x][j][r] - m[x][r]) * qs[x][r]);
                             sum[x][r] += p;
-                            // (vs * put may be infinite beside a weight of zero)
-                            u[r] = !KV8 ? p : p > 0.f ? p * (vs[j] * put[x][r]) : 0.f;
+                            // (in this order: vs * put may be infinite where p is zero or tiny, and p * vs
+                            // vanish; p * put is finite once the row has its place, and what is lost of
+                            // it below 2^-149 is below 2^-28 of the largest weight under any scale)
+                            u[r] = KV8 ? p * put[x][r] * vs[j] : p;
                         }
                         if constexpr (KV8) {
 #pragma unroll

@@ -3,6 +3,8 @@ one: a weight that is zero stays so beside any value, and one that is not is kep
 wherever its row's values lie.  Against the fp64 form (paged_ref.py, where the
 tolerances are derived; the joins of shared prefixes are covered by the (L + 16) u
 of their sums, as every row but those that must be exact sees 100 keys or more)."""
+import math
+
 import pytest
 import torch
 
@@ -217,3 +219,29 @@ def test_a_scale_of_the_largest_size_is_forgotten(dtype):
     q[:, 0::2, 0], q[:, 1::2, 0] = 1.0, 4.0
     scale = 0.6931472
     _compare(bt, q, _run(vc, bt, q, scale), scale)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("byte", [30, 100, 140, 200])
+@pytest.mark.parametrize("gap", [40, 100, 122])
+@pytest.mark.parametrize("ns,cs", [([1, 1], [300, 20]), ([2, 3], [9, 95]), ([40], [77])])
+def test_tiny_weights_of_values_beside_zeros(ns, cs, gap, byte, dtype):
+    """Key 0 has nearly all the weight and a value of zero; the result is the others',
+    2^-gap of their values."""
+    vc = lib()
+    bt = Batch8(ns, cs, 1, 128, 16, dtype, seed=6)
+    bt.ks.view(torch.uint8)[bt.ks.view(torch.uint8) < 255] = 120
+    bt.k8.view(torch.uint8)[..., 0] = 0xf0                   # -128 * 2^-7
+    for b in range(bt.B):
+        bt.k8.view(torch.uint8)[bt.table[b][0], :, 0, 0] = 0
+    bt.k = paged8_ref.values(bt.k8, bt.ks).to(dtype).cuda()
+    _scale_values(bt, {b: range(1, bt.lens[b]) for b in range(bt.B)}, byte)
+    _scale_values(bt, {b: [0] for b in range(bt.B)}, 10, zero=True)
+    q = torch.zeros(bt.T, 4, 128, dtype=dtype, device="cuda")
+    q[..., 0] = 8.0
+    scale = gap * math.log(2) / 8
+    # Below fp32's normal numbers: a row's place is 2^126 at most, a weight there is rounded
+    # to 2^-24 at the finest, off by half of it, and meets codes of 448 at most: 2^-25 *
+    # 2^-126 * 448 < 2^-142 per key.  A bf16 result is rounded to 2^-133.
+    lost = max(bt.lens) * 2.0 ** -142 + (2.0 ** -134 if dtype == BF else 2.0 ** -150)
+    _compare(bt, q, _run(vc, bt, q, scale), scale, lost=lost)
