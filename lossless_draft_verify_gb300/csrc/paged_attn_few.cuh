@@ -448,8 +448,8 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                             const float p = ex2((s[x][j][r] - m[x][r]) * qs[x][r]);
                             sum[x][r] += p;
                             // (in this order: vs * put may be infinite where p is zero or tiny, and p * vs
-                            // vanish; p * put is finite once the row has its place, and what is lost of
-                            // it below 2^-149 is below 2^-28 of the largest weight under any scale)
+                            // vanish; p * put is finite once the row has its place, and what it loses below
+                            // 2^-149 is below 2^-28 of the largest weight under any scale)
                             u[r] = KV8 ? p * put[x][r] * vs[j] : p;
                         }
                         if constexpr (KV8) {
@@ -465,6 +465,20 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                 }
                 if (!__any_sync(0xffffffffu, far) || moves == 2) break;   // (one move is enough, for finite rows)
                 // rarely: the maximum, or the place of the weights, moves
+                if constexpr (KV8) {
+                    // a value row of zeros has no size, whatever its scale says (a quarter
+                    // of a row per lane)
+#pragma unroll
+                    for (int j = 0; j < 2 * kBlocks; ++j) {
+                        const uint4 *row = reinterpret_cast<const uint4 *>(tV + (g + 8 * j) * D + q4 * (D / 4));
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i) any |= row[i].x | row[i].y | row[i].z | row[i].w;
+                        any |= __shfl_xor_sync(0xffffffffu, any, 1);
+                        any |= __shfl_xor_sync(0xffffffffu, any, 2);
+                        if ((any & 0x7f7f7f7fu) == 0) vs[j] = 0.f;
+                    }
+                }
 #pragma unroll
                 for (int x = 0; x < NB; ++x)
 #pragma unroll
@@ -484,10 +498,11 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
                         if constexpr (KV8) {
                             const float big = over_keys([&](int j) { return ex2((s[x][j][r] - mn) * qs[x][r]) * vs[j]; });
                             const float lv = fminf(fmaxf(level[x][r] * alpha, big), 3e38f);      // (infinite, it would stay so)
-                            // kTop over the level's power of two, the exponent within fp32's range; a row
-                            // that has seen no key keeps its place
-                            const uint32_t ex = min(max(__float_as_uint(lv) >> 23, 7u), 253u);
-                            to = lv > 0.f ? scale_of(254u - ex) * kTop : put[x][r];
+                            // kTop over the level's power of two, 2^115 at most (a row that has seen no
+                            // value: any that comes fits there or moves it), so that weights of up to
+                            // kGrown stay finite beside a scale that was set to zero above
+                            const uint32_t ex = min(max(__float_as_uint(lv) >> 23, 18u), 253u);
+                            to = scale_of(254u - ex) * kTop;
                             from = 1.f / put[x][r];
                             level[x][r] = lv;
                         }

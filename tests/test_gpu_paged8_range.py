@@ -240,8 +240,36 @@ def test_tiny_weights_of_values_beside_zeros(ns, cs, gap, byte, dtype):
     q = torch.zeros(bt.T, 4, 128, dtype=dtype, device="cuda")
     q[..., 0] = 8.0
     scale = gap * math.log(2) / 8
-    # Below fp32's normal numbers: a row's place is 2^126 at most, a weight there is rounded
-    # to 2^-24 at the finest, off by half of it, and meets codes of 448 at most: 2^-25 *
-    # 2^-126 * 448 < 2^-142 per key.  A bf16 result is rounded to 2^-133.
-    lost = max(bt.lens) * 2.0 ** -142 + (2.0 ** -134 if dtype == BF else 2.0 ** -150)
+    # A row's place is 2^115 at most, a weight there is rounded to 2^-24 at the finest, off
+    # by half of it, and meets codes of 448 at most: 2^-25 * 2^-115 * 448 < 2^-131 per key.
+    # A bf16 result is rounded to 2^-133.
+    lost = max(bt.lens) * 2.0 ** -131 + (2.0 ** -134 if dtype == BF else 2.0 ** -150)
     _compare(bt, q, _run(vc, bt, q, scale), scale, lost=lost)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("zero,byte", [(127, 80), (200, 119), (254, 100), (40, 20)])
+@pytest.mark.parametrize("ns,cs", [([1, 1], [300, 1000]), ([2, 3], [1023, 95]), ([40], [200])])
+def test_rows_of_zeros_under_any_scale(ns, cs, zero, byte, dtype):
+    """Two keys in three have values of zero under a larger scale than the others (of
+    another quantizer, say): they take their weight, and nothing else."""
+    vc = lib()
+    for d in (64, 128):
+        bt = Batch8(ns, cs, 2, d, 16, dtype, seed=8)
+        _scale_values(bt, {b: [i for i in range(L) if i % 3] for b, L in enumerate(bt.lens)}, zero, zero=True)
+        _scale_values(bt, {b: range(0, L, 3) for b, L in enumerate(bt.lens)}, byte)
+        q = bt.randn(bt.T, 8, d)
+        _compare(bt, q, _run(vc, bt, q, 0.1), 0.1)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("case", range(len(SHARED)))
+def test_rows_of_zeros_after_a_shared_prefix(case, dtype):
+    vc = lib()
+    ns, own, first, prefix, Hq, Hkv, d, page = SHARED[case]
+    cs = [c + prefix[max(g for g, f in enumerate(first) if f <= b)] for b, c in enumerate(own)]
+    bt = Batch8(ns, cs, Hkv, d, page, dtype, seed=case)
+    sh = Shared(bt, first, prefix, 8)
+    _scale_values(bt, {b: [i for i in range(L) if i % 3 == 1] for b, L in enumerate(bt.lens)}, 170, zero=True)
+    q = bt.randn(bt.T, Hq, d)
+    _compare(bt, q, _run(vc, bt, q, d ** -0.5, sh), d ** -0.5)
