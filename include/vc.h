@@ -905,7 +905,12 @@ vc_status vc_paged_evict(const float *scores, int scores_stride, const vc_paged_
  * halves being joined in fp32 before the one rounding to dt.  The workspace holds
  * both halves of every row: 8 (d + 3) bytes per row and query head, beside
  * vc_paged_attn's.  Over prefixes of fewer than some thousand tokens it may take
- * longer than vc_paged_attn, by some 20 us at most (GB300).
+ * longer than vc_paged_attn (GB300, 32/8 heads of 128): decode steps with short
+ * contexts of their own 1 to 12 us; with long ones up to 1.7 times (32 sequences, a
+ * prefix of 128 and 4000 of their own: bf16 101 and 121 us, 8-bit 58 and 94, fp32 588 and
+ * 888); chunks of hundreds of tokens, whose halves pass through memory in fp32, up to
+ * 2.5 times (16 of 256 over a prefix of 512: bf16 82 and 202, 8-bit 94 and 212, fp32
+ * 1153 and 1335).
  * seq_start (device int32 [n + 1], ascending), len (device int32 [n]); with n = 0
  * both may be NULL.  VC_PAGED_BAD_LENGTH also reports a range outside [0, B] or
  * descending or a length outside [0, max_blocks * page] (its sequences attend on
@@ -983,6 +988,9 @@ vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, c
  * Batches of at least 4096 rows T * Hq / Hkv / B (bf16) hold their pages as bf16
  * in the workspace, 4 d bytes per table slot and kv head, where that is 1 GiB at most.
  * The order of a row's sums depends on the lengths of the whole batch.
+ * Kernels are chosen by the batch's average rows T * Hq / Hkv / B: a long chunk among many
+ * decoding sequences is better a call of its own (31 tokens over 4000 and a chunk of 97
+ * over 30000, 32/8 heads of 128: 360 us together, 134 apart).
  * A workspace for T rows (vc_paged_attn_shared's, too) is enough for fewer.
  */
 size_t vc_paged8_attn_workspace_bytes(const vc_paged8_cache *cache, int T, int Hq);

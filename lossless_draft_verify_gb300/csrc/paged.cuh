@@ -190,8 +190,11 @@ struct Cost {
 // and whole units of 3, 8, 12, of 2, 2, 4 and of 2, 1, 3, one token of one sequence over
 // 1000 (32/8 heads of 128) 23.9, 11.6 and 10.7 us, of 16 over 500 21.5, 12.8 and 12.6, of
 // 16 over 32768 the same.  A unit that is little longer (kSlack) than a piece is not cut
-// either: cutting, and without, 128 sequences of 150 tokens 26.5 and 19.9 us, 96 20.8 and
-// 17.8, 128 of 250 30.3 and 27.0.
+// either: of units longer than a piece a piece holds one middle at most, so that a warp
+// takes at most kSlack tiles more, some 4 us, and the batch needs no parts, whose merge
+// takes about as long.  (Of shorter units a piece can hold several middles, and one taken
+// whole may be another unit's length too much; they are cut.)  Cutting, and without, 128
+// sequences of 150 tokens 26.5 and 19.9 us, 96 20.8 and 17.8, 128 of 250 30.3 and 27.0.
 struct CostFew {
     static constexpr bool kByTiles = true;
     static constexpr int kUnitCost = 2;
@@ -603,7 +606,14 @@ cudaError_t attn_tc(const Pool &P, const WorkDim &W, int d, const void *q, int H
 cudaError_t attn_tc_planned(const Pool &P, const WorkDim &W, int d, const void *q, int Hq, float sl2, const Halves &H,
                             const Parts &parts, int32_t *status, cudaStream_t st);
 // paged_attn_few.cuh: for batches of few rows: pieces per warp, row tiles of few_rows()
-// (0: the batch has too many), of fp32 rows 8 or 16 in all batches.  Over 8-bit pages,
+// (0: the batch has too many), of fp32 rows 8 or 16 in all batches.  The host knows the
+// batch's average only (lengths lie on the device), and each kernel does badly what the
+// other is for: 8-bit pages, 32/8 heads of 128, 31 decoding sequences over 4000 with one
+// chunk of 97 over 30000 (16 rows on average) 360 us here, with one of 98 192 on the tensor
+// cores, as two calls 57 and 77; 127 over 1000 with one of 385 1223, 386 499, apart 61 and
+// 288; 15 over 32768 with one of 2048 over 30000 1694, apart 169 and 763.  The bound is that
+// of batches of one kind: at 16 rows 70 us here and 122 there, from 24 on there is nothing
+// between them.  Over 8-bit pages,
 // and planned batches over bf16 ones: begun beside the kernel launched before, which
 // is waited for at the end only, unless it is the plan's (first)
 constexpr int few_keys(int d, bool kv8) { return 4096 / (kv8 ? d : 2 * d); }      // of a tile: 4 KB

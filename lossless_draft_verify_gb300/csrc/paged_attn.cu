@@ -374,6 +374,8 @@ struct SharedLayout {
 // and 14, 17 us, over 8192 34, 33 and 21, 20, over 32768 48, 50 and 40, 31; 8 over 512
 // 29, 30 and 16, 17, over 8192 34, 40 and 26, 23, over 32768 48, 49 and 57, 45; 16 over
 // 512 29, 31 and 17, 19, over 8192 35, 41 and 38, 34, over 32768 51, 52 and 99, 75.
+// One group of 32 over 8000 beside 15 of two over 100: 64 and 52 us (without sharing 156
+// and 87).
 constexpr long kGroupRows = 32;
 
 SharedLayout shared_layout(vc_dtype dt, int d, int T, int G, int Hq, int B, long cap, int n_groups, bool kv8)

@@ -1,6 +1,7 @@
 // paged_attn_few.cuh -- causal attention over 8-bit pages, and over bf16 pages in
 // planned batches, for batches of few rows (decoding, drafting): up to 16 (query,
-// head) rows per kv head; and of fp32 rows over 8-bit pages in all batches.
+// head) rows per kv head, on the batch's average; and of fp32 rows over 8-bit pages in
+// all batches.
 //
 //   out_i = sum_j p_ij 2^f_j v_j / sum_j p_ij,  p_ij = exp(scale 2^e_j q_i . k_j)
 //
@@ -25,7 +26,8 @@
 // those of the copies.
 //
 // bf16 pages (KV8 false) take the same products of bf16 operands: K through ldmatrix,
-// V through its transposing form, and nothing is scaled.  They serve the own slots of
+// V through its transposing form, and nothing is scaled; the weights are rounded to bf16,
+// as in the tensor-core kernel.  They serve the own slots of
 // sequences that share a prefix, a few hundred tokens each, for which the tensor-core
 // kernel's 8 us per unit are too many, and the prefixes of small groups.
 //
@@ -37,9 +39,11 @@
 //
 // Ranges.  q is scaled by its row's largest exponent to 2^14 (beside the roundings to
 // 11 or 22 bits, an element is off by at most 2^-39 of the row's largest; rows below
-// 2^-112 are taken as of that size).  The running maximum is raised when it has grown by more than 2^8, as in the tensor-core kernel.  The weights p 2^f, which
-// become f16, are scaled by a power of two per row such that the largest so far lies
-// at 2^6: what is lost below f16's smallest number is 2^-31 of it per key.
+// 2^-112 are taken as of that size).  The running maximum is raised when it has grown by
+// more than 2^8, as in the tensor-core kernel, and with a row's first key.  The weights
+// p 2^f, which become f16, are scaled by a power of two per row, its place, such that the
+// largest so far lies at 2^6: what is lost below f16's smallest number is 2^-31 of it per
+// key.  They may grow to 2^15 before the place moves.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -273,7 +277,7 @@ attn_few_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__
         };
         auto head_row = [&](int r) { return row_of(it.out_tok0(), r); };      // of out and lse_out
         if (key0 < 0) {
-            // ---- a part begins; Q: row g of each block, scaled to [1, 2) at its largest ----
+            // ---- a part begins; Q: row g of each block (8-bit pages: its largest in [kQTop, 2 kQTop)) ----
             key0 = it.t_lo * BN;
             kall = it.last(row0 / A.W.G);                    // keys every row sees
 #pragma unroll

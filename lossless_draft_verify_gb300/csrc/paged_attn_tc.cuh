@@ -38,9 +38,11 @@
 // eight more warps (12-19) write them as bf16 tiles, scale included, into the
 // ring that the products read.  code * 2^e is a bf16 number, so this rounds
 // nothing: the output is that of bf16 pages which hold the same numbers.  It serves
-// 17 to 4095 rows per sequence and kv head: nine tokens of 16 sequences over 16384 (36
-// rows) 216 us, 1024 over 30000 467; the expansion of a tile is what is added to the
-// chain (169 us and, of 2048 over 30000, 728 of 917 without its arithmetic).
+// batches of 17 to 4095 rows per sequence and kv head on average, planned ones, and
+// those whose expanded pages would not fit (paged_attn.cu): nine tokens of 16 sequences
+// over 16384 (36 rows) 217 us, 512 tokens over 30000 (2048 rows) 245.  The expansion of a
+// tile is what is added to the chain: of the 217 us 48 are its arithmetic, and 189 of
+// the 917 of 2048 tokens over 30000, which now expand their pages once.
 //
 // V rows past the sequence's end may hold any bits and 0 * NaN is not 0: those
 // that share the last page with tokens are cleared in shared memory, further
