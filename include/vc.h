@@ -981,10 +981,11 @@ vc_status vc_paged8_read(const vc_paged8_cache *cache, const int32_t *q_start, c
  * over 8-bit pages, as on pages that hold the values: codes and scales enter the
  * products exactly, whatever the scales.  bf16 rows: the softmax weights are rounded
  * to bf16, in batches of at most 16 rows T * Hq / Hkv / B to f16 instead, placed by
- * their row's largest weighted value (a weight below 2^-31 of that is lost); there q
- * is exact down to 2^-39 of its row's largest element.  fp32 rows: q and the weights
- * as two f16 terms, 22 bits, sums in fp32.  A weighted value may also be off by 2^-131;
- * the keys' number times the largest |value| stays below 1e36.
+ * their row's largest weight times scale of a value row that is not all zeros (a weight
+ * times scale below 2^-31 of that is lost); there q is exact down to 2^-39 of its row's
+ * largest element.  fp32 rows: q and the weights as two f16 terms, 22 bits, sums in fp32.
+ * A weighted value may also be off by 2^-131; the keys' number times the largest |value|
+ * stays below 1e36.
  * Batches of at least 4096 rows T * Hq / Hkv / B (bf16) hold their pages as bf16
  * in the workspace, 4 d bytes per table slot and kv head, where that is 1 GiB at most.
  * The order of a row's sums depends on the lengths of the whole batch.
